@@ -34,6 +34,7 @@ __all__ = [
     "spmm_check_wait_timeout", "spmm_plan_create_range", "spmm_partition_rows",
     "spmm_plan_prepare_blocks",
     "PlanInfo", "REDUCE", "FAMILY", "lib", "build_library",
+    "ExpertRoutes", "BlockSelection", "block_means", "select_blocks",
 ]
 
 REDUCE = {"sum": 0, "mean": 1, "max": 2}
@@ -501,3 +502,7 @@ def spmm_mean(rowptr, col, val, mat):
 
 def spmm_max(rowptr, col, val, mat):
     return spmm(rowptr, col, val, mat, "max")
+
+
+# products whose sparse matrix the model chooses (built on the names above)
+from .dynamic import BlockSelection, ExpertRoutes, block_means, select_blocks  # noqa: E402

@@ -1,0 +1,625 @@
+// Selected-block attention, backward. With P = exp(scale Q K^T - lse),
+// dP = dO V^T, delta = <dO, O> and dS = scale P (dP - delta):
+//   dQ = dS K       by query, like the forward;
+//   dV = P^T dO, dK = dS^T Q       by key block, over the queries that chose it:
+// the transpose of the selection, as one bit per query in a row of words per
+// (sequence, kv head, block), set with integer atomics (order-independent).
+#include "blocks.cuh"
+
+namespace spmm {
+namespace {
+
+struct BwdArgs {
+    BlkArgs a;
+    const void *out, *dout;
+    int64_t do_sb, do_st, do_sh;
+    const float *lse;
+    float *delta;            // [B, Tq, Hq]
+    void *dq, *dk, *dv;
+    uint32_t *bits;          // [B, Hk, NB, words]
+    int words;               // ceil(Tq / 32)
+    int chunks;              // ranges of queries per key block
+    int chunk_words;
+    float *part;             // [chunks][2][B, Tk, Hk, D] when chunks > 1
+    int64_t part_stride;     // B Tk Hk D
+    int gt;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(128) k_delta(BwdArgs p, int64_t rows) {
+    constexpr int U = D / 8;
+    const int64_t i = (int64_t)blockIdx.x * (128 / U) + threadIdx.x / U;
+    const int u = threadIdx.x % U;
+    float s = 0.0f;
+    if (i < rows) {
+        const int head = (int)(i % p.a.Hq);
+        const int64_t bt = i / p.a.Hq;
+        const int64_t t = bt % p.a.Tq, b = bt / p.a.Tq;
+        float x[8], y[8];
+        ld_pack<T, 8>((const T *)p.out + i * D + u * 8, x);
+        ld_pack<T, 8>((const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + u * 8, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+    }
+#pragma unroll
+    for (int o = U / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (i < rows && u == 0) p.delta[i] = s;
+}
+
+__global__ void k_set_bits(BwdArgs p, int64_t entries) {
+    const BlkArgs &a = p.a;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= entries) return;
+    const int64_t row = i / a.n;
+    const int j = (int)(i % a.n);
+    const int32_t *list = a.blocks + row * a.n;
+    if (!blk_entry_ok(list, j, a.NB)) return;
+    const int h = (int)(row % a.Hk);
+    const int64_t bt = row / a.Hk;
+    const int t = (int)(bt % a.Tq);
+    const int64_t b = bt / a.Tq;
+    atomicOr(p.bits + ((b * a.Hk + h) * a.NB + list[j]) * p.words + (t >> 5), 1u << (t & 31));
+}
+
+// fp16 has 5 bits of exponent: weights and gradients well below 2^-14 would lose
+// their digits in it. So P is held as P 2^14 (at most 2^14, up to its rounding),
+// and dS as dS 2^e, where a warp lowers its e (and rescales what it has summed)
+// whenever a tile's largest |dS| would reach 2^15; both are exact powers of two,
+// taken out of the sums at the end. bf16 has fp32's exponent and needs neither.
+template <typename T> constexpr bool kNarrow = std::is_same<T, __half>::value;
+template <typename T> constexpr float kPShift = kNarrow<T> ? 14.0f : 0.0f;
+template <typename T> constexpr float kPUnit = kNarrow<T> ? 1.0f / 16384.0f : 1.0f;
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
+
+struct DsScale {
+    int e = 100;
+    // Folds in one tile's largest finite |dS| (per lane); returns the factor for
+    // what is summed already (1 mostly; the same in the whole warp).
+    __device__ __forceinline__ float lower(float lane_max) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(lane_max));
+        const int want = 14 - ((int)(m >> 23) - 127);
+        if (want >= e) return 1.0f;
+        const float f = pow2i(max(want - e, -126));
+        e = want;
+        return f;
+    }
+};
+
+__device__ __forceinline__ float finite_max(float m, float x) {
+    x = fabsf(x);
+    return x < INFINITY ? fmaxf(m, x) : m;       // false for NaN
+}
+
+// ----------------------------------------------------------------- dQ
+constexpr int kRowWarps = 4;
+constexpr int kRowThreads = 32 * kRowWarps;
+
+// Two keys' rows (r, r + 8) of a slice as the A operand over D.
+template <typename T, int D>
+__device__ __forceinline__ void load_keys(uint4 (&x)[D / 32][2], const T *p, int64_t st, int key0,
+                                          int limit, int r, int c) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int key = key0 + r + 8 * e;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i)
+            x[i][e] = key < limit ? __ldg((const uint4 *)(p + key * st + 32 * i + 8 * c))
+                                  : make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kRowThreads) k_dq_rows(BwdArgs p) {
+    constexpr int R = 8 * NT;
+    __shared__ float sm[kRowWarps][R][D + 4];
+    const BlkArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int gt = blockIdx.x % p.gt;
+    const int64_t list_id = blockIdx.x / p.gt;
+    const int h = (int)(list_id % a.Hk);
+    const int64_t bt = list_id / a.Hk;
+    const int t = (int)(bt % a.Tq), b = (int)(bt / a.Tq);
+    const int g0 = gt * R, ng = min(a.G - g0, R);
+    const int limit = blk_limit(a, blk_len(a, b), t);
+    const int32_t *list = a.blocks + list_id * a.n;
+    const float scale2 = a.scale * kLog2e;
+    const int head0 = h * a.G + g0;
+    const int64_t row0 = bt * a.Hq + head0;
+
+    uint4 q[NT][D / 32], g[NT][D / 32];
+    const T *qp = (const T *)a.q + b * a.q_sb + t * a.q_st + head0 * a.q_sh;
+    const T *gp = (const T *)p.dout + b * p.do_sb + t * p.do_st + head0 * p.do_sh;
+    float lse2[NT][2], delta[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int row = 8 * i + r;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            q[i][d] = row < ng ? __ldg((const uint4 *)(qp + row * a.q_sh + 32 * d + 8 * c)) : zero;
+            g[i][d] = row < ng ? __ldg((const uint4 *)(gp + row * p.do_sh + 32 * d + 8 * c)) : zero;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int w = 8 * i + 2 * c + e;
+            const float x = w < ng ? p.lse[row0 + w] * kLog2e : -INFINITY;
+            lse2[i][e] = x == -INFINITY ? INFINITY : x;     // a row without keys: P = 0
+            delta[i][e] = w < ng ? p.delta[row0 + w] : 0.0f;
+        }
+    }
+    float o[D / 16][NT][4] = {};
+    DsScale ds_scale;
+    const T *kp = (const T *)a.k + b * a.k_sb + h * a.k_sh;
+    const T *vp = (const T *)a.v + b * a.v_sb + h * a.v_sh;
+    const int per = a.block / 16, all = a.n * per;
+    for (int s = warp; s < all; s += kRowWarps) {
+        const int j = s / per;
+        if (!blk_entry_ok(list, j, a.NB)) continue;
+        const int key0 = list[j] * a.block + (s % per) * 16;
+        if (key0 >= limit) continue;
+        uint4 x[D / 32][2];
+        float st[NT][4] = {}, dp[NT][4] = {};
+        load_keys<T, D>(x, kp, a.k_st, key0, limit, r, c);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+                mma16816<T>(st[i], x[d][0].x, x[d][1].x, x[d][0].y, x[d][1].y, q[i][d].x, q[i][d].y);
+                mma16816<T>(st[i], x[d][0].z, x[d][1].z, x[d][0].w, x[d][1].w, q[i][d].z, q[i][d].w);
+            }
+        load_keys<T, D>(x, vp, a.v_st, key0, limit, r, c);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+                mma16816<T>(dp[i], x[d][0].x, x[d][1].x, x[d][0].y, x[d][1].y, g[i][d].x, g[i][d].y);
+                mma16816<T>(dp[i], x[d][0].z, x[d][1].z, x[d][0].w, x[d][1].w, g[i][d].z, g[i][d].w);
+            }
+        uint4 kt[D / 64][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 2 * c + (e & 1) + (e >> 1) * 8;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+                kt[i][e] = key < limit ? __ldg((const uint4 *)(kp + key * a.k_st + 64 * i + 8 * r))
+                                       : make_uint4(0, 0, 0, 0);
+        }
+        float ds_max = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool seen = key0 + r + (e >> 1) * 8 < limit;
+                const float pr = ex2(fmaf(st[i][e], scale2, -lse2[i][e & 1]));
+                st[i][e] = seen ? pr * (dp[i][e] - delta[i][e & 1]) * a.scale : 0.0f;
+                if constexpr (kNarrow<T>) ds_max = finite_max(ds_max, st[i][e]);
+            }
+        if constexpr (kNarrow<T>) {
+            const float f = ds_scale.lower(ds_max);
+            if (f != 1.0f)
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[d][i][e] *= f;
+            const float u = pow2i(ds_scale.e);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[i][e] *= u;
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const uint32_t b0 = movmatrix(pack2<T>(st[i][0], st[i][1]));
+            const uint32_t b1 = movmatrix(pack2<T>(st[i][2], st[i][3]));
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                const int u = d / 4, w = d % 4;
+                const uint32_t k0 = (&kt[u][0].x)[w], k1 = (&kt[u][1].x)[w];
+                const uint32_t k8 = (&kt[u][2].x)[w], k9 = (&kt[u][3].x)[w];
+                mma16816<T>(o[d][i], __byte_perm(k0, k1, 0x5410), __byte_perm(k0, k1, 0x7632),
+                            __byte_perm(k8, k9, 0x5410), __byte_perm(k8, k9, 0x7632), b0, b1);
+            }
+        }
+    }
+    const float unit = kNarrow<T> ? pow2i(-ds_scale.e) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                float *x = &sm[warp][8 * i + 2 * c + e][64 * (d / 4) + 8 * r + 2 * (d % 4)];
+                x[0] = o[d][i][e] * unit;
+                x[1] = o[d][i][e + 2] * unit;
+            }
+    __syncthreads();
+    constexpr int U = D / 8;
+    for (int i = threadIdx.x; i < R * U; i += kRowThreads) {
+        const int row = i / U, d = i % U * 8;
+        if (row >= ng) continue;
+        float x[8] = {};
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += sm[w][row][d + e];
+        st_pack<T, 8>((T *)p.dq + (row0 + row) * D + d, x);
+    }
+}
+
+// ------------------------------------------------------------- dK and dV
+// A CTA per (tile of KT = 16 W keys of one block, kv head, sequence, range of
+// queries), a warp per 16 keys. The range's words are expanded to a list of
+// queries, whose (query, head) rows are taken 32 at a time: Q and dO rows are
+// gathered into shared memory by asynchronous copies, two tiles in flight.
+constexpr int kRt = 32;             // rows per tile
+constexpr int kSegWords = 32;       // words expanded at a time (1024 queries)
+
+// 16-byte chunk `i` of row `row` of a [rows][D] tile: the chunks of eight
+// consecutive rows at the same i fall in different banks.
+template <int D> __device__ __forceinline__ uint32_t tile_at(int row, int i) {
+    return (uint32_t)(row * D * 2 + ((i ^ (row & 7)) << 4));
+}
+
+template <typename T, int D, int W>
+__global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
+    constexpr int KT = 16 * W, C = D / 8, threads = 32 * W;
+    extern __shared__ __align__(128) unsigned char smem[];
+    // K, V [KT][D]; two stages of Q, dO [kRt][D]; then per stage lse, delta, limit [kRt]
+    const uint32_t sK = smem_addr(smem), sV = sK + KT * D * 2, sQ = sV + KT * D * 2;
+    constexpr int stage_bytes = 2 * kRt * D * 2;
+    float *row_f = (float *)(smem + 2 * KT * D * 2 + 2 * stage_bytes);   // [2][3][kRt]
+    int *list = (int *)(row_f + 2 * 3 * kRt);                            // [1024]
+    __shared__ int word_base[kSegWords + 1];
+
+    const BlkArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const int tiles = a.block / KT;
+    const int tile = blockIdx.x % tiles, blk = blockIdx.x / tiles;
+    const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk;
+    const int chunk = blockIdx.z;
+    const int key0 = blk * a.block + tile * KT;
+    if (key0 >= a.Tk) return;
+    const int len = blk_len(a, b);
+    const uint32_t *bits = p.bits + ((int64_t)blockIdx.y * a.NB + blk) * p.words;
+    const int w_end = min(p.words, (chunk + 1) * p.chunk_words);
+    const float scale2 = a.scale * kLog2e, ds_unit = a.scale * kPUnit<T>;
+
+    const T *kp = (const T *)a.k + b * a.k_sb + h * a.k_sh;
+    const T *vp = (const T *)a.v + b * a.v_sb + h * a.v_sh;
+    for (int i = threadIdx.x; i < KT * C; i += threads) {
+        const int row = i / C, d = i % C;
+        const int key = key0 + row;
+        const bool live = key < len;
+        cp16(sK + tile_at<D>(row, d), kp + (live ? key : 0) * a.k_st + d * 8, live);
+        cp16(sV + tile_at<D>(row, d), vp + (live ? key : 0) * a.v_st + d * 8, live);
+    }
+    cp_commit();
+
+    float dk[D / 8][4] = {}, dv[D / 8][4] = {};
+    DsScale ds_scale;
+    for (int w0 = chunk * p.chunk_words; w0 < w_end; w0 += kSegWords) {
+        __syncthreads();
+        if (warp == 0) {                         // counts of the words, then the list
+            const uint32_t x = w0 + lane < w_end ? bits[w0 + lane] : 0u;
+            int n = __popc(x), incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            word_base[lane] = incl - n;
+            if (lane == 31) word_base[32] = incl;
+            int at = incl - n;
+            for (uint32_t m = x; m; m &= m - 1) list[at++] = (w0 + lane) * 32 + __ffs(m) - 1;
+        }
+        __syncthreads();
+        const int rows = word_base[32] * a.G;
+        const int steps = (rows + kRt - 1) / kRt;
+        auto fetch = [&](int step) {
+            const uint32_t base = sQ + (step & 1) * stage_bytes;
+            for (int i = threadIdx.x; i < kRt * C; i += threads) {
+                const int row = i / C, d = i % C, f = step * kRt + row;
+                const bool live = f < rows;
+                const int t = live ? list[f / a.G] : 0, head = h * a.G + (live ? f % a.G : 0);
+                cp16(base + tile_at<D>(row, d),
+                     (const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + d * 8, live);
+                cp16(base + kRt * D * 2 + tile_at<D>(row, d),
+                     (const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + d * 8, live);
+            }
+            cp_commit();
+            for (int row = threadIdx.x; row < kRt; row += threads) {
+                const int f = step * kRt + row;
+                float x = INFINITY, y = 0.0f;
+                int limit = 0;
+                if (f < rows) {
+                    const int t = list[f / a.G];
+                    const int64_t i = ((int64_t)b * a.Tq + t) * a.Hq + h * a.G + f % a.G;
+                    x = p.lse[i] * kLog2e;
+                    if (x == -INFINITY) x = INFINITY;        // a row without keys: P = 0
+                    y = p.delta[i];
+                    limit = blk_limit(a, len, t);
+                }
+                float *m = row_f + (step & 1) * 3 * kRt;
+                m[row] = x;
+                m[kRt + row] = y;
+                m[2 * kRt + row] = __int_as_float(limit);
+            }
+        };
+        if (steps) fetch(0);
+        for (int step = 0; step < steps; ++step) {
+            if (step + 1 < steps) {
+                fetch(step + 1);
+                cp_wait<1>();
+            } else {
+                cp_wait<0>();
+            }
+            __syncthreads();
+            const uint32_t tq = sQ + (step & 1) * stage_bytes, tg = tq + kRt * D * 2;
+            const float *m = row_f + (step & 1) * 3 * kRt;
+            float st[4][4] = {}, dp[4][4] = {};
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t ka[4], va[4];
+                // A: rows (keys) lane % 16 of the warp's 16, chunk 2 kk + lane / 16
+                const uint32_t at = tile_at<D>(warp * 16 + (lane & 15), 2 * kk + (lane >> 4));
+                ldsm4(sK + at, ka);
+                ldsm4(sV + at, va);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // B: rows 16 i + (lane / 16) 8 + lane % 8, chunk 2 kk + (lane / 8) % 2
+                    uint32_t x[4];
+                    const uint32_t bt = tile_at<D>(16 * i + (lane >> 4) * 8 + (lane & 7),
+                                                   2 * kk + ((lane >> 3) & 1));
+                    ldsm4(tq + bt, x);
+                    mma16816<T>(st[2 * i], ka[0], ka[1], ka[2], ka[3], x[0], x[1]);
+                    mma16816<T>(st[2 * i + 1], ka[0], ka[1], ka[2], ka[3], x[2], x[3]);
+                    ldsm4(tg + bt, x);
+                    mma16816<T>(dp[2 * i], va[0], va[1], va[2], va[3], x[0], x[1]);
+                    mma16816<T>(dp[2 * i + 1], va[0], va[1], va[2], va[3], x[2], x[3]);
+                }
+            }
+            uint32_t pa[4][2], da[4][2];         // P^T and dS^T of n-tile i, keys r and r + 8
+            float ds_max = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 8 * i + 2 * c;
+                const float2 l = *(const float2 *)(m + row), d = *(const float2 *)(m + kRt + row);
+                const int2 lim = *(const int2 *)(m + 2 * kRt + row);
+                float pr[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = key0 + warp * 16 + r + (e >> 1) * 8;
+                    const bool seen = key < (e & 1 ? lim.y : lim.x);
+                    pr[e] = seen ? ex2(fmaf(st[i][e], scale2, kPShift<T> - (e & 1 ? l.y : l.x))) : 0.0f;
+                    st[i][e] = seen ? pr[e] * (dp[i][e] - (e & 1 ? d.y : d.x)) * ds_unit : 0.0f;
+                    if constexpr (kNarrow<T>) ds_max = finite_max(ds_max, st[i][e]);
+                }
+                pa[i][0] = pack2<T>(pr[0], pr[1]);
+                pa[i][1] = pack2<T>(pr[2], pr[3]);
+            }
+            float u = 1.0f;
+            if constexpr (kNarrow<T>) {
+                const float f = ds_scale.lower(ds_max);
+                if (f != 1.0f)
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dk[n][e] *= f;
+                u = pow2i(ds_scale.e);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                da[i][0] = pack2<T>(st[i][0] * u, st[i][1] * u);
+                da[i][1] = pack2<T>(st[i][2] * u, st[i][3] * u);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)          // 16 rows at a time
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t x[4];
+                    // B: row 16 i + lane % 16, chunk 2 n + lane / 16, transposed
+                    const uint32_t bt = tile_at<D>(16 * i + (lane & 15), 2 * n + (lane >> 4));
+                    ldsm4_t(tg + bt, x);
+                    mma16816<T>(dv[2 * n], pa[2 * i][0], pa[2 * i][1], pa[2 * i + 1][0],
+                                pa[2 * i + 1][1], x[0], x[1]);
+                    mma16816<T>(dv[2 * n + 1], pa[2 * i][0], pa[2 * i][1], pa[2 * i + 1][0],
+                                pa[2 * i + 1][1], x[2], x[3]);
+                    ldsm4_t(tq + bt, x);
+                    mma16816<T>(dk[2 * n], da[2 * i][0], da[2 * i][1], da[2 * i + 1][0],
+                                da[2 * i + 1][1], x[0], x[1]);
+                    mma16816<T>(dk[2 * n + 1], da[2 * i][0], da[2 * i][1], da[2 * i + 1][0],
+                                da[2 * i + 1][1], x[2], x[3]);
+                }
+            __syncthreads();
+        }
+    }
+    cp_wait<0>();
+    const float k_unit = kNarrow<T> ? pow2i(-ds_scale.e) : 1.0f, v_unit = kPUnit<T>;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dk[n][e] *= k_unit;
+            dv[n][e] *= v_unit;
+        }
+    // keys r and r + 8 of the warp's 16, elements 8 n + 2 c and the next
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int key = key0 + warp * 16 + r + 8 * e;
+        if (key >= a.Tk) continue;
+        const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + h) * D + 2 * c;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+            if (p.chunks == 1) {
+                *(uint32_t *)((T *)p.dk + at + 8 * n) = pack2<T>(dk[n][2 * e], dk[n][2 * e + 1]);
+                *(uint32_t *)((T *)p.dv + at + 8 * n) = pack2<T>(dv[n][2 * e], dv[n][2 * e + 1]);
+            } else {
+                float *x = p.part + (int64_t)(2 * chunk) * p.part_stride + at + 8 * n;
+                *(float2 *)x = make_float2(dk[n][2 * e], dk[n][2 * e + 1]);
+                *(float2 *)(x + p.part_stride) = make_float2(dv[n][2 * e], dv[n][2 * e + 1]);
+            }
+        }
+    }
+}
+
+// The ranges' parts, added in order.
+template <typename T> __global__ void __launch_bounds__(256) k_dkdv_join(BwdArgs p) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= p.part_stride) return;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        float s[8];
+        ld_pack<float, 8>(p.part + w * p.part_stride + i, s);
+        for (int ch = 1; ch < p.chunks; ++ch) {
+            float x[8];
+            ld_pack<float, 8>(p.part + (2 * ch + w) * p.part_stride + i, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += x[e];
+        }
+        st_pack<T, 8>((T *)(w ? p.dv : p.dk) + i, s);
+    }
+}
+
+// ------------------------------------------------------------------- host
+struct BwdPlan {
+    int64_t words, chunk_words, chunks;
+    int64_t bits_bytes, delta_bytes, part_bytes;
+    int W;
+};
+
+// Ranges of queries per key block: enough CTAs to fill the SMs several times
+// over (and to cut up a block that every query chose), each of 256 queries or more.
+BwdPlan bwd_plan(const spmm_blocks_shape *s) {
+    BwdPlan p;
+    const int64_t NB = (s->Tk + s->block - 1) / s->block;
+    p.W = s->block == 16 ? 1 : s->block == 32 ? 2 : 4;
+    p.words = (s->Tq + 31) / 32;
+    const int64_t ctas = std::max<int64_t>(1, s->B * s->Hk * NB * (s->block / (16 * p.W)));
+    int64_t chunks = std::min<int64_t>((152 * 8 * (4 / p.W) + ctas - 1) / ctas, (p.words + 7) / 8);
+    chunks = std::max<int64_t>(1, std::min<int64_t>(chunks, 64));
+    p.chunk_words = std::max<int64_t>(1, (p.words + chunks - 1) / chunks);
+    p.chunks = std::max<int64_t>(1, (p.words + p.chunk_words - 1) / p.chunk_words);
+    p.bits_bytes = round_up(s->B * s->Hk * NB * p.words * 4, 256);
+    p.delta_bytes = round_up(s->B * s->Tq * s->Hq * 4, 256);
+    p.part_bytes = p.chunks > 1 ? p.chunks * 2 * s->B * s->Tk * s->Hk * s->D * 4 : 0;
+    return p;
+}
+
+template <typename T, int D, int W>
+cudaError_t launch_dkdv(const BwdArgs &p, const BwdPlan &bp, int64_t B, cudaStream_t s) {
+    constexpr int KT = 16 * W;
+    const size_t smem = 2 * KT * D * 2 + 4 * kRt * D * 2 + 2 * 3 * kRt * 4 + kSegWords * 32 * 4;
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_dkdv<T, D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.a.NB * (p.a.block / KT)), (unsigned)(B * p.a.Hk),
+                    (unsigned)p.chunks);
+    k_dkdv<T, D, W><<<grid, 32 * W, smem, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s, cudaStream_t cs) {
+    const int64_t rows = s->B * s->Tq * s->Hq, lists = s->B * s->Tq * s->Hk;
+    cudaError_t e = cudaSuccess;
+    constexpr int per = 128 / (D / 8);
+    k_delta<T, D><<<(unsigned)((rows + per - 1) / per), 128, 0, cs>>>(p, rows);
+    count_launch();
+    if (p.a.G <= 8) {
+        p.gt = 1;
+        k_dq_rows<T, D, 1><<<(unsigned)lists, kRowThreads, 0, cs>>>(p);
+    } else {
+        p.gt = (p.a.G + 15) / 16;
+        k_dq_rows<T, D, 2><<<(unsigned)(lists * p.gt), kRowThreads, 0, cs>>>(p);
+    }
+    count_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess || s->Tk == 0) return e;
+    e = cudaMemsetAsync(p.bits, 0, (size_t)bp.bits_bytes, cs);
+    if (e != cudaSuccess) return e;
+    const int64_t entries = lists * s->n;
+    k_set_bits<<<(unsigned)((entries + 255) / 256), 256, 0, cs>>>(p, entries);
+    count_launch();
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (bp.W == 1) e = launch_dkdv<T, D, 1>(p, bp, s->B, cs);
+    else if (bp.W == 2) e = launch_dkdv<T, D, 2>(p, bp, s->B, cs);
+    else e = launch_dkdv<T, D, 4>(p, bp, s->B, cs);
+    if (e != cudaSuccess || p.chunks == 1) return e;
+    k_dkdv_join<T><<<(unsigned)((p.part_stride / 8 + 255) / 256), 256, 0, cs>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace spmm
+
+extern "C" {
+
+int64_t spmm_blocks_backward_workspace(const spmm_blocks_shape *s) {
+    using namespace spmm;
+    if (blk_check(s, true) != SPMM_OK) return 0;
+    const BwdPlan p = bwd_plan(s);
+    return p.bits_bytes + p.delta_bytes + p.part_bytes;
+}
+
+spmm_status spmm_blocks_backward(const spmm_blocks_shape *s, spmm_rows q, spmm_rows k,
+                                 spmm_rows v, const int32_t *blocks, const void *out,
+                                 const float *lse, spmm_rows dout, void *dq, void *dk, void *dv,
+                                 void *work, int64_t work_bytes, void *stream) {
+    using namespace spmm;
+    const spmm_status st = blk_check(s, true);
+    if (st != SPMM_OK) return st;
+    if (s->B == 0 || (s->Tq == 0 && s->Tk == 0)) return SPMM_OK;
+    cudaStream_t cs = (cudaStream_t)stream;
+    if (s->Tk > 0 && (!dk || !dv || (uintptr_t)dk % 16 || (uintptr_t)dv % 16))
+        return SPMM_ERR_INVALID_ARG;
+    if (s->Tq == 0) {
+        const size_t bytes = (size_t)(s->B * s->Tk * s->Hk * s->D * 2);
+        cudaError_t e = cudaMemsetAsync(dk, 0, bytes, cs);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dv, 0, bytes, cs);
+        return cuda_status(e);
+    }
+    if (!blocks || !lse || !out || (uintptr_t)out % 16 || !dq || (uintptr_t)dq % 16)
+        return SPMM_ERR_INVALID_ARG;
+    if (!rows_ok(q, 2) || !rows_ok(dout, 2) ||
+        (s->Tk > 0 && (!rows_ok(k, 2) || !rows_ok(v, 2))))
+        return SPMM_ERR_INVALID_ARG;
+    const BwdPlan bp = bwd_plan(s);
+    if (!work || (uintptr_t)work % 16 || work_bytes < bp.bits_bytes + bp.delta_bytes + bp.part_bytes)
+        return SPMM_ERR_INVALID_ARG;
+    if (s->B * s->Hk > 65535 || s->B * s->Tq * s->Hk > INT32_MAX / s->n)
+        return SPMM_ERR_UNSUPPORTED;
+    BwdArgs p{};
+    p.a = blk_args(s, blocks);
+    set_rows(p.a.q, p.a.q_sb, p.a.q_st, p.a.q_sh, q);
+    set_rows(p.a.k, p.a.k_sb, p.a.k_st, p.a.k_sh, k);
+    set_rows(p.a.v, p.a.v_sb, p.a.v_st, p.a.v_sh, v);
+    set_rows(p.dout, p.do_sb, p.do_st, p.do_sh, dout);
+    p.out = out;
+    p.lse = lse;
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    char *w = (char *)work;
+    p.bits = (uint32_t *)w;
+    p.delta = (float *)(w + bp.bits_bytes);
+    p.part = (float *)(w + bp.bits_bytes + bp.delta_bytes);
+    p.part_stride = s->B * s->Tk * s->Hk * s->D;
+    p.words = (int)bp.words;
+    p.chunks = (int)bp.chunks;
+    p.chunk_words = (int)bp.chunk_words;
+    cudaError_t e;
+    if (s->dtype == SPMM_BF16)
+        e = s->D == 64 ? launch_bwd<__nv_bfloat16, 64>(p, bp, s, cs)
+                       : launch_bwd<__nv_bfloat16, 128>(p, bp, s, cs);
+    else
+        e = s->D == 64 ? launch_bwd<__half, 64>(p, bp, s, cs) : launch_bwd<__half, 128>(p, bp, s, cs);
+    return cuda_status(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,443 @@
+// Selected-block attention, the cheap score: the mean key of each block, the
+// product of every query group's summed rows with those means, and the n best
+// blocks of each query.
+#include "blocks.cuh"
+
+namespace spmm {
+namespace {
+
+// ------------------------------------------------------------------ means
+// A CTA per (block, sequence, kv head): D / 8 threads share a key row, the
+// others take the next rows; the partial sums are added in row-group order.
+constexpr int kMeanThreads = 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kMeanThreads) k_block_means(BlkArgs a, int D, int new_keys,
+                                                             float *__restrict__ means) {
+    __shared__ float part[kMeanThreads * 8];
+    const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk;
+    const int len = blk_len(a, b);
+    int c = blockIdx.x;
+    if (new_keys >= 0) {
+        c += max(len - new_keys, 0) / a.block;
+        if (c * a.block >= len) return;
+    }
+    if (c >= a.NB) return;
+    const int units = D / 8, rows = kMeanThreads / units;
+    const int u = threadIdx.x % units, g = threadIdx.x / units;
+    const int k0 = c * a.block, k1 = min(k0 + a.block, len);
+    float acc[8] = {};
+    if (g < rows) {
+        const T *k = (const T *)a.k + b * a.k_sb + h * a.k_sh + u * 8;
+        for (int i = k0 + g; i < k1; i += rows) {
+            float x[8];
+            ld_pack<T, 8>(k + i * a.k_st, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] += x[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part[(g * units + u) * 8 + e] = acc[e];
+    }
+    __syncthreads();
+    const float count = (float)max(k1 - k0, 1);
+    for (int d = threadIdx.x; d < D; d += kMeanThreads) {
+        float s = 0.0f;
+        for (int i = 0; i < rows; ++i) s += part[i * D + d];
+        means[(((int64_t)b * a.NB + c) * a.Hk + h) * D + d] = __fdiv_rn(s, count);
+    }
+}
+
+// ----------------------------------------------------------------- scores
+// score[row, c], row = (b, t, h) in that order, written for the candidates only:
+// causal c < position / block (the block of the position itself is always
+// taken), else c < blocks that hold a key.
+struct SelArgs {
+    BlkArgs a;
+    int D;
+    int64_t rows;            // B Tq Hk
+    const float *means;
+    float *score;            // [rows, NB]
+    float *qs;               // [B, Hk, Tq, D], the groups' sums (tiled scores only)
+    int32_t *out;
+};
+
+// First block that is not a candidate; *own = the block that is always taken, or -1.
+__device__ __forceinline__ int candidates(const BlkArgs &a, int b, int t, int *own) {
+    const int limit = blk_limit(a, blk_len(a, b), t);
+    *own = -1;
+    if (limit == 0) return 0;
+    if (!a.causal) return (limit + a.block - 1) / a.block;
+    *own = (limit - 1) / a.block;
+    return *own;
+}
+
+// Few queries: a warp per 8 blocks of one row; the lanes split D.
+template <typename T>
+__global__ void __launch_bounds__(128) k_score_few(SelArgs s) {
+    const BlkArgs &a = s.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = blockIdx.y;
+    const int h = (int)(row % a.Hk);
+    const int64_t bt = row / a.Hk;
+    const int t = (int)(bt % a.Tq), b = (int)(bt / a.Tq);
+    int own;
+    const int cand = candidates(a, b, t, &own);
+    const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
+    if (c0 >= cand) return;
+    float dot[8] = {};
+    for (int d = lane * 8; d < s.D; d += 256) {
+        float q[8] = {};
+        const T *p = (const T *)a.q + b * a.q_sb + t * a.q_st + (int64_t)h * a.G * a.q_sh + d;
+        for (int g = 0; g < a.G; ++g) {
+            float x[8];
+            ld_pack<T, 8>(p + g * a.q_sh, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] += x[e];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (c0 + i < cand) {
+                float m[8];
+                ld_pack<float, 8>(s.means + (((int64_t)b * a.NB + c0 + i) * a.Hk + h) * s.D + d, m);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dot[i] = fmaf(q[e], m[e], dot[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
+    if (lane == 0)
+        for (int i = 0; i < 8; ++i)
+            if (c0 + i < cand) s.score[row * a.NB + c0 + i] = dot[i];
+}
+
+// Many queries: the groups' sums once, then 64 x 64 tiles of their product with
+// the means, fp32 throughout (the list that a query gets must not depend on the
+// rounding of a 16-bit product).
+template <typename T>
+__global__ void __launch_bounds__(256) k_group_sum(SelArgs s) {
+    const BlkArgs &a = s.a;
+    const int units = s.D / 8;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= s.rows * units) return;
+    const int u = (int)(i % units);
+    const int64_t row = i / units;               // (b, h, t)
+    const int t = (int)(row % a.Tq);
+    const int64_t bh = row / a.Tq;
+    const int h = (int)(bh % a.Hk), b = (int)(bh / a.Hk);
+    const T *p = (const T *)a.q + b * a.q_sb + t * a.q_st + (int64_t)h * a.G * a.q_sh + u * 8;
+    float q[8] = {};
+    for (int g = 0; g < a.G; ++g) {
+        float x[8];
+        ld_pack<T, 8>(p + g * a.q_sh, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] += x[e];
+    }
+    st_pack<float, 8>(s.qs + row * s.D + u * 8, q);
+}
+
+constexpr int kSt = 64;      // tile of queries and of blocks
+constexpr int kSk = 32;      // depth of one step
+
+__global__ void __launch_bounds__(256) k_score_tiles(SelArgs s) {
+    __shared__ float qt[kSk][kSt + 4], mt[kSk][kSt + 4];
+    const BlkArgs &a = s.a;
+    const int bh = blockIdx.z, b = bh / a.Hk, h = bh % a.Hk;
+    const int t0 = blockIdx.y * kSt, c0 = blockIdx.x * kSt;
+    int own;
+    if (c0 >= candidates(a, b, min(t0 + kSt, a.Tq) - 1, &own)) return;
+    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+    float acc[4][4] = {};
+    for (int d0 = 0; d0 < s.D; d0 += kSk) {
+        for (int i = threadIdx.x; i < kSt * kSk / 4; i += 256) {
+            const int r = i / (kSk / 4), d = i % (kSk / 4) * 4;
+            float4 x = make_float4(0, 0, 0, 0), y = x;
+            if (d0 + d < s.D) {
+                if (t0 + r < a.Tq)
+                    x = *(const float4 *)(s.qs + ((int64_t)bh * a.Tq + t0 + r) * s.D + d0 + d);
+                if (c0 + r < a.NB)
+                    y = *(const float4 *)(s.means +
+                                          (((int64_t)b * a.NB + c0 + r) * a.Hk + h) * s.D + d0 + d);
+            }
+            qt[d][r] = x.x; qt[d + 1][r] = x.y; qt[d + 2][r] = x.z; qt[d + 3][r] = x.w;
+            mt[d][r] = y.x; mt[d + 1][r] = y.y; mt[d + 2][r] = y.z; mt[d + 3][r] = y.w;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int d = 0; d < kSk; ++d) {
+            const float4 x = *(const float4 *)&qt[d][ty * 4], y = *(const float4 *)&mt[d][tx * 4];
+            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + ty * 4 + i;
+        if (t >= a.Tq) continue;
+        float *p = s.score + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.NB;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (c0 + tx * 4 + j < a.NB) p[c0 + tx * 4 + j] = acc[i][j];
+    }
+}
+
+// ------------------------------------------------------------------- best
+// A warp per row. Scores become unsigned keys of the same order; the want-th
+// largest key is found by bisection between the row's extremes, counting the
+// keys at or above the middle; all keys above it and the lowest-indexed ones
+// equal to it are taken, in index order. R registers a lane hold the row's keys
+// when it has at most 32 R candidates; R = 0 reads them again at every step.
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (isnan(x)) return 0u;
+    x += 0.0f;                                  // -0 and +0 are equal scores
+    const uint32_t u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+template <int R> struct RowKeys {
+    uint32_t key[R > 0 ? R : 1];
+    const float *p;
+    int cand, lane;
+    __device__ __forceinline__ void load(const float *row, int cand_, int lane_) {
+        p = row;
+        cand = cand_;
+        lane = lane_;
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int c = i * 32 + lane;
+                key[i] = c < cand ? order_key(p[c]) : 0u;
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t at(int i) const {
+        if constexpr (R > 0) return key[i];
+        const int c = i * 32 + lane;
+        return c < cand ? order_key(p[c]) : 0u;
+    }
+    // keys >= x among the candidates (x > 0)
+    __device__ __forceinline__ int count(uint32_t x) const {
+        int n = 0;
+        if constexpr (R > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) n += key[i] >= x ? 1 : 0;
+        } else {
+            for (int i = 0; i * 32 < cand; ++i) n += at(i) >= x ? 1 : 0;
+        }
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+    __device__ __forceinline__ void extremes(uint32_t &lo, uint32_t &hi) const {
+        lo = 0xffffffffu;
+        hi = 0u;
+        const int steps = R > 0 ? R : (cand + 31) / 32;
+#pragma unroll
+        for (int i = 0; i < steps; ++i) {
+            const uint32_t x = at(i);
+            hi = max(hi, x);
+            if (i * 32 + lane < cand) lo = min(lo, x);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+    }
+};
+
+template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
+    const BlkArgs &a = s.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= s.rows) return;
+    const int64_t bt = row / a.Hk;
+    const int t = (int)(bt % a.Tq), b = (int)(bt / a.Tq);
+    int own;
+    const int cand = candidates(a, b, t, &own);
+    const int want = min(cand, a.n - (own >= 0 ? 1 : 0));
+    int32_t *out = s.out + row * a.n;
+    int done = 0;
+    if (want > 0 && want < cand) {
+        RowKeys<R> keys;
+        keys.load(s.score + row * a.NB, cand, lane);
+        // the largest x with count(keys >= x) >= want
+        uint32_t lo, hi;
+        keys.extremes(lo, hi);
+        int n_lo = cand;                        // count(keys >= lo)
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo) / 2 + 1;
+            const int n = keys.count(mid);
+            if (n >= want) {
+                lo = mid;
+                n_lo = n;
+                if (n == want) break;
+            } else {
+                hi = mid - 1;
+            }
+        }
+        // exactly want keys >= lo, or lo is the want-th key and some equal ones stay out
+        int spare = n_lo - want;                // of the keys equal to lo, the last ones
+        int equal = 0;
+        if (spare > 0) equal = n_lo - (lo == 0xffffffffu ? 0 : keys.count(lo + 1)) - spare;
+        const int steps = R > 0 ? R : (cand + 31) / 32;
+#pragma unroll
+        for (int i = 0; i < steps; ++i) {
+            const int c = i * 32 + lane;
+            const uint32_t x = keys.at(i);
+            bool take = c < cand && x >= lo;
+            if (spare > 0) {
+                const bool tie = take && x == lo;
+                const unsigned ties = __ballot_sync(0xffffffffu, tie);
+                if (tie && __popc(ties & ((1u << lane) - 1u)) >= equal) take = false;
+                equal -= min(equal, __popc(ties));
+            }
+            const unsigned m = __ballot_sync(0xffffffffu, take);
+            if (take) out[done + __popc(m & ((1u << lane) - 1u))] = c;
+            done += __popc(m);
+        }
+    } else if (want > 0) {
+        for (int c = lane; c < cand; c += 32) out[c] = c;
+        done = cand;
+    }
+    if (own >= 0) {
+        if (lane == 0) out[done] = own;
+        ++done;
+    }
+    for (int j = done + lane; j < a.n; j += 32) out[j] = -1;
+}
+
+__global__ void k_check_lists(BlkArgs a, int64_t rows, int32_t *bad) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= rows * a.n) return;
+    const int j = (int)(i % a.n);
+    const int c = a.blocks[i];
+    bool ok = c == -1 || (unsigned)c < (unsigned)a.NB;
+    if (j > 0 && c != -1) ok = ok && a.blocks[i - 1] != -1 && c > a.blocks[i - 1];
+    if (!ok) *bad = 1;
+}
+
+__global__ void k_zero_word(int32_t *p) { *p = 0; }
+
+// ------------------------------------------------------------------- host
+// From this many queries on, 64-query tiles read each mean once per tile instead
+// of once per query; below it the tile's unused rows cost more.
+constexpr int64_t kTiledQueries = 24;
+
+template <typename T>
+cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t st) {
+    const BlkArgs &a = s.a;
+    if (!tiles) {                // rows in grid.y
+        k_score_few<T><<<dim3((unsigned)((a.NB + 31) / 32), (unsigned)s.rows), 128, 0, st>>>(s);
+        count_launch();
+    } else {
+        const int64_t n = s.rows * (s.D / 8);
+        k_group_sum<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s);
+        k_score_tiles<<<dim3((unsigned)((a.NB + kSt - 1) / kSt), (unsigned)((a.Tq + kSt - 1) / kSt),
+                             (unsigned)(B * a.Hk)),
+                        256, 0, st>>>(s);
+        count_launch(2);
+    }
+    return cudaGetLastError();
+}
+
+bool tiled(const spmm_blocks_shape *s) {
+    return s->Tq >= kTiledQueries || s->B * s->Tq * s->Hk > 65535;
+}
+
+}  // namespace
+}  // namespace spmm
+
+extern "C" {
+
+spmm_status spmm_blocks_means(const spmm_blocks_shape *s, spmm_rows k, int64_t new_keys,
+                              float *means, void *stream) {
+    using namespace spmm;
+    const spmm_status st = blk_check(s, false);
+    if (st != SPMM_OK) return st;
+    if (s->B == 0 || s->Tk == 0 || new_keys == 0) return SPMM_OK;
+    if (!means || !rows_ok(k, dtype_bytes(s->dtype))) return SPMM_ERR_INVALID_ARG;
+    if (s->B * s->Hk > 65535) return SPMM_ERR_UNSUPPORTED;
+    BlkArgs a = blk_args(s, nullptr);
+    set_rows(a.k, a.k_sb, a.k_st, a.k_sh, k);
+    const int64_t most = new_keys < 0 ? a.NB : std::min<int64_t>(a.NB, new_keys / s->block + 2);
+    const int nk = (int)std::min<int64_t>(new_keys, INT32_MAX);
+    const dim3 grid((unsigned)most, (unsigned)(s->B * s->Hk));
+    cudaStream_t cs = (cudaStream_t)stream;
+    const int D = (int)s->D;
+    if (s->dtype == SPMM_F32) k_block_means<float><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, means);
+    else if (s->dtype == SPMM_BF16)
+        k_block_means<__nv_bfloat16><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, means);
+    else k_block_means<__half><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, means);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+int64_t spmm_blocks_select_workspace(const spmm_blocks_shape *s) {
+    using namespace spmm;
+    if (blk_check(s, false) != SPMM_OK) return 0;
+    const int64_t NB = (s->Tk + s->block - 1) / s->block, rows = s->B * s->Tq * s->Hk;
+    return round_up(rows * NB * 4, 16) + (tiled(s) ? rows * s->D * 4 : 0);
+}
+
+spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const float *means,
+                               int32_t *blocks, void *work, int64_t work_bytes, void *stream) {
+    using namespace spmm;
+    const spmm_status st = blk_check(s, false);
+    if (st != SPMM_OK) return st;
+    if (s->B == 0 || s->Tq == 0) return SPMM_OK;
+    if (!blocks || !rows_ok(q, dtype_bytes(s->dtype))) return SPMM_ERR_INVALID_ARG;
+    if (s->Tk > 0 && (!means || (uintptr_t)means % 16)) return SPMM_ERR_INVALID_ARG;
+    const int64_t need = spmm_blocks_select_workspace(s);
+    if (need && (!work || work_bytes < need)) return SPMM_ERR_INVALID_ARG;
+    if (tiled(s) && (s->B * s->Hk > 65535 || (s->Tq + kSt - 1) / kSt > 65535))
+        return SPMM_ERR_UNSUPPORTED;
+    SelArgs g{};
+    g.a = blk_args(s, nullptr);
+    set_rows(g.a.q, g.a.q_sb, g.a.q_st, g.a.q_sh, q);
+    g.D = (int)s->D;
+    g.rows = s->B * s->Tq * s->Hk;
+    g.means = means;
+    g.score = (float *)work;
+    g.qs = (float *)((char *)work + round_up(g.rows * g.a.NB * 4, 16));
+    g.out = blocks;
+    cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = cudaSuccess;
+    if (g.a.NB > 0) {
+        if (s->dtype == SPMM_F32) e = launch_scores<float>(g, s->B, tiled(s), cs);
+        else if (s->dtype == SPMM_BF16) e = launch_scores<__nv_bfloat16>(g, s->B, tiled(s), cs);
+        else e = launch_scores<__half>(g, s->B, tiled(s), cs);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    const unsigned grid = (unsigned)((g.rows + 3) / 4);
+    const int NB = g.a.NB;
+    if (NB <= 32) k_best<1><<<grid, 128, 0, cs>>>(g);
+    else if (NB <= 128) k_best<4><<<grid, 128, 0, cs>>>(g);
+    else if (NB <= 512) k_best<16><<<grid, 128, 0, cs>>>(g);
+    else if (NB <= 1024) k_best<32><<<grid, 128, 0, cs>>>(g);
+    else k_best<0><<<grid, 128, 0, cs>>>(g);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+spmm_status spmm_blocks_check(const spmm_blocks_shape *s, const int32_t *blocks, int32_t *bad,
+                              void *stream) {
+    using namespace spmm;
+    const spmm_status st = blk_check(s, false);
+    if (st != SPMM_OK) return st;
+    const int64_t rows = s->B * s->Tq * s->Hk;
+    if (!bad || (rows && !blocks)) return SPMM_ERR_INVALID_ARG;
+    cudaStream_t cs = (cudaStream_t)stream;
+    k_zero_word<<<1, 1, 0, cs>>>(bad);
+    count_launch();
+    if (rows) {
+        if ((rows * s->n + 255) / 256 > INT32_MAX) return SPMM_ERR_UNSUPPORTED;
+        k_check_lists<<<(unsigned)((rows * s->n + 255) / 256), 256, 0, cs>>>(
+            blk_args(s, blocks), rows, bad);
+        count_launch();
+    }
+    return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -1,0 +1,480 @@
+"""Selected-block attention on the GPU against plain 64-bit forms: block means,
+the selection (exactly, on inputs whose scores are exact in fp32; within the
+scores' fp32 error otherwise), attention and its gradients within the bound of
+fp32 sums, weights rounded once to the inputs' type, and one final rounding."""
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+import dynamic_ref as ref  # noqa: E402
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def sdm(cuda_device):
+    import sparse_dense_matrix_gb300 as m
+    return m
+
+
+def randn(dev, seed, *shape):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    return torch.randn(*shape, generator=g, device=dev)
+
+
+def grid(x, dt):
+    """Multiples of 1/8: sums and block means are exact in fp32."""
+    return ((x * 8).round() / 8).to(dt)
+
+
+def random_lists(seed, B, Tq, Hk, n, NB, empty=0.0):
+    """Ascending lists of up to n distinct blocks, some of them empty."""
+    g = torch.Generator().manual_seed(seed)
+    out = torch.full((B, Tq, Hk, n), -1, dtype=torch.int32)
+    for b in range(B):
+        for t in range(Tq):
+            for h in range(Hk):
+                if torch.rand(1, generator=g) < empty:
+                    continue
+                m = int(torch.randint(1, min(n, NB) + 1, (1,), generator=g))
+                out[b, t, h, :m] = torch.randperm(NB, generator=g)[:m].sort().values
+    return out
+
+
+# -------------------------------------------------------------------- means
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("B,Tk,Hk,D,block,lengths", [
+    (1, 1, 1, 64, 16, None), (2, 333, 3, 128, 64, [333, 100]), (3, 130, 2, 96, 32, [0, 1, 130]),
+    (1, 64, 2, 8, 16, [64]), (2, 300, 1, 256, 128, [129, 500])])
+def test_means(sdm, cuda_device, dtype, B, Tk, Hk, D, block, lengths):
+    k = randn(cuda_device, D, B, Tk, Hk, D).to(DT[dtype])
+    L = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=cuda_device)
+    for b in range(B):
+        if lengths is not None:
+            k[b, min(lengths[b], Tk):] = float("nan")      # past the length: never used
+    got = sdm.block_means(k, block, L)
+    want = ref.means(k, block, lengths)
+    ref.close(got, want, 2 * block * ref.E32 * k.nan_to_num().abs().max().double())
+
+
+def test_means_of_new_keys(sdm, cuda_device):
+    B, Tk, Hk, D, block = 3, 200, 2, 64, 32
+    k = randn(cuda_device, 1, B, Tk, Hk, D).bfloat16()
+    L = torch.tensor([200, 65, 0], dtype=torch.int32, device=cuda_device)
+    want = sdm.block_means(k, block, L)
+    for new in (1, 8, 40):
+        m = sdm.block_means(k, block, (L - new).clamp(min=0))
+        before = m.clone()
+        assert sdm.block_means(k, block, L, out=m, new_keys=new) is m
+        for b in range(B):
+            for c in range(-(-Tk // block)):
+                old = (c + 1) * block <= max(int(L[b]) - new, 0) or c * block >= int(L[b])
+                assert torch.equal(m[b, c], before[b, c] if old else want[b, c]), (new, b, c)
+
+
+# ---------------------------------------------------------------- selection
+SELECT = [  # B, Tq, Tk, Hq, Hk, D, block, n, lengths
+    (1, 1, 1, 1, 1, 64, 16, 1, None), (1, 1, 500, 4, 2, 64, 16, 4, None),
+    (3, 2, 333, 6, 2, 128, 32, 5, [333, 0, 1]), (1, 23, 400, 8, 1, 64, 16, 3, None),
+    (2, 24, 400, 2, 2, 128, 16, 7, [400, 17]), (1, 200, 200, 4, 4, 64, 16, 30, None),
+    (2, 65, 700, 3, 1, 96, 64, 1, [700, 64]), (1, 3, 9000, 2, 1, 64, 16, 40, None),
+    (1, 30, 20000, 1, 1, 64, 16, 16, None)]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("B,Tq,Tk,Hq,Hk,D,block,n,lengths", SELECT)
+def test_select_exact_scores(sdm, cuda_device, B, Tq, Tk, Hq, Hk, D, block, n, lengths, causal):
+    """Values on a coarse grid: scores are exact, many of them equal. (A mean over
+    a partly filled block is not; there the lengths are whole blocks.)"""
+    if not causal:
+        lengths = [x // block * block for x in (lengths or [Tk] * B)]
+    L = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=cuda_device)
+    q = (randn(cuda_device, 2, B, Tq, Hq, D) * 0.5).round().bfloat16()
+    k = (randn(cuda_device, 3, B, Tk, Hk, D) * 0.3).round().bfloat16()
+    m = sdm.block_means(k, block, L)
+    sel = sdm.select_blocks(q, m, n, block, Tk, L, causal)
+    want, _ = ref.select(q, m, n, block, Tk, L, causal)
+    assert torch.equal(sel.blocks.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("Tq", [5, 100])
+def test_select_any_scores(sdm, cuda_device, dtype, Tq):
+    """Real values: no block left out may beat one taken by more than the scores' error."""
+    B, Tk, Hq, Hk, D, block, n = 2, 1000, 8, 2, 128, 16, 9
+    q = randn(cuda_device, 4, B, Tq, Hq, D).to(DT[dtype])
+    k = randn(cuda_device, 5, B, Tk, Hk, D).to(DT[dtype])
+    m = sdm.block_means(k, block)
+    got = sdm.select_blocks(q, m, n, block, Tk).blocks.cpu()
+    _, score = ref.select(q, m, n, block, Tk, None, True)
+    mag = torch.einsum("bthd,bchd->bthc", q.double().abs().view(B, Tq, Hk, -1, D).sum(3),
+                       m.double().abs()).cpu()
+    for b in range(B):
+        for t in range(Tq):
+            for h in range(Hk):
+                last = (Tk - Tq + t) // block
+                row = got[b, t, h].tolist()
+                assert row == sorted(set(row)) and row[-1] == last and row[0] >= 0
+                out = [c for c in range(last) if c not in row]
+                tol = 2 * (D + 8) * ref.E32 * mag[b, t, h].max().item()
+                assert score[b, t, h, row[:-1]].min() >= score[b, t, h, out].max() - tol
+
+
+def test_select_nan_and_infinite_scores(sdm, cuda_device):
+    m = torch.zeros(1, 8, 1, 64, device=cuda_device)
+    m[0, :, 0, 0] = torch.tensor([float("nan"), 1, float("-inf"), float("inf"), 0, -0.0, 2, 0])
+    q = torch.zeros(1, 1, 1, 64, device=cuda_device)
+    q[..., 0] = 1
+    # inf * 0 is NaN in the other elements' products only where m is infinite there
+    for n, want in ((2, [3, 7]), (3, [3, 6, 7]), (5, [1, 3, 4, 6, 7]), (6, [1, 3, 4, 5, 6, 7]),
+                    (7, [1, 2, 3, 4, 5, 6, 7]), (8, [0, 1, 2, 3, 4, 5, 6, 7])):
+        got = sdm.select_blocks(q, m, n, 16, 128).blocks.cpu().flatten().tolist()
+        assert got == want, (n, got)
+
+
+# ---------------------------------------------------------------- attention
+CASES = [  # B, Tq, Tk, Hq, Hk, D, block, n, lengths
+    (1, 1, 1, 1, 1, 64, 16, 1, None),
+    (2, 1, 500, 8, 2, 128, 64, 4, [500, 77]),
+    (4, 1, 300, 14, 2, 64, 32, 12, [0, 1, 33, 300]),
+    (1, 1, 4096, 32, 4, 128, 64, 64, None),
+    (3, 5, 200, 9, 1, 64, 16, 3, [200, 3, 0]),
+    (1, 70, 70, 16, 1, 128, 16, 5, None),
+    (2, 130, 333, 6, 2, 128, 128, 3, [333, 140]),
+    (1, 200, 257, 20, 1, 64, 32, 9, None),
+    (2, 97, 97, 3, 3, 128, 64, 2, [97, 50]),
+    (1, 300, 1000, 4, 4, 64, 16, 20, None),
+    (1, 33, 129, 40, 1, 128, 128, 2, None),
+    (1, 1100, 1100, 2, 1, 64, 64, 6, None),
+]
+
+
+def inputs(dev, case, dtype, seed=7, scale=1.0):
+    B, Tq, Tk, Hq, Hk, D, block, n, lengths = case
+    dt = DT[dtype]
+    q, k, v = (randn(dev, seed + i, B, T, H, D).to(dt)
+               for i, (T, H) in enumerate(((Tq, Hq), (Tk, Hk), (Tk, Hk))))
+    blocks = random_lists(seed, B, Tq, Hk, n, -(-Tk // block), 0.1).to(dev)
+    L = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=dev)
+    return (q * scale).to(dt), k, v, blocks, L
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", CASES)
+def test_attend_and_backward(sdm, cuda_device, case, dtype, causal):
+    B, Tq, Tk, Hq, Hk, D, block, n, lengths = case
+    q, k, v, blocks, L = inputs(cuda_device, case, dtype)
+    sel = sdm.BlockSelection(blocks, block, Tk, L, causal)
+    grad = randn(cuda_device, 99, *q.shape).to(q.dtype)
+    out, lse = sel.attend(q, k, v)
+    dq, dk, dv = sel.backward(grad, q, k, v, out, lse)
+    want = ref.attend(q, k, v, blocks, block, L, causal, grad=grad)
+    for name, got in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.close(got, want[name], want["tol_" + name], name)
+    # the same again, bit for bit
+    out2, lse2 = sel.attend(q, k, v)
+    again = (out2, lse2, *sel.backward(grad, q, k, v, out, lse))
+    assert all(torch.equal(a, b) for a, b in zip((out, lse, dq, dk, dv), again))
+
+
+@pytest.mark.parametrize("qscale,scale", [(30.0, None), (1.0, 0.0), (0.01, -1.0)])
+def test_sharp_flat_and_negative_scales(sdm, cuda_device, qscale, scale):
+    case = (1, 40, 300, 4, 2, 64, 32, 4, None)
+    q, k, v, blocks, L = inputs(cuda_device, case, "fp16", scale=qscale)
+    sel = sdm.BlockSelection(blocks, 32, 300, L)
+    grad = randn(cuda_device, 98, *q.shape).to(q.dtype)
+    out, lse = sel.attend(q, k, v, scale)
+    got = dict(zip(("dq", "dk", "dv"), sel.backward(grad, q, k, v, out, lse, scale)), out=out, lse=lse)
+    want = ref.attend(q, k, v, blocks, 32, L, True, scale, grad)
+    for name in got:
+        ref.close(got[name], want[name], want["tol_" + name], name)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), float("-inf"), "lowest"])
+@pytest.mark.parametrize("Tq", [1, 60])
+def test_masked_places_hold_anything(sdm, cuda_device, fill, Tq):
+    """Keys past the length, in the future and in blocks nobody chose, and rows of q
+    and of the gradient whose query sees nothing."""
+    case = (2, Tq, 300, 4, 2, 128, 32, 3, [220, 30])
+    q, k, v, blocks, L = inputs(cuda_device, case, "bf16")
+    blocks[blocks == 2] = -1                     # nobody chooses block 2
+    blocks = blocks.masked_fill((blocks < 0).cummax(-1).values, -1)
+    sel = sdm.BlockSelection(blocks, 32, 300, L)
+    grad = randn(cuda_device, 97, *q.shape).to(q.dtype)
+
+    def run(k, v):
+        out, lse = sel.attend(q, k, v)
+        return (out, lse, *sel.backward(grad, q, k, v, out, lse))
+
+    k[:, 64:96] = v[:, 64:96] = 0
+    for b, n in enumerate([220, 30]):
+        k[b, n:] = v[b, n:] = 0
+    clean = run(k, v)
+    x = torch.finfo(k.dtype).min if fill == "lowest" else fill
+    k, v = k.clone(), v.clone()
+    k[:, 64:96] = v[:, 64:96] = x
+    for b, n in enumerate([220, 30]):
+        k[b, n:] = v[b, n:] = x
+    for a, b in zip(clean, run(k, v)):
+        assert torch.equal(a, b)
+
+
+def test_future_keys_in_own_block(sdm, cuda_device):
+    """The causal edge inside a block: a query's result does not change with later keys."""
+    B, T, D = 1, 64, 64
+    q, k, v = (randn(cuda_device, i, B, T, 1, D).half() for i in range(3))
+    blocks = torch.zeros(B, T, 1, 1, dtype=torch.int32, device=cuda_device)
+    out, lse = sdm.BlockSelection(blocks, 64, T).attend(q, k, v)
+    for t in (0, 1, 15, 16, 40, 63):
+        k2, v2 = k.clone(), v.clone()
+        k2[:, t + 1:] = v2[:, t + 1:] = float("nan")
+        o2, l2 = sdm.BlockSelection(blocks, 64, T).attend(q, k2, v2)
+        assert torch.equal(o2[:, t], out[:, t]) and torch.equal(l2[:, t], lse[:, t])
+
+
+def test_nan_and_infinity_in_seen_places(sdm, cuda_device):
+    """They reach the rows that see them, and no other."""
+    B, T, D = 1, 80, 64
+    q, k, v = (randn(cuda_device, i, B, T, 2, D).half() for i in range(3))
+    blocks = torch.arange(5, device=cuda_device, dtype=torch.int32).expand(1, T, 2, 5)
+    blocks = torch.where(blocks <= torch.arange(T, device=cuda_device)[:, None, None] // 16,
+                         blocks, -1).contiguous()
+    sel = sdm.BlockSelection(blocks, 16, T)
+    clean, _ = sel.attend(q, k, v)
+    k[0, 40, 0] = float("nan")
+    v[0, 20, 1, 3] = float("inf")
+    out, lse = sel.attend(q, k, v)
+    assert torch.isnan(out[0, 40:, 0]).all() and torch.isnan(lse[0, 40:, 0]).all()
+    assert torch.equal(out[0, :40, 0], clean[0, :40, 0])
+    assert torch.isinf(out[0, 20:, 1, 3]).all()
+    assert torch.equal(out[0, :20], clean[0, :20])
+
+
+@pytest.mark.parametrize("Tq", [1, 90])
+def test_strides_and_orders(sdm, cuda_device, Tq):
+    """q, k, v cut out of one fused projection, and [B, H, T, D] caches."""
+    B, Tk, Hq, Hk, D, block, n = 2, 150, 4, 2, 64, 16, 4
+    blocks = random_lists(3, B, Tq, Hk, n, -(-Tk // block)).to(cuda_device)
+    sel = sdm.BlockSelection(blocks, block, Tk)
+    fused = randn(cuda_device, 5, B, Tk, Hq + 2 * Hk, D).bfloat16()
+    q, k, v = fused[:, :Tq, :Hq], fused[:, :, Hq:Hq + Hk], fused[:, :, Hq + Hk:]
+    grad = randn(cuda_device, 6, Tq, B, Hq, D).bfloat16().transpose(0, 1)
+
+    def run(q, k, v, grad):
+        out, lse = sel.attend(q, k, v)
+        return (out, lse, *sel.backward(grad, q, k, v, out, lse))
+
+    want = run(q.contiguous(), k.contiguous(), v.contiguous(), grad.contiguous())
+    heads_first = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in (q, k, v)]
+    shared = grad[:, :1, :1].expand(grad.shape)            # one row for every query and head
+    for got in (run(q, k, v, grad), run(*heads_first, grad)):
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    a, b = run(q, k, v, shared), run(q, k, v, shared.contiguous())
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    m = sdm.block_means(k, block)
+    assert torch.equal(m, sdm.block_means(k.contiguous(), block))
+    assert torch.equal(sdm.select_blocks(q, m, n, block, Tk).blocks,
+                       sdm.select_blocks(q.contiguous(), m, n, block, Tk).blocks)
+
+
+def test_single_token_equals_prompt(sdm, cuda_device):
+    """Token by token over a cache against the same positions of one prompt."""
+    B, T, Hq, Hk, D, block, n = 2, 130, 8, 2, 64, 16, 3
+    q, k, v = (grid(randn(cuda_device, i, B, T, H, D), torch.bfloat16)
+               for i, H in ((0, Hq), (1, Hk), (2, Hk)))
+    m = sdm.block_means(k, block)
+    whole = sdm.select_blocks(q, m, n, block, T)
+    out, lse = whole.attend(q, k, v)
+    means = torch.zeros_like(m)
+    tol = 2 * ref.U[torch.bfloat16] * v.abs().max().item() * 2
+    for t in range(T):
+        L = torch.full((B,), t + 1, dtype=torch.int32, device=cuda_device)
+        sdm.block_means(k, block, L, out=means, new_keys=1)
+        one = sdm.select_blocks(q[:, t:t + 1], means, n, block, T, L)
+        assert torch.equal(one.blocks[:, 0], whole.blocks[:, t])
+        o, l = one.attend(q[:, t:t + 1], k, v)
+        ref.close(o[:, 0], out[:, t].double(), tol, f"token {t}")
+        ref.close(l[:, 0], lse[:, t].double(), 1e-4, f"token {t}")
+
+
+def test_gradient_against_differences(sdm, cuda_device):
+    """Directional derivatives of the 64-bit form by central differences (error
+    about h^2 = 1e-8 of a loss of size 100) against the kernel's gradients, whose
+    bounds add up over the direction."""
+    case = (1, 50, 120, 4, 2, 64, 16, 4, None)
+    q, k, v, blocks, L = inputs(cuda_device, case, "fp16")
+    sel = sdm.BlockSelection(blocks, 16, 120)
+    grad = randn(cuda_device, 96, *q.shape).half()
+    out, lse = sel.attend(q, k, v)
+    got = sel.backward(grad, q, k, v, out, lse)
+    want = ref.attend(q, k, v, blocks, 16, grad=grad)
+
+    def loss(q_, k_, v_):
+        total = 0.0
+        for i in range(4):
+            h = i // 2
+            chosen = torch.zeros(50, 9, dtype=torch.bool, device=q.device)
+            chosen.scatter_(1, torch.where(blocks[0, :, h] >= 0, blocks[0, :, h], 8).long(), True)
+            mask = chosen[:, :8].repeat_interleave(16, 1)[:, :120]
+            mask &= torch.arange(120, device=q.device) <= 70 + torch.arange(50, device=q.device)[:, None]
+            s = (q_[0, :, i] @ k_[0, :, h].T / 8).masked_fill(~mask, -math.inf)
+            p = torch.where(mask.any(1, keepdim=True), torch.softmax(s, 1), 0.0).nan_to_num()
+            total = total + (p @ v_[0, :, h] * grad[0, :, i].double()).sum()
+        return total
+
+    x = [t.double() for t in (q, k, v)]
+    for w, name in enumerate(("dq", "dk", "dv")):
+        d = randn(cuda_device, 50 + w, *x[w].shape).double()
+        step = 1e-4
+        up, down = list(x), list(x)
+        up[w], down[w] = x[w] + step * d, x[w] - step * d
+        slope = (loss(*up) - loss(*down)) / (2 * step)
+        tol = (want["tol_" + name] * d.abs()).sum() + 1e-4
+        assert abs(slope - (got[w].double() * d).sum()) <= tol, name
+        exact = (want[name] * d).sum()                     # and the formula's own, tightly
+        assert abs(slope - exact) <= 1e-4 * max(1.0, abs(exact.item())), name
+
+
+def test_cache_past_32_bit_offsets(sdm, cuda_device):
+    """A cache of 2^31 + elements a head-dim apart: the last blocks lie beyond."""
+    Tk, Hk, D, block = 2 ** 21 + 77, 8, 128, 64
+    k = torch.zeros(1, Tk, Hk, D, dtype=torch.bfloat16, device=cuda_device)
+    v = torch.zeros_like(k)
+    q = randn(cuda_device, 1, 1, 1, 16, D).bfloat16()
+    NB = -(-Tk // block)
+    blocks = torch.tensor([0, 5, NB - 2, NB - 1], dtype=torch.int32, device=cuda_device)
+    small_k = randn(cuda_device, 2, 1, 4 * block, Hk, D).bfloat16()
+    small_v = randn(cuda_device, 3, 1, 4 * block, Hk, D).bfloat16()
+    tail = Tk - (NB - 1) * block
+    for i, c in enumerate(blocks.tolist()):
+        n = block if i < 3 else tail
+        k[:, c * block:c * block + n] = small_k[:, i * block:i * block + n]
+        v[:, c * block:c * block + n] = small_v[:, i * block:i * block + n]
+    T4 = 3 * block + tail
+    sel = sdm.BlockSelection(blocks.expand(1, 1, Hk, 4).contiguous(), block, Tk)
+    four = torch.arange(4, dtype=torch.int32, device=cuda_device).expand(1, 1, Hk, 4).contiguous()
+    small = sdm.BlockSelection(four, block, T4)
+    out, lse = sel.attend(q, k, v)
+    o4, l4 = small.attend(q, small_k[:, :T4], small_v[:, :T4])
+    assert torch.equal(out, o4) and torch.equal(lse, l4)
+    m = sdm.block_means(k, block)
+    m4 = sdm.block_means(small_k[:, :T4].contiguous(), block)
+    assert torch.equal(m[:, blocks.long()], m4)
+    grad = randn(cuda_device, 4, *q.shape).bfloat16()
+    dq, dk, dv = sel.backward(grad, q, k, v, out, lse)
+    want = small.backward(grad, q, small_k[:, :T4].contiguous(), small_v[:, :T4].contiguous(), o4, l4)
+    assert torch.equal(dq, want[0])
+    for i, c in enumerate(blocks.tolist()):
+        n = block if i < 3 else tail
+        for big, few in ((dk, want[1]), (dv, want[2])):
+            assert torch.equal(big[:, c * block:c * block + n], few[:, i * block:i * block + n])
+    assert not dk[:, 64:320].any() and not dv[:, 64:320].any()
+
+
+def test_streams_and_graphs(sdm, cuda_device):
+    B, T, Hq, Hk, D, block, n = 1, 100, 4, 2, 64, 16, 4
+    q, k, v = (grid(randn(cuda_device, i, B, T, H, D), torch.float16)
+               for i, H in ((0, Hq), (1, Hk), (2, Hk)))
+    grad = randn(cuda_device, 3, *q.shape).half()
+
+    def step(stream=None):
+        m = sdm.block_means(k, block, stream=stream)
+        sel = sdm.select_blocks(q, m, n, block, T, stream=stream)
+        out, lse = sel.attend(q, k, v, stream=stream)
+        return (sel.blocks, out, lse, *sel.backward(grad, q, k, v, out, lse, stream=stream))
+
+    want = step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = step(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    k.copy_(grid(randn(cuda_device, 9, *k.shape), torch.float16))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, step()))
+
+
+def test_empty(sdm, cuda_device):
+    dt = torch.bfloat16
+    z = lambda *s: torch.zeros(*s, dtype=dt, device=cuda_device)  # noqa: E731
+    # no keys: every query sees nothing
+    sel = sdm.select_blocks(z(2, 3, 4, 64), sdm.block_means(z(2, 0, 2, 64), 16), 2, 16, 0)
+    assert (sel.blocks == -1).all()
+    q, k = torch.ones_like(z(2, 3, 4, 64)), z(2, 0, 2, 64)
+    out, lse = sel.attend(q, k, k)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    dq, dk, dv = sel.backward(q, q, k, k, out, lse)
+    assert (dq == 0).all() and dk.shape == k.shape and dv.shape == k.shape
+    # no queries, no sequences
+    for B, Tq in ((2, 0), (0, 3)):
+        q, k = z(B, Tq, 4, 64), z(B, 40, 2, 64)
+        sel = sdm.select_blocks(q, sdm.block_means(k, 16), 2, 16, 40)
+        out, lse = sel.attend(q, k, k)
+        dq, dk, dv = sel.backward(q, q, k, k, out, lse)
+        assert out.shape == q.shape and (dk == 0).all() and (dv == 0).all()
+
+
+def test_refusals(sdm, cuda_device):
+    dev = cuda_device
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=dev)  # noqa: E731
+    q, k = z(1, 4, 4, 64), z(1, 64, 2, 64)
+    m = sdm.block_means(k, 16)
+    with pytest.raises(ValueError):
+        sdm.block_means(k, 48)
+    with pytest.raises(ValueError):
+        sdm.block_means(z(1, 8, 1, 12), 16)
+    with pytest.raises(ValueError):
+        sdm.block_means(k, 16, new_keys=1)
+    with pytest.raises(TypeError):
+        sdm.block_means(k.double(), 16)
+    with pytest.raises(ValueError):
+        sdm.block_means(k.cpu(), 16)
+    with pytest.raises(ValueError):
+        sdm.select_blocks(q, m, 0, 16, 64)
+    with pytest.raises(ValueError):
+        sdm.select_blocks(q, m, 2, 16, 65)
+    with pytest.raises(ValueError):
+        sdm.select_blocks(z(1, 4, 3, 64), m, 2, 16, 64)
+    with pytest.raises(TypeError):
+        sdm.select_blocks(q, m.half(), 2, 16, 64)
+    with pytest.raises(TypeError):
+        sdm.select_blocks(q, m, 2, 16, 64, torch.tensor([64], device=dev))
+    good = torch.tensor([0, 3, -1], dtype=torch.int32, device=dev).expand(1, 4, 2, 3).contiguous()
+    sel = sdm.BlockSelection(good, 16, 64)
+    for bad in ([0, 4, -1], [1, 0, -1], [0, 0, -1], [-1, 2, 3], [-2, 0, 1]):
+        x = good.clone()
+        x[0, 3, 1] = torch.tensor(bad, dtype=torch.int32)
+        with pytest.raises(sdm.SpmmError):
+            sdm.BlockSelection(x, 16, 64)
+        # unchecked, such entries are skipped: no fault
+        o, _ = sdm.BlockSelection(x, 16, 64, validate=False).attend(q, k, k)
+        assert (o == 0).all()
+    with pytest.raises(TypeError):
+        sel.attend(q.float(), k.float(), k.float())
+    with pytest.raises(TypeError):
+        sel.attend(q, k.half(), k)
+    with pytest.raises(ValueError):
+        sel.attend(z(1, 4, 4, 32), z(1, 64, 2, 32), z(1, 64, 2, 32))
+    with pytest.raises(ValueError):
+        sel.attend(q, z(1, 63, 2, 64), k)
+    with pytest.raises(ValueError):
+        sel.attend(z(1, 4, 5, 64), k, k)
+    with pytest.raises(ValueError):
+        sel.attend(z(1, 4, 4, 128)[..., ::2], k, k)
+    with pytest.raises(ValueError):
+        sel.attend(q, z(1, 64, 2, 65)[..., 1:], k)
+    out, lse = sel.attend(q, k, k)
+    with pytest.raises(ValueError):
+        sel.backward(q[:, :3], q, k, k, out, lse)
+    with pytest.raises(ValueError):
+        sel.backward(q, q, k, k, out, lse[..., :2])
+    dq, _, _ = sel.backward(q, q, k, k, out, lse)
+    assert (dq == 0).all()
