@@ -30,6 +30,13 @@ extern "C" {
 
 typedef enum { SPMM_F32 = 0, SPMM_BF16 = 1, SPMM_F16 = 2 } spmm_dtype;
 
+/*
+ * spmm_dynamic_sync -- wait for `stream`, then report SPMM_ERR_TIMEOUT if a
+ * bounded device-side wait of one of these calls gave up since the last time
+ * (its outputs are then incomplete), and clear that. Synchronous.
+ */
+spmm_status spmm_dynamic_sync(void *stream);
+
 /* ------------------------------------------------------------------ routes */
 
 /* Largest number of experts (the sort keeps a counter per warp and expert in

@@ -34,7 +34,7 @@ __all__ = [
     "spmm_check_wait_timeout", "spmm_plan_create_range", "spmm_partition_rows",
     "spmm_plan_prepare_blocks",
     "PlanInfo", "REDUCE", "FAMILY", "lib", "build_library",
-    "ExpertRoutes", "BlockSelection", "block_means", "select_blocks",
+    "ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync",
 ]
 
 REDUCE = {"sum": 0, "mean": 1, "max": 2}
@@ -504,5 +504,9 @@ def spmm_max(rowptr, col, val, mat):
     return spmm(rowptr, col, val, mat, "max")
 
 
-# products whose sparse matrix the model chooses (built on the names above)
-from .dynamic import BlockSelection, ExpertRoutes, block_means, select_blocks  # noqa: E402
+def __getattr__(name):
+    """The products whose sparse matrix the model chooses (they import torch)."""
+    if name in ("ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync"):
+        from . import dynamic
+        return getattr(dynamic, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "dyn.cuh"
+#include "tma.cuh"
 
 namespace spmm {
 
@@ -81,10 +82,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&x)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
                  : "r"(addr));
-}
-
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return (uint32_t)__cvta_generic_to_shared(p);
 }
 
 // 16 bytes global -> shared, asynchronously; zeros when !live (src is not read).

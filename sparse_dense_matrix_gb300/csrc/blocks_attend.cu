@@ -7,10 +7,17 @@
 // memory straight into fragments: a lane reads 16 adjacent bytes of a key's row
 // and the order of the summed index is permuted to suit (Q is read the same
 // way; for V^T two keys' words are interleaved).
-#include "blocks.cuh"
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "blocks_tile.cuh"
 
 namespace spmm {
 namespace {
+
+__device__ int32_t g_dynamic_err[kErrWords];
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 constexpr int kRowWarps = 4;
 constexpr int kRowThreads = 32 * kRowWarps;
@@ -244,6 +251,222 @@ __global__ void __launch_bounds__(128) k_attend_join(RowArgs p, int R, int64_t r
     if (d == 0) p.lse[i] = (sum != 0.0f ? base + log2f(sum) : -INFINITY) * kLn2;
 }
 
+// ------------------------------------------------------------- by tile of rows
+struct AttendTileArgs {
+    TileArgs t;
+    void *out;
+    float *lse;
+};
+
+// One row, key by key, for rows whose tile gave a result that is not finite: in
+// the tile a value that is infinite or NaN times the weight 0 of a row that does
+// not see it spoils that row too; here each row meets the keys it sees only.
+template <typename T, int D>
+__device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, int h, int t, int head) {
+    const BlkArgs &a = p.t.a;
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int limit = blk_limit(a, blk_len(a, b), t);
+    const float scale2 = a.scale * kLog2e;
+    float q[E], o[E] = {}, m = -INFINITY, l = 0.0f;
+    ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
+    const int32_t *list = a.blocks + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.n;
+    for (int j = 0; j < a.n; ++j) {
+        if (!blk_entry_ok(list, j, a.NB)) continue;
+        const int k0 = list[j] * a.block, k1 = min(k0 + a.block, limit);
+        for (int key = k0; key < k1; ++key) {
+            float x[E], dot = 0.0f;
+            ld_pack<T, E>((const T *)a.k + b * a.k_sb + key * a.k_st + h * a.k_sh + lane * E, x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) dot = fmaf(q[e], x[e], dot);
+#pragma unroll
+            for (int w = 16; w; w >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, w);
+            const float s = dot * scale2, mx = fmaxf(m, s);
+            const float base = mx == -INFINITY ? 0.0f : mx;
+            const float corr = ex2(m - base), pr = ex2(s - base);
+            m = mx;
+            l = fmaf(l, corr, pr);
+            ld_pack<T, E>((const T *)a.v + b * a.v_sb + key * a.v_st + h * a.v_sh + lane * E, x);
+            const float pt = to_f32(from_f32<T>(pr));
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(pt, x[e], o[e] * corr);
+        }
+    }
+    const float inv = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= inv;
+    const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
+    st_pack<T, E>((T *)p.out + row * D + lane * E, o);
+    if (lane == 0) p.lse[row] = l != 0.0f ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <typename T, int D, int KB>
+__global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(const __grid_constant__
+                                                                    AttendTileArgs p) {
+    using S = TileSmem<D, KB>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[S::stages], empty[S::stages];
+    __shared__ TileStage info[S::stages];
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const BlkArgs &a = p.t.a;
+    const TilePlace at(p.t);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kTileWarps);
+        }
+        mbar_init_fence();
+    }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    if (warp == kTileWarps) {
+        tile_produce<D, KB>(p.t, at, smem, full, empty, info);
+        return;
+    }
+    const int len = blk_len(a, at.b);
+    const float scale2 = a.scale * kLog2e;
+    // rows r and r + 8 of the warp's 16
+    int t[2], head[2], limit[2], qi[2];
+    const T *qp[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t f = at.f0 + warp * 16 + r + 8 * e;
+        const bool live = f < p.t.rows;
+        t[e] = live ? (int)(f / a.G) : at.t_first;
+        head[e] = at.h * a.G + (live ? (int)(f - (int64_t)t[e] * a.G) : 0);
+        qi[e] = t[e] - at.t_first;
+        limit[e] = live ? blk_limit(a, len, t[e]) : 0;
+        qp[e] = limit[e] ? (const T *)a.q + at.b * a.q_sb + t[e] * a.q_st + head[e] * a.q_sh : nullptr;
+    }
+    uint32_t q[D / 16][4];
+    load_row_frags<T, D>(q, qp[0], qp[1], c);
+    const int least_limit = __reduce_min_sync(0xffffffffu, min(limit[0], limit[1]));
+
+    float o[D / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
+    int stage = 0;
+    uint32_t parity = 0;
+    while (mbar_wait(&full[stage], parity, p.t.err)) {
+        const int key0 = info[stage].key0;
+        if (key0 < 0) break;
+        bool mine[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            mine[e] = (info[stage].mask[qi[e] >> 5] >> (qi[e] & 31) & 1u) && key0 < limit[e];
+        if (__any_sync(0xffffffffu, mine[0] || mine[1])) {
+            const uint32_t sk = smem + stage * S::stage, sv = sk + S::operand;
+            if (key0 + KB > len) zero_tail<D, KB>(sv, len - key0);
+            float s[KB / 8][4] = {};
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int n = 0; n < KB / 16; ++n) {
+                    uint32_t x[4];
+                    ldsm4(sk + panel_at<KB>(16 * n + (lane >> 4) * 8 + (lane & 7),
+                                            2 * i + ((lane >> 3) & 1)), x);
+                    mma16816<T>(s[2 * n], q[i][0], q[i][1], q[i][2], q[i][3], x[0], x[1]);
+                    mma16816<T>(s[2 * n + 1], q[i][0], q[i][1], q[i][2], q[i][3], x[2], x[3]);
+                }
+            // a key past some row's limit, or rows that did not choose the block
+            const bool whole = key0 + KB <= least_limit;
+            float corr[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < KB / 8; ++n)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        float x = s[n][2 * e + w] * scale2;
+                        if (!mine[e] || (!whole && key0 + 8 * n + 2 * c + w >= limit[e]))
+                            x = -INFINITY;
+                        s[n][2 * e + w] = x;
+                        mx = fmaxf(mx, x);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                mx = fmaxf(mx, m[e]);
+                const float base = mx == -INFINITY ? 0.0f : mx;
+                corr[e] = ex2(m[e] - base);
+                m[e] = mx;
+                float sum = 0.0f;
+#pragma unroll
+                for (int n = 0; n < KB / 8; ++n)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        s[n][2 * e + w] = ex2(s[n][2 * e + w] - base);
+                        sum += s[n][2 * e + w];
+                    }
+                l[e] = fmaf(l[e], corr[e], sum);
+            }
+            if (__any_sync(0xffffffffu, corr[0] != 1.0f || corr[1] != 1.0f)) {
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[n][0] *= corr[0];
+                    o[n][1] *= corr[0];
+                    o[n][2] *= corr[1];
+                    o[n][3] *= corr[1];
+                }
+            }
+            // P is rounded to the inputs' type for the matrix instruction; l sums
+            // the unrounded weights
+#pragma unroll
+            for (int i = 0; i < KB / 16; ++i) {
+                const uint32_t a0 = pack2<T>(s[2 * i][0], s[2 * i][1]);
+                const uint32_t a1 = pack2<T>(s[2 * i][2], s[2 * i][3]);
+                const uint32_t a2 = pack2<T>(s[2 * i + 1][0], s[2 * i + 1][1]);
+                const uint32_t a3 = pack2<T>(s[2 * i + 1][2], s[2 * i + 1][3]);
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t x[4];
+                    ldsm4_t(sv + panel_at<KB>(16 * i + (lane & 15), 2 * n + (lane >> 4)), x);
+                    mma16816<T>(o[2 * n], a0, a1, a2, a3, x[0], x[1]);
+                    mma16816<T>(o[2 * n + 1], a0, a1, a2, a3, x[2], x[3]);
+                }
+            }
+            if (key0 + KB > len) fence_proxy_async_shared();   // zeros, then the next copy
+            __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == S::stages) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+    unsigned redo = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        float odd = l[e] * 0.0f;                   // NaN if anything is not finite
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+            odd = fmaf(o[n][2 * e], 0.0f, odd);
+            odd = fmaf(o[n][2 * e + 1], 0.0f, odd);
+        }
+        const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f);
+        const bool live = at.f0 + warp * 16 + r + 8 * e < p.t.rows;
+        redo |= __ballot_sync(0xffffffffu, c == 0 && live && (bad >> (4 * r) & 15u)) << e;
+        if (!live) continue;
+        const float inv = l[e] != 0.0f ? __fdiv_rn(1.0f, l[e]) : 0.0f;
+        const int64_t row = ((int64_t)at.b * a.Tq + t[e]) * a.Hq + head[e];
+        T *out = (T *)p.out + row * D + 2 * c;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            *(uint32_t *)(out + 8 * n) = pack2<T>(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
+        if (c == 0)
+            p.lse[row] = l[e] != 0.0f ? ((m[e] == -INFINITY ? 0.0f : m[e]) + log2f(l[e])) * kLn2
+                                      : -INFINITY;
+    }
+    __syncwarp();
+    while (redo) {                                  // bit 4 r + e: row r + 8 e
+        const int bit = __ffs(redo) - 1;
+        redo &= redo - 1;
+        const int64_t f = at.f0 + warp * 16 + (bit >> 2) + 8 * (bit & 1);
+        const int tt = (int)(f / a.G);
+        attend_row_alone<T, D>(p, at.b, at.h, tt, at.h * a.G + (int)(f - (int64_t)tt * a.G));
+    }
+}
+
 // ------------------------------------------------------------------- host
 struct RowPlan {
     int nt, gt, splits;
@@ -280,14 +503,87 @@ cudaError_t launch_rows(const RowArgs &p, const RowPlan &rp, int64_t rows, cudaS
     return cudaGetLastError();
 }
 
+template <typename T, int D, int KB>
+cudaError_t launch_tile(const AttendTileArgs &p, int64_t B, cudaStream_t s) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k_attend_tile<T, D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             TileSmem<D, KB>::bytes);
+    if (e != cudaSuccess) return e;
+    k_attend_tile<T, D, KB><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), kTileThreads,
+                              TileSmem<D, KB>::bytes, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_tile(const AttendTileArgs &p, int64_t B, cudaStream_t s) {
+    if (p.t.a.block == 16) return launch_tile<T, D, 16>(p, B, s);
+    if (p.t.a.block == 32) return launch_tile<T, D, 32>(p, B, s);
+    return launch_tile<T, D, 64>(p, B, s);
+}
+
+// By tile when every kv head has at least two tiles of rows.
+bool by_tile(const spmm_blocks_shape *s) {
+    return s->Tk > 0 && s->Tq * (s->Hq / s->Hk) >= 2 * kTileRows && s->B * s->Hk <= 65535;
+}
+
 }  // namespace
+
+cudaError_t dynamic_err(int32_t **err) {
+    return cudaGetSymbolAddress((void **)err, g_dynamic_err);
+}
+
+cudaError_t encode_rows(const spmm_rows &r, const spmm_blocks_shape *s, int box_rows,
+                        CUtensorMap *map) {
+    if (!g_encode) {
+        cudaDriverEntryPointQueryResult q;
+        void *fn = nullptr;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                               cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn)
+            return e != cudaSuccess ? e : cudaErrorNotSupported;
+        g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)s->D, (cuuint64_t)s->Tk, (cuuint64_t)s->Hk,
+                                (cuuint64_t)s->B};
+    // the stride of a dimension of one means nothing, and may be any number
+    const cuuint64_t strides[3] = {(cuuint64_t)(s->Tk > 1 ? r.st * 2 : 16),
+                                   (cuuint64_t)(s->Hk > 1 ? r.sh * 2 : 16),
+                                   (cuuint64_t)(s->B > 1 ? r.sb * 2 : 16)};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult e = g_encode(
+        map, s->dtype == SPMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+        4, const_cast<void *>(r.data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace spmm
 
 extern "C" {
 
+spmm_status spmm_dynamic_sync(void *stream) {
+    using namespace spmm;
+    cudaStream_t s = (cudaStream_t)stream;
+    int32_t *err = nullptr, word = 0;
+    cudaError_t e = dynamic_err(&err);
+    if (e == cudaSuccess)
+        e = cudaMemcpyAsync(&word, err + kErrTimeout, sizeof(word), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && word) {
+        e = cudaMemsetAsync(err + kErrTimeout, 0, sizeof(word), s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e == cudaSuccess) return SPMM_ERR_TIMEOUT;
+    }
+    return cuda_status(e);
+}
+
 int64_t spmm_blocks_attend_workspace(const spmm_blocks_shape *s) {
     using namespace spmm;
     if (blk_check(s, true) != SPMM_OK) return 0;
+    if (by_tile(s)) return 0;
     const RowPlan p = row_plan(s);
     if (p.splits == 1) return 0;
     return p.items * p.splits * 8 * p.nt * (s->D + 1) * 4;
@@ -305,11 +601,33 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
         return SPMM_ERR_INVALID_ARG;
     const int64_t need = spmm_blocks_attend_workspace(s);
     if (need && (!work || (uintptr_t)work % 16 || work_bytes < need)) return SPMM_ERR_INVALID_ARG;
+    cudaStream_t cs = (cudaStream_t)stream;
     RowArgs p{};
     p.a = blk_args(s, blocks);
     set_rows(p.a.q, p.a.q_sb, p.a.q_st, p.a.q_sh, q);
     set_rows(p.a.k, p.a.k_sb, p.a.k_st, p.a.k_sh, k);
     set_rows(p.a.v, p.a.v_sb, p.a.v_st, p.a.v_sh, v);
+    if (by_tile(s)) {
+        AttendTileArgs t{};
+        t.t.a = p.a;
+        t.t.rows = s->Tq * p.a.G;
+        t.t.tiles = (int)((t.t.rows + kTileRows - 1) / kTileRows);
+        t.out = out;
+        t.lse = lse;
+        const int box = (int)std::min<int64_t>(s->block, 64);
+        cudaError_t e = dynamic_err(&t.t.err);
+        if (e == cudaSuccess) e = encode_rows(k, s, box, &t.t.k_map);
+        if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
+        if (e == cudaSuccess) {
+            if (s->dtype == SPMM_BF16)
+                e = s->D == 64 ? launch_tile<__nv_bfloat16, 64>(t, s->B, cs)
+                               : launch_tile<__nv_bfloat16, 128>(t, s->B, cs);
+            else
+                e = s->D == 64 ? launch_tile<__half, 64>(t, s->B, cs)
+                               : launch_tile<__half, 128>(t, s->B, cs);
+        }
+        return cuda_status(e);
+    }
     const RowPlan rp = row_plan(s);
     if (rp.items * rp.splits > INT32_MAX) return SPMM_ERR_UNSUPPORTED;
     p.gt = rp.gt;
@@ -318,7 +636,6 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
     p.lse = lse;
     p.part_o = (float *)work;
     p.part_lse = p.part_o + rp.items * rp.splits * 8 * rp.nt * s->D;
-    cudaStream_t cs = (cudaStream_t)stream;
     const int64_t rows = s->B * s->Tq * s->Hq;
     cudaError_t e;
     if (s->dtype == SPMM_BF16)

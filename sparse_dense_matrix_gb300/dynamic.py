@@ -17,13 +17,21 @@ from __future__ import annotations
 import ctypes
 import math
 
-from . import SpmmError, _check, _stream_handle, lib
+import torch
+
+from . import SpmmError, _check, lib
 
 __all__ = ["ExpertRoutes", "BlockSelection", "block_means", "select_blocks",
-           "ROUTES_MAX_EXPERTS", "BLOCK_SIZES"]
+           "dynamic_sync", "ROUTES_MAX_EXPERTS", "BLOCK_SIZES"]
 
 ROUTES_MAX_EXPERTS = 2048
 BLOCK_SIZES = (16, 32, 64, 128)
+
+# A small call's time is mostly the host's: the current device and stream are
+# read directly (0.15 us; building a torch.cuda.Stream object takes 3 us), and
+# each check below costs one attribute access.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class _Rows(ctypes.Structure):
@@ -40,6 +48,7 @@ class _Shape(ctypes.Structure):
 def _declare():
     vp, i64, i32, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(_Shape)
     sigs = {
+        "spmm_dynamic_sync": ([vp], i32),
         "spmm_routes_workspace": ([i64] * 3, i64),
         "spmm_routes_sort": ([vp, i64, i64, i64, vp, vp, vp, i64, vp], i32),
         "spmm_routes_dispatch": ([i32, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp], i32),
@@ -63,29 +72,20 @@ def _declare():
 
 
 _declare()
-_DTYPE = None
-
-
-def _dtypes():
-    global _DTYPE
-    if _DTYPE is None:
-        import torch
-        _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    return _DTYPE
+_DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_INT, _FLOAT, _HALVES = (torch.int32,), (torch.float32,), (torch.bfloat16, torch.float16)
 
 
 def _elsewhere(dev, stream):
     """A context in which `dev` and `stream` are current, or None if they are."""
-    import torch
     if stream is None:
-        return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return None if _current_device() == dev.index else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
     return torch.cuda.stream(stream)
 
 
 def _tensor(t, name, dtypes, ndim, dev=None):
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -101,11 +101,22 @@ def _tensor(t, name, dtypes, ndim, dev=None):
 
 def _dense(t, name, dtypes, shape, dev):
     _tensor(t, name, dtypes, len(shape), dev)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+def dynamic_sync(stream=None) -> None:
+    """Wait for the stream; SpmmError (SPMM_ERR_TIMEOUT) if a bounded device-side wait of
+    one of these calls gave up since the last time."""
+    handle = _raw_stream(_current_device()) if stream is None else stream.cuda_stream
+    _check(lib.spmm_dynamic_sync(handle), "spmm_dynamic_sync")
+
+
+def _scratch(like, need):
+    return like.new_empty(need, dtype=torch.uint8) if need else None
 
 
 # -------------------------------------------------------------------- routes
@@ -126,8 +137,7 @@ class ExpertRoutes:
     """
 
     def __init__(self, ids, num_experts: int, stream=None):
-        import torch
-        _tensor(ids, "ids", (torch.int32,), 2)
+        _tensor(ids, "ids", _INT, 2)
         if not ids.is_contiguous():
             raise ValueError("ids must be contiguous")
         E = int(num_experts)
@@ -135,83 +145,81 @@ class ExpertRoutes:
             raise ValueError(f"num_experts must be in [0, {ROUTES_MAX_EXPERTS}], got {E}")
         self.device = dev = ids.device
         self.num_experts = E
-        self.T, self.k = T, k = ids.shape
+        self.T, self.k = ids.shape
         ctx = _elsewhere(dev, stream)
-        if ctx is not None:
+        if ctx is None:
+            self._sort(ids)
+        else:
             with ctx:
                 self._sort(ids)
-        else:
-            self._sort(ids)
 
     def _sort(self, ids):
-        import torch
-        T, k, E, dev = self.T, self.k, self.num_experts, self.device
-        self.slots = torch.empty((T, k), dtype=torch.int32, device=dev)
-        self.offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        T, k, E = self.T, self.k, self.num_experts
+        self.slots = torch.empty_like(ids)
+        self.offsets = ids.new_empty(E + 1)
         need = lib.spmm_routes_workspace(T, k, E)
-        work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _check(lib.spmm_routes_sort(ids.data_ptr(), T, k, E, self.slots.data_ptr(),
-                                    self.offsets.data_ptr(),
-                                    None if work is None else work.data_ptr(), need,
-                                    _stream_handle(None)), "spmm_routes_sort")
+        work = _scratch(ids, need)
+        # what every product's call begins its list of routes with
+        self._routes = (self.slots.data_ptr(), self.offsets.data_ptr(), T, k, E)
+        st = lib.spmm_routes_sort(ids.data_ptr(), T, k, E, *self._routes[:2],
+                                  None if work is None else work.data_ptr(), need,
+                                  _raw_stream(self.device.index))
+        if st:
+            _check(st, "spmm_routes_sort")
 
     def _by_token(self, x, name):
-        _tensor(x, name, _dtypes(), 2, self.device)
-        if x.shape[0] != self.T:
+        _tensor(x, name, _DTYPE, 2, self.device)
+        T, H = x.shape
+        if T != self.T:
             raise ValueError(f"{name} must be [{self.T}, H], got {list(x.shape)}")
-        if x.shape[1] > 1 and x.stride(1) != 1:
+        ld, step = x.stride()
+        if step != 1 and H > 1:
             raise ValueError(f"{name} must have adjacent elements in a row")
-        return x
+        return H, ld
 
-    def _by_slot(self, y, name, like=None):
-        _tensor(y, name, _dtypes(), 2, self.device)
-        H = y.shape[1] if like is None else like.shape[1]
-        if tuple(y.shape) != (self.T * self.k, H):
-            raise ValueError(f"{name} must be [{self.T * self.k}, {H}], got {list(y.shape)}")
-        if like is not None and y.dtype != like.dtype:
-            raise TypeError(f"{name} must be {like.dtype}, got {y.dtype}")
+    def _by_slot(self, y, name, H=None):
+        _tensor(y, name, _DTYPE, 2, self.device)
+        P, width = y.shape
+        if P != self.T * self.k or (H is not None and width != H):
+            raise ValueError(f"{name} must be [{self.T * self.k}, {'H' if H is None else H}], "
+                             f"got {list(y.shape)}")
         if not y.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        return y
+        return width
 
     def _weights(self, w):
-        import torch
         if w is None:
             return None
-        return _dense(w, "weights", (torch.float32,), (self.T, self.k), self.device).data_ptr()
+        return _dense(w, "weights", _FLOAT, (self.T, self.k), self.device).data_ptr()
 
     def dispatch(self, x, stream=None):
         """xs [T * k, H]: token t's row at each of its slots."""
-        import torch
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
                 return self.dispatch(x)
-        self._by_token(x, "x")
-        H = x.shape[1]
-        xs = torch.empty((self.T * self.k, H), dtype=x.dtype, device=self.device)
-        _check(lib.spmm_routes_dispatch(_dtypes()[x.dtype], x.data_ptr(), x.stride(0),
-                                        self.slots.data_ptr(), self.offsets.data_ptr(), self.T,
-                                        self.k, self.num_experts, H, xs.data_ptr(),
-                                        _stream_handle(None)), "spmm_routes_dispatch")
+        H, ld = self._by_token(x, "x")
+        xs = x.new_empty((self.T * self.k, H))
+        st = lib.spmm_routes_dispatch(_DTYPE[x.dtype], x.data_ptr(), ld, *self._routes, H,
+                                      xs.data_ptr(), _raw_stream(self.device.index))
+        if st:
+            _check(st, "spmm_routes_dispatch")
         return xs
 
     def combine(self, y, weights=None, stream=None):
         """out [T, H]: sum over j of weights[t, j] (float32; None: 1) times y at the slot of
         (t, j), summed in fp32 in the order of j."""
-        import torch
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
                 return self.combine(y, weights)
-        self._by_slot(y, "y")
+        H = self._by_slot(y, "y")
         w = self._weights(weights)
-        H = y.shape[1]
-        out = torch.empty((self.T, H), dtype=y.dtype, device=self.device)
-        _check(lib.spmm_routes_combine(_dtypes()[y.dtype], y.data_ptr(), w, self.slots.data_ptr(),
-                                       self.offsets.data_ptr(), self.T, self.k, self.num_experts,
-                                       H, out.data_ptr(), _stream_handle(None)),
-               "spmm_routes_combine")
+        out = y.new_empty((self.T, H))
+        st = lib.spmm_routes_combine(_DTYPE[y.dtype], y.data_ptr(), w, *self._routes, H,
+                                     out.data_ptr(), _raw_stream(self.device.index))
+        if st:
+            _check(st, "spmm_routes_combine")
         return out
 
     def dispatch_backward(self, grad, stream=None):
@@ -221,41 +229,36 @@ class ExpertRoutes:
     def combine_backward(self, grad, y, weights=None, stream=None):
         """(dy [T * k, H], dweights float32 [T, k]) of ``combine(y, weights)``, given the
         gradient [T, H] of its result; dweights is None without weights."""
-        import torch
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
                 return self.combine_backward(grad, y, weights)
-        self._by_token(grad, "grad")
-        self._by_slot(y, "y", grad)
+        H, ld = self._by_token(grad, "grad")
+        self._by_slot(y, "y", H)
+        if y.dtype != grad.dtype:
+            raise TypeError(f"y must be {grad.dtype}, got {y.dtype}")
         w = self._weights(weights)
         dy = torch.empty_like(y)
-        dw = None if w is None else torch.empty((self.T, self.k), dtype=torch.float32,
-                                                device=self.device)
-        _check(lib.spmm_routes_combine_backward(
-            _dtypes()[y.dtype], grad.data_ptr(), grad.stride(0), y.data_ptr(), w,
-            self.slots.data_ptr(), self.offsets.data_ptr(), self.T, self.k, self.num_experts,
-            y.shape[1], dy.data_ptr(), None if dw is None else dw.data_ptr(),
-            _stream_handle(None)), "spmm_routes_combine_backward")
+        dw = None if w is None else torch.empty_like(weights)
+        st = lib.spmm_routes_combine_backward(
+            _DTYPE[y.dtype], grad.data_ptr(), ld, y.data_ptr(), w, *self._routes, H, dy.data_ptr(),
+            None if dw is None else dw.data_ptr(), _raw_stream(self.device.index))
+        if st:
+            _check(st, "spmm_routes_combine_backward")
         return dy, dw
 
 
 # -------------------------------------------------------------------- blocks
-def _rows(t):
-    sb, st, sh, _ = t.stride()
-    return _Rows(t.data_ptr(), sb, st, sh)
-
-
 def _heads(t, name, dtypes, dev=None):
-    """A [B, T, heads, D] tensor whose rows are adjacent elements at 16-byte boundaries."""
+    """The rows of a [B, T, heads, D] tensor: adjacent elements at 16-byte boundaries."""
     _tensor(t, name, dtypes, 4, dev)
     sb, st, sh, sd = t.stride()
-    e = t.element_size()
-    if t.numel() and ((sd != 1 and t.shape[3] > 1) or sb * e % 16 or st * e % 16 or sh * e % 16
-                      or t.data_ptr() % 16):
-        raise ValueError(f"{name} must have adjacent elements in a row and rows at 16-byte "
-                         f"boundaries (strides {tuple(t.stride())})")
-    return t
+    at, e = t.data_ptr(), t.element_size()
+    if ((sb | st | sh) * e | at) % 16 or (sd != 1 and t.shape[3] > 1):
+        if t.numel():
+            raise ValueError(f"{name} must have adjacent elements in a row and rows at 16-byte "
+                             f"boundaries (strides {tuple(t.stride())})")
+    return _Rows(at, sb, st, sh)
 
 
 def _block_size(block):
@@ -265,10 +268,7 @@ def _block_size(block):
 
 
 def _lengths_ptr(lengths, B, dev):
-    import torch
-    if lengths is None:
-        return None
-    return _dense(lengths, "lengths", (torch.int32,), (B,), dev).data_ptr()
+    return None if lengths is None else _dense(lengths, "lengths", _INT, (B,), dev).data_ptr()
 
 
 def block_means(k, block: int = 64, lengths=None, out=None, new_keys: int | None = None,
@@ -278,8 +278,7 @@ def block_means(k, block: int = 64, lengths=None, out=None, new_keys: int | None
     ``k`` [B, Tk, Hk, D]; sequence b holds lengths[b] keys (int32 [B]; None: Tk). With
     ``new_keys`` and ``out`` (the means so far) only the blocks that hold one of each
     sequence's last new_keys keys are computed again, after those keys were appended."""
-    import torch
-    _heads(k, "k", _dtypes())
+    rows = _heads(k, "k", _DTYPE)
     dev = k.device
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -293,13 +292,15 @@ def block_means(k, block: int = 64, lengths=None, out=None, new_keys: int | None
     if new_keys is not None and (out is None or new_keys < 0):
         raise ValueError("new_keys (>= 0) updates the means given as out")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = k.new_empty(shape, dtype=torch.float32)
     else:
-        _dense(out, "out", (torch.float32,), shape, dev)
-    s = _Shape(B, 1, Tk, Hk, Hk, D, block, 1, _dtypes()[k.dtype], 1, 1.0,
+        _dense(out, "out", _FLOAT, shape, dev)
+    s = _Shape(B, 1, Tk, Hk, Hk, D, block, 1, _DTYPE[k.dtype], 1, 1.0,
                _lengths_ptr(lengths, B, dev))
-    _check(lib.spmm_blocks_means(s, _rows(k), -1 if new_keys is None else new_keys, out.data_ptr(),
-                                 _stream_handle(None)), "spmm_blocks_means")
+    st = lib.spmm_blocks_means(s, rows, -1 if new_keys is None else new_keys, out.data_ptr(),
+                               _raw_stream(dev.index))
+    if st:
+        _check(st, "spmm_blocks_means")
     return out
 
 
@@ -312,8 +313,7 @@ def select_blocks(q, means, n: int, block: int, num_keys: int, lengths=None, cau
     Query i is at position lengths[b] - Tq + i; causal lists hold the block of that
     position and the n - 1 best ones before it, others the n best of the sequence's
     blocks. Ties go to the lowest block."""
-    import torch
-    _heads(q, "q", _dtypes())
+    rows = _heads(q, "q", _DTYPE)
     dev = q.device
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
@@ -321,7 +321,7 @@ def select_blocks(q, means, n: int, block: int, num_keys: int, lengths=None, cau
             return select_blocks(q, means, n, block, num_keys, lengths, causal)
     B, Tq, Hq, D = q.shape
     block, n, Tk = _block_size(block), int(n), int(num_keys)
-    _tensor(means, "means", (torch.float32,), 4, dev)
+    _tensor(means, "means", _FLOAT, 4, dev)
     Hk = means.shape[2]
     if n < 1 or Tk < 0:
         raise ValueError(f"n must be at least 1 and num_keys at least 0, got {n} and {Tk}")
@@ -329,16 +329,20 @@ def select_blocks(q, means, n: int, block: int, num_keys: int, lengths=None, cau
         raise ValueError(f"{Hq} query heads do not divide into {Hk} groups")
     if D % 8 or not 8 <= D <= 256:
         raise ValueError(f"the width of a query must be a multiple of 8 up to 256, got {D}")
-    _dense(means, "means", (torch.float32,), (B, -(-Tk // block), Hk, D), dev)
-    s = _Shape(B, Tq, Tk, Hq, Hk, D, block, n, _dtypes()[q.dtype], int(bool(causal)), 1.0,
+    _dense(means, "means", _FLOAT, (B, -(-Tk // block), Hk, D), dev)
+    s = _Shape(B, Tq, Tk, Hq, Hk, D, block, n, _DTYPE[q.dtype], 1 if causal else 0, 1.0,
                _lengths_ptr(lengths, B, dev))
-    blocks = torch.empty((B, Tq, Hk, n), dtype=torch.int32, device=dev)
+    blocks = q.new_empty((B, Tq, Hk, n), dtype=torch.int32)
     need = lib.spmm_blocks_select_workspace(s)
-    work = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _check(lib.spmm_blocks_select(s, _rows(q), means.data_ptr() or None, blocks.data_ptr(),
-                                  None if work is None else work.data_ptr(), need,
-                                  _stream_handle(None)), "spmm_blocks_select")
-    return BlockSelection(blocks, block, Tk, lengths, causal, validate=False)
+    work = _scratch(q, need)
+    st = lib.spmm_blocks_select(s, rows, means.data_ptr() or None, blocks.data_ptr(),
+                                None if work is None else work.data_ptr(), need,
+                                _raw_stream(dev.index))
+    if st:
+        _check(st, "spmm_blocks_select")
+    sel = BlockSelection.__new__(BlockSelection)
+    sel._set(blocks, block, Tk, lengths, causal, s.lengths)
+    return sel
 
 
 class BlockSelection:
@@ -351,48 +355,49 @@ class BlockSelection:
 
     def __init__(self, blocks, block: int, num_keys: int, lengths=None, causal: bool = True,
                  validate: bool = True):
-        import torch
-        _tensor(blocks, "blocks", (torch.int32,), 4)
+        _tensor(blocks, "blocks", _INT, 4)
         if not blocks.is_contiguous():
             raise ValueError("blocks must be contiguous")
-        self.device = blocks.device
-        self.blocks, self.block, self.num_keys = blocks, _block_size(block), int(num_keys)
-        self.lengths, self.causal = lengths, bool(causal)
         B, Tq, Hk, n = blocks.shape
-        if Hk < 1 or n < 1 or self.num_keys < 0:
+        num_keys = int(num_keys)
+        if Hk < 1 or n < 1 or num_keys < 0:
             raise ValueError(f"blocks must be [B, Tq, Hk >= 1, n >= 1], got {list(blocks.shape)}")
-        self._lengths = _lengths_ptr(lengths, B, self.device)
+        self._set(blocks, _block_size(block), num_keys, lengths, causal,
+                  _lengths_ptr(lengths, B, blocks.device))
         if validate:
             with torch.cuda.device(self.device):
-                bad = torch.empty(1, dtype=torch.int32, device=self.device)
-                s = _Shape(B, Tq, self.num_keys, Hk, Hk, 64, self.block, n, 1, int(self.causal),
-                           1.0, self._lengths)
+                bad = blocks.new_empty(1)
+                s = _Shape(B, Tq, num_keys, Hk, Hk, 64, self.block, n, 1, int(self.causal), 1.0,
+                           self._lengths)
                 _check(lib.spmm_blocks_check(s, blocks.data_ptr() or None, bad.data_ptr(),
-                                             _stream_handle(None)), "spmm_blocks_check")
+                                             _raw_stream(self.device.index)), "spmm_blocks_check")
                 if int(bad.item()):
                     raise SpmmError(2, "a list of blocks is not strictly ascending block numbers "
                                        "followed by -1")
 
-    def _shape(self, q, k, v, scale):
-        import torch
-        kinds = (torch.bfloat16, torch.float16)
-        _heads(q, "q", kinds, self.device)
-        same = (q.dtype,)
-        _heads(k, "k", same, self.device)
-        _heads(v, "v", same, self.device)
+    def _set(self, blocks, block, num_keys, lengths, causal, lengths_ptr):
+        self.device, self.blocks, self.block = blocks.device, blocks, block
+        self.num_keys, self.lengths, self.causal = num_keys, lengths, bool(causal)
+        self._lengths = lengths_ptr
+
+    def _problem(self, q, k, v, scale):
+        """The call's shape, and the rows of q, k and v."""
+        dev = self.device
+        rows = (_heads(q, "q", _HALVES, dev), _heads(k, "k", (q.dtype,), dev),
+                _heads(v, "v", (q.dtype,), dev))
         B, Tq, Hk, n = self.blocks.shape
-        Hq, D = q.shape[2:]
-        if q.shape[:2] != (B, Tq) or Hq % Hk or Hq < 1:
+        Bq, T, Hq, D = q.shape
+        if Bq != B or T != Tq or Hq % Hk or Hq < 1:
             raise ValueError(f"q must be [{B}, {Tq}, a multiple of {Hk}, D], got {list(q.shape)}")
-        if D not in (64, 128):
+        if D != 64 and D != 128:
             raise ValueError(f"the width of a head must be 64 or 128, got {D}")
         want = (B, self.num_keys, Hk, D)
-        if tuple(k.shape) != want or tuple(v.shape) != want:
+        if k.shape != want or v.shape != want:
             raise ValueError(f"k and v must be {list(want)}, got {list(k.shape)} and "
                              f"{list(v.shape)}")
         scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-        return _Shape(B, Tq, self.num_keys, Hq, Hk, D, self.block, n, _dtypes()[q.dtype],
-                      int(self.causal), scale, self._lengths)
+        return _Shape(B, Tq, self.num_keys, Hq, Hk, D, self.block, n, _DTYPE[q.dtype],
+                      1 if self.causal else 0, scale, self._lengths), rows
 
     def attend(self, q, k, v, scale: float | None = None, stream=None):
         """(out [B, Tq, Hq, D], lse float32 [B, Tq, Hq]): softmax attention over the seen keys of
@@ -401,44 +406,42 @@ class BlockSelection:
 
         q, k, v: bfloat16 or float16, D 64 or 128, k and v [B, num_keys, Hk, D]; any
         strides with adjacent elements in a row and rows at 16-byte boundaries."""
-        import torch
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
                 return self.attend(q, k, v, scale)
-        s = self._shape(q, k, v, scale)
-        out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=self.device)
+        s, rows = self._problem(q, k, v, scale)
+        out = q.new_empty(q.shape)
+        lse = q.new_empty(q.shape[:3], dtype=torch.float32)
         need = lib.spmm_blocks_attend_workspace(s)
-        work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        _check(lib.spmm_blocks_attend(s, _rows(q), _rows(k), _rows(v), self.blocks.data_ptr(),
-                                      out.data_ptr(), lse.data_ptr(),
-                                      None if work is None else work.data_ptr(), need,
-                                      _stream_handle(None)), "spmm_blocks_attend")
+        work = _scratch(q, need)
+        st = lib.spmm_blocks_attend(s, *rows, self.blocks.data_ptr(), out.data_ptr(),
+                                    lse.data_ptr(), None if work is None else work.data_ptr(),
+                                    need, _raw_stream(self.device.index))
+        if st:
+            _check(st, "spmm_blocks_attend")
         return out, lse
 
     def backward(self, grad, q, k, v, out, lse, scale: float | None = None, stream=None):
         """(dq, dk, dv) of ``attend(q, k, v, scale)`` = (out, lse), given the gradient of out.
         The selection is a constant; keys that nothing attends to get 0."""
-        import torch
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
                 return self.backward(grad, q, k, v, out, lse, scale)
-        s = self._shape(q, k, v, scale)
-        _heads(grad, "grad", (q.dtype,), self.device)
+        s, rows = self._problem(q, k, v, scale)
+        g = _heads(grad, "grad", (q.dtype,), self.device)
         if grad.shape != q.shape:
             raise ValueError(f"grad must be {list(q.shape)}, got {list(grad.shape)}")
         _dense(out, "out", (q.dtype,), q.shape, self.device)
-        _dense(lse, "lse", (torch.float32,), q.shape[:3], self.device)
-        dq = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=self.device)
-        dv = torch.empty(v.shape, dtype=q.dtype, device=self.device)
+        _dense(lse, "lse", _FLOAT, q.shape[:3], self.device)
+        dq, dk, dv = q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape)
         need = lib.spmm_blocks_backward_workspace(s)
-        work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        _check(lib.spmm_blocks_backward(s, _rows(q), _rows(k), _rows(v), self.blocks.data_ptr(),
-                                        out.data_ptr(), lse.data_ptr(), _rows(grad), dq.data_ptr(),
-                                        dk.data_ptr(), dv.data_ptr(),
-                                        None if work is None else work.data_ptr(), need,
-                                        _stream_handle(None)), "spmm_blocks_backward")
+        work = _scratch(q, need)
+        st = lib.spmm_blocks_backward(s, *rows, self.blocks.data_ptr(), out.data_ptr(),
+                                      lse.data_ptr(), g, dq.data_ptr(), dk.data_ptr(),
+                                      dv.data_ptr(), None if work is None else work.data_ptr(),
+                                      need, _raw_stream(self.device.index))
+        if st:
+            _check(st, "spmm_blocks_backward")
         return dq, dk, dv
