@@ -300,46 +300,58 @@ __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, in
     if (lane == 0) p.lse[row] = l != 0.0f ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int D, int KB>
-__global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(const __grid_constant__
-                                                                    AttendTileArgs p) {
-    using S = TileSmem<D, KB>;
+// Variants: kLargeWarps consumer warps take the whole SM (11 and the producer
+// are three per quarter of it, which leaves each 168 registers); kSmallWarps
+// leave room for two CTAs, for problems with too few rows to give every SM two
+// large tiles.
+constexpr int kLargeWarps = 11, kSmallWarps = 4;
+template <int D, int KB, int W>
+using AttendSmem = TileSmem<D, KB, W, 1, (W == kLargeWarps ? 227 : 113) * 1024>;
+
+template <typename T, int D, int KB, int W>
+__global__ void __launch_bounds__(32 * (W + 1), W == kLargeWarps ? 1 : 2)
+    k_attend_tile(const __grid_constant__ AttendTileArgs p) {
+    using S = AttendSmem<D, KB, W>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[S::stages], empty[S::stages];
-    __shared__ TileStage info[S::stages];
+    __shared__ TileStage<W> info[S::stages];
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const BlkArgs &a = p.t.a;
-    const TilePlace at(p.t);
+    const TilePlace at(p.t, 16 * W);
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::stages; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kTileWarps);
+            mbar_init(&empty[i], W);
         }
         mbar_init_fence();
     }
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    if (warp == kTileWarps) {
-        tile_produce<D, KB>(p.t, at, smem, full, empty, info);
+    if (warp == W) {
+        tile_produce<S, D, KB, W>(
+            p.t, at, smem, full, empty, info,
+            (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_lists));
         return;
     }
     const int len = blk_len(a, at.b);
     const float scale2 = a.scale * kLog2e;
-    // rows r and r + 8 of the warp's 16
-    int t[2], head[2], limit[2], qi[2];
-    const T *qp[2];
+    // the warp's Q rows; then rows r and r + 8 of its 16
+    const uint32_t sq = smem + S::at_rows + warp * 16 * D * 2;
+    {
+        int64_t row;
+        const bool live = at.row_of(p.t, len, warp * 16 + (lane & 15), row);
+        fetch_rows<T, D>(sq, (const T *)a.q, live, at.offset(p.t, row, a.q_sb, a.q_st, a.q_sh));
+    }
+    int limit[2], qi[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int64_t f = at.f0 + warp * 16 + r + 8 * e;
-        const bool live = f < p.t.rows;
-        t[e] = live ? (int)(f / a.G) : at.t_first;
-        head[e] = at.h * a.G + (live ? (int)(f - (int64_t)t[e] * a.G) : 0);
-        qi[e] = t[e] - at.t_first;
-        limit[e] = live ? blk_limit(a, len, t[e]) : 0;
-        qp[e] = limit[e] ? (const T *)a.q + at.b * a.q_sb + t[e] * a.q_st + head[e] * a.q_sh : nullptr;
+        const int t = f < p.t.rows ? (int)(f / a.G) : at.t_first;
+        qi[e] = t - at.t_first;
+        limit[e] = f < p.t.rows ? blk_limit(a, len, t) : 0;
     }
-    uint32_t q[D / 16][4];
-    load_row_frags<T, D>(q, qp[0], qp[1], c);
+    cp_wait<0>();
+    __syncwarp();
     const int least_limit = __reduce_min_sync(0xffffffffu, min(limit[0], limit[1]));
 
     float o[D / 8][4] = {}, m[2] = {-INFINITY, -INFINITY}, l[2] = {};
@@ -357,15 +369,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(const __grid_co
             if (key0 + KB > len) zero_tail<D, KB>(sv, len - key0);
             float s[KB / 8][4] = {};
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i)
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t q[4];
+                ldsm4(sq + rows_at<D>(lane & 15, 2 * i + (lane >> 4)), q);
 #pragma unroll
                 for (int n = 0; n < KB / 16; ++n) {
                     uint32_t x[4];
                     ldsm4(sk + panel_at<KB>(16 * n + (lane >> 4) * 8 + (lane & 7),
                                             2 * i + ((lane >> 3) & 1)), x);
-                    mma16816<T>(s[2 * n], q[i][0], q[i][1], q[i][2], q[i][3], x[0], x[1]);
-                    mma16816<T>(s[2 * n + 1], q[i][0], q[i][1], q[i][2], q[i][3], x[2], x[3]);
+                    mma16816<T>(s[2 * n], q[0], q[1], q[2], q[3], x[0], x[1]);
+                    mma16816<T>(s[2 * n + 1], q[0], q[1], q[2], q[3], x[2], x[3]);
                 }
+            }
             // a key past some row's limit, or rows that did not choose the block
             const bool whole = key0 + KB <= least_limit;
             float corr[2];
@@ -448,7 +463,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_attend_tile(const __grid_co
         redo |= __ballot_sync(0xffffffffu, c == 0 && live && (bad >> (4 * r) & 15u)) << e;
         if (!live) continue;
         const float inv = l[e] != 0.0f ? __fdiv_rn(1.0f, l[e]) : 0.0f;
-        const int64_t row = ((int64_t)at.b * a.Tq + t[e]) * a.Hq + head[e];
+        const int64_t row = at.out_row(p.t, at.f0 + warp * 16 + r + 8 * e);
         T *out = (T *)p.out + row * D + 2 * c;
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
@@ -503,28 +518,29 @@ cudaError_t launch_rows(const RowArgs &p, const RowPlan &rp, int64_t rows, cudaS
     return cudaGetLastError();
 }
 
-template <typename T, int D, int KB>
-cudaError_t launch_tile(const AttendTileArgs &p, int64_t B, cudaStream_t s) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(k_attend_tile<T, D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             TileSmem<D, KB>::bytes);
+template <typename T, int D, int KB, int W>
+cudaError_t launch_tile(AttendTileArgs &p, int64_t B, cudaStream_t s) {
+    constexpr int bytes = AttendSmem<D, KB, W>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_attend_tile<T, D, KB, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    k_attend_tile<T, D, KB><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), kTileThreads,
-                              TileSmem<D, KB>::bytes, s>>>(p);
+    p.t.tiles = (int)((p.t.rows + 16 * W - 1) / (16 * W));
+    k_attend_tile<T, D, KB, W><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)),
+                                 32 * (W + 1), bytes, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t launch_tile(const AttendTileArgs &p, int64_t B, cudaStream_t s) {
-    if (p.t.a.block == 16) return launch_tile<T, D, 16>(p, B, s);
-    if (p.t.a.block == 32) return launch_tile<T, D, 32>(p, B, s);
-    return launch_tile<T, D, 64>(p, B, s);
-}
-
-// By tile when every kv head has at least two tiles of rows.
-bool by_tile(const spmm_blocks_shape *s) {
-    return s->Tk > 0 && s->Tq * (s->Hq / s->Hk) >= 2 * kTileRows && s->B * s->Hk <= 65535;
+cudaError_t launch_tile(AttendTileArgs &p, bool large, int64_t B, cudaStream_t s) {
+    if (large) {
+        if (p.t.a.block == 16) return launch_tile<T, D, 16, kLargeWarps>(p, B, s);
+        if (p.t.a.block == 32) return launch_tile<T, D, 32, kLargeWarps>(p, B, s);
+        return launch_tile<T, D, 64, kLargeWarps>(p, B, s);
+    }
+    if (p.t.a.block == 16) return launch_tile<T, D, 16, kSmallWarps>(p, B, s);
+    if (p.t.a.block == 32) return launch_tile<T, D, 32, kSmallWarps>(p, B, s);
+    return launch_tile<T, D, 64, kSmallWarps>(p, B, s);
 }
 
 }  // namespace
@@ -583,7 +599,7 @@ spmm_status spmm_dynamic_sync(void *stream) {
 int64_t spmm_blocks_attend_workspace(const spmm_blocks_shape *s) {
     using namespace spmm;
     if (blk_check(s, true) != SPMM_OK) return 0;
-    if (by_tile(s)) return 0;
+    if (blocks_by_tile(s)) return 0;
     const RowPlan p = row_plan(s);
     if (p.splits == 1) return 0;
     return p.items * p.splits * 8 * p.nt * (s->D + 1) * 4;
@@ -607,11 +623,10 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
     set_rows(p.a.q, p.a.q_sb, p.a.q_st, p.a.q_sh, q);
     set_rows(p.a.k, p.a.k_sb, p.a.k_st, p.a.k_sh, k);
     set_rows(p.a.v, p.a.v_sb, p.a.v_st, p.a.v_sh, v);
-    if (by_tile(s)) {
+    if (blocks_by_tile(s)) {
         AttendTileArgs t{};
         t.t.a = p.a;
         t.t.rows = s->Tq * p.a.G;
-        t.t.tiles = (int)((t.t.rows + kTileRows - 1) / kTileRows);
         t.out = out;
         t.lse = lse;
         const int box = (int)std::min<int64_t>(s->block, 64);
@@ -620,11 +635,11 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
         if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
         if (e == cudaSuccess) {
             if (s->dtype == SPMM_BF16)
-                e = s->D == 64 ? launch_tile<__nv_bfloat16, 64>(t, s->B, cs)
-                               : launch_tile<__nv_bfloat16, 128>(t, s->B, cs);
+                e = s->D == 64 ? launch_tile<__nv_bfloat16, 64>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs)
+                               : launch_tile<__nv_bfloat16, 128>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs);
             else
-                e = s->D == 64 ? launch_tile<__half, 64>(t, s->B, cs)
-                               : launch_tile<__half, 128>(t, s->B, cs);
+                e = s->D == 64 ? launch_tile<__half, 64>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs)
+                               : launch_tile<__half, 128>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs);
         }
         return cuda_status(e);
     }

@@ -4,7 +4,7 @@
 //   dV = P^T dO, dK = dS^T Q       by key block, over the queries that chose it:
 // the transpose of the selection, as one bit per query in a row of words per
 // (sequence, kv head, block), set with integer atomics (order-independent).
-#include "blocks.cuh"
+#include "blocks_tile.cuh"
 
 namespace spmm {
 namespace {
@@ -58,6 +58,8 @@ __global__ void k_set_bits(BwdArgs p, int64_t entries) {
     const int64_t bt = row / a.Hk;
     const int t = (int)(bt % a.Tq);
     const int64_t b = bt / a.Tq;
+    // a query that sees none of the block's keys adds nothing, whatever its rows hold
+    if (list[j] * a.block >= blk_limit(a, blk_len(a, (int)b), t)) return;
     atomicOr(p.bits + ((b * a.Hk + h) * a.NB + list[j]) * p.words + (t >> 5), 1u << (t & 31));
 }
 
@@ -246,6 +248,235 @@ __global__ void __launch_bounds__(kRowThreads) k_dq_rows(BwdArgs p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += sm[w][row][d + e];
         st_pack<T, 8>((T *)p.dq + (row0 + row) * D + d, x);
+    }
+}
+
+// ---------------------------------------------------------- dQ by tile of rows
+struct DqTileArgs {
+    TileArgs t;
+    const void *dout;
+    int64_t do_sb, do_st, do_sh;
+    const float *lse, *delta;
+    void *dq;
+};
+
+// One row, key by key, for rows whose tile gave a result that is not finite (an
+// infinite or NaN key times the weight 0 of a row that does not see it).
+template <typename T, int D>
+__device__ __noinline__ void dq_row_alone(const DqTileArgs &p, int b, int h, int t, int head) {
+    const BlkArgs &a = p.t.a;
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int limit = blk_limit(a, blk_len(a, b), t);
+    const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
+    const float lse2 = p.lse[row] * kLog2e, delta = p.delta[row];
+    float q[E], g[E], o[E] = {};
+    ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
+    ld_pack<T, E>((const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + lane * E, g);
+    const int32_t *list = a.blocks + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.n;
+    for (int j = 0; j < a.n && lse2 != -INFINITY; ++j) {
+        if (!blk_entry_ok(list, j, a.NB)) continue;
+        const int k0 = list[j] * a.block, k1 = min(k0 + a.block, limit);
+        for (int key = k0; key < k1; ++key) {
+            float k[E], v[E], sk = 0.0f, sv = 0.0f;
+            ld_pack<T, E>((const T *)a.k + b * a.k_sb + key * a.k_st + h * a.k_sh + lane * E, k);
+            ld_pack<T, E>((const T *)a.v + b * a.v_sb + key * a.v_st + h * a.v_sh + lane * E, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                sk = fmaf(q[e], k[e], sk);
+                sv = fmaf(g[e], v[e], sv);
+            }
+#pragma unroll
+            for (int w = 16; w; w >>= 1) {
+                sk += __shfl_xor_sync(0xffffffffu, sk, w);
+                sv += __shfl_xor_sync(0xffffffffu, sv, w);
+            }
+            const float ds = ex2(fmaf(sk, a.scale * kLog2e, -lse2)) * (sv - delta) * a.scale;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(ds, k[e], o[e]);
+        }
+    }
+    st_pack<T, E>((T *)p.dq + row * D + lane * E, o);
+}
+
+constexpr int kDqLarge = 8, kDqSmall = 4;
+template <int D, int KB, int W>
+using DqSmem = TileSmem<D, KB, W, 2, (W == kDqLarge ? 227 : 113) * 1024>;
+
+// dS is used twice over in bf16, as its rounded value plus what that left out:
+// the rows of dS sum to 0, so dQ = dS K is what remains after the keys' common
+// part cancels, and one rounding of dS to 8 bits would show in it (error 1.5
+// times that of rounding dQ alone; 1.27 times with both parts).
+template <typename T, int D, int KB, int W>
+__global__ void __launch_bounds__(32 * (W + 1), W == kDqLarge ? 1 : 2)
+    k_dq_tile(const __grid_constant__ DqTileArgs p) {
+    using S = DqSmem<D, KB, W>;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[S::stages], empty[S::stages];
+    __shared__ TileStage<W> info[S::stages];
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const BlkArgs &a = p.t.a;
+    const TilePlace at(p.t, 16 * W);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], W);
+        }
+        mbar_init_fence();
+    }
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    if (warp == W) {
+        tile_produce<S, D, KB, W>(
+            p.t, at, smem, full, empty, info,
+            (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_lists));
+        return;
+    }
+    const int len = blk_len(a, at.b);
+    const float scale2 = a.scale * kLog2e;
+    const uint32_t sq = smem + S::at_rows + warp * 16 * D * 2, sg = sq + S::rows;
+    {
+        int64_t row;
+        const bool live = at.row_of(p.t, len, warp * 16 + (lane & 15), row);
+        fetch_rows<T, D>(sq, (const T *)a.q, live, at.offset(p.t, row, a.q_sb, a.q_st, a.q_sh));
+        fetch_rows<T, D>(sg, (const T *)p.dout, live,
+                         at.offset(p.t, row, p.do_sb, p.do_st, p.do_sh));
+    }
+    int limit[2], qi[2];
+    float lse2[2], delta[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t f = at.f0 + warp * 16 + r + 8 * e;
+        const bool live = f < p.t.rows;
+        const int t = live ? (int)(f / a.G) : at.t_first;
+        qi[e] = t - at.t_first;
+        limit[e] = live ? blk_limit(a, len, t) : 0;
+        const float x = live ? p.lse[at.out_row(p.t, f)] * kLog2e : -INFINITY;
+        lse2[e] = x == -INFINITY ? INFINITY : x;            // a row without keys: P = 0
+        delta[e] = live ? p.delta[at.out_row(p.t, f)] : 0.0f;
+    }
+    cp_wait<0>();
+    __syncwarp();
+    const int least_limit = __reduce_min_sync(0xffffffffu, min(limit[0], limit[1]));
+
+    float o[D / 8][4] = {};
+    DsScale ds_scale;
+    int stage = 0;
+    uint32_t parity = 0;
+    while (mbar_wait(&full[stage], parity, p.t.err)) {
+        const int key0 = info[stage].key0;
+        if (key0 < 0) break;
+        bool mine[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            mine[e] = (info[stage].mask[qi[e] >> 5] >> (qi[e] & 31) & 1u) && key0 < limit[e];
+        if (__any_sync(0xffffffffu, mine[0] || mine[1])) {
+            const uint32_t sk = smem + stage * S::stage, sv = sk + S::operand;
+            if (key0 + KB > len) zero_tail<D, KB>(sk, len - key0);
+            float s[KB / 8][4] = {}, dp[KB / 8][4] = {};
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                uint32_t q[4], g[4];
+                ldsm4(sq + rows_at<D>(lane & 15, 2 * i + (lane >> 4)), q);
+                ldsm4(sg + rows_at<D>(lane & 15, 2 * i + (lane >> 4)), g);
+#pragma unroll
+                for (int n = 0; n < KB / 16; ++n) {
+                    uint32_t x[4], y[4];
+                    const uint32_t at_ = panel_at<KB>(16 * n + (lane >> 4) * 8 + (lane & 7),
+                                                      2 * i + ((lane >> 3) & 1));
+                    ldsm4(sk + at_, x);
+                    ldsm4(sv + at_, y);
+                    mma16816<T>(s[2 * n], q[0], q[1], q[2], q[3], x[0], x[1]);
+                    mma16816<T>(s[2 * n + 1], q[0], q[1], q[2], q[3], x[2], x[3]);
+                    mma16816<T>(dp[2 * n], g[0], g[1], g[2], g[3], y[0], y[1]);
+                    mma16816<T>(dp[2 * n + 1], g[0], g[1], g[2], g[3], y[2], y[3]);
+                }
+            }
+            const bool whole = key0 + KB <= least_limit;
+            float ds_max = 0.0f;
+#pragma unroll
+            for (int n = 0; n < KB / 8; ++n)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int e = w >> 1;
+                    float x = ex2(fmaf(s[n][w], scale2, -lse2[e])) * (dp[n][w] - delta[e]) * a.scale;
+                    if (!mine[e] || (!whole && key0 + 8 * n + 2 * c + (w & 1) >= limit[e])) x = 0.0f;
+                    s[n][w] = x;
+                    if constexpr (kNarrow<T>) ds_max = finite_max(ds_max, x);
+                }
+            if constexpr (kNarrow<T>) {
+                const float f = ds_scale.lower(ds_max);
+                if (f != 1.0f)
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) o[n][w] *= f;
+                const float u = pow2i(ds_scale.e);
+#pragma unroll
+                for (int n = 0; n < KB / 8; ++n)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) s[n][w] *= u;
+            }
+#pragma unroll
+            for (int i = 0; i < KB / 16; ++i) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float x = s[2 * i + (w >> 1)][2 * (w & 1)];
+                    const float y = s[2 * i + (w >> 1)][2 * (w & 1) + 1];
+                    hi[w] = pack2<T>(x, y);
+                    if constexpr (!kNarrow<T>)
+                        lo[w] = pack2<T>(x - __uint_as_float(hi[w] << 16),
+                                         y - __uint_as_float(hi[w] & 0xffff0000u));
+                }
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t x[4];
+                    ldsm4_t(sk + panel_at<KB>(16 * i + (lane & 15), 2 * n + (lane >> 4)), x);
+                    mma16816<T>(o[2 * n], hi[0], hi[1], hi[2], hi[3], x[0], x[1]);
+                    mma16816<T>(o[2 * n + 1], hi[0], hi[1], hi[2], hi[3], x[2], x[3]);
+                    if constexpr (!kNarrow<T>) {
+                        mma16816<T>(o[2 * n], lo[0], lo[1], lo[2], lo[3], x[0], x[1]);
+                        mma16816<T>(o[2 * n + 1], lo[0], lo[1], lo[2], lo[3], x[2], x[3]);
+                    }
+                }
+            }
+            if (key0 + KB > len) fence_proxy_async_shared();   // zeros, then the next copy
+            __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == S::stages) {
+            stage = 0;
+            parity ^= 1;
+        }
+    }
+    const float unit = kNarrow<T> ? pow2i(-ds_scale.e) : 1.0f;
+    unsigned redo = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float odd = 0.0f;                          // NaN if anything is not finite
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+            odd = fmaf(o[n][2 * e], 0.0f, odd);
+            odd = fmaf(o[n][2 * e + 1], 0.0f, odd);
+        }
+        const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f);
+        const int64_t f = at.f0 + warp * 16 + r + 8 * e;
+        const bool live = f < p.t.rows;
+        redo |= __ballot_sync(0xffffffffu, c == 0 && live && (bad >> (4 * r) & 15u)) << e;
+        if (!live) continue;
+        T *out = (T *)p.dq + at.out_row(p.t, f) * D + 2 * c;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            *(uint32_t *)(out + 8 * n) = pack2<T>(o[n][2 * e] * unit, o[n][2 * e + 1] * unit);
+    }
+    __syncwarp();
+    while (redo) {                                  // bit 4 r + e: row r + 8 e
+        const int bit = __ffs(redo) - 1;
+        redo &= redo - 1;
+        const int64_t f = at.f0 + warp * 16 + (bit >> 2) + 8 * (bit & 1);
+        const int t = (int)(f / a.G);
+        dq_row_alone<T, D>(p, at.b, at.h, t, at.h * a.G + (int)(f - (int64_t)t * a.G));
     }
 }
 
@@ -522,22 +753,67 @@ cudaError_t launch_dkdv(const BwdArgs &p, const BwdPlan &bp, int64_t B, cudaStre
     return cudaGetLastError();
 }
 
+template <typename T, int D, int KB, int W>
+cudaError_t launch_dq_tile(DqTileArgs &p, int64_t B, cudaStream_t s) {
+    constexpr int bytes = DqSmem<D, KB, W>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_dq_tile<T, D, KB, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    p.t.tiles = (int)((p.t.rows + 16 * W - 1) / (16 * W));
+    k_dq_tile<T, D, KB, W><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), 32 * (W + 1),
+                             bytes, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
 template <typename T, int D>
-cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s, cudaStream_t cs) {
+cudaError_t launch_dq_tile(DqTileArgs &p, bool large, int64_t B, cudaStream_t s) {
+    if (large) {
+        if (p.t.a.block == 16) return launch_dq_tile<T, D, 16, kDqLarge>(p, B, s);
+        if (p.t.a.block == 32) return launch_dq_tile<T, D, 32, kDqLarge>(p, B, s);
+        return launch_dq_tile<T, D, 64, kDqLarge>(p, B, s);
+    }
+    if (p.t.a.block == 16) return launch_dq_tile<T, D, 16, kDqSmall>(p, B, s);
+    if (p.t.a.block == 32) return launch_dq_tile<T, D, 32, kDqSmall>(p, B, s);
+    return launch_dq_tile<T, D, 64, kDqSmall>(p, B, s);
+}
+
+template <typename T, int D>
+cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s, spmm_rows k,
+                       spmm_rows v, cudaStream_t cs) {
     const int64_t rows = s->B * s->Tq * s->Hq, lists = s->B * s->Tq * s->Hk;
     cudaError_t e = cudaSuccess;
     constexpr int per = 128 / (D / 8);
     k_delta<T, D><<<(unsigned)((rows + per - 1) / per), 128, 0, cs>>>(p, rows);
     count_launch();
-    if (p.a.G <= 8) {
-        p.gt = 1;
-        k_dq_rows<T, D, 1><<<(unsigned)lists, kRowThreads, 0, cs>>>(p);
+    if (blocks_by_tile(s)) {
+        DqTileArgs t{};
+        t.t.a = p.a;
+        t.t.rows = s->Tq * p.a.G;
+        t.dout = p.dout;
+        t.do_sb = p.do_sb;
+        t.do_st = p.do_st;
+        t.do_sh = p.do_sh;
+        t.lse = p.lse;
+        t.delta = p.delta;
+        t.dq = p.dq;
+        const int box = (int)std::min<int64_t>(s->block, 64);
+        e = dynamic_err(&t.t.err);
+        if (e == cudaSuccess) e = encode_rows(k, s, box, &t.t.k_map);
+        if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
+        if (e == cudaSuccess)
+            e = launch_dq_tile<T, D>(t, blocks_large_tiles(s, 16 * kDqLarge), s->B, cs);
     } else {
-        p.gt = (p.a.G + 15) / 16;
-        k_dq_rows<T, D, 2><<<(unsigned)(lists * p.gt), kRowThreads, 0, cs>>>(p);
+        if (p.a.G <= 8) {
+            p.gt = 1;
+            k_dq_rows<T, D, 1><<<(unsigned)lists, kRowThreads, 0, cs>>>(p);
+        } else {
+            p.gt = (p.a.G + 15) / 16;
+            k_dq_rows<T, D, 2><<<(unsigned)(lists * p.gt), kRowThreads, 0, cs>>>(p);
+        }
+        count_launch();
+        e = cudaGetLastError();
     }
-    count_launch();
-    e = cudaGetLastError();
     if (e != cudaSuccess || s->Tk == 0) return e;
     e = cudaMemsetAsync(p.bits, 0, (size_t)bp.bits_bytes, cs);
     if (e != cudaSuccess) return e;
@@ -615,10 +891,10 @@ spmm_status spmm_blocks_backward(const spmm_blocks_shape *s, spmm_rows q, spmm_r
     p.chunk_words = (int)bp.chunk_words;
     cudaError_t e;
     if (s->dtype == SPMM_BF16)
-        e = s->D == 64 ? launch_bwd<__nv_bfloat16, 64>(p, bp, s, cs)
-                       : launch_bwd<__nv_bfloat16, 128>(p, bp, s, cs);
+        e = s->D == 64 ? launch_bwd<__nv_bfloat16, 64>(p, bp, s, k, v, cs)
+                       : launch_bwd<__nv_bfloat16, 128>(p, bp, s, k, v, cs);
     else
-        e = s->D == 64 ? launch_bwd<__half, 64>(p, bp, s, cs) : launch_bwd<__half, 128>(p, bp, s, cs);
+        e = s->D == 64 ? launch_bwd<__half, 64>(p, bp, s, k, v, cs) : launch_bwd<__half, 128>(p, bp, s, k, v, cs);
     return cuda_status(e);
 }
 

@@ -1,4 +1,4 @@
-// Selected-block attention by tile of rows: R = 16 W adjacent (query, head) rows
+// Selected-block attention by tile of rows: 16 W adjacent (query, head) rows
 // of one kv head per CTA, a consumer warp per 16 rows. A producer warp merges
 // the lists of the tile's queries (all ascending, so the next block is the
 // smallest of the lists' heads) and has the tensor-copy engine bring each block
@@ -12,25 +12,32 @@
 
 namespace spmm {
 
-constexpr int kTileWarps = 8;                      // consumer warps
-constexpr int kTileRows = 16 * kTileWarps;
-constexpr int kTileThreads = 32 * (kTileWarps + 1);
-constexpr int kTileLists = kTileRows / 32;         // lists per producer lane, words of bits
-
-struct TileStage {
+template <int W> struct TileStage {
     int key0;                                      // first key, or -1: no more blocks
-    uint32_t mask[kTileLists];                     // bit of each query of the tile
+    uint32_t mask[(W + 1) / 2];                    // bit of each query of the tile
 };
 
 // Shared memory: `stages` of K then V, KB keys each, as D / 64 panels of KB rows
 // of 128 bytes, the 16-byte chunks of a row permuted by the copy's 128-byte
-// swizzle; then the barriers and what the producer says of each stage.
-template <int D, int KB> struct TileSmem {
+// swizzle; then `tiles` operands of 16 W rows. `budget` bytes in all.
+template <int D, int KB, int W, int tiles, int budget> struct TileSmem {
     static constexpr int operand = KB * D * 2;
     static constexpr int stage = 2 * operand;
-    static constexpr int stages = (D == 128 ? 6 : 8) * 64 / KB > 16 ? 16 : (D == 128 ? 6 : 8) * 64 / KB;
-    static constexpr int bytes = stages * stage + 1024 /* alignment */;
+    static constexpr int rows = 16 * W * D * 2;    // one operand of the tile's own rows
+    // the lists of the tile's queries, when they fit: 16 entries for each of 16 W
+    static constexpr int lists = 16 * W * 16 * 4;
+    static constexpr int fit = (budget - 1024 /* alignment */ - lists - tiles * rows) / stage;
+    static constexpr int stages = fit > 16 ? 16 : fit;
+    static constexpr int at_rows = stages * stage, at_lists = at_rows + tiles * rows;
+    static constexpr int bytes = at_lists + lists + 1024;
+    static_assert(stages >= 2, "the ring needs two stages");
 };
+
+// 16-byte chunk `chunk` of row `row` of a [rows][D] operand that threads fill:
+// eight consecutive rows' chunks fall in different banks.
+template <int D> __device__ __forceinline__ uint32_t rows_at(int row, int chunk) {
+    return (uint32_t)(row * D * 2 + ((chunk ^ (row & 7)) << 4));
+}
 
 template <int KB> __device__ __forceinline__ uint32_t panel_at(int row, int chunk) {
     return (uint32_t)((chunk >> 3) * KB * 128 + row * 128 + (((chunk ^ row) & 7) << 4));
@@ -51,7 +58,7 @@ struct TileArgs {
     BlkArgs a;
     CUtensorMap k_map, v_map;
     int64_t rows;            // Tq G rows of one kv head
-    int tiles;               // ceil(rows / kTileRows)
+    int tiles;               // of rows per kv head
     int32_t *err;
 };
 
@@ -60,53 +67,83 @@ struct TilePlace {
     int b, h;
     int64_t f0;              // first row, f = t G + g
     int t_first, nq;         // the tile's queries
-    __device__ __forceinline__ TilePlace(const TileArgs &p) {
+    __device__ __forceinline__ TilePlace(const TileArgs &p, int tile_rows) {
         const int hb = blockIdx.y;
         h = hb % p.a.Hk;
         b = hb / p.a.Hk;
-        f0 = (int64_t)(p.tiles - 1 - (int)blockIdx.x) * kTileRows;
-        const int64_t f1 = min(p.rows, f0 + kTileRows) - 1;
+        f0 = (int64_t)(p.tiles - 1 - (int)blockIdx.x) * tile_rows;
+        const int64_t f1 = min(p.rows, f0 + tile_rows) - 1;
         t_first = (int)(f0 / p.a.G);
         nq = (int)(f1 / p.a.G) - t_first + 1;
     }
+    // Row `i` of the tile as a row of [B, Tq, Hq]; whether it sees any key.
+    __device__ __forceinline__ int64_t out_row(const TileArgs &p, int64_t f) const {
+        return (int64_t)b * p.a.Tq * p.a.Hq + f / p.a.G * p.a.Hq + h * p.a.G + f % p.a.G;
+    }
+    __device__ __forceinline__ bool row_of(const TileArgs &p, int len, int i, int64_t &f) const {
+        f = f0 + i;
+        return f < p.rows && blk_limit(p.a, len, (int)(f / p.a.G)) > 0;
+    }
+    // Element offset of that row in a strided [B, Tq, Hq, D] tensor.
+    __device__ __forceinline__ int64_t offset(const TileArgs &p, int64_t f, int64_t sb, int64_t st,
+                                              int64_t sh) const {
+        return b * sb + f / p.a.G * st + (h * p.a.G + f % p.a.G) * sh;
+    }
 };
 
-template <int D, int KB>
+template <typename S, int D, int KB, int W>
 __device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace &at,
                                              uint32_t smem, uint64_t *full, uint64_t *empty,
-                                             TileStage *info) {
-    using S = TileSmem<D, KB>;
+                                             TileStage<W> *info, int32_t *lists) {
+    constexpr int kTileLists = (W + 1) / 2;              // lists per lane, words of bits
     const BlkArgs &a = p.a;
     const int lane = threadIdx.x & 31;
     const int len = blk_len(a, at.b);
     constexpr int kNone = INT_MAX;
-    const int32_t *list[kTileLists];
-    int j[kTileLists], head[kTileLists], end[kTileLists];     // end: first block out of sight
-    auto next = [&](int i) {
+    // The lists go to shared memory first: a step of the merge then waits for no
+    // load from global memory (about 700 cycles, more than a step's arithmetic).
+    const int32_t *base = a.blocks + (((int64_t)at.b * a.Tq + at.t_first) * a.Hk + at.h) * a.n;
+    const int64_t pitch = (int64_t)a.Hk * a.n;
+    const bool staged = (int64_t)at.nq * a.n * 4 <= S::lists;
+    if (staged) {
+        for (int q = lane; q < at.nq; q += 32) {
+#pragma unroll 8
+            for (int j = 0; j < a.n; ++j) lists[q * a.n + j] = base[q * pitch + j];
+        }
+        __syncwarp();
+    }
+    const int32_t *list[kTileLists];               // the next entry
+    int left[kTileLists], head[kTileLists], prev[kTileLists];
+    int end[kTileLists];                           // first block out of sight
+    auto advance = [&](int i) {
         // entries below the one before them or out of range are skipped
-        head[i] = kNone;
-        while (j[i] < a.n) {
-            const int at_ = j[i]++;
-            if (blk_entry_ok(list[i], at_, a.NB)) {
-                const int c = list[i][at_];
-                if (c < end[i]) head[i] = c;
+        int c = kNone;
+        while (left[i] > 0) {
+            --left[i];
+            const int x = *list[i]++;
+            const bool ok = (unsigned)x < (unsigned)a.NB && x > prev[i];
+            prev[i] = x;
+            if (ok) {
+                c = x < end[i] ? x : kNone;
                 break;
             }
         }
+        head[i] = c;
     };
 #pragma unroll
     for (int i = 0; i < kTileLists; ++i) {
         const int q = i * 32 + lane;
-        j[i] = a.n;
-        end[i] = 0;
-        list[i] = a.blocks;
+        left[i] = end[i] = 0;
+        head[i] = kNone;
+        prev[i] = -1;
+        list[i] = lists;
         if (q < at.nq) {
             const int t = at.t_first + q;
-            list[i] = a.blocks + (((int64_t)at.b * a.Tq + t) * a.Hk + at.h) * a.n;
-            j[i] = 0;
+            list[i] = staged ? lists + q * a.n : base + q * pitch;
+            left[i] = a.n;
             end[i] = (blk_limit(a, len, t) + a.block - 1) / a.block;
+            advance(i);
         }
-        next(i);
     }
     int stage = 0, issued = 0;
     uint32_t parity = 1;                           // the ring starts empty
@@ -114,14 +151,17 @@ __device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace 
     while (ok) {
         int least = head[0];
 #pragma unroll
-        for (int i = 1; i < kTileLists; ++i) least = min(least, head[i]);
+        for (int i = 1; i < kTileLists; ++i)
+            if (32 * i < at.nq) least = min(least, head[i]);
         least = __reduce_min_sync(0xffffffffu, least);
         uint32_t mask[kTileLists];
 #pragma unroll
         for (int i = 0; i < kTileLists; ++i) {
+            mask[i] = 0;
+            if (32 * i >= at.nq) continue;         // usually all but the first 32 queries
             const bool mine = least != kNone && head[i] == least;
             mask[i] = __ballot_sync(0xffffffffu, mine);
-            if (mine) next(i);
+            if (mine) advance(i);
         }
         const int parts = least == kNone ? 1 : a.block / KB;
         for (int s = 0; s < parts; ++s) {
@@ -178,22 +218,32 @@ __device__ __forceinline__ void zero_tail(uint32_t operand, int from) {
     __syncwarp();
 }
 
-// A fragments (16 rows x D) of two strided rows per lane, straight from memory.
+// One warp's 16 rows of a strided tensor into its part of shared memory: lanes
+// 0 to 15 say of rows 0 to 15 where they start; a row that is not live is 0.
 template <typename T, int D>
-__device__ __forceinline__ void load_row_frags(uint32_t (&x)[D / 16][4], const T *r0, const T *r1,
-                                               int c) {
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const T *p, bool live, int64_t offset) {
+    const int lane = threadIdx.x & 31;
+    const int64_t mine = live ? offset : -1;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        x[i][0] = r0 ? __ldg((const uint32_t *)(r0 + 16 * i + 2 * c)) : 0u;
-        x[i][1] = r1 ? __ldg((const uint32_t *)(r1 + 16 * i + 2 * c)) : 0u;
-        x[i][2] = r0 ? __ldg((const uint32_t *)(r0 + 16 * i + 8 + 2 * c)) : 0u;
-        x[i][3] = r1 ? __ldg((const uint32_t *)(r1 + 16 * i + 8 + 2 * c)) : 0u;
+    for (int i = 0; i < D / 16; ++i) {             // 32 chunks at a time
+        const int row = i * 32 / (D / 8) + lane / (D / 8), chunk = lane % (D / 8);
+        const int64_t at = __shfl_sync(0xffffffffu, mine, row);
+        cp16(dst + rows_at<D>(row, chunk), p + (at < 0 ? 0 : at + chunk * 8), at >= 0);
     }
+    cp_commit();
 }
 
 // ------------------------------------------------------------------- host
 cudaError_t encode_rows(const spmm_rows &r, const spmm_blocks_shape *s, int box_rows,
                         CUtensorMap *map);
+
+// By tile from 128 rows a kv head on; large tiles when they give every SM two.
+inline bool blocks_by_tile(const spmm_blocks_shape *s) {
+    return s->Tk > 0 && s->Tq * (s->Hq / s->Hk) >= 128 && s->B * s->Hk <= 65535;
+}
+inline bool blocks_large_tiles(const spmm_blocks_shape *s, int tile_rows) {
+    return s->B * s->Hk * (s->Tq * (s->Hq / s->Hk) / tile_rows) >= 2 * 152;
+}
 
 // Device word that a bounded wait which gave up sets (spmm_dynamic_sync reads it).
 cudaError_t dynamic_err(int32_t **err);
