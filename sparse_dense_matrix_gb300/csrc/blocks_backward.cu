@@ -4,26 +4,10 @@
 //   dV = P^T dO, dK = dS^T Q       by key block, over the queries that chose it:
 // the transpose of the selection, as one bit per query in a row of words per
 // (sequence, kv head, block), set with integer atomics (order-independent).
-#include "blocks_tile.cuh"
+#include "blocks_keys.cuh"
 
 namespace spmm {
 namespace {
-
-struct BwdArgs {
-    BlkArgs a;
-    const void *out, *dout;
-    int64_t do_sb, do_st, do_sh;
-    const float *lse;
-    float *delta;            // [B, Tq, Hq]
-    void *dq, *dk, *dv;
-    uint32_t *bits;          // [B, Hk, NB, words]
-    int words;               // ceil(Tq / 32)
-    int chunks;              // ranges of queries per key block
-    int chunk_words;
-    float *part;             // [chunks][2][B, Tk, Hk, D] when chunks > 1
-    int64_t part_stride;     // B Tk Hk D
-    int gt;
-};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(128) k_delta(BwdArgs p, int64_t rows) {
@@ -676,6 +660,17 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
             dk[n][e] *= k_unit;
             dv[n][e] *= v_unit;
         }
+    unsigned redo = 0;                           // bit 4 r + e: key r + 8 e is not finite
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float odd = 0.0f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+            odd += (dk[n][2 * e] + dk[n][2 * e + 1] + dv[n][2 * e] + dv[n][2 * e + 1]) * 0.0f;
+        const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f);
+        const bool live = key0 + warp * 16 + r + 8 * e < a.Tk;
+        redo |= __ballot_sync(0xffffffffu, c == 0 && live && (bad >> (4 * r) & 15u)) << e;
+    }
     // keys r and r + 8 of the warp's 16, elements 8 n + 2 c and the next
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -693,6 +688,11 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
                 *(float2 *)(x + p.part_stride) = make_float2(dv[n][2 * e], dv[n][2 * e + 1]);
             }
         }
+    }
+    __syncwarp();
+    for (; redo; redo &= redo - 1) {
+        const int bit = __ffs(redo) - 1;
+        dkdv_key_alone<T, D>(p, b, h, key0 + warp * 16 + (bit >> 2) + 8 * (bit & 1), chunk);
     }
 }
 
@@ -719,7 +719,16 @@ struct BwdPlan {
     int64_t words, chunk_words, chunks;
     int64_t bits_bytes, delta_bytes, part_bytes;
     int W;
+    bool keys;               // k_dkdv_keys
 };
+
+// The tensor-core kernel: bf16 (fp16 needs dS scaled as it goes, which sums in
+// tensor memory do not allow), heads of 128 (its second products' M), blocks of
+// whole 64-key tiles, and enough rows that its 128-row steps fill.
+bool by_keys(const spmm_blocks_shape *s) {
+    return s->dtype == SPMM_BF16 && s->D == kKeysD && s->block % kKeysN == 0 &&
+           s->Tq * (s->Hq / s->Hk) >= 2 * kKeysRows;
+}
 
 // Ranges of queries per key block: enough CTAs to fill the SMs several times
 // over (and to cut up a block that every query chose), each of 256 queries or more.
@@ -731,6 +740,17 @@ BwdPlan bwd_plan(const spmm_blocks_shape *s) {
     const int64_t ctas = std::max<int64_t>(1, s->B * s->Hk * NB * (s->block / (16 * p.W)));
     int64_t chunks = std::min<int64_t>((152 * 8 * (4 / p.W) + ctas - 1) / ctas, (p.words + 7) / 8);
     chunks = std::max<int64_t>(1, std::min<int64_t>(chunks, 64));
+    p.keys = by_keys(s);
+    if (p.keys) {
+        // One CTA fills an SM: some four rounds of them. A block that every query
+        // chose is cut up too, into ranges of 2048 queries, or more where that
+        // would make more than eight (each range adds a partial dK and dV).
+        const int64_t k_ctas = std::max<int64_t>(1, s->B * s->Hk * NB * (s->block / kKeysN));
+        chunks = std::min<int64_t>((152 * 4 + k_ctas - 1) / k_ctas, (p.words + 7) / 8);
+        chunks = std::max<int64_t>(
+            {chunks, std::min<int64_t>((p.words + 63) / 64, 8),
+             (p.words + kKeysMaxWords - 1) / kKeysMaxWords, 1});
+    }
     p.chunk_words = std::max<int64_t>(1, (p.words + chunks - 1) / chunks);
     p.chunks = std::max<int64_t>(1, (p.words + p.chunk_words - 1) / p.chunk_words);
     p.bits_bytes = round_up(s->B * s->Hk * NB * p.words * 4, 256);
@@ -749,6 +769,19 @@ cudaError_t launch_dkdv(const BwdArgs &p, const BwdPlan &bp, int64_t B, cudaStre
     const dim3 grid((unsigned)(p.a.NB * (p.a.block / KT)), (unsigned)(B * p.a.Hk),
                     (unsigned)p.chunks);
     k_dkdv<T, D, W><<<grid, 32 * W, smem, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_keys(BwdArgs &p, int64_t B, cudaStream_t s) {
+    cudaError_t e = dynamic_err(&p.err);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_dkdv_keys<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kKeysSmem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(p.a.NB * (p.a.block / kKeysN)), (unsigned)(B * p.a.Hk),
+                    (unsigned)p.chunks);
+    k_dkdv_keys<T><<<grid, kKeysThreads, kKeysSmem, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
@@ -822,7 +855,9 @@ cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (bp.W == 1) e = launch_dkdv<T, D, 1>(p, bp, s->B, cs);
+    if (bp.keys) {
+        if constexpr (D == kKeysD && !kNarrow<T>) e = launch_keys<T>(p, s->B, cs);
+    } else if (bp.W == 1) e = launch_dkdv<T, D, 1>(p, bp, s->B, cs);
     else if (bp.W == 2) e = launch_dkdv<T, D, 2>(p, bp, s->B, cs);
     else e = launch_dkdv<T, D, 4>(p, bp, s->B, cs);
     if (e != cudaSuccess || p.chunks == 1) return e;

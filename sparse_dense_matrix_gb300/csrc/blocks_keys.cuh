@@ -1,0 +1,366 @@
+// dK and dV of selected-block attention on the fifth-generation tensor cores
+// (bf16, heads of 128, blocks of 64 keys and more). A CTA owns 64 keys of one
+// kv head and a range of queries; the (query, head) rows that chose its block
+// are gathered 128 at a time:
+//   S = Q K^T, dP = dO V^T          128 rows x 64 keys, both operands K-major
+//   P = exp(scale S - lse), dS = scale P (dP - delta)      a thread per row
+//   dV^T += dO^T P, dK^T += Q^T dS  128 elements x 64 keys, summed over the rows
+// The gathered rows and P, dS serve as MN-major operands in the second pair of
+// products, so nothing is transposed in memory. Four warps gather rows by
+// asynchronous copies into two stages, one thread issues the products, eight
+// warps make P and dS, each half of a row's keys.
+#pragma once
+
+#include "blocks_tile.cuh"
+#include "umma.cuh"
+
+namespace spmm {
+
+struct BwdArgs {
+    BlkArgs a;
+    const void *out, *dout;
+    int64_t do_sb, do_st, do_sh;
+    const float *lse;
+    float *delta;            // [B, Tq, Hq]
+    void *dq, *dk, *dv;
+    uint32_t *bits;          // [B, Hk, NB, words]
+    int words;               // ceil(Tq / 32)
+    int chunks;              // ranges of queries per key block
+    int chunk_words;
+    float *part;             // [chunks][2][B, Tk, Hk, D] when chunks > 1
+    int64_t part_stride;     // B Tk Hk D
+    int gt;
+    int32_t *err;
+};
+
+// One key, row by row, for keys whose tile gave a result that is not finite: in
+// the tile a row of q or of the gradient that is not finite, times the weight 0
+// of a key that it does not see, spoils that key too.
+template <typename T, int D>
+__device__ __noinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, int key, int chunk) {
+    const BlkArgs &a = p.a;
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int len = blk_len(a, b);
+    const uint32_t *bits = p.bits + (((int64_t)b * a.Hk + h) * a.NB + key / a.block) * p.words;
+    const int w1 = min(p.words, (chunk + 1) * p.chunk_words);
+    float k[E] = {}, v[E] = {}, dk[E] = {}, dv[E] = {};
+    if (key < len) {
+        ld_pack<T, E>((const T *)a.k + b * a.k_sb + key * a.k_st + h * a.k_sh + lane * E, k);
+        ld_pack<T, E>((const T *)a.v + b * a.v_sb + key * a.v_st + h * a.v_sh + lane * E, v);
+    }
+    for (int w = chunk * p.chunk_words; w < w1; ++w)
+        for (uint32_t m = bits[w]; m; m &= m - 1) {
+            const int t = w * 32 + __ffs(m) - 1;
+            if (key >= blk_limit(a, len, t)) continue;
+            for (int g = 0; g < a.G; ++g) {
+                const int head = h * a.G + g;
+                const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
+                float q[E], o[E], s = 0.0f, d = 0.0f;
+                ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
+                ld_pack<T, E>((const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + lane * E,
+                              o);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    s = fmaf(q[e], k[e], s);
+                    d = fmaf(o[e], v[e], d);
+                }
+#pragma unroll
+                for (int x = 16; x; x >>= 1) {
+                    s += __shfl_xor_sync(0xffffffffu, s, x);
+                    d += __shfl_xor_sync(0xffffffffu, d, x);
+                }
+                const float pr = ex2(fmaf(s, a.scale * kLog2e, -p.lse[row] * kLog2e));
+                const float ds = pr * (d - p.delta[row]) * a.scale;
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    dk[e] = fmaf(ds, q[e], dk[e]);
+                    dv[e] = fmaf(pr, o[e], dv[e]);
+                }
+            }
+        }
+    const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + h) * D + lane * E;
+    if (p.chunks == 1) {
+        st_pack<T, E>((T *)p.dk + at, dk);
+        st_pack<T, E>((T *)p.dv + at, dv);
+    } else {
+        float *x = p.part + (int64_t)(2 * chunk) * p.part_stride + at;
+        st_pack<float, E>(x, dk);
+        st_pack<float, E>(x + p.part_stride, dv);
+    }
+}
+
+constexpr int kKeysD = 128;                // width of a head
+constexpr int kKeysN = 64;                 // keys per CTA
+constexpr int kKeysRows = 128;             // rows per step
+constexpr int kKeysThreads = 13 * 32;      // 8 softmax warps, 4 loaders, 1 issuer
+constexpr int kKeysMaxWords = 256;         // a CTA's range: up to 8192 queries
+constexpr int kKeysPanelK = kKeysN * 128, kKeysPanelR = kKeysRows * 128;   // bytes
+constexpr int kKeysK = 0, kKeysV = 2 * kKeysPanelK, kKeysStage0 = 4 * kKeysPanelK;
+constexpr int kKeysStage = 4 * kKeysPanelR;                                // Q, dO
+constexpr int kKeysP = kKeysStage0 + 2 * kKeysStage, kKeysDs = kKeysP + kKeysPanelR;
+constexpr int kKeysStats = kKeysDs + kKeysPanelR;                          // [2][3][128] floats
+constexpr int kKeysList = kKeysStats + 2 * 3 * kKeysRows * 4;              // queries, 16 bits
+constexpr int kKeysSmem = kKeysList + kKeysMaxWords * 32 * 2 + 1024;
+// tensor memory columns
+constexpr int kTmS = 0, kTmDp = 64, kTmStage = 128, kTmDv = 256, kTmDk = 320, kTmColumns = 512;
+
+template <typename T>
+__global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) {
+    constexpr int D = kKeysD, C = D / 8;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    unsigned char *sp = smem_raw + (smem - smem_addr(smem_raw));
+    float *stats = (float *)(sp + kKeysStats);
+    uint16_t *list = (uint16_t *)(sp + kKeysList);
+    __shared__ uint64_t full[2], ready[2], made, done[2];
+    __shared__ uint32_t tmem_slot, odd[2];
+    __shared__ int n_queries;
+
+    const BlkArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = a.block / kKeysN;
+    const int blk = blockIdx.x / parts;
+    const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk, chunk = blockIdx.z;
+    const int key0 = blk * a.block + blockIdx.x % parts * kKeysN;
+    if (key0 >= a.Tk) return;
+    const int len = blk_len(a, b);
+    const int t_base = chunk * p.chunk_words * 32;
+
+    if (warp == 0) {                             // the range's queries, ascending
+        const uint32_t *bits = p.bits + ((int64_t)blockIdx.y * a.NB + blk) * p.words;
+        const int w0 = chunk * p.chunk_words, w1 = min(p.words, w0 + p.chunk_words);
+        int base = 0;
+        for (int w = w0; w < w1; w += 32) {
+            const uint32_t x = w + lane < w1 ? bits[w + lane] : 0u;
+            int incl = __popc(x);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            int at = base + incl - __popc(x);
+            for (uint32_t m = x; m; m &= m - 1) list[at++] = (w + lane - w0) * 32 + __ffs(m) - 1;
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            n_queries = base;
+            odd[0] = odd[1] = 0;
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&full[i], 128);
+                mbar_init(&ready[i], 1);
+                mbar_init(&done[i], 1);
+            }
+            mbar_init(&made, 256);
+            mbar_init_fence();
+        }
+    } else if (warp == 12) {
+        tmem_alloc(&tmem_slot, kTmColumns);
+        mma_fence_before();
+    }
+    __syncthreads();
+    mma_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int rows = n_queries * a.G;
+    const int steps = (rows + kKeysRows - 1) / kKeysRows;
+
+    if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------ gather rows
+        const T *qp = (const T *)a.q + b * a.q_sb + (int64_t)h * a.G * a.q_sh;
+        const T *gp = (const T *)p.dout + b * p.do_sb + (int64_t)h * a.G * p.do_sh;
+        const int i0 = threadIdx.x - 256;
+        if (steps) {
+            const T *kp = (const T *)a.k + b * a.k_sb + h * a.k_sh;
+            const T *vp = (const T *)a.v + b * a.v_sb + h * a.v_sh;
+            for (int i = i0; i < kKeysN * C; i += 128) {
+                const int row = i / C, ch = i % C;
+                const bool live = key0 + row < len;
+                const int64_t key = live ? key0 + row : 0;
+                const uint32_t at = (ch >> 3) * kKeysPanelK + chunk_at(row, ch & 7);
+                cp16(smem + kKeysK + at, kp + key * a.k_st + ch * 8, live);
+                cp16(smem + kKeysV + at, vp + key * a.v_st + ch * 8, live);
+            }
+        }
+        for (int j = 0; j < steps; ++j) {
+            const int st = j & 1;
+            if (j >= 2 && !mbar_wait_poll(&done[st], ((j >> 1) - 1) & 1, p.err)) break;
+            const int f = j * kKeysRows + i0;
+            int64_t q_at = -1, g_at = 0;
+            float lse2 = INFINITY, delta = 0.0f;
+            int limit = 0;
+            if (f < rows) {
+                const int q = f / a.G, g = f - q * a.G, t = t_base + list[q];
+                q_at = t * a.q_st + g * a.q_sh;
+                g_at = t * p.do_st + g * p.do_sh;
+                const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + h * a.G + g;
+                lse2 = p.lse[row] * kLog2e;
+                if (lse2 == -INFINITY) lse2 = INFINITY;      // a row without keys: P = 0
+                delta = p.delta[row];
+                limit = blk_limit(a, len, t);
+            }
+            const uint32_t base = smem + kKeysStage0 + st * kKeysStage;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int row = 2 * i + (lane >> 4), ch = lane & 15;
+                const int64_t x = __shfl_sync(0xffffffffu, q_at, row);
+                const int64_t y = __shfl_sync(0xffffffffu, g_at, row);
+                const uint32_t at = base + (ch >> 3) * kKeysPanelR +
+                                    chunk_at((warp - 8) * 32 + row, ch & 7);
+                cp16(at, qp + (x < 0 ? 0 : x + ch * 8), x >= 0);
+                cp16(at + 2 * kKeysPanelR, gp + (x < 0 ? 0 : y + ch * 8), x >= 0);
+            }
+            cp_commit();
+            float *m = stats + st * 3 * kKeysRows + i0;
+            m[0] = lse2;
+            m[kKeysRows] = delta;
+            m[2 * kKeysRows] = __int_as_float(limit);
+            cp_wait<0>();
+            fence_proxy_async_shared();
+            mbar_arrive(&full[st]);
+        }
+    } else if (warp == 12) {
+        // ------------------------------------------------ issue the products
+        if (lane == 0) {
+            constexpr uint32_t kk = instr_f16<T>(128, kKeysN, false, false);
+            constexpr uint32_t mn = instr_f16<T>(128, kKeysN, true, true);
+            auto second = [&](int j) {
+                const uint32_t rows_ = smem + kKeysStage0 + (j & 1) * kKeysStage;
+#pragma unroll
+                for (int i = 0; i < kKeysRows / 16; ++i) {
+                    mma_f16(tmem + kTmDv, desc_mn(rows_ + 2 * kKeysPanelR + i * 2048, kKeysPanelR),
+                            desc_mn(smem + kKeysP + i * 2048, kKeysPanelR), mn, j > 0 || i > 0);
+                    mma_f16(tmem + kTmDk, desc_mn(rows_ + i * 2048, kKeysPanelR),
+                            desc_mn(smem + kKeysDs + i * 2048, kKeysPanelR), mn, j > 0 || i > 0);
+                }
+                mma_commit(&done[j & 1]);
+            };
+            bool ok = true;
+            for (int j = 0; j < steps && ok; ++j) {
+                ok = mbar_wait_poll(&full[j & 1], (j >> 1) & 1, p.err);
+                if (!ok) break;
+                mma_fence_after();
+                const uint32_t rows_ = smem + kKeysStage0 + (j & 1) * kKeysStage;
+                const uint32_t tm = tmem + (j & 1) * kTmStage;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t r = (i >> 2) * kKeysPanelR + (i & 3) * 32;
+                    const uint32_t k = (i >> 2) * kKeysPanelK + (i & 3) * 32;
+                    mma_f16(tm + kTmS, desc_k(rows_ + r), desc_k(smem + kKeysK + k), kk, i > 0);
+                    mma_f16(tm + kTmDp, desc_k(rows_ + 2 * kKeysPanelR + r),
+                            desc_k(smem + kKeysV + k), kk, i > 0);
+                }
+                mma_commit(&ready[j & 1]);
+                if (j > 0) {
+                    ok = mbar_wait_poll(&made, (j - 1) & 1, p.err);
+                    if (!ok) break;
+                    mma_fence_after();
+                    second(j - 1);
+                }
+            }
+            if (ok && steps) {
+                if (mbar_wait_poll(&made, (steps - 1) & 1, p.err)) {
+                    mma_fence_after();
+                    second(steps - 1);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ P and dS, then the result
+        const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const float scale2 = a.scale * kLog2e;
+        bool ok = true;
+        for (int j = 0; j < steps; ++j) {
+            const int st = j & 1;
+            ok = mbar_wait_poll(&full[st], (j >> 1) & 1, p.err) &&
+                 mbar_wait_poll(&ready[st], (j >> 1) & 1, p.err);
+            if (!ok) break;
+            mma_fence_after();
+            uint32_t s[32], dp[32];
+            tmem_ld32(tmem + lanes + st * kTmStage + kTmS + half * 32, s);
+            tmem_ld32(tmem + lanes + st * kTmStage + kTmDp + half * 32, dp);
+            const float *m = stats + st * 3 * kKeysRows + row;
+            const float lse2 = m[0], delta = m[kKeysRows];
+            const int seen = __float_as_int(m[2 * kKeysRows]) - (key0 + half * 32);
+            tmem_wait_ld();
+            uint32_t pp[16], dd[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float pr[2], ds[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    pr[e] = ex2(fmaf(__uint_as_float(s[i + e]), scale2, -lse2));
+                    ds[e] = pr[e] * (__uint_as_float(dp[i + e]) - delta) * a.scale;
+                    if (i + e >= seen) pr[e] = ds[e] = 0.0f;
+                }
+                pp[i / 2] = pack2<T>(pr[0], pr[1]);
+                dd[i / 2] = pack2<T>(ds[0], ds[1]);
+            }
+            // the products of the step before read the buffers that are written now
+            if (j > 0) ok = mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.err);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t at = smem + chunk_at(row, half * 4 + i);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kKeysP),
+                             "r"(pp[4 * i]), "r"(pp[4 * i + 1]), "r"(pp[4 * i + 2]),
+                             "r"(pp[4 * i + 3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kKeysDs),
+                             "r"(dd[4 * i]), "r"(dd[4 * i + 1]), "r"(dd[4 * i + 2]),
+                             "r"(dd[4 * i + 3])
+                             : "memory");
+            }
+            fence_proxy_async_shared();
+            mma_fence_before();
+            mbar_arrive(&made);
+        }
+        if (ok && steps) ok = mbar_wait_poll(&done[(steps - 1) & 1], ((steps - 1) >> 1) & 1, p.err);
+        mma_fence_after();
+        // warps 0-3 write dV, 4-7 dK: a thread has element `row` of all 64 keys
+        uint32_t x[2][32];
+        uint32_t bad[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (steps) {
+                tmem_ld32(tmem + lanes + (half ? kTmDk : kTmDv) + i * 32, x[i]);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[i][e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                if ((x[i][e] & 0x7f800000u) == 0x7f800000u) bad[i] |= 1u << e;
+        }
+        const int64_t step = (int64_t)a.Hk * D;
+        const int64_t at = ((int64_t)b * a.Tk + key0) * step + h * D + row;
+        const int n = min(kKeysN, a.Tk - key0);
+        if (p.chunks == 1) {
+            T *out = (T *)(half ? p.dk : p.dv) + at;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (i < n) out[i * step] = from_f32<T>(__uint_as_float(x[i >> 5][i & 31]));
+        } else {
+            float *out = p.part + (int64_t)(2 * chunk + (half ? 0 : 1)) * p.part_stride + at;
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+                if (i < n) out[i * step] = __uint_as_float(x[i >> 5][i & 31]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (bad[i]) atomicOr(&odd[i], bad[i]);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int i = warp; i < n; i += 8)
+            if (odd[i >> 5] >> (i & 31) & 1u) dkdv_key_alone<T, D>(p, b, h, key0 + i, chunk);
+        mma_fence_before();
+    }
+    __syncthreads();
+    if (warp == 12) {
+        mma_fence_after();
+        tmem_free(tmem, kTmColumns);
+    }
+}
+
+}  // namespace spmm
