@@ -93,7 +93,8 @@ __device__ __noinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, int 
 constexpr int kKeysD = 128;                // width of a head
 constexpr int kKeysN = 64;                 // keys per CTA
 constexpr int kKeysRows = 128;             // rows per step
-constexpr int kKeysThreads = 13 * 32;      // 8 softmax warps, 4 loaders, 1 issuer
+constexpr int kKeysLoaders = 8, kKeysIssuer = 8 + kKeysLoaders;   // after 8 softmax warps
+constexpr int kKeysThreads = 32 * (kKeysIssuer + 1);
 constexpr int kKeysMaxWords = 256;         // a CTA's range: up to 8192 queries
 constexpr int kKeysPanelK = kKeysN * 128, kKeysPanelR = kKeysRows * 128;   // bytes
 constexpr int kKeysK = 0, kKeysV = 2 * kKeysPanelK, kKeysStage0 = 4 * kKeysPanelK;
@@ -147,14 +148,14 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
             n_queries = base;
             odd[0] = odd[1] = 0;
             for (int i = 0; i < 2; ++i) {
-                mbar_init(&full[i], 128);
+                mbar_init(&full[i], 32 * kKeysLoaders);
                 mbar_init(&ready[i], 1);
                 mbar_init(&done[i], 1);
             }
             mbar_init(&made, 256);
             mbar_init_fence();
         }
-    } else if (warp == 12) {
+    } else if (warp == kKeysIssuer) {
         tmem_alloc(&tmem_slot, kTmColumns);
         mma_fence_before();
     }
@@ -164,15 +165,17 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
     const int rows = n_queries * a.G;
     const int steps = (rows + kKeysRows - 1) / kKeysRows;
 
-    if (warp >= 8 && warp < 12) {
+    if (warp >= 8 && warp < kKeysIssuer) {
         // ------------------------------------------------ gather rows
         const T *qp = (const T *)a.q + b * a.q_sb + (int64_t)h * a.G * a.q_sh;
         const T *gp = (const T *)p.dout + b * p.do_sb + (int64_t)h * a.G * p.do_sh;
-        const int i0 = threadIdx.x - 256;
+        // a warp gathers kPer rows of a step; its lanes 0 .. kPer - 1 know where they are
+        constexpr int kPer = kKeysRows / kKeysLoaders;
+        const int i0 = threadIdx.x - 256, row0 = (warp - 8) * kPer;
         if (steps) {
             const T *kp = (const T *)a.k + b * a.k_sb + h * a.k_sh;
             const T *vp = (const T *)a.v + b * a.v_sb + h * a.v_sh;
-            for (int i = i0; i < kKeysN * C; i += 128) {
+            for (int i = i0; i < kKeysN * C; i += 32 * kKeysLoaders) {
                 const int row = i / C, ch = i % C;
                 const bool live = key0 + row < len;
                 const int64_t key = live ? key0 + row : 0;
@@ -183,47 +186,49 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
         }
         for (int j = 0; j < steps; ++j) {
             const int st = j & 1;
-            if (j >= 2 && !mbar_wait_poll(&done[st], ((j >> 1) - 1) & 1, p.err)) break;
-            const int f = j * kKeysRows + i0;
+            const int f = j * kKeysRows + row0 + lane;
             int64_t q_at = -1, g_at = 0;
             float lse2 = INFINITY, delta = 0.0f;
             int limit = 0;
-            if (f < rows) {
+            if (lane < kPer && f < rows) {
                 const int q = f / a.G, g = f - q * a.G, t = t_base + list[q];
                 q_at = t * a.q_st + g * a.q_sh;
                 g_at = t * p.do_st + g * p.do_sh;
                 const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + h * a.G + g;
                 lse2 = p.lse[row] * kLog2e;
-                if (lse2 == -INFINITY) lse2 = INFINITY;      // a row without keys: P = 0
                 delta = p.delta[row];
                 limit = blk_limit(a, len, t);
             }
+            // the stage was last read by the second products of step j - 2
+            if (j >= 2 && !mbar_wait_poll(&done[st], ((j >> 1) - 1) & 1, p.err)) break;
             const uint32_t base = smem + kKeysStage0 + st * kKeysStage;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kPer / 2; ++i) {
                 const int row = 2 * i + (lane >> 4), ch = lane & 15;
                 const int64_t x = __shfl_sync(0xffffffffu, q_at, row);
                 const int64_t y = __shfl_sync(0xffffffffu, g_at, row);
-                const uint32_t at = base + (ch >> 3) * kKeysPanelR +
-                                    chunk_at((warp - 8) * 32 + row, ch & 7);
+                const uint32_t at = base + (ch >> 3) * kKeysPanelR + chunk_at(row0 + row, ch & 7);
                 cp16(at, qp + (x < 0 ? 0 : x + ch * 8), x >= 0);
                 cp16(at + 2 * kKeysPanelR, gp + (x < 0 ? 0 : y + ch * 8), x >= 0);
             }
             cp_commit();
-            float *m = stats + st * 3 * kKeysRows + i0;
-            m[0] = lse2;
-            m[kKeysRows] = delta;
-            m[2 * kKeysRows] = __int_as_float(limit);
+            if (lane < kPer) {
+                float *m = stats + st * 3 * kKeysRows + row0 + lane;
+                m[0] = lse2 == -INFINITY ? INFINITY : lse2;  // a row without keys: P = 0
+                m[kKeysRows] = delta;
+                m[2 * kKeysRows] = __int_as_float(limit);
+            }
             cp_wait<0>();
             fence_proxy_async_shared();
             mbar_arrive(&full[st]);
         }
-    } else if (warp == 12) {
+    } else if (warp == kKeysIssuer) {
         // ------------------------------------------------ issue the products
         if (lane == 0) {
             constexpr uint32_t kk = instr_f16<T>(128, kKeysN, false, false);
             constexpr uint32_t mn = instr_f16<T>(128, kKeysN, true, true);
             auto second = [&](int j) {
+                mma_fence_after();
                 const uint32_t rows_ = smem + kKeysStage0 + (j & 1) * kKeysStage;
 #pragma unroll
                 for (int i = 0; i < kKeysRows / 16; ++i) {
@@ -234,10 +239,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                 }
                 mma_commit(&done[j & 1]);
             };
-            bool ok = true;
-            for (int j = 0; j < steps && ok; ++j) {
-                ok = mbar_wait_poll(&full[j & 1], (j >> 1) & 1, p.err);
-                if (!ok) break;
+            auto first = [&](int j) {
                 mma_fence_after();
                 const uint32_t rows_ = smem + kKeysStage0 + (j & 1) * kKeysStage;
                 const uint32_t tm = tmem + (j & 1) * kTmStage;
@@ -250,17 +252,28 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                             desc_k(smem + kKeysV + k), kk, i > 0);
                 }
                 mma_commit(&ready[j & 1]);
-                if (j > 0) {
-                    ok = mbar_wait_poll(&made, (j - 1) & 1, p.err);
-                    if (!ok) break;
-                    mma_fence_after();
-                    second(j - 1);
-                }
-            }
-            if (ok && steps) {
-                if (mbar_wait_poll(&made, (steps - 1) & 1, p.err)) {
-                    mma_fence_after();
-                    second(steps - 1);
+            };
+            // A step's first products and the second ones of the step before wait for
+            // different things: whichever is ready goes first (the second ones free
+            // the stage that the gathering warps wait for).
+            bool ok = true;
+            for (int j = 0; j <= steps && ok && steps; ++j) {
+                bool a_left = j < steps, b_left = j > 0;
+                const uint64_t t0 = global_ns();
+                for (uint32_t spin = 1; a_left || b_left; ++spin) {
+                    if (a_left && mbar_poll(&full[j & 1], (j >> 1) & 1)) {
+                        first(j);
+                        a_left = false;
+                    }
+                    if (b_left && mbar_poll(&made, (j - 1) & 1)) {
+                        second(j - 1);
+                        b_left = false;
+                    }
+                    if (spin >= kSpinLimit || ((spin & 255) == 0 && global_ns() - t0 > kWaitLimitNs)) {
+                        ok = !a_left && !b_left;
+                        if (!ok) atomicOr(p.err + kErrTimeout, 1);
+                        break;
+                    }
                 }
             }
         }
@@ -285,14 +298,16 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
             const int seen = __float_as_int(m[2 * kKeysRows]) - (key0 + half * 32);
             tmem_wait_ld();
             uint32_t pp[16], dd[16];
+            const bool whole = __all_sync(0xffffffffu, seen >= 32);
+            const float ds_off = -delta * a.scale;
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
                 float pr[2], ds[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     pr[e] = ex2(fmaf(__uint_as_float(s[i + e]), scale2, -lse2));
-                    ds[e] = pr[e] * (__uint_as_float(dp[i + e]) - delta) * a.scale;
-                    if (i + e >= seen) pr[e] = ds[e] = 0.0f;
+                    ds[e] = pr[e] * fmaf(__uint_as_float(dp[i + e]), a.scale, ds_off);
+                    if (!whole && i + e >= seen) pr[e] = ds[e] = 0.0f;
                 }
                 pp[i / 2] = pack2<T>(pr[0], pr[1]);
                 dd[i / 2] = pack2<T>(ds[0], ds[1]);
@@ -357,7 +372,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
         mma_fence_before();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kKeysIssuer) {
         mma_fence_after();
         tmem_free(tmem, kTmColumns);
     }
