@@ -159,10 +159,8 @@ spmm_status spmm_blocks_check(const spmm_blocks_shape *s, const int32_t *blocks,
  * [B, Tq, Hq], the natural logarithm of the sum of exp(scale q . k). A query
  * that sees no key gives 0 and -infinity. D is 64 or 128.
  */
-int64_t spmm_blocks_attend_workspace(const spmm_blocks_shape *s);
 spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
-                               const int32_t *blocks, void *out, float *lse, void *work,
-                               int64_t work_bytes, void *stream);
+                               const int32_t *blocks, void *out, float *lse, void *stream);
 
 /*
  * spmm_blocks_backward -- the gradients of out with respect to q, k and v (the

@@ -25,11 +25,9 @@ constexpr int kRowThreads = 32 * kRowWarps;
 struct RowArgs {
     BlkArgs a;
     int gt;                  // tiles of 8 NT rows per group
-    int splits;              // CTAs per list
+    int splits;              // CTAs per list: the CTAs of a cluster
     void *out;               // [B, Tq, Hq, D]
     float *lse;              // [B, Tq, Hq]
-    float *part_o;           // [item][splits][8 NT][D]: O / l of a split's keys
-    float *part_lse;         // [item][splits][8 NT], in powers of 2
 };
 
 // Registers of 16 keys: rows r and r + 8 of the slice for K, keys 2c, 2c+1,
@@ -63,10 +61,22 @@ __device__ __forceinline__ void load_slice(Slice<D> &x, const T *k, const T *v, 
     }
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// The same shared variable of CTA `rank` of the cluster (this one is `mine`).
+__device__ __forceinline__ const float *peer(const float *x, int rank, int mine) {
+    if (rank == mine) return x;
+    uint64_t y;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(y) : "l"(x), "r"(rank));
+    return (const float *)y;
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
     constexpr int R = 8 * NT;                       // rows of the CTA
-    __shared__ float sm_o[kRowWarps][R][D + 4];
+    __shared__ __align__(16) float sm_o[kRowWarps][R][D + 4];
     __shared__ float sm_m[kRowWarps][R], sm_l[kRowWarps][R];
     const BlkArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -109,15 +119,21 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
     const T *vp = (const T *)a.v + b * a.v_sb + h * a.v_sh;
     const int per = a.block / 16;                   // slices per block
     const int all = a.n * per;
-    const int s0 = (int)((int64_t)all * split / p.splits);
     const int s1 = (int)((int64_t)all * (split + 1) / p.splits);
-    for (int s = s0 + warp; s < s1; s += kRowWarps) {
-        const int j = s / per;
-        if (!blk_entry_ok(list, j, a.NB)) continue;
-        const int key0 = list[j] * a.block + (s % per) * 16;
-        if (key0 >= limit) continue;
-        Slice<D> x;
-        load_slice<T, D>(x, kp, vp, a.k_st, a.v_st, key0, limit, r, c);
+    int s = (int)((int64_t)all * split / p.splits) + warp;
+    // first key of the warp's next slice that counts, or -1
+    auto next = [&]() {
+        for (; s < s1; s += kRowWarps) {
+            const int j = s / per;
+            if (!blk_entry_ok(list, j, a.NB)) continue;
+            const int key0 = list[j] * a.block + (s % per) * 16;
+            if (key0 >= limit) continue;
+            s += kRowWarps;
+            return key0;
+        }
+        return -1;
+    };
+    auto add = [&](const Slice<D> &x, int key0) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             float st[4] = {};
@@ -163,6 +179,29 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
                             __byte_perm(k8, k9, 0x5410), __byte_perm(k8, k9, 0x7632), b0, b1);
             }
         }
+    };
+    auto load = [&](Slice<D> &x, int key0) {
+        if (key0 >= 0) load_slice<T, D>(x, kp, vp, a.k_st, a.v_st, key0, limit, r, c);
+    };
+    if constexpr (NT == 1) {                        // the next slice is on its way meanwhile
+        Slice<D> x, y;
+        int kx = next(), ky;
+        load(x, kx);
+        while (kx >= 0) {
+            ky = next();
+            load(y, ky);
+            add(x, kx);
+            if (ky < 0) break;
+            kx = next();
+            load(x, kx);
+            add(y, ky);
+        }
+    } else {
+        Slice<D> x;
+        for (int kx = next(); kx >= 0; kx = next()) {
+            load(x, kx);
+            add(x, kx);
+        }
     }
     // the warps' parts
 #pragma unroll
@@ -188,67 +227,47 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
             }
         }
     __syncthreads();
-    constexpr int U = D / 8;
-    for (int i = threadIdx.x; i < R * U; i += kRowThreads) {
-        const int row = i / U, d = i % U * 8;
-        if (row >= ng) continue;
+    // the CTA's parts join in its first warp's buffers, an element per thread
+    __shared__ float cta_m[R], cta_l[R];
+    for (int i = threadIdx.x; i < R * D; i += kRowThreads) {
+        const int row = i / D, d = i % D;
         float mx = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, sm_m[w][row]);
         const float base = mx == -INFINITY ? 0.0f : mx;
-        float sum = 0.0f, x[8] = {};
+        float sum = 0.0f, x = 0.0f;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
             const float f = ex2(sm_m[w][row] - base);
             sum = fmaf(sm_l[w][row], f, sum);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(sm_o[w][row][d + e], f, x[e]);
+            x = fmaf(sm_o[w][row][d], f, x);
         }
-        const float inv = sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;   // NaN stays NaN
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv;
-        const float lse2 = sum != 0.0f ? base + log2f(sum) : -INFINITY;
-        if (p.splits == 1) {
-            const int64_t o_row = (int64_t)bt * a.Hq + h * a.G + g0 + row;
-            st_pack<T, 8>((T *)p.out + o_row * D + d, x);
-            if (d == 0) p.lse[o_row] = lse2 * kLn2;
-        } else {
-            const int64_t o_row = ((int64_t)item * p.splits + split) * R + row;
-            st_pack<float, 8>(p.part_o + o_row * D + d, x);
-            if (d == 0) p.part_lse[o_row] = lse2;
+        sm_o[0][row][d] = x;
+        if (d == 0) {
+            cta_m[row] = mx;
+            cta_l[row] = sum;
         }
     }
-}
-
-// The splits' parts of a row: out = sum_s 2^(lse_s - lse) O_s.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) k_attend_join(RowArgs p, int R, int64_t rows) {
-    constexpr int U = D / 8;
-    const int64_t i = (int64_t)blockIdx.x * (128 / U) + threadIdx.x / U;   // (b, t, head)
-    if (i >= rows) return;
-    const int d = threadIdx.x % U * 8;
-    const BlkArgs &a = p.a;
-    const int head = (int)(i % a.Hq);
-    const int64_t bt = i / a.Hq;
-    const int h = head / a.G, g = head % a.G;
-    const int64_t first = ((bt * a.Hk + h) * p.gt + g / R) * p.splits * R + g % R;
-    float mx = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) mx = fmaxf(mx, p.part_lse[first + (int64_t)s * R]);
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    float sum = 0.0f, x[8] = {};
-    for (int s = 0; s < p.splits; ++s) {
-        const float f = ex2(p.part_lse[first + (int64_t)s * R] - base);
-        float y[8];
-        ld_pack<float, 8>(p.part_o + (first + (int64_t)s * R) * D + d, y);
-        sum += f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fmaf(y[e], f, x[e]);
+    // Then the cluster's CTAs, each finishing a share of the elements from
+    // everybody's shared memory: no second launch, no scratch.
+    if (p.splits > 1) cluster_barrier();
+    else __syncthreads();
+    for (int i = split * kRowThreads + threadIdx.x; i < ng * D; i += p.splits * kRowThreads) {
+        const int row = i / D, d = i % D;
+        float mx = -INFINITY, sum = 0.0f, x = 0.0f;
+        for (int v = 0; v < p.splits; ++v) mx = fmaxf(mx, *peer(&cta_m[row], v, split));
+        const float base = mx == -INFINITY ? 0.0f : mx;
+        for (int v = 0; v < p.splits; ++v) {
+            const float f = ex2(*peer(&cta_m[row], v, split) - base);
+            sum = fmaf(*peer(&cta_l[row], v, split), f, sum);
+            x = fmaf(*peer(&sm_o[0][row][d], v, split), f, x);
+        }
+        x *= sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;                // NaN stays NaN
+        const int64_t o_row = (int64_t)bt * a.Hq + h * a.G + g0 + row;
+        ((T *)p.out)[o_row * D + d] = from_f32<T>(x);
+        if (d == 0) p.lse[o_row] = sum != 0.0f ? (base + log2f(sum)) * kLn2 : -INFINITY;
     }
-    const float inv = sum != 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= inv;
-    st_pack<T, 8>((T *)p.out + i * D + d, x);
-    if (d == 0) p.lse[i] = (sum != 0.0f ? base + log2f(sum) : -INFINITY) * kLn2;
+    if (p.splits > 1) cluster_barrier();            // nobody leaves while it is read
 }
 
 // ------------------------------------------------------------- by tile of rows
@@ -260,7 +279,8 @@ struct AttendTileArgs {
 
 // One row, key by key, for rows whose tile gave a result that is not finite: in
 // the tile a value that is infinite or NaN times the weight 0 of a row that does
-// not see it spoils that row too; here each row meets the keys it sees only.
+// not see it spoils that row's sums too (not its lse); here each row meets the
+// keys it sees only.
 template <typename T, int D>
 __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, int h, int t, int head) {
     const BlkArgs &a = p.t.a;
@@ -297,7 +317,6 @@ __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, in
     for (int e = 0; e < E; ++e) o[e] *= inv;
     const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
     st_pack<T, E>((T *)p.out + row * D + lane * E, o);
-    if (lane == 0) p.lse[row] = l != 0.0f ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // Variants: kLargeWarps consumer warps take the whole SM (11 and the producer
@@ -488,8 +507,8 @@ struct RowPlan {
     int64_t items;
 };
 
-// Splits of a list: enough CTAs for a few per SM, while each warp of a split
-// keeps at least one slice of 16 keys.
+// Splits of a list, a power of two up to a portable cluster's 8: enough CTAs for
+// some four per SM, while each warp of a split keeps a slice of 16 keys.
 RowPlan row_plan(const spmm_blocks_shape *s) {
     RowPlan p;
     const int64_t G = s->Hq / s->Hk;
@@ -497,25 +516,27 @@ RowPlan row_plan(const spmm_blocks_shape *s) {
     p.gt = (int)((G + 8 * p.nt - 1) / (8 * p.nt));
     p.items = s->B * s->Tq * s->Hk * p.gt;
     const int64_t slices = s->n * (s->block / 16);
-    int64_t most = std::max<int64_t>(1, slices / kRowWarps);
-    most = std::min<int64_t>(most, 64);
-    const int64_t want = p.items > 0 ? (152 * 4 + p.items - 1) / p.items : 1;
-    p.splits = (int)std::max<int64_t>(1, std::min(most, want));
+    p.splits = 1;
+    while (p.splits < 8 && 2 * p.splits * kRowWarps <= slices && p.items * p.splits < 152 * 4)
+        p.splits *= 2;
     return p;
 }
 
 template <typename T, int D>
-cudaError_t launch_rows(const RowArgs &p, const RowPlan &rp, int64_t rows, cudaStream_t s) {
-    const unsigned grid = (unsigned)(rp.items * rp.splits);
-    if (rp.nt == 1) k_attend_rows<T, D, 1><<<grid, kRowThreads, 0, s>>>(p);
-    else k_attend_rows<T, D, 2><<<grid, kRowThreads, 0, s>>>(p);
+cudaError_t launch_rows(const RowArgs &p, const RowPlan &rp, cudaStream_t s) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)rp.splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(rp.items * rp.splits));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = rp.splits > 1 ? 1 : 0;
     count_launch();
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || rp.splits == 1) return e;
-    constexpr int per = 128 / (D / 8);
-    k_attend_join<T, D><<<(unsigned)((rows + per - 1) / per), 128, 0, s>>>(p, 8 * rp.nt, rows);
-    count_launch();
-    return cudaGetLastError();
+    return rp.nt == 1 ? cudaLaunchKernelEx(&cfg, k_attend_rows<T, D, 1>, p)
+                      : cudaLaunchKernelEx(&cfg, k_attend_rows<T, D, 2>, p);
 }
 
 template <typename T, int D, int KB, int W>
@@ -596,18 +617,8 @@ spmm_status spmm_dynamic_sync(void *stream) {
     return cuda_status(e);
 }
 
-int64_t spmm_blocks_attend_workspace(const spmm_blocks_shape *s) {
-    using namespace spmm;
-    if (blk_check(s, true) != SPMM_OK) return 0;
-    if (blocks_by_tile(s)) return 0;
-    const RowPlan p = row_plan(s);
-    if (p.splits == 1) return 0;
-    return p.items * p.splits * 8 * p.nt * (s->D + 1) * 4;
-}
-
 spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
-                               const int32_t *blocks, void *out, float *lse, void *work,
-                               int64_t work_bytes, void *stream) {
+                               const int32_t *blocks, void *out, float *lse, void *stream) {
     using namespace spmm;
     const spmm_status st = blk_check(s, true);
     if (st != SPMM_OK) return st;
@@ -615,8 +626,6 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
     if (!blocks || !lse || !out || (uintptr_t)out % 16) return SPMM_ERR_INVALID_ARG;
     if (!rows_ok(q, 2) || (s->Tk > 0 && (!rows_ok(k, 2) || !rows_ok(v, 2))))
         return SPMM_ERR_INVALID_ARG;
-    const int64_t need = spmm_blocks_attend_workspace(s);
-    if (need && (!work || (uintptr_t)work % 16 || work_bytes < need)) return SPMM_ERR_INVALID_ARG;
     cudaStream_t cs = (cudaStream_t)stream;
     RowArgs p{};
     p.a = blk_args(s, blocks);
@@ -649,16 +658,13 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
     p.splits = rp.splits;
     p.out = out;
     p.lse = lse;
-    p.part_o = (float *)work;
-    p.part_lse = p.part_o + rp.items * rp.splits * 8 * rp.nt * s->D;
-    const int64_t rows = s->B * s->Tq * s->Hq;
     cudaError_t e;
     if (s->dtype == SPMM_BF16)
-        e = s->D == 64 ? launch_rows<__nv_bfloat16, 64>(p, rp, rows, cs)
-                       : launch_rows<__nv_bfloat16, 128>(p, rp, rows, cs);
+        e = s->D == 64 ? launch_rows<__nv_bfloat16, 64>(p, rp, cs)
+                       : launch_rows<__nv_bfloat16, 128>(p, rp, cs);
     else
-        e = s->D == 64 ? launch_rows<__half, 64>(p, rp, rows, cs)
-                       : launch_rows<__half, 128>(p, rp, rows, cs);
+        e = s->D == 64 ? launch_rows<__half, 64>(p, rp, cs)
+                       : launch_rows<__half, 128>(p, rp, cs);
     return cuda_status(e);
 }
 

@@ -247,21 +247,18 @@ template <int R> struct RowKeys {
     }
 };
 
-template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
+// One warp writes row's list; score: the row's scores (shared or global memory).
+template <int R>
+__device__ __forceinline__ void best_of_row(const SelArgs &s, int64_t row, const float *score,
+                                            int cand, int own) {
     const BlkArgs &a = s.a;
     const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= s.rows) return;
-    const int64_t bt = row / a.Hk;
-    const int t = (int)(bt % a.Tq), b = (int)(bt / a.Tq);
-    int own;
-    const int cand = candidates(a, b, t, &own);
     const int want = min(cand, a.n - (own >= 0 ? 1 : 0));
     int32_t *out = s.out + row * a.n;
     int done = 0;
     if (want > 0 && want < cand) {
         RowKeys<R> keys;
-        keys.load(s.score + row * a.NB, cand, lane);
+        keys.load(score, cand, lane);
         // the largest x with count(keys >= x) >= want
         uint32_t lo, hi;
         keys.extremes(lo, hi);
@@ -308,6 +305,68 @@ template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
     for (int j = done + lane; j < a.n; j += 32) out[j] = -1;
 }
 
+template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
+    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (row >= s.rows) return;
+    const int64_t bt = row / s.a.Hk;
+    int own;
+    const int cand = candidates(s.a, (int)(bt / s.a.Tq), (int)(bt % s.a.Tq), &own);
+    best_of_row<R>(s, row, s.score + row * s.a.NB, cand, own);
+}
+
+// Few queries over at most 32 R blocks: a CTA per row, scores in shared memory,
+// the list by its first warp; one launch and no scratch. Eight elements a lane:
+// D / 8 lanes share a block, so a warp scores 32 / L blocks at a time, U deep.
+template <typename T, int R, int L>
+__global__ void __launch_bounds__(256) k_select_row(SelArgs s) {
+    constexpr int kPer = 32 / L, kU = 4;
+    __shared__ float score[32 * R];
+    const BlkArgs &a = s.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x;
+    const int h = (int)(row % a.Hk);
+    const int64_t bt = row / a.Hk;
+    const int t = (int)(bt % a.Tq), b = (int)(bt / a.Tq);
+    int own;
+    const int cand = candidates(a, b, t, &own);
+    if (cand > a.n - (own >= 0 ? 1 : 0)) {         // else every block is taken
+        const int d = lane % L * 8;
+        const bool live = d < s.D;
+        float q[8] = {};
+        const T *p = (const T *)a.q + b * a.q_sb + t * a.q_st + (int64_t)h * a.G * a.q_sh + d;
+        for (int g = 0; g < a.G && live; ++g) {
+            float x[8];
+            ld_pack<T, 8>(p + g * a.q_sh, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] += x[e];
+        }
+        const float *means = s.means + ((int64_t)b * a.NB * a.Hk + h) * s.D + d;
+        for (int c0 = warp * kPer * kU; c0 < cand; c0 += warps * kPer * kU) {
+            float dot[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int c = c0 + u * kPer + lane / L;
+                dot[u] = 0.0f;
+                if (live && c < cand) {
+                    float m[8];
+                    ld_pack<float, 8>(means + (int64_t)c * a.Hk * s.D, m);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dot[u] = fmaf(q[e], m[e], dot[u]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+                const int c = c0 + u * kPer + lane / L;
+                if (lane % L == 0 && c < cand) score[c] = dot[u];
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) best_of_row<R>(s, row, score, cand, own);
+}
+
 __global__ void k_check_lists(BlkArgs a, int64_t rows, int32_t *bad) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= rows * a.n) return;
@@ -342,8 +401,28 @@ cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t 
     return cudaGetLastError();
 }
 
+// Up to this many blocks a row's scores stay in its CTA.
+constexpr int64_t kRowBlocks = 1024;
+
+template <typename T, int R> void launch_select_row(const SelArgs &s, int threads, cudaStream_t st) {
+    if (s.D <= 64) k_select_row<T, R, 8><<<(unsigned)s.rows, threads, 0, st>>>(s);
+    else if (s.D <= 128) k_select_row<T, R, 16><<<(unsigned)s.rows, threads, 0, st>>>(s);
+    else k_select_row<T, R, 32><<<(unsigned)s.rows, threads, 0, st>>>(s);
+    count_launch();
+}
+
+template <typename T> cudaError_t launch_select_row(const SelArgs &s, cudaStream_t st) {
+    if (s.a.NB <= 128) launch_select_row<T, 4>(s, 128, st);
+    else if (s.a.NB <= 512) launch_select_row<T, 16>(s, 256, st);
+    else launch_select_row<T, 32>(s, 256, st);
+    return cudaGetLastError();
+}
+
 bool tiled(const spmm_blocks_shape *s) {
     return s->Tq >= kTiledQueries || s->B * s->Tq * s->Hk > 65535;
+}
+bool by_row(const spmm_blocks_shape *s) {
+    return !tiled(s) && s->Tk <= kRowBlocks * s->block;
 }
 
 }  // namespace
@@ -376,7 +455,7 @@ spmm_status spmm_blocks_means(const spmm_blocks_shape *s, spmm_rows k, int64_t n
 
 int64_t spmm_blocks_select_workspace(const spmm_blocks_shape *s) {
     using namespace spmm;
-    if (blk_check(s, false) != SPMM_OK) return 0;
+    if (blk_check(s, false) != SPMM_OK || by_row(s)) return 0;
     const int64_t NB = (s->Tk + s->block - 1) / s->block, rows = s->B * s->Tq * s->Hk;
     return round_up(rows * NB * 4, 16) + (tiled(s) ? rows * s->D * 4 : 0);
 }
@@ -404,6 +483,12 @@ spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const fl
     g.out = blocks;
     cudaStream_t cs = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
+    if (by_row(s)) {
+        if (s->dtype == SPMM_F32) e = launch_select_row<float>(g, cs);
+        else if (s->dtype == SPMM_BF16) e = launch_select_row<__nv_bfloat16>(g, cs);
+        else e = launch_select_row<__half>(g, cs);
+        return cuda_status(e);
+    }
     if (g.a.NB > 0) {
         if (s->dtype == SPMM_F32) e = launch_scores<float>(g, s->B, tiled(s), cs);
         else if (s->dtype == SPMM_BF16) e = launch_scores<__nv_bfloat16>(g, s->B, tiled(s), cs);

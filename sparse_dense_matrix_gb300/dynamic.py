@@ -59,8 +59,7 @@ def _declare():
         "spmm_blocks_select_workspace": ([S], i64),
         "spmm_blocks_select": ([S, _Rows, vp, vp, vp, i64, vp], i32),
         "spmm_blocks_check": ([S, vp, vp, vp], i32),
-        "spmm_blocks_attend_workspace": ([S], i64),
-        "spmm_blocks_attend": ([S, _Rows, _Rows, _Rows, vp, vp, vp, vp, i64, vp], i32),
+        "spmm_blocks_attend": ([S, _Rows, _Rows, _Rows, vp, vp, vp, vp], i32),
         "spmm_blocks_backward_workspace": ([S], i64),
         "spmm_blocks_backward": ([S, _Rows, _Rows, _Rows, vp, vp, vp, _Rows, vp, vp, vp, vp, i64,
                                   vp], i32),
@@ -413,11 +412,8 @@ class BlockSelection:
         s, rows = self._problem(q, k, v, scale)
         out = q.new_empty(q.shape)
         lse = q.new_empty(q.shape[:3], dtype=torch.float32)
-        need = lib.spmm_blocks_attend_workspace(s)
-        work = _scratch(q, need)
         st = lib.spmm_blocks_attend(s, *rows, self.blocks.data_ptr(), out.data_ptr(),
-                                    lse.data_ptr(), None if work is None else work.data_ptr(),
-                                    need, _raw_stream(self.device.index))
+                                    lse.data_ptr(), _raw_stream(self.device.index))
         if st:
             _check(st, "spmm_blocks_attend")
         return out, lse

@@ -77,10 +77,10 @@ def test_blocks_refuse_shapes(dyn, bad, status):
     assert L.spmm_blocks_means(s, r, -1, PTR, None) == status
     assert L.spmm_blocks_select(s, r, PTR, PTR, PTR, 1 << 40, None) == status
     assert L.spmm_blocks_check(s, PTR, PTR, None) == status
-    assert L.spmm_blocks_attend(s, r, r, r, PTR, PTR, PTR, PTR, 1 << 40, None) == status
+    assert L.spmm_blocks_attend(s, r, r, r, PTR, PTR, PTR, None) == status
     assert L.spmm_blocks_backward(s, r, r, r, PTR, PTR, PTR, r, PTR, PTR, PTR, PTR, 1 << 40,
                                   None) == status
-    assert L.spmm_blocks_attend_workspace(s) == 0
+    assert L.spmm_blocks_select_workspace(s) == 0 and L.spmm_blocks_backward_workspace(s) == 0
 
 
 def test_blocks_refuse_tensors(dyn):
@@ -92,19 +92,18 @@ def test_blocks_refuse_tensors(dyn):
         for at in range(3):
             t = [r, r, r]
             t[at] = bad
-            assert L.spmm_blocks_attend(s, *t, PTR, PTR, PTR, PTR, big, None) == INVALID
+            assert L.spmm_blocks_attend(s, *t, PTR, PTR, PTR, None) == INVALID
         assert L.spmm_blocks_backward(s, r, r, r, PTR, PTR, PTR, bad, PTR, PTR, PTR, PTR, big,
                                       None) == INVALID
-    assert L.spmm_blocks_attend(s, r, r, r, None, PTR, PTR, PTR, big, None) == INVALID
-    assert L.spmm_blocks_attend(s, r, r, r, PTR, PTR, None, PTR, big, None) == INVALID
-    assert L.spmm_blocks_select(s, r, PTR, PTR, None, 0, None) == INVALID
+    assert L.spmm_blocks_attend(s, r, r, r, None, PTR, PTR, None) == INVALID
+    assert L.spmm_blocks_attend(s, r, r, r, PTR, PTR, None, None) == INVALID
+    assert L.spmm_blocks_select(shape(dyn, Tq=100), r, PTR, PTR, None, 0, None) == INVALID
     need = L.spmm_blocks_backward_workspace(s)
     assert need > 0
     assert L.spmm_blocks_backward(s, r, r, r, PTR, PTR, PTR, r, PTR, PTR, PTR, PTR, need - 1,
                                   None) == INVALID
     # widths and types of the matrix kernels
     for bad in (dict(D=32), dict(dtype=0)):
-        assert L.spmm_blocks_attend(shape(dyn, **bad), r, r, r, PTR, PTR, PTR, PTR, big,
-                                    None) == UNSUPPORTED
+        assert L.spmm_blocks_attend(shape(dyn, **bad), r, r, r, PTR, PTR, PTR, None) == UNSUPPORTED
     # nothing to do is no error
-    assert L.spmm_blocks_attend(shape(dyn, B=0), r, r, r, None, None, None, None, 0, None) == 0
+    assert L.spmm_blocks_attend(shape(dyn, B=0), r, r, r, None, None, None, None) == 0

@@ -478,3 +478,68 @@ def test_refusals(sdm, cuda_device):
         sel.backward(q, q, k, k, out, lse[..., :2])
     dq, _, _ = sel.backward(q, q, k, k, out, lse)
     assert (dq == 0).all()
+
+
+MORE = [  # B, Tq, Tk, Hq, Hk, D, block, n, lengths
+    (2, 700, 900, 8, 2, 128, 64, 6, [900, 450]),
+    (1, 2100, 2100, 4, 1, 128, 64, 5, None),
+    (1, 333, 333, 5, 5, 128, 128, 2, None),
+    (3, 1, 9000, 12, 4, 128, 16, 40, [9000, 7, 4000]),
+    (1, 9, 40000, 4, 2, 64, 32, 10, None),
+    (1, 24, 1500, 64, 1, 64, 64, 8, None),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", MORE)
+def test_attend_and_backward_more(sdm, cuda_device, case, dtype):
+    """Many rows per block, ranges of queries, a block that every query chose."""
+    B, Tq, Tk, Hq, Hk, D, block, n, lengths = case
+    q, k, v, blocks, L = inputs(cuda_device, case, dtype, seed=11)
+    blocks[..., 0] = torch.where(blocks[..., 0] >= 0, 0, -1)       # still ascending
+    blocks = torch.where((blocks == 0).cumsum(-1) > 1, blocks, blocks)
+    sel = sdm.BlockSelection(blocks.contiguous(), block, Tk, L)
+    grad = randn(cuda_device, 95, *q.shape).to(q.dtype)
+    out, lse = sel.attend(q, k, v)
+    dq, dk, dv = sel.backward(grad, q, k, v, out, lse)
+    want = ref.attend(q, k, v, blocks, block, L, True, grad=grad)
+    for name, got in (("out", out), ("lse", lse), ("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.close(got, want[name], want["tol_" + name], name)
+    again = (*sel.attend(q, k, v), *sel.backward(grad, q, k, v, out, lse))
+    assert all(torch.equal(a, b) for a, b in zip((out, lse, dq, dk, dv), again))
+    sdm.dynamic_sync()
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("fp16", 128)])
+def test_a_row_that_is_not_finite_stays_its_own(sdm, cuda_device, dtype, D):
+    """A NaN gradient row, and an infinite value: they reach the keys and rows that
+    see them, and no other of the same block."""
+    T, block = 320, 64
+    case = (1, T, T, 4, 2, D, block, 3, None)
+    q, k, v, blocks, L = inputs(cuda_device, case, dtype, seed=13)
+    own = torch.arange(T, device=cuda_device, dtype=torch.int32) // block
+    blocks = own[None, :, None, None].expand(1, T, 2, 1).contiguous()
+    sel = sdm.BlockSelection(blocks, block, T)
+    grad = randn(cuda_device, 94, *q.shape).to(q.dtype)
+    out, lse = sel.attend(q, k, v)
+    clean = sel.backward(grad, q, k, v, out, lse)
+    grad[0, 100, 0] = float("nan")           # sees keys 64 .. 100 of kv head 0
+    dq, dk, dv = sel.backward(grad, q, k, v, out, lse)
+    assert torch.isnan(dv[0, 64:101, 0]).all() and torch.isnan(dk[0, 64:101, 0]).all()
+    u = ref.U[q.dtype]
+    for got, want in ((dk, clean[1]), (dv, clean[2])):
+        for rest in (got[0, :64, 0] - want[0, :64, 0], got[0, 101:, 0] - want[0, 101:, 0],
+                     got[0, :, 1] - want[0, :, 1]):
+            # a key summed on its own is rounded once, from unrounded weights
+            assert rest.abs().max() <= 4 * u * want.abs().max() + 4 * u * 8
+    assert torch.isnan(dq[0, 100, 0]).all()
+    keep = torch.arange(T, device=cuda_device) != 100
+    assert torch.equal(dq[0, keep], clean[0][0, keep])
+    v2 = v.clone()
+    v2[0, 200, 1] = float("inf")             # seen by rows 200 .. 255 of heads 2 and 3
+    out2, lse2 = sel.attend(q, k, v2)
+    assert torch.equal(lse2, lse)
+    assert torch.isinf(out2[0, 200:256, 2:]).all()
+    assert torch.equal(out2[0, :200, 2:], out[0, :200, 2:]) or \
+        (out2[0, :200, 2:] - out[0, :200, 2:]).abs().max() <= 4 * u * out.abs().max()
+    assert torch.equal(out2[0, 256:], out[0, 256:]) and torch.equal(out2[:, :, :2], out[:, :, :2])
