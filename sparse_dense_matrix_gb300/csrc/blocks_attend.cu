@@ -19,8 +19,8 @@ namespace {
 __device__ int32_t g_dynamic_err[kErrWords];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
-constexpr int kRowWarps = 4;
-constexpr int kRowThreads = 32 * kRowWarps;
+// Warps of a CTA: eight for one n-tile (two CTAs per SM, 128 registers), four for two.
+template <int NT> constexpr int kRowWarps = NT == 1 ? 8 : 4;
 
 struct RowArgs {
     BlkArgs a;
@@ -74,10 +74,11 @@ __device__ __forceinline__ const float *peer(const float *x, int rank, int mine)
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
+__global__ void __launch_bounds__(32 * kRowWarps<NT>, 2) k_attend_rows(RowArgs p) {
     constexpr int R = 8 * NT;                       // rows of the CTA
-    __shared__ __align__(16) float sm_o[kRowWarps][R][D + 4];
-    __shared__ float sm_m[kRowWarps][R], sm_l[kRowWarps][R];
+    constexpr int W = kRowWarps<NT>, threads = 32 * W;
+    __shared__ __align__(16) float sm_o[W][R][D + 4];
+    __shared__ float sm_m[W][R], sm_l[W][R];
     const BlkArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int64_t item = blockIdx.x / p.splits;
@@ -123,12 +124,12 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
     int s = (int)((int64_t)all * split / p.splits) + warp;
     // first key of the warp's next slice that counts, or -1
     auto next = [&]() {
-        for (; s < s1; s += kRowWarps) {
+        for (; s < s1; s += W) {
             const int j = s / per;
             if (!blk_entry_ok(list, j, a.NB)) continue;
             const int key0 = list[j] * a.block + (s % per) * 16;
             if (key0 >= limit) continue;
-            s += kRowWarps;
+            s += W;
             return key0;
         }
         return -1;
@@ -180,28 +181,12 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
             }
         }
     };
-    auto load = [&](Slice<D> &x, int key0) {
-        if (key0 >= 0) load_slice<T, D>(x, kp, vp, a.k_st, a.v_st, key0, limit, r, c);
-    };
-    if constexpr (NT == 1) {                        // the next slice is on its way meanwhile
-        Slice<D> x, y;
-        int kx = next(), ky;
-        load(x, kx);
-        while (kx >= 0) {
-            ky = next();
-            load(y, ky);
-            add(x, kx);
-            if (ky < 0) break;
-            kx = next();
-            load(x, kx);
-            add(y, ky);
-        }
-    } else {
-        Slice<D> x;
-        for (int kx = next(); kx >= 0; kx = next()) {
-            load(x, kx);
-            add(x, kx);
-        }
+    // One slice at a time: the other warps of the SM cover its loads (a second
+    // slice in registers would halve their number)
+    Slice<D> x;
+    for (int key0 = next(); key0 >= 0; key0 = next()) {
+        load_slice<T, D>(x, kp, vp, a.k_st, a.v_st, key0, limit, r, c);
+        add(x, key0);
     }
     // the warps' parts
 #pragma unroll
@@ -229,15 +214,15 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
     __syncthreads();
     // the CTA's parts join in its first warp's buffers, an element per thread
     __shared__ float cta_m[R], cta_l[R];
-    for (int i = threadIdx.x; i < R * D; i += kRowThreads) {
+    for (int i = threadIdx.x; i < R * D; i += threads) {
         const int row = i / D, d = i % D;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) mx = fmaxf(mx, sm_m[w][row]);
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, sm_m[w][row]);
         const float base = mx == -INFINITY ? 0.0f : mx;
         float sum = 0.0f, x = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float f = ex2(sm_m[w][row] - base);
             sum = fmaf(sm_l[w][row], f, sum);
             x = fmaf(sm_o[w][row][d], f, x);
@@ -252,7 +237,7 @@ __global__ void __launch_bounds__(kRowThreads) k_attend_rows(RowArgs p) {
     // everybody's shared memory: no second launch, no scratch.
     if (p.splits > 1) cluster_barrier();
     else __syncthreads();
-    for (int i = split * kRowThreads + threadIdx.x; i < ng * D; i += p.splits * kRowThreads) {
+    for (int i = split * threads + threadIdx.x; i < ng * D; i += p.splits * threads) {
         const int row = i / D, d = i % D;
         float mx = -INFINITY, sum = 0.0f, x = 0.0f;
         for (int v = 0; v < p.splits; ++v) mx = fmaxf(mx, *peer(&cta_m[row], v, split));
@@ -507,8 +492,9 @@ struct RowPlan {
     int64_t items;
 };
 
-// Splits of a list, a power of two up to a portable cluster's 8: enough CTAs for
-// some four per SM, while each warp of a split keeps a slice of 16 keys.
+// Splits of a list, a power of two up to a portable cluster's 8, while they still
+// fit the SMs two at a time (a second wave costs more than longer lists do) and
+// each warp keeps a slice of 16 keys.
 RowPlan row_plan(const spmm_blocks_shape *s) {
     RowPlan p;
     const int64_t G = s->Hq / s->Hk;
@@ -517,7 +503,8 @@ RowPlan row_plan(const spmm_blocks_shape *s) {
     p.items = s->B * s->Tq * s->Hk * p.gt;
     const int64_t slices = s->n * (s->block / 16);
     p.splits = 1;
-    while (p.splits < 8 && 2 * p.splits * kRowWarps <= slices && p.items * p.splits < 152 * 4)
+    const int64_t warps = p.nt == 1 ? kRowWarps<1> : kRowWarps<2>;
+    while (p.splits < 8 && 2 * p.splits * warps <= slices && 2 * p.items * p.splits <= 152 * 2)
         p.splits *= 2;
     return p;
 }
@@ -530,7 +517,7 @@ cudaError_t launch_rows(const RowArgs &p, const RowPlan &rp, cudaStream_t s) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(rp.items * rp.splits));
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(32 * (rp.nt == 1 ? kRowWarps<1> : kRowWarps<2>));
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = rp.splits > 1 ? 1 : 0;

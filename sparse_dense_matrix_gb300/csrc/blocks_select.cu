@@ -318,8 +318,8 @@ template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
 // the list by its first warp; one launch and no scratch. Eight elements a lane:
 // D / 8 lanes share a block, so a warp scores 32 / L blocks at a time, U deep.
 template <typename T, int R, int L>
-__global__ void __launch_bounds__(256) k_select_row(SelArgs s) {
-    constexpr int kPer = 32 / L, kU = 4;
+__global__ void __launch_bounds__(512) k_select_row(SelArgs s) {
+    constexpr int kPer = 32 / L, kU = 8;
     __shared__ float score[32 * R];
     const BlkArgs &a = s.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -413,8 +413,8 @@ template <typename T, int R> void launch_select_row(const SelArgs &s, int thread
 
 template <typename T> cudaError_t launch_select_row(const SelArgs &s, cudaStream_t st) {
     if (s.a.NB <= 128) launch_select_row<T, 4>(s, 128, st);
-    else if (s.a.NB <= 512) launch_select_row<T, 16>(s, 256, st);
-    else launch_select_row<T, 32>(s, 256, st);
+    else if (s.a.NB <= 512) launch_select_row<T, 16>(s, 512, st);
+    else launch_select_row<T, 32>(s, 512, st);
     return cudaGetLastError();
 }
 
