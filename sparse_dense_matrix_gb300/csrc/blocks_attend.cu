@@ -12,6 +12,7 @@
 #include <cstring>
 
 #include "blocks_tile.cuh"
+#include "umma.cuh"
 
 namespace spmm {
 namespace {
@@ -486,6 +487,257 @@ __global__ void __launch_bounds__(32 * (W + 1), W == kLargeWarps ? 1 : 2)
     }
 }
 
+// ------------------------------------------- by tile of rows, on tensor memory
+// The tile's 128 rows against each block of its union: S = Q K^T and O += P V by
+// tcgen05.mma, S, P and O in tensor memory, a thread per row between the two
+// products. A row that did not choose a block has P = 0 there. O is rescaled only
+// when a row's maximum has grown by more than 2^8 since (its P then reach 2^8 at
+// most, and l and O carry the same factor). Two CTAs share an SM: one's products
+// run under the other's exponentials.
+constexpr int kMmaRows = 128, kMmaKeys = 64, kMmaThreads = 192;   // 4 + producer + issuer
+template <int D> using MmaSmem = TileSmem<D, kMmaKeys, 8, 1, 113 * 1024>;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_constant__
+                                                                  AttendTileArgs p) {
+    using S = MmaSmem<D>;
+    constexpr int KB = kMmaKeys, C = D / 8, panel = kMmaRows * 128;
+    constexpr int kTmO = 128, columns = 256;         // S and P of two steps, then O
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[S::stages], empty[S::stages], ready[2], made[2], done[2];
+    __shared__ TileStage<8> info[S::stages];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const BlkArgs &a = p.t.a;
+    const TilePlace at(p.t, kMmaRows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int len = blk_len(a, at.b);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&ready[0], 1);
+        mbar_init(&ready[1], 1);
+        mbar_init(&made[0], kMmaRows);
+        mbar_init(&made[1], kMmaRows);
+        mbar_init(&done[0], 1);
+        mbar_init(&done[1], 1);
+        mbar_init_fence();
+    }
+    if (warp == 5) {
+        tmem_alloc(&tmem_slot, columns);
+        mma_fence_before();
+    }
+    const int row = threadIdx.x;                     // of warps 0 to 3
+    if (warp < 4) {
+        int64_t f;
+        const bool live = at.row_of(p.t, len, row, f);
+        const int64_t mine = live ? at.offset(p.t, f, a.q_sb, a.q_st, a.q_sh) : -1;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {                // 32 chunks at a time
+            const int r = i * (32 / C) + lane / C, ch = lane % C;
+            const int64_t x = __shfl_sync(0xffffffffu, mine, r);
+            cp16(smem + S::at_rows + (ch >> 3) * panel + chunk_at(warp * 32 + r, ch & 7),
+                 (const T *)a.q + (x < 0 ? 0 : x + ch * 8), x >= 0);
+        }
+        cp_commit();
+        cp_wait<0>();
+        fence_proxy_async_shared();
+    }
+    __syncthreads();
+    mma_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 4) {
+        tile_produce<S, D, KB, 8>(
+            p.t, at, smem, full, empty, info,
+            (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_lists));
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t qk = instr_f16<T>(kMmaRows, KB, false, false);
+            constexpr uint32_t pv = instr_f16<T>(kMmaRows, D, false, true);
+            // S of a step and O of the step before wait for different things:
+            // whichever is ready goes first. S takes the columns of the P of two
+            // steps before, which its product must have read: two products that
+            // write different columns need not run in the order of their issue.
+            bool more = true, ok = true;
+            for (int j = 0; ok && (more || j > 0); ++j) {
+                const int st = j % S::stages;
+                bool a_left = true, b_left = j > 0;
+                const uint64_t t0 = global_ns();
+                for (uint32_t spin = 1; a_left || b_left; ++spin) {
+                    if (a_left && mbar_poll(&full[st], (j / S::stages) & 1) &&
+                        (j < 2 || mbar_poll(&done[j & 1], ((j - 2) >> 1) & 1))) {
+                        a_left = false;
+                        const int key0 = info[st].key0;
+                        more = key0 >= 0;
+                        if (more) {
+                            const uint32_t k = smem + st * S::stage;
+                            if (key0 + KB > len) {   // values past the length may be anything
+                                for (int i = (len - key0) * C; i < KB * C; ++i)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                     k + S::operand + panel_at<KB>(i / C, i % C)),
+                                                 "r"(0)
+                                                 : "memory");
+                                fence_proxy_async_shared();
+                            }
+                            mma_fence_after();
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i)
+                                mma_f16(tmem + (j & 1) * KB,
+                                        desc_k(smem + S::at_rows + (i >> 2) * panel + (i & 3) * 32),
+                                        desc_k(k + (i >> 2) * KB * 128 + (i & 3) * 32), qk, i > 0);
+                            mma_commit(&ready[j & 1]);
+                        }
+                    }
+                    if (b_left && mbar_poll(&made[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
+                        b_left = false;
+                        const int before = (j - 1) % S::stages;
+                        const uint32_t v = smem + before * S::stage + S::operand;
+                        mma_fence_after();
+#pragma unroll
+                        for (int i = 0; i < KB / 16; ++i)
+                            mma_f16_ta(tmem + kTmO, tmem + ((j - 1) & 1) * KB + i * 8,
+                                       desc_mn(v + i * 2048, KB * 128), pv, j > 1 || i > 0);
+                        mma_commit(&empty[before]);
+                        mma_commit(&done[(j - 1) & 1]);
+                    }
+                    if (spin >= kSpinLimit || ((spin & 255) == 0 && global_ns() - t0 > kWaitLimitNs)) {
+                        ok = !a_left && !b_left;
+                        if (!ok) atomicOr(p.t.err + kErrTimeout, 1);
+                        break;
+                    }
+                }
+                if (!more) break;                    // the last O went with the closing stage
+            }
+        }
+        __syncwarp();
+    } else {
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const int64_t f = at.f0 + row;
+        const bool live = f < p.t.rows;
+        const int t = live ? (int)(f / a.G) : at.t_first;
+        const int limit = live ? blk_limit(a, len, t) : 0;
+        const int qi = t - at.t_first;
+        const float scale2 = a.scale * kLog2e;
+        float m = -INFINITY, l = 0.0f;               // m: what P is relative to, in powers of 2
+        int j = 0;
+        bool ok = true;
+        for (;; ++j) {
+            const int st = j % S::stages;
+            ok = mbar_wait_poll(&full[st], (j / S::stages) & 1, p.t.err);
+            if (!ok) break;
+            const int key0 = info[st].key0;
+            if (key0 < 0) break;
+            const bool mine = (info[st].mask[qi >> 5] >> (qi & 31) & 1u) && key0 < limit;
+            ok = mbar_wait_poll(&ready[j & 1], (j >> 1) & 1, p.t.err);
+            if (!ok) break;
+            mma_fence_after();
+            const uint32_t s_at = tmem + lanes + (j & 1) * KB;
+            uint32_t pp[32];
+            if (__any_sync(0xffffffffu, mine)) {
+                uint32_t s[2][32];
+                tmem_ld32(s_at, s[0]);
+                tmem_ld32(s_at + 32, s[1]);
+                tmem_wait_ld();
+                const int seen = mine ? limit - key0 : 0;
+                if (__any_sync(0xffffffffu, seen < KB)) {
+#pragma unroll
+                    for (int i = 0; i < KB; ++i)
+                        if (i >= seen) s[i >> 5][i & 31] = 0xff800000u;   // -infinity
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < KB; ++i) mx = fmaxf(mx, __uint_as_float(s[i >> 5][i & 31]));
+                mx *= scale2;
+                if (!mine) mx = -INFINITY;
+                float corr = 1.0f;
+                if (m == -INFINITY) {
+                    m = mx;                          // nothing of this row is in O yet
+                } else if (mx > m + 8.0f) {
+                    corr = ex2(m - mx);
+                    m = mx;
+                }
+                if (j > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
+                    ok = mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.t.err);
+                    if (!ok) break;
+                    mma_fence_after();
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t o[32];
+                        tmem_ld32(tmem + lanes + kTmO + 32 * i, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                        tmem_st32(tmem + lanes + kTmO + 32 * i, o);
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < KB; i += 2) {
+                    float x = ex2(fmaf(__uint_as_float(s[i >> 5][i & 31]), scale2, -base));
+                    float y = ex2(fmaf(__uint_as_float(s[i >> 5][(i & 31) + 1]), scale2, -base));
+                    if (!mine) x = y = 0.0f;
+                    sum += x + y;
+                    pp[i / 2] = pack2<T>(x, y);      // l sums the unrounded weights
+                }
+                l = fmaf(l, corr, sum);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) pp[i] = 0u;
+            }
+            tmem_st32(s_at, pp);
+            tmem_wait_st();
+            mma_fence_before();
+            mbar_arrive(&made[j & 1]);   // two: a warp may be a step ahead of another
+        }
+        if (ok && j > 0) mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.t.err);
+        mma_fence_after();
+        float odd = l * 0.0f;                        // NaN if anything is not finite
+        const float inv = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+        const int64_t o_row = at.out_row(p.t, f);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            if (j > 0) {
+                tmem_ld32(tmem + lanes + kTmO + 32 * i, o);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) x[w] = __uint_as_float(o[e + w]) * inv;
+                    st_pack<T, 8>((T *)p.out + o_row * D + 32 * i + e, x);
+                }
+            }
+        }
+        if (live)
+            p.lse[o_row] = l != 0.0f ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2 : -INFINITY;
+        unsigned redo = __ballot_sync(0xffffffffu, live && odd != 0.0f);
+        for (; redo; redo &= redo - 1) {
+            const int64_t g = at.f0 + warp * 32 + __ffs(redo) - 1;
+            const int tt = (int)(g / a.G);
+            attend_row_alone<T, D>(p, at.b, at.h, tt, at.h * a.G + (int)(g - (int64_t)tt * a.G));
+        }
+        mma_fence_before();
+    }
+    __syncthreads();
+    if (warp == 5) {
+        mma_fence_after();
+        tmem_free(tmem, columns);
+    }
+}
+
 // ------------------------------------------------------------------- host
 struct RowPlan {
     int nt, gt, splits;
@@ -539,8 +791,22 @@ cudaError_t launch_tile(AttendTileArgs &p, int64_t B, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, int D> cudaError_t launch_mma(AttendTileArgs &p, int64_t B, cudaStream_t s) {
+    constexpr int bytes = MmaSmem<D>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_attend_mma<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    p.t.tiles = (int)((p.t.rows + kMmaRows - 1) / kMmaRows);
+    k_attend_mma<T, D><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), kMmaThreads, bytes,
+                         s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
 template <typename T, int D>
 cudaError_t launch_tile(AttendTileArgs &p, bool large, int64_t B, cudaStream_t s) {
+    // on tensor memory: blocks of whole 64-key steps, and a scale that keeps the order
+    if (p.t.a.block % kMmaKeys == 0 && p.t.a.scale > 0.0f) return launch_mma<T, D>(p, B, s);
     if (large) {
         if (p.t.a.block == 16) return launch_tile<T, D, 16, kLargeWarps>(p, B, s);
         if (p.t.a.block == 32) return launch_tile<T, D, 32, kLargeWarps>(p, B, s);

@@ -46,6 +46,17 @@ __device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
+// The same with A in tensor memory: row r of A in lane r, two adjacent 16-bit
+// elements to a column.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t instr,
+                                           bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(instr), "r"((uint32_t)accumulate)
+        : "memory");
+}
+
 // The barrier receives one arrival when this thread's earlier MMAs are done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(
