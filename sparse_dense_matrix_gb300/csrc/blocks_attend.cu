@@ -504,8 +504,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
     constexpr int KB = kMmaKeys, C = D / 8, panel = kMmaRows * 128;
     constexpr int kTmO = 128, columns = 256;         // S and P of two steps, then O
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t full[S::stages], empty[S::stages], ready[2], made[2], done[2];
-    __shared__ TileStage<8> info[S::stages];
+    // K and V have a ring each: a step's K is read by its S alone, and the K of a
+    // later step comes in its place while the step's P is still being made
+    constexpr int N = S::stages;
+    __shared__ uint64_t k_full[N], k_empty[N], v_full[N], v_empty[N], ready[2], made[2], done[2];
+    __shared__ TileStage<8> info[N + 2];             // alive from a step's K to its P
     __shared__ uint32_t tmem_slot;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const BlkArgs &a = p.t.a;
@@ -513,12 +516,14 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int len = blk_len(a, at.b);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < S::stages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+        for (int i = 0; i < N; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
-        mbar_init(&ready[0], 1);
-        mbar_init(&ready[1], 1);
+        mbar_init(&ready[0], 2);
+        mbar_init(&ready[1], 2);
         mbar_init(&made[0], kMmaRows);
         mbar_init(&made[1], kMmaRows);
         mbar_init(&done[0], 1);
@@ -549,11 +554,65 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
     mma_fence_after();
     const uint32_t tmem = tmem_slot;
 
+    const uint32_t sk = smem, sv = smem + N * S::operand;
     if (warp == 4) {
-        tile_produce<S, D, KB, 8>(
-            p.t, at, smem, full, empty, info,
-            (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_lists));
+        // ------------------------------------------------ bring K, and V a step later
+        TileMerge<8> merge(p.t, at, (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) +
+                                                S::at_lists), S::lists);
+        int j = 0, v_key0 = -1;                      // of step j - 1
+        bool ok = true, last = false;
+        auto bring_v = [&]() {                       // V of step j - 1
+            if (v_key0 < 0) return;
+            const int st = (j - 1) % N;
+            ok = mbar_wait_poll(&v_empty[st], (((j - 1) / N) & 1) ^ 1, p.t.err);
+            if (ok && lane == 0) {
+                mbar_arrive_expect_tx(&v_full[st], S::operand);
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x)
+                    tensor4d_g2s(sv + st * S::operand + x * KB * 128, &p.t.v_map, 64 * x, v_key0,
+                                 at.h, at.b, &v_full[st]);
+            }
+            __syncwarp();
+        };
+        while (ok && !last) {
+            const int least = merge.step();
+            last = least == merge.kNone;
+            const int parts = last ? 1 : a.block / KB;
+            for (int s = 0; s < parts && ok; ++s) {
+                const int key0 = last ? -1 : least * a.block + s * KB;
+                if (key0 >= a.Tk) break;             // the second half of a last, short block
+                const int st = j % N;
+                ok = mbar_wait_poll(&k_empty[st], ((j / N) & 1) ^ 1, p.t.err);
+                if (!ok) break;
+                if (lane == 0) {
+                    TileStage<8> &x = info[j % (N + 2)];
+                    x.key0 = key0;
+#pragma unroll
+                    for (int i = 0; i < merge.kLists; ++i) x.mask[i] = merge.mask[i];
+                    if (key0 < 0) {
+                        mbar_arrive(&k_full[st]);
+                    } else {
+                        mbar_arrive_expect_tx(&k_full[st], S::operand);
+#pragma unroll
+                        for (int y = 0; y < D / 64; ++y)
+                            tensor4d_g2s(sk + st * S::operand + y * KB * 128, &p.t.k_map, 64 * y,
+                                         key0, at.h, at.b, &k_full[st]);
+                    }
+                }
+                __syncwarp();
+                bring_v();
+                v_key0 = key0;
+                ++j;
+            }
+        }
+        if (!ok) {  // somebody gave up: see the copies in flight land before the CTA ends
+            for (int i = max(0, j - N); i < j; ++i) {
+                mbar_wait(&k_full[i % N], (i / N) & 1, p.t.err);
+                mbar_wait(&v_full[i % N], (i / N) & 1, p.t.err);
+            }
+        }
     } else if (warp == 5) {
+        // ------------------------------------------------ issue the products
         if (lane == 0) {
             constexpr uint32_t qk = instr_f16<T>(kMmaRows, KB, false, false);
             constexpr uint32_t pv = instr_f16<T>(kMmaRows, D, false, true);
@@ -562,26 +621,21 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
             // steps before, which its product must have read: two products that
             // write different columns need not run in the order of their issue.
             bool more = true, ok = true;
-            for (int j = 0; ok && (more || j > 0); ++j) {
-                const int st = j % S::stages;
+            int v_key0 = -1;                         // of step j - 1
+            for (int j = 0; ok && more; ++j) {
+                const int st = j % N, before = (j + N - 1) % N;
                 bool a_left = true, b_left = j > 0;
+                int key0 = -1;
                 const uint64_t t0 = global_ns();
                 for (uint32_t spin = 1; a_left || b_left; ++spin) {
-                    if (a_left && mbar_poll(&full[st], (j / S::stages) & 1) &&
-                        (j < 2 || mbar_poll(&done[j & 1], ((j - 2) >> 1) & 1))) {
+                    if (a_left && mbar_test(&k_full[st], (j / N) & 1) &&
+                        (j < 2 || mbar_test(&done[j & 1], ((j - 2) >> 1) & 1))) {
                         a_left = false;
-                        const int key0 = info[st].key0;
+                        key0 = info[j % (N + 2)].key0;
                         more = key0 >= 0;
+                        mbar_arrive(&ready[j & 1]);  // of what the bringing warp said
                         if (more) {
-                            const uint32_t k = smem + st * S::stage;
-                            if (key0 + KB > len) {   // values past the length may be anything
-                                for (int i = (len - key0) * C; i < KB * C; ++i)
-                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                     k + S::operand + panel_at<KB>(i / C, i % C)),
-                                                 "r"(0)
-                                                 : "memory");
-                                fence_proxy_async_shared();
-                            }
+                            const uint32_t k = sk + st * S::operand;
                             mma_fence_after();
 #pragma unroll
                             for (int i = 0; i < D / 16; ++i)
@@ -589,18 +643,29 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                                         desc_k(smem + S::at_rows + (i >> 2) * panel + (i & 3) * 32),
                                         desc_k(k + (i >> 2) * KB * 128 + (i & 3) * 32), qk, i > 0);
                             mma_commit(&ready[j & 1]);
+                            mma_commit(&k_empty[st]);
+                        } else {
+                            mbar_arrive(&ready[j & 1]);
                         }
                     }
-                    if (b_left && mbar_poll(&made[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
+                    if (b_left && mbar_test(&made[(j - 1) & 1], ((j - 1) >> 1) & 1) &&
+                        mbar_test(&v_full[before], ((j - 1) / N) & 1)) {
                         b_left = false;
-                        const int before = (j - 1) % S::stages;
-                        const uint32_t v = smem + before * S::stage + S::operand;
+                        const uint32_t v = sv + before * S::operand;
+                        if (v_key0 + KB > len) {     // values past the length may be anything
+                            for (int i = (len - v_key0) * C; i < KB * C; ++i)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 v + panel_at<KB>(i / C, i % C)),
+                                             "r"(0)
+                                             : "memory");
+                            fence_proxy_async_shared();
+                        }
                         mma_fence_after();
 #pragma unroll
                         for (int i = 0; i < KB / 16; ++i)
                             mma_f16_ta(tmem + kTmO, tmem + ((j - 1) & 1) * KB + i * 8,
                                        desc_mn(v + i * 2048, KB * 128), pv, j > 1 || i > 0);
-                        mma_commit(&empty[before]);
+                        mma_commit(&v_empty[before]);
                         mma_commit(&done[(j - 1) & 1]);
                     }
                     if (spin >= kSpinLimit || ((spin & 255) == 0 && global_ns() - t0 > kWaitLimitNs)) {
@@ -609,7 +674,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                         break;
                     }
                 }
-                if (!more) break;                    // the last O went with the closing stage
+                v_key0 = key0;
             }
         }
         __syncwarp();
@@ -625,15 +690,13 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
         int j = 0;
         bool ok = true;
         for (;; ++j) {
-            const int st = j % S::stages;
-            ok = mbar_wait_poll(&full[st], (j / S::stages) & 1, p.t.err);
-            if (!ok) break;
-            const int key0 = info[st].key0;
-            if (key0 < 0) break;
-            const bool mine = (info[st].mask[qi >> 5] >> (qi & 31) & 1u) && key0 < limit;
             ok = mbar_wait_poll(&ready[j & 1], (j >> 1) & 1, p.t.err);
             if (!ok) break;
             mma_fence_after();
+            const TileStage<8> &step = info[j % (N + 2)];
+            const int key0 = step.key0;
+            if (key0 < 0) break;
+            const bool mine = (step.mask[qi >> 5] >> (qi & 31) & 1u) && key0 < limit;
             const uint32_t s_at = tmem + lanes + (j & 1) * KB;
             uint32_t pp[32];
             if (__any_sync(0xffffffffu, mine)) {

@@ -261,11 +261,11 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                 bool a_left = j < steps, b_left = j > 0;
                 const uint64_t t0 = global_ns();
                 for (uint32_t spin = 1; a_left || b_left; ++spin) {
-                    if (a_left && mbar_poll(&full[j & 1], (j >> 1) & 1)) {
+                    if (a_left && mbar_test(&full[j & 1], (j >> 1) & 1)) {
                         first(j);
                         a_left = false;
                     }
-                    if (b_left && mbar_poll(&made, (j - 1) & 1)) {
+                    if (b_left && mbar_test(&made, (j - 1) & 1)) {
                         second(j - 1);
                         b_left = false;
                     }

@@ -91,37 +91,27 @@ struct TilePlace {
     }
 };
 
-template <typename S, int D, int KB, int W>
-__device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace &at,
-                                             uint32_t smem, uint64_t *full, uint64_t *empty,
-                                             TileStage<W> *info, int32_t *lists) {
-    constexpr int kTileLists = (W + 1) / 2;              // lists per lane, words of bits
-    const BlkArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const int len = blk_len(a, at.b);
-    constexpr int kNone = INT_MAX;
-    // The lists go to shared memory first: a step of the merge then waits for no
-    // load from global memory (about 700 cycles, more than a step's arithmetic).
-    const int32_t *base = a.blocks + (((int64_t)at.b * a.Tq + at.t_first) * a.Hk + at.h) * a.n;
-    const int64_t pitch = (int64_t)a.Hk * a.n;
-    const bool staged = (int64_t)at.nq * a.n * 4 <= S::lists;
-    if (staged) {
-        for (int q = lane; q < at.nq; q += 32) {
-#pragma unroll 8
-            for (int j = 0; j < a.n; ++j) lists[q * a.n + j] = base[q * pitch + j];
-        }
-        __syncwarp();
-    }
-    const int32_t *list[kTileLists];               // the next entry
-    int left[kTileLists], head[kTileLists], prev[kTileLists];
-    int end[kTileLists];                           // first block out of sight
-    auto advance = [&](int i) {
+// The merge of a tile's lists, by one warp: step() gives the next block of the
+// union (kNone after the last) and the bits of the queries that chose it. All
+// lists are ascending, so that is the smallest of their heads. The lists go to
+// shared memory first where they fit: a step then waits for no load from global
+// memory (about 700 cycles, more than a step's arithmetic).
+template <int W> struct TileMerge {
+    static constexpr int kLists = (W + 1) / 2;     // lists per lane, words of bits
+    static constexpr int kNone = INT_MAX;
+    const int32_t *list[kLists];                   // the next entry
+    int left[kLists], head[kLists], prev[kLists];
+    int end[kLists];                               // first block out of sight
+    int nq, NB;
+    uint32_t mask[kLists];
+
+    __device__ __forceinline__ void advance(int i) {
         // entries below the one before them or out of range are skipped
         int c = kNone;
         while (left[i] > 0) {
             --left[i];
             const int x = *list[i]++;
-            const bool ok = (unsigned)x < (unsigned)a.NB && x > prev[i];
+            const bool ok = (unsigned)x < (unsigned)NB && x > prev[i];
             prev[i] = x;
             if (ok) {
                 c = x < end[i] ? x : kNone;
@@ -129,50 +119,82 @@ __device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace 
             }
         }
         head[i] = c;
-    };
+    }
+
+    __device__ __forceinline__ TileMerge(const TileArgs &p, const TilePlace &at, int32_t *lists,
+                                         int lists_bytes) {
+        const BlkArgs &a = p.a;
+        const int lane = threadIdx.x & 31, len = blk_len(a, at.b);
+        nq = at.nq;
+        NB = a.NB;
+        const int32_t *base =
+            a.blocks + (((int64_t)at.b * a.Tq + at.t_first) * a.Hk + at.h) * a.n;
+        const int64_t pitch = (int64_t)a.Hk * a.n;
+        const bool staged = (int64_t)nq * a.n * 4 <= lists_bytes;
+        if (staged) {
+            for (int q = lane; q < nq; q += 32) {
+#pragma unroll 8
+                for (int j = 0; j < a.n; ++j) lists[q * a.n + j] = base[q * pitch + j];
+            }
+            __syncwarp();
+        }
 #pragma unroll
-    for (int i = 0; i < kTileLists; ++i) {
-        const int q = i * 32 + lane;
-        left[i] = end[i] = 0;
-        head[i] = kNone;
-        prev[i] = -1;
-        list[i] = lists;
-        if (q < at.nq) {
-            const int t = at.t_first + q;
-            list[i] = staged ? lists + q * a.n : base + q * pitch;
-            left[i] = a.n;
-            end[i] = (blk_limit(a, len, t) + a.block - 1) / a.block;
-            advance(i);
+        for (int i = 0; i < kLists; ++i) {
+            const int q = i * 32 + lane;
+            left[i] = end[i] = 0;
+            head[i] = kNone;
+            prev[i] = -1;
+            list[i] = lists;
+            if (q < nq) {
+                list[i] = staged ? lists + q * a.n : base + q * pitch;
+                left[i] = a.n;
+                end[i] = (blk_limit(a, len, at.t_first + q) + a.block - 1) / a.block;
+                advance(i);
+            }
         }
     }
-    int stage = 0, issued = 0;
-    uint32_t parity = 1;                           // the ring starts empty
-    bool ok = true;
-    while (ok) {
+
+    __device__ __forceinline__ int step() {
         int least = head[0];
 #pragma unroll
-        for (int i = 1; i < kTileLists; ++i)
-            if (32 * i < at.nq) least = min(least, head[i]);
+        for (int i = 1; i < kLists; ++i)
+            if (32 * i < nq) least = min(least, head[i]);
         least = __reduce_min_sync(0xffffffffu, least);
-        uint32_t mask[kTileLists];
 #pragma unroll
-        for (int i = 0; i < kTileLists; ++i) {
+        for (int i = 0; i < kLists; ++i) {
             mask[i] = 0;
-            if (32 * i >= at.nq) continue;         // usually all but the first 32 queries
+            if (32 * i >= nq) continue;            // usually all but the first 32 queries
             const bool mine = least != kNone && head[i] == least;
             mask[i] = __ballot_sync(0xffffffffu, mine);
             if (mine) advance(i);
         }
-        const int parts = least == kNone ? 1 : a.block / KB;
+        return least;
+    }
+};
+
+template <typename S, int D, int KB, int W>
+__device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace &at,
+                                             uint32_t smem, uint64_t *full, uint64_t *empty,
+                                             TileStage<W> *info, int32_t *lists) {
+    const BlkArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    TileMerge<W> merge(p, at, lists, S::lists);
+    int stage = 0, issued = 0;
+    uint32_t parity = 1;                           // the ring starts empty
+    bool ok = true;
+    while (ok) {
+        const int least = merge.step();
+        const bool last = least == merge.kNone;
+        const int parts = last ? 1 : a.block / KB;
         for (int s = 0; s < parts; ++s) {
-            const int key0 = least == kNone ? -1 : least * a.block + s * KB;
+            const int key0 = last ? -1 : least * a.block + s * KB;
             if (key0 >= a.Tk) break;               // the second half of a last, short block
             ok = mbar_wait(&empty[stage], parity, p.err);
             if (!ok) break;
             if (lane == 0) {
                 info[stage].key0 = key0;
 #pragma unroll
-                for (int i = 0; i < kTileLists; ++i) info[stage].mask[i] = mask[i];
+                for (int i = 0; i < merge.kLists; ++i) info[stage].mask[i] = merge.mask[i];
                 if (key0 < 0) {
                     mbar_arrive(&full[stage]);
                 } else {
@@ -194,7 +216,7 @@ __device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace 
                 parity ^= 1;
             }
         }
-        if (least == kNone) break;
+        if (last) break;
     }
     if (!ok) {      // a consumer gave up: see the copies in flight land before the CTA ends
         for (int i = 0; i < S::stages && i < issued; ++i) {
