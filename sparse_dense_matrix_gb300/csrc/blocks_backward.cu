@@ -692,7 +692,25 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
     __syncwarp();
     for (; redo; redo &= redo - 1) {
         const int bit = __ffs(redo) - 1;
-        dkdv_key_alone<T, D>(p, b, h, key0 + warp * 16 + (bit >> 2) + 8 * (bit & 1), chunk);
+        constexpr int E = D / 32;
+        const int key = key0 + warp * 16 + (bit >> 2) + 8 * (bit & 1);
+        float x[E], y[E];
+        dkdv_key_alone<T, D>(
+            p, b, h, key,
+            [&](auto body) {
+                for (int w = chunk * p.chunk_words; w < w_end; ++w)
+                    for (uint32_t m = bits[w]; m; m &= m - 1) body(w * 32 + __ffs(m) - 1);
+            },
+            x, y);
+        const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + h) * D + lane * E;
+        if (p.chunks == 1) {
+            st_pack<T, E>((T *)p.dk + at, x);
+            st_pack<T, E>((T *)p.dv + at, y);
+        } else {
+            float *part = p.part + (int64_t)(2 * chunk) * p.part_stride + at;
+            st_pack<float, E>(part, x);
+            st_pack<float, E>(part + p.part_stride, y);
+        }
     }
 }
 
@@ -719,7 +737,8 @@ struct BwdPlan {
     int64_t words, chunk_words, chunks;
     int64_t bits_bytes, delta_bytes, part_bytes;
     int W;
-    bool keys;               // k_dkdv_keys
+    bool keys;               // k_dkdv_keys, over at most so many tiles and items
+    int64_t tiles = 0, items = 0;
 };
 
 // The tensor-core kernel: bf16 (fp16 needs dS scaled as it goes, which sums in
@@ -740,22 +759,20 @@ BwdPlan bwd_plan(const spmm_blocks_shape *s) {
     const int64_t ctas = std::max<int64_t>(1, s->B * s->Hk * NB * (s->block / (16 * p.W)));
     int64_t chunks = std::min<int64_t>((152 * 8 * (4 / p.W) + ctas - 1) / ctas, (p.words + 7) / 8);
     chunks = std::max<int64_t>(1, std::min<int64_t>(chunks, 64));
-    p.keys = by_keys(s);
-    if (p.keys) {
-        // One CTA fills an SM: some four rounds of them. A block that every query
-        // chose is cut up too, into ranges of 2048 queries, or more where that
-        // would make more than eight (each range adds a partial dK and dV).
-        const int64_t k_ctas = std::max<int64_t>(1, s->B * s->Hk * NB * (s->block / kKeysN));
-        chunks = std::min<int64_t>((152 * 4 + k_ctas - 1) / k_ctas, (p.words + 7) / 8);
-        chunks = std::max<int64_t>(
-            {chunks, std::min<int64_t>((p.words + 63) / 64, 8),
-             (p.words + kKeysMaxWords - 1) / kKeysMaxWords, 1});
-    }
     p.chunk_words = std::max<int64_t>(1, (p.words + chunks - 1) / chunks);
     p.chunks = std::max<int64_t>(1, (p.words + p.chunk_words - 1) / p.chunk_words);
     p.bits_bytes = round_up(s->B * s->Hk * NB * p.words * 4, 256);
     p.delta_bytes = round_up(s->B * s->Tq * s->Hq * 4, 256);
     p.part_bytes = p.chunks > 1 ? p.chunks * 2 * s->B * s->Tk * s->Hk * s->D * 4 : 0;
+    p.keys = by_keys(s);
+    if (p.keys) {
+        const int64_t parts = s->block / kKeysN;
+        p.tiles = s->B * s->Hk * NB * parts;
+        p.items = p.tiles + s->B * s->Tq * s->Hk * s->n * parts / kKeysSegment;   // at most
+        p.chunks = 1;
+        p.part_bytes = round_up((p.tiles + 1) * 4, 256) + round_up(p.items * 8, 256) +
+                       p.items * 2 * kKeysN * kKeysD * 4;
+    }
     return p;
 }
 
@@ -773,16 +790,23 @@ cudaError_t launch_dkdv(const BwdArgs &p, const BwdPlan &bp, int64_t B, cudaStre
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t launch_keys(BwdArgs &p, int64_t B, cudaStream_t s) {
+template <typename T> cudaError_t launch_keys(BwdArgs &p, const BwdPlan &bp, cudaStream_t s) {
+    char *w = (char *)p.part;
+    p.keys.tiles = bp.tiles;
+    p.keys.first = (int32_t *)w;
+    p.keys.item = (int2 *)(w + round_up((bp.tiles + 1) * 4, 256));
+    p.keys.part = (float *)((char *)p.keys.item + round_up(bp.items * 8, 256));
     cudaError_t e = dynamic_err(&p.err);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_dkdv_keys<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kKeysSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.a.NB * (p.a.block / kKeysN)), (unsigned)(B * p.a.Hk),
-                    (unsigned)p.chunks);
-    k_dkdv_keys<T><<<grid, kKeysThreads, kKeysSmem, s>>>(p);
-    count_launch();
+    const int64_t blocks = bp.tiles / (p.a.block / kKeysN);
+    k_key_counts<<<(unsigned)((blocks + 7) / 8), 256, 0, s>>>(p);
+    k_key_items<<<1, 1024, 0, s>>>(p);
+    k_dkdv_keys<T><<<(unsigned)bp.items, kKeysThreads, kKeysSmem, s>>>(p);
+    k_keys_join<T><<<(unsigned)bp.tiles, 256, 0, s>>>(p);
+    count_launch(4);
     return cudaGetLastError();
 }
 
@@ -856,8 +880,10 @@ cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (bp.keys) {
-        if constexpr (D == kKeysD && !kNarrow<T>) e = launch_keys<T>(p, s->B, cs);
-    } else if (bp.W == 1) e = launch_dkdv<T, D, 1>(p, bp, s->B, cs);
+        if constexpr (D == kKeysD && !kNarrow<T>) e = launch_keys<T>(p, bp, cs);
+        return e;
+    }
+    if (bp.W == 1) e = launch_dkdv<T, D, 1>(p, bp, s->B, cs);
     else if (bp.W == 2) e = launch_dkdv<T, D, 2>(p, bp, s->B, cs);
     else e = launch_dkdv<T, D, 4>(p, bp, s->B, cs);
     if (e != cudaSuccess || p.chunks == 1) return e;

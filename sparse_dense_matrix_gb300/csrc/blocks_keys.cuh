@@ -16,6 +16,18 @@
 
 namespace spmm {
 
+// Work of k_dkdv_keys: a 64-key tile's queries in segments of at most
+// kKeysSegment, an item each, so that a block which every query chose is shared
+// out like the rest. tile = ((b Hk + h) NB + block) parts + part.
+constexpr int kKeysSegment = 512;
+
+struct KeyItems {
+    int32_t *first;          // [tiles + 1]: a tile's first item
+    int2 *item;              // (tile, segment), `first[tiles]` of them
+    float *part;             // [item][dK, dV][64][D], for tiles of several items
+    int64_t tiles;
+};
+
 struct BwdArgs {
     BlkArgs a;
     const void *out, *dout;
@@ -31,63 +43,54 @@ struct BwdArgs {
     int64_t part_stride;     // B Tk Hk D
     int gt;
     int32_t *err;
+    KeyItems keys;
 };
 
 // One key, row by row, for keys whose tile gave a result that is not finite: in
 // the tile a row of q or of the gradient that is not finite, times the weight 0
-// of a key that it does not see, spoils that key too.
-template <typename T, int D>
-__device__ __noinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, int key, int chunk) {
+// of a key that it does not see, spoils that key too. `each` calls its argument
+// for every query that chose the key's block; lane l gets elements l E ..
+template <typename T, int D, typename F>
+__device__ __forceinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, int key, F each,
+                                               float (&dk)[D / 32], float (&dv)[D / 32]) {
     const BlkArgs &a = p.a;
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     const int len = blk_len(a, b);
-    const uint32_t *bits = p.bits + (((int64_t)b * a.Hk + h) * a.NB + key / a.block) * p.words;
-    const int w1 = min(p.words, (chunk + 1) * p.chunk_words);
-    float k[E] = {}, v[E] = {}, dk[E] = {}, dv[E] = {};
+    float k[E] = {}, v[E] = {};
     if (key < len) {
         ld_pack<T, E>((const T *)a.k + b * a.k_sb + key * a.k_st + h * a.k_sh + lane * E, k);
         ld_pack<T, E>((const T *)a.v + b * a.v_sb + key * a.v_st + h * a.v_sh + lane * E, v);
     }
-    for (int w = chunk * p.chunk_words; w < w1; ++w)
-        for (uint32_t m = bits[w]; m; m &= m - 1) {
-            const int t = w * 32 + __ffs(m) - 1;
-            if (key >= blk_limit(a, len, t)) continue;
-            for (int g = 0; g < a.G; ++g) {
-                const int head = h * a.G + g;
-                const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
-                float q[E], o[E], s = 0.0f, d = 0.0f;
-                ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
-                ld_pack<T, E>((const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + lane * E,
-                              o);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    s = fmaf(q[e], k[e], s);
-                    d = fmaf(o[e], v[e], d);
-                }
+    for (int e = 0; e < E; ++e) dk[e] = dv[e] = 0.0f;
+    each([&](int t) {
+        if (key >= blk_limit(a, len, t)) return;
+        for (int g = 0; g < a.G; ++g) {
+            const int head = h * a.G + g;
+            const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
+            float q[E], o[E], s = 0.0f, d = 0.0f;
+            ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
+            ld_pack<T, E>((const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + lane * E, o);
 #pragma unroll
-                for (int x = 16; x; x >>= 1) {
-                    s += __shfl_xor_sync(0xffffffffu, s, x);
-                    d += __shfl_xor_sync(0xffffffffu, d, x);
-                }
-                const float pr = ex2(fmaf(s, a.scale * kLog2e, -p.lse[row] * kLog2e));
-                const float ds = pr * (d - p.delta[row]) * a.scale;
+            for (int e = 0; e < E; ++e) {
+                s = fmaf(q[e], k[e], s);
+                d = fmaf(o[e], v[e], d);
+            }
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    dk[e] = fmaf(ds, q[e], dk[e]);
-                    dv[e] = fmaf(pr, o[e], dv[e]);
-                }
+            for (int x = 16; x; x >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, x);
+                d += __shfl_xor_sync(0xffffffffu, d, x);
+            }
+            const float pr = ex2(fmaf(s, a.scale * kLog2e, -p.lse[row] * kLog2e));
+            const float ds = pr * (d - p.delta[row]) * a.scale;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                dk[e] = fmaf(ds, q[e], dk[e]);
+                dv[e] = fmaf(pr, o[e], dv[e]);
             }
         }
-    const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + h) * D + lane * E;
-    if (p.chunks == 1) {
-        st_pack<T, E>((T *)p.dk + at, dk);
-        st_pack<T, E>((T *)p.dv + at, dv);
-    } else {
-        float *x = p.part + (int64_t)(2 * chunk) * p.part_stride + at;
-        st_pack<float, E>(x, dk);
-        st_pack<float, E>(x + p.part_stride, dv);
-    }
+    });
 }
 
 constexpr int kKeysD = 128;                // width of a head
@@ -95,14 +98,13 @@ constexpr int kKeysN = 64;                 // keys per CTA
 constexpr int kKeysRows = 128;             // rows per step
 constexpr int kKeysLoaders = 8, kKeysIssuer = 8 + kKeysLoaders;   // after 8 softmax warps
 constexpr int kKeysThreads = 32 * (kKeysIssuer + 1);
-constexpr int kKeysMaxWords = 256;         // a CTA's range: up to 8192 queries
 constexpr int kKeysPanelK = kKeysN * 128, kKeysPanelR = kKeysRows * 128;   // bytes
 constexpr int kKeysK = 0, kKeysV = 2 * kKeysPanelK, kKeysStage0 = 4 * kKeysPanelK;
 constexpr int kKeysStage = 4 * kKeysPanelR;                                // Q, dO
 constexpr int kKeysP = kKeysStage0 + 2 * kKeysStage, kKeysDs = kKeysP + kKeysPanelR;
 constexpr int kKeysStats = kKeysDs + kKeysPanelR;                          // [2][3][128] floats
-constexpr int kKeysList = kKeysStats + 2 * 3 * kKeysRows * 4;              // queries, 16 bits
-constexpr int kKeysSmem = kKeysList + kKeysMaxWords * 32 * 2 + 1024;
+constexpr int kKeysList = kKeysStats + 2 * 3 * kKeysRows * 4;              // the segment's queries
+constexpr int kKeysSmem = kKeysList + kKeysSegment * 4 + 1024;
 // tensor memory columns
 constexpr int kTmS = 0, kTmDp = 64, kTmStage = 128, kTmDv = 256, kTmDk = 320, kTmColumns = 512;
 
@@ -113,27 +115,29 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     unsigned char *sp = smem_raw + (smem - smem_addr(smem_raw));
     float *stats = (float *)(sp + kKeysStats);
-    uint16_t *list = (uint16_t *)(sp + kKeysList);
+    int32_t *list = (int32_t *)(sp + kKeysList);
     __shared__ uint64_t full[2], ready[2], made, done[2];
     __shared__ uint32_t tmem_slot, odd[2];
     __shared__ int n_queries;
 
     const BlkArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((int)blockIdx.x >= p.keys.first[p.keys.tiles]) return;
+    const int2 item = p.keys.item[blockIdx.x];
+    const bool alone = p.keys.first[item.x + 1] - p.keys.first[item.x] == 1;
     const int parts = a.block / kKeysN;
-    const int blk = blockIdx.x / parts;
-    const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk, chunk = blockIdx.z;
-    const int key0 = blk * a.block + blockIdx.x % parts * kKeysN;
+    const int blk_id = item.x / parts, blk = blk_id % a.NB;
+    const int b = blk_id / a.NB / a.Hk, h = blk_id / a.NB % a.Hk;
+    const int key0 = blk * a.block + item.x % parts * kKeysN;
     if (key0 >= a.Tk) return;
     const int len = blk_len(a, b);
-    const int t_base = chunk * p.chunk_words * 32;
 
-    if (warp == 0) {                             // the range's queries, ascending
-        const uint32_t *bits = p.bits + ((int64_t)blockIdx.y * a.NB + blk) * p.words;
-        const int w0 = chunk * p.chunk_words, w1 = min(p.words, w0 + p.chunk_words);
+    if (warp == 0) {                             // the segment's queries, ascending
+        const uint32_t *bits = p.bits + (int64_t)blk_id * p.words;
+        const int from = item.y * kKeysSegment, to = from + kKeysSegment;
         int base = 0;
-        for (int w = w0; w < w1; w += 32) {
-            const uint32_t x = w + lane < w1 ? bits[w + lane] : 0u;
+        for (int w = 0; w < p.words && base < to; w += 32) {
+            const uint32_t x = w + lane < p.words ? bits[w + lane] : 0u;
             int incl = __popc(x);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -141,9 +145,11 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                 if (lane >= o) incl += y;
             }
             int at = base + incl - __popc(x);
-            for (uint32_t m = x; m; m &= m - 1) list[at++] = (w + lane - w0) * 32 + __ffs(m) - 1;
+            for (uint32_t m = x; m; m &= m - 1, ++at)
+                if (at >= from && at < to) list[at - from] = (w + lane) * 32 + __ffs(m) - 1;
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
+        base = max(0, min(base, to) - from);
         if (lane == 0) {
             n_queries = base;
             odd[0] = odd[1] = 0;
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
             float lse2 = INFINITY, delta = 0.0f;
             int limit = 0;
             if (lane < kPer && f < rows) {
-                const int q = f / a.G, g = f - q * a.G, t = t_base + list[q];
+                const int q = f / a.G, g = f - q * a.G, t = list[q];
                 q_at = t * a.q_st + g * a.q_sh;
                 g_at = t * p.do_st + g * p.do_sh;
                 const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + h * a.G + g;
@@ -349,32 +355,121 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
             for (int e = 0; e < 32; ++e)
                 if ((x[i][e] & 0x7f800000u) == 0x7f800000u) bad[i] |= 1u << e;
         }
-        const int64_t step = (int64_t)a.Hk * D;
-        const int64_t at = ((int64_t)b * a.Tk + key0) * step + h * D + row;
+        // to the gradients, or to the item's part of them
+        const int64_t step = alone ? (int64_t)a.Hk * D : D;
+        const int64_t first =
+            alone ? ((int64_t)b * a.Tk + key0) * step + h * D
+                  : ((int64_t)blockIdx.x * 2 + (half ? 0 : 1)) * (kKeysN * D);
         const int n = min(kKeysN, a.Tk - key0);
-        if (p.chunks == 1) {
-            T *out = (T *)(half ? p.dk : p.dv) + at;
+        T *out = (T *)(half ? p.dk : p.dv) + first + row;
+        float *part = p.keys.part + first + row;
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (i < n) out[i * step] = from_f32<T>(__uint_as_float(x[i >> 5][i & 31]));
-        } else {
-            float *out = p.part + (int64_t)(2 * chunk + (half ? 0 : 1)) * p.part_stride + at;
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-                if (i < n) out[i * step] = __uint_as_float(x[i >> 5][i & 31]);
+        for (int i = 0; i < kKeysN; ++i) {
+            const float y = __uint_as_float(x[i >> 5][i & 31]);
+            if (i >= n) break;
+            if (alone) out[i * step] = from_f32<T>(y);
+            else part[i * step] = y;
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             if (bad[i]) atomicOr(&odd[i], bad[i]);
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        for (int i = warp; i < n; i += 8)
-            if (odd[i >> 5] >> (i & 31) & 1u) dkdv_key_alone<T, D>(p, b, h, key0 + i, chunk);
+        for (int i = warp; i < n; i += 8) {
+            if (!(odd[i >> 5] >> (i & 31) & 1u)) continue;
+            constexpr int E = D / 32;
+            float dk[E], dv[E];
+            dkdv_key_alone<T, D>(
+                p, b, h, key0 + i,
+                [&](auto body) {
+                    for (int q = 0; q < n_queries; ++q) body(list[q]);
+                },
+                dk, dv);
+            if (alone) {
+                const int64_t at = ((int64_t)b * a.Tk + key0 + i) * step + h * D + lane * E;
+                st_pack<T, E>((T *)p.dk + at, dk);
+                st_pack<T, E>((T *)p.dv + at, dv);
+            } else {
+                float *y = p.keys.part + (int64_t)blockIdx.x * 2 * kKeysN * D + i * D + lane * E;
+                st_pack<float, E>(y, dk);
+                st_pack<float, E>(y + kKeysN * D, dv);
+            }
+        }
         mma_fence_before();
     }
     __syncthreads();
     if (warp == kKeysIssuer) {
         mma_fence_after();
         tmem_free(tmem, kTmColumns);
+    }
+}
+
+// Items: a warp counts a block's queries, one CTA numbers the segments.
+__global__ void __launch_bounds__(256) k_key_counts(const BwdArgs p) {
+    const int64_t blk = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, parts = p.a.block / kKeysN;
+    if (blk * parts >= p.keys.tiles) return;
+    int n = 0;
+    for (int w = lane; w < p.words; w += 32) n += __popc(p.bits[blk * p.words + w]);
+    n = __reduce_add_sync(0xffffffffu, n);
+    // a tile that nobody chose has an item too: it writes zeros
+    if (lane < parts) p.keys.first[blk * parts + lane] = max(1, (n + kKeysSegment - 1) / kKeysSegment);
+}
+
+__global__ void __launch_bounds__(1024) k_key_items(const BwdArgs p) {
+    __shared__ int warp_sum[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int carry = 0;
+    for (int64_t i0 = 0; i0 < p.keys.tiles; i0 += 1024) {
+        const int64_t i = i0 + tid;
+        const int n = i < p.keys.tiles ? p.keys.first[i] : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_sum[warp] = x;
+        __syncthreads();
+        int below = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) {
+            below += w < warp ? warp_sum[w] : 0;
+            all += warp_sum[w];
+        }
+        const int at = carry + below + x - n;
+        if (i < p.keys.tiles) {
+            p.keys.first[i] = at;
+            for (int s = 0; s < n; ++s) p.keys.item[at + s] = make_int2((int)i, s);
+        }
+        carry += all;
+        __syncthreads();
+    }
+    if (tid == 0) p.keys.first[p.keys.tiles] = carry;
+}
+
+// The parts of a tile of several items, added in the items' order.
+template <typename T> __global__ void __launch_bounds__(256) k_keys_join(const BwdArgs p) {
+    constexpr int D = kKeysD, U = kKeysN * D / 8;
+    const BlkArgs &a = p.a;
+    const int64_t tile = blockIdx.x;
+    const int i0 = p.keys.first[tile], i1 = p.keys.first[tile + 1];
+    if (i1 - i0 == 1) return;
+    const int parts = a.block / kKeysN;
+    const int64_t blk_id = tile / parts;
+    const int key0 = (int)(blk_id % a.NB) * a.block + (int)(tile % parts) * kKeysN;
+    const int64_t b = blk_id / a.NB / a.Hk;
+    const int h = (int)(blk_id / a.NB % a.Hk);
+    for (int u = threadIdx.x; u < 2 * U; u += 256) {
+        const int w = u / U, key = u % U / (D / 8), d = u % (D / 8) * 8;
+        if (key0 + key >= a.Tk) continue;
+        float sum[8] = {};
+        for (int i = i0; i < i1; ++i) {
+            float x[8];
+            ld_pack<float, 8>(p.keys.part + (((int64_t)i * 2 + w) * kKeysN + key) * D + d, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += x[e];
+        }
+        st_pack<T, 8>((T *)(w ? p.dv : p.dk) + ((b * a.Tk + key0 + key) * a.Hk + h) * D + d, sum);
     }
 }
 
