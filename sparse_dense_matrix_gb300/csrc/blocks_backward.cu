@@ -464,6 +464,240 @@ __global__ void __launch_bounds__(32 * (W + 1), W == kDqLarge ? 1 : 2)
     }
 }
 
+// ------------------------------------------- dQ by tile of rows, on tensor memory
+// As the forward on tensor memory, for bf16 (fp16's dS needs its scale): 128 rows
+// against each block of their union, S = Q K^T and dP = dO V^T, dS by eight warps
+// (half a row's keys a thread), dQ += dS K with dS in tensor memory, twice over
+// as above. One CTA fills an SM: S and dP of a step run under the dS of the one
+// before.
+constexpr int kDqRows = 128, kDqKeys = 64, kDqThreads = 320;   // 8 + producer + issuer
+template <int D> using DqMmaSmem = TileSmem<D, kDqKeys, 8, 2, 227 * 1024>;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant__ DqTileArgs p) {
+    using S = DqMmaSmem<D>;
+    constexpr int KB = kDqKeys, C = D / 8, panel = kDqRows * 128, N = S::stages;
+    // tensor memory: two steps' S and dP, their dS (rounded, remainder), dQ
+    constexpr int kTmDp = 64, kTmStep = 128, kTmDs = 256, kTmDq = 384, columns = 512;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[N], empty[N], ready[2], made[2], done[2];
+    __shared__ TileStage<8> info[N];
+    __shared__ uint32_t tmem_slot, odd_rows[4];
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sq = smem + S::at_rows, sg = sq + S::rows;
+    const BlkArgs &a = p.t.a;
+    const TilePlace at(p.t, kDqRows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int len = blk_len(a, at.b);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < N; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ready[i], 2);
+            mbar_init(&made[i], 256);
+            mbar_init(&done[i], 1);
+        }
+        mbar_init_fence();
+    }
+    if (threadIdx.x < 4) odd_rows[threadIdx.x] = 0;
+    if (warp == 9) {
+        tmem_alloc(&tmem_slot, columns);
+        mma_fence_before();
+    }
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;     // of warps 0 to 7
+    if (warp < 8) {                                 // warps 0-3 fetch Q, 4-7 dO
+        int64_t f;
+        const bool live = at.row_of(p.t, len, row, f);
+        const int64_t mine = !live ? -1
+                             : half ? at.offset(p.t, f, p.do_sb, p.do_st, p.do_sh)
+                                    : at.offset(p.t, f, a.q_sb, a.q_st, a.q_sh);
+        const T *src = (const T *)(half ? p.dout : a.q);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int r = i * (32 / C) + lane / C, ch = lane % C;
+            const int64_t x = __shfl_sync(0xffffffffu, mine, r);
+            cp16((half ? sg : sq) + (ch >> 3) * panel + chunk_at((warp & 3) * 32 + r, ch & 7),
+                 src + (x < 0 ? 0 : x + ch * 8), x >= 0);
+        }
+        cp_commit();
+        cp_wait<0>();
+        fence_proxy_async_shared();
+    }
+    __syncthreads();
+    mma_fence_after();
+    const uint32_t tmem = tmem_slot;
+
+    if (warp == 8) {
+        tile_produce<S, D, KB, 8>(
+            p.t, at, smem, full, empty, info,
+            (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_lists));
+    } else if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t qk = instr_f16<T>(kDqRows, KB, false, false);
+            constexpr uint32_t sk = instr_f16<T>(kDqRows, D, false, true);
+            bool more = true, ok = true;
+            for (int j = 0; ok && more; ++j) {
+                const int st = j % N, before = (j + N - 1) % N;
+                bool a_left = true, b_left = j > 0;
+                const uint64_t t0 = global_ns();
+                for (uint32_t spin = 1; a_left || b_left; ++spin) {
+                    // S and dP take the columns that step j - 2's dS was made from,
+                    // and its dS those that step j's will: its product comes first
+                    if (a_left && mbar_test(&full[st], (j / N) & 1) &&
+                        (j < 2 || mbar_test(&done[j & 1], ((j - 2) >> 1) & 1))) {
+                        a_left = false;
+                        const int key0 = info[st].key0;
+                        more = key0 >= 0;
+                        mbar_arrive(&ready[j & 1]);  // of what the producer said
+                        if (more) {
+                            const uint32_t k = smem + st * S::stage, v = k + S::operand;
+                            if (key0 + KB > len) {   // keys past the length may be anything
+                                for (int i = (len - key0) * C; i < KB * C; ++i)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                     k + panel_at<KB>(i / C, i % C)),
+                                                 "r"(0)
+                                                 : "memory");
+                                fence_proxy_async_shared();
+                            }
+                            const uint32_t tm = tmem + (j & 1) * kTmStep;
+                            mma_fence_after();
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                const uint32_t r = (i >> 2) * panel + (i & 3) * 32;
+                                const uint32_t c = (i >> 2) * KB * 128 + (i & 3) * 32;
+                                mma_f16(tm, desc_k(sq + r), desc_k(k + c), qk, i > 0);
+                                mma_f16(tm + kTmDp, desc_k(sg + r), desc_k(v + c), qk, i > 0);
+                            }
+                            mma_commit(&ready[j & 1]);
+                        } else {
+                            mbar_arrive(&ready[j & 1]);
+                        }
+                    }
+                    if (b_left && mbar_test(&made[(j - 1) & 1], ((j - 1) >> 1) & 1)) {
+                        b_left = false;
+                        const uint32_t k = smem + before * S::stage;
+                        const uint32_t ds = tmem + kTmDs + ((j - 1) & 1) * KB;
+                        mma_fence_after();
+#pragma unroll
+                        for (int w = 0; w < 2; ++w)  // the rounded dS, then the remainder
+#pragma unroll
+                            for (int i = 0; i < KB / 16; ++i)
+                                mma_f16_ta(tmem + kTmDq, ds + w * 32 + i * 8,
+                                           desc_mn(k + i * 2048, KB * 128), sk,
+                                           j > 1 || w > 0 || i > 0);
+                        mma_commit(&empty[before]);
+                        mma_commit(&done[(j - 1) & 1]);
+                    }
+                    if (spin >= kSpinLimit || ((spin & 255) == 0 && global_ns() - t0 > kWaitLimitNs)) {
+                        ok = !a_left && !b_left;
+                        if (!ok) atomicOr(p.t.err + kErrTimeout, 1);
+                        break;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int64_t f = at.f0 + row;
+        const bool live = f < p.t.rows;
+        const int t = live ? (int)(f / a.G) : at.t_first;
+        const int limit = live ? blk_limit(a, len, t) : 0;
+        const int qi = t - at.t_first;
+        const int64_t o_row = at.out_row(p.t, live ? f : at.f0);
+        const float scale2 = a.scale * kLog2e;
+        float lse2 = live ? p.lse[o_row] * kLog2e : -INFINITY;
+        if (lse2 == -INFINITY) lse2 = INFINITY;      // a row without keys: P = 0
+        const float ds_off = live ? -p.delta[o_row] * a.scale : 0.0f;
+        int j = 0;
+        bool ok = true;
+        for (;; ++j) {
+            ok = mbar_wait_poll(&ready[j & 1], (j >> 1) & 1, p.t.err);
+            if (!ok) break;
+            mma_fence_after();
+            const TileStage<8> &step = info[j % N];
+            const int key0 = step.key0;
+            if (key0 < 0) break;
+            const bool mine = (step.mask[qi >> 5] >> (qi & 31) & 1u) && key0 < limit;
+            uint32_t hi[16], lo[16];
+            if (__any_sync(0xffffffffu, mine)) {
+                uint32_t s[32], dp[32];
+                tmem_ld32(tmem + lanes + (j & 1) * kTmStep + half * 32, s);
+                tmem_ld32(tmem + lanes + (j & 1) * kTmStep + kTmDp + half * 32, dp);
+                tmem_wait_ld();
+                const int seen = mine ? limit - key0 - half * 32 : 0;
+                const bool whole = __all_sync(0xffffffffu, seen >= 32);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float ds[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        ds[e] = ex2(fmaf(__uint_as_float(s[i + e]), scale2, -lse2)) *
+                                fmaf(__uint_as_float(dp[i + e]), a.scale, ds_off);
+                        if (!whole && i + e >= seen) ds[e] = 0.0f;
+                    }
+                    const uint32_t x = pack2<T>(ds[0], ds[1]);
+                    hi[i / 2] = x;
+                    lo[i / 2] = pack2<T>(ds[0] - __uint_as_float(x << 16),
+                                         ds[1] - __uint_as_float(x & 0xffff0000u));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) hi[i] = lo[i] = 0u;
+            }
+            const uint32_t to = tmem + lanes + kTmDs + (j & 1) * KB + half * 16;
+            tmem_st16(to, hi);
+            tmem_st16(to + 32, lo);
+            tmem_wait_st();
+            mma_fence_before();
+            mbar_arrive(&made[j & 1]);   // two: a warp may be a step ahead of another
+        }
+        if (ok && j > 0) mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.t.err);
+        mma_fence_after();
+        float odd = 0.0f;                            // NaN if anything is not finite
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {           // half of the row's elements
+            const int d = half * (D / 2) + 32 * i;
+            uint32_t o[32];
+            if (j > 0) {
+                tmem_ld32(tmem + lanes + kTmDq + d, o);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) odd = fmaf(__uint_as_float(o[e]), 0.0f, odd);
+            if (live) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int w = 0; w < 8; ++w) x[w] = __uint_as_float(o[e + w]);
+                    st_pack<T, 8>((T *)p.dq + o_row * D + d + e, x);
+                }
+            }
+        }
+        const unsigned bad = __ballot_sync(0xffffffffu, live && odd != 0.0f);
+        if (lane == 0 && bad) atomicOr(&odd_rows[warp & 3], bad);
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        for (int r = warp; r < kDqRows; r += 8) {
+            if (!(odd_rows[r >> 5] >> (r & 31) & 1u)) continue;
+            const int64_t g = at.f0 + r;
+            const int tt = (int)(g / a.G);
+            dq_row_alone<T, D>(p, at.b, at.h, tt, at.h * a.G + (int)(g - (int64_t)tt * a.G));
+        }
+        mma_fence_before();
+    }
+    __syncthreads();
+    if (warp == 9) {
+        mma_fence_after();
+        tmem_free(tmem, columns);
+    }
+}
+
 // ------------------------------------------------------------- dK and dV
 // A CTA per (tile of KT = 16 W keys of one block, kv head, sequence, range of
 // queries), a warp per 16 keys. The range's words are expanded to a list of
@@ -805,7 +1039,7 @@ template <typename T> cudaError_t launch_keys(BwdArgs &p, const BwdPlan &bp, cud
     k_key_counts<<<(unsigned)((blocks + 7) / 8), 256, 0, s>>>(p);
     k_key_items<<<1, 1024, 0, s>>>(p);
     k_dkdv_keys<T><<<(unsigned)bp.items, kKeysThreads, kKeysSmem, s>>>(p);
-    k_keys_join<T><<<(unsigned)bp.tiles, 256, 0, s>>>(p);
+    k_keys_join<T><<<dim3((unsigned)bp.tiles, 8), 256, 0, s>>>(p);
     count_launch(4);
     return cudaGetLastError();
 }
@@ -823,8 +1057,22 @@ cudaError_t launch_dq_tile(DqTileArgs &p, int64_t B, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, int D> cudaError_t launch_dq_mma(DqTileArgs &p, int64_t B, cudaStream_t s) {
+    constexpr int bytes = DqMmaSmem<D>::bytes;
+    const cudaError_t e = cudaFuncSetAttribute(
+        k_dq_mma<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    p.t.tiles = (int)((p.t.rows + kDqRows - 1) / kDqRows);
+    k_dq_mma<T, D><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), kDqThreads, bytes, s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
 template <typename T, int D>
 cudaError_t launch_dq_tile(DqTileArgs &p, bool large, int64_t B, cudaStream_t s) {
+    if constexpr (!kNarrow<T>) {
+        if (p.t.a.block % kDqKeys == 0) return launch_dq_mma<T, D>(p, B, s);
+    }
     if (large) {
         if (p.t.a.block == 16) return launch_dq_tile<T, D, 16, kDqLarge>(p, B, s);
         if (p.t.a.block == 32) return launch_dq_tile<T, D, 32, kDqLarge>(p, B, s);

@@ -459,7 +459,7 @@ template <typename T> __global__ void __launch_bounds__(256) k_keys_join(const B
     const int key0 = (int)(blk_id % a.NB) * a.block + (int)(tile % parts) * kKeysN;
     const int64_t b = blk_id / a.NB / a.Hk;
     const int h = (int)(blk_id / a.NB % a.Hk);
-    for (int u = threadIdx.x; u < 2 * U; u += 256) {
+    for (int u = blockIdx.y * 256 + threadIdx.x; u < 2 * U; u += 256 * gridDim.y) {
         const int w = u / U, key = u % U / (D / 8), d = u % (D / 8) * 8;
         if (key0 + key >= a.Tk) continue;
         float sum[8] = {};
