@@ -57,7 +57,6 @@ struct SelArgs {
     int64_t rows;            // B Tq Hk
     const float *means;
     float *score;            // [rows, NB]
-    float *qs;               // [B, Hk, Tq, D], the groups' sums (tiled scores only)
     int32_t *out;
 };
 
@@ -113,68 +112,69 @@ __global__ void __launch_bounds__(128) k_score_few(SelArgs s) {
             if (c0 + i < cand) s.score[row * a.NB + c0 + i] = dot[i];
 }
 
-// Many queries: the groups' sums once, then 64 x 64 tiles of their product with
-// the means, fp32 throughout (the list that a query gets must not depend on the
-// rounding of a 16-bit product).
-template <typename T>
-__global__ void __launch_bounds__(256) k_group_sum(SelArgs s) {
-    const BlkArgs &a = s.a;
-    const int units = s.D / 8;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= s.rows * units) return;
-    const int u = (int)(i % units);
-    const int64_t row = i / units;               // (b, h, t)
-    const int t = (int)(row % a.Tq);
-    const int64_t bh = row / a.Tq;
-    const int h = (int)(bh % a.Hk), b = (int)(bh / a.Hk);
-    const T *p = (const T *)a.q + b * a.q_sb + t * a.q_st + (int64_t)h * a.G * a.q_sh + u * 8;
-    float q[8] = {};
-    for (int g = 0; g < a.G; ++g) {
-        float x[8];
-        ld_pack<T, 8>(p + g * a.q_sh, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] += x[e];
-    }
-    st_pack<float, 8>(s.qs + row * s.D + u * 8, q);
-}
+// Many queries: 64 x 128 tiles of the groups' sums times the means, fp32
+// throughout (the list that a query gets must not depend on the rounding of a
+// 16-bit product). The heads of a group are added as their rows are loaded, again
+// for every 128 blocks: a quarter of the tile's arithmetic at 8 heads, and cheaper
+// than a launch that writes the sums (20 us at 8192 x 32 heads of 128).
+constexpr int kSt = 64, kSc = 128;      // tile of queries and of blocks
+constexpr int kSk = 32;                 // depth of one step
 
-constexpr int kSt = 64;      // tile of queries and of blocks
-constexpr int kSk = 32;      // depth of one step
-
-__global__ void __launch_bounds__(256) k_score_tiles(SelArgs s) {
-    __shared__ float qt[kSk][kSt + 4], mt[kSk][kSt + 4];
+template <typename T> __global__ void __launch_bounds__(256) k_score_tiles(SelArgs s) {
+    __shared__ float qt[kSk][kSt + 4], mt[kSk][kSc + 4];
     const BlkArgs &a = s.a;
     const int bh = blockIdx.z, b = bh / a.Hk, h = bh % a.Hk;
-    const int t0 = blockIdx.y * kSt, c0 = blockIdx.x * kSt;
+    const int t0 = blockIdx.y * kSt, c0 = blockIdx.x * kSc;
     int own;
     if (c0 >= candidates(a, b, min(t0 + kSt, a.Tq) - 1, &own)) return;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
+    const int qr = threadIdx.x / 4, qd = threadIdx.x % 4 * 8;     // row and elements it loads
+    const T *qp = (const T *)a.q + b * a.q_sb + min(t0 + qr, a.Tq - 1) * a.q_st +
+                  (int64_t)h * a.G * a.q_sh + qd;
+    float acc[4][8] = {};
     for (int d0 = 0; d0 < s.D; d0 += kSk) {
-        for (int i = threadIdx.x; i < kSt * kSk / 4; i += 256) {
-            const int r = i / (kSk / 4), d = i % (kSk / 4) * 4;
-            float4 x = make_float4(0, 0, 0, 0), y = x;
-            if (d0 + d < s.D) {
-                if (t0 + r < a.Tq)
-                    x = *(const float4 *)(s.qs + ((int64_t)bh * a.Tq + t0 + r) * s.D + d0 + d);
-                if (c0 + r < a.NB)
-                    y = *(const float4 *)(s.means +
-                                          (((int64_t)b * a.NB + c0 + r) * a.Hk + h) * s.D + d0 + d);
+        float q[8] = {};
+        if (d0 + qd < s.D) {
+#pragma unroll 4
+            for (int g = 0; g < a.G; ++g) {
+                float x[8];
+                ld_pack<T, 8>(qp + g * a.q_sh + d0, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q[e] += x[e];
             }
-            qt[d][r] = x.x; qt[d + 1][r] = x.y; qt[d + 2][r] = x.z; qt[d + 3][r] = x.w;
-            mt[d][r] = y.x; mt[d + 1][r] = y.y; mt[d + 2][r] = y.z; mt[d + 3][r] = y.w;
+        }
+        float4 m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (threadIdx.x + 256 * i) / 8, d = threadIdx.x % 8 * 4;
+            m[i] = make_float4(0, 0, 0, 0);
+            if (d0 + d < s.D && c0 + r < a.NB)
+                m[i] = *(const float4 *)(s.means +
+                                         (((int64_t)b * a.NB + c0 + r) * a.Hk + h) * s.D + d0 + d);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qt[qd + e][qr] = q[e];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (threadIdx.x + 256 * i) / 8, d = threadIdx.x % 8 * 4;
+            mt[d][r] = m[i].x;
+            mt[d + 1][r] = m[i].y;
+            mt[d + 2][r] = m[i].z;
+            mt[d + 3][r] = m[i].w;
         }
         __syncthreads();
 #pragma unroll
         for (int d = 0; d < kSk; ++d) {
-            const float4 x = *(const float4 *)&qt[d][ty * 4], y = *(const float4 *)&mt[d][tx * 4];
-            const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            const float4 x = *(const float4 *)&qt[d][ty * 4];
+            const float4 y = *(const float4 *)&mt[d][tx * 4], z = *(const float4 *)&mt[d][64 + tx * 4];
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+            const float ys[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
+                for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(xs[i], ys[j], acc[i][j]);
         }
-        __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -182,8 +182,10 @@ __global__ void __launch_bounds__(256) k_score_tiles(SelArgs s) {
         if (t >= a.Tq) continue;
         float *p = s.score + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.NB;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c0 + tx * 4 + j < a.NB) p[c0 + tx * 4 + j] = acc[i][j];
+        for (int j = 0; j < 8; ++j) {
+            const int c = c0 + (j >> 2) * 64 + tx * 4 + (j & 3);
+            if (c < a.NB) p[c] = acc[i][j];
+        }
     }
 }
 
@@ -391,12 +393,10 @@ cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t 
         k_score_few<T><<<dim3((unsigned)((a.NB + 31) / 32), (unsigned)s.rows), 128, 0, st>>>(s);
         count_launch();
     } else {
-        const int64_t n = s.rows * (s.D / 8);
-        k_group_sum<T><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(s);
-        k_score_tiles<<<dim3((unsigned)((a.NB + kSt - 1) / kSt), (unsigned)((a.Tq + kSt - 1) / kSt),
-                             (unsigned)(B * a.Hk)),
-                        256, 0, st>>>(s);
-        count_launch(2);
+        k_score_tiles<T><<<dim3((unsigned)((a.NB + kSc - 1) / kSc),
+                                (unsigned)((a.Tq + kSt - 1) / kSt), (unsigned)(B * a.Hk)),
+                           256, 0, st>>>(s);
+        count_launch();
     }
     return cudaGetLastError();
 }
@@ -457,7 +457,7 @@ int64_t spmm_blocks_select_workspace(const spmm_blocks_shape *s) {
     using namespace spmm;
     if (blk_check(s, false) != SPMM_OK || by_row(s)) return 0;
     const int64_t NB = (s->Tk + s->block - 1) / s->block, rows = s->B * s->Tq * s->Hk;
-    return round_up(rows * NB * 4, 16) + (tiled(s) ? rows * s->D * 4 : 0);
+    return rows * NB * 4;
 }
 
 spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const float *means,
@@ -479,7 +479,6 @@ spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const fl
     g.rows = s->B * s->Tq * s->Hk;
     g.means = means;
     g.score = (float *)work;
-    g.qs = (float *)((char *)work + round_up(g.rows * g.a.NB * 4, 16));
     g.out = blocks;
     cudaStream_t cs = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
