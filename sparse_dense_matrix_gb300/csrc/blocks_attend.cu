@@ -507,7 +507,8 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
     // K and V have a ring each: a step's K is read by its S alone, and the K of a
     // later step comes in its place while the step's P is still being made
     constexpr int N = S::stages;
-    __shared__ uint64_t k_full[N], k_empty[N], v_full[N], v_empty[N], ready[2], made[2], done[2];
+    // (S done: ready, which is also when its K may go; P V done: done, and its V)
+    __shared__ uint64_t k_full[N], v_full[N], ready[N], done[N], made[2];
     __shared__ TileStage<8> info[N + 2];             // alive from a step's K to its P
     __shared__ uint32_t tmem_slot;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -518,16 +519,12 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
     if (threadIdx.x == 0) {
         for (int i = 0; i < N; ++i) {
             mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
             mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
+            mbar_init(&ready[i], 2);
+            mbar_init(&done[i], 1);
         }
-        mbar_init(&ready[0], 2);
-        mbar_init(&ready[1], 2);
         mbar_init(&made[0], kMmaRows);
         mbar_init(&made[1], kMmaRows);
-        mbar_init(&done[0], 1);
-        mbar_init(&done[1], 1);
         mbar_init_fence();
     }
     if (warp == 5) {
@@ -564,7 +561,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
         auto bring_v = [&]() {                       // V of step j - 1
             if (v_key0 < 0) return;
             const int st = (j - 1) % N;
-            ok = mbar_wait_poll(&v_empty[st], (((j - 1) / N) & 1) ^ 1, p.t.err);
+            ok = mbar_wait_poll(&done[st], (((j - 1) / N) & 1) ^ 1, p.t.err);
             if (ok && lane == 0) {
                 mbar_arrive_expect_tx(&v_full[st], S::operand);
 #pragma unroll
@@ -582,7 +579,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                 const int key0 = last ? -1 : least * a.block + s * KB;
                 if (key0 >= a.Tk) break;             // the second half of a last, short block
                 const int st = j % N;
-                ok = mbar_wait_poll(&k_empty[st], ((j / N) & 1) ^ 1, p.t.err);
+                ok = mbar_wait_poll(&ready[st], ((j / N) & 1) ^ 1, p.t.err);
                 if (!ok) break;
                 if (lane == 0) {
                     TileStage<8> &x = info[j % (N + 2)];
@@ -629,11 +626,11 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                 const uint64_t t0 = global_ns();
                 for (uint32_t spin = 1; a_left || b_left; ++spin) {
                     if (a_left && mbar_test(&k_full[st], (j / N) & 1) &&
-                        (j < 2 || mbar_test(&done[j & 1], ((j - 2) >> 1) & 1))) {
+                        (j < 2 || mbar_test(&done[(j - 2) % N], ((j - 2) / N) & 1))) {
                         a_left = false;
                         key0 = info[j % (N + 2)].key0;
                         more = key0 >= 0;
-                        mbar_arrive(&ready[j & 1]);  // of what the bringing warp said
+                        mbar_arrive(&ready[st]);  // of what the bringing warp said
                         if (more) {
                             const uint32_t k = sk + st * S::operand;
                             mma_fence_after();
@@ -642,10 +639,9 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                                 mma_f16(tmem + (j & 1) * KB,
                                         desc_k(smem + S::at_rows + (i >> 2) * panel + (i & 3) * 32),
                                         desc_k(k + (i >> 2) * KB * 128 + (i & 3) * 32), qk, i > 0);
-                            mma_commit(&ready[j & 1]);
-                            mma_commit(&k_empty[st]);
+                            mma_commit(&ready[st]);
                         } else {
-                            mbar_arrive(&ready[j & 1]);
+                            mbar_arrive(&ready[st]);
                         }
                     }
                     if (b_left && mbar_test(&made[(j - 1) & 1], ((j - 1) >> 1) & 1) &&
@@ -665,8 +661,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                         for (int i = 0; i < KB / 16; ++i)
                             mma_f16_ta(tmem + kTmO, tmem + ((j - 1) & 1) * KB + i * 8,
                                        desc_mn(v + i * 2048, KB * 128), pv, j > 1 || i > 0);
-                        mma_commit(&v_empty[before]);
-                        mma_commit(&done[(j - 1) & 1]);
+                        mma_commit(&done[before]);
                     }
                     if (spin >= kSpinLimit || ((spin & 255) == 0 && global_ns() - t0 > kWaitLimitNs)) {
                         ok = !a_left && !b_left;
@@ -690,7 +685,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
         int j = 0;
         bool ok = true;
         for (;; ++j) {
-            ok = mbar_wait_poll(&ready[j & 1], (j >> 1) & 1, p.t.err);
+            ok = mbar_wait_poll(&ready[j % N], (j / N) & 1, p.t.err);
             if (!ok) break;
             mma_fence_after();
             const TileStage<8> &step = info[j % (N + 2)];
@@ -723,7 +718,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                     m = mx;
                 }
                 if (j > 0 && __any_sync(0xffffffffu, corr != 1.0f)) {
-                    ok = mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.t.err);
+                    ok = mbar_wait_poll(&done[(j - 1) % N], ((j - 1) / N) & 1, p.t.err);
                     if (!ok) break;
                     mma_fence_after();
 #pragma unroll
@@ -757,7 +752,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
             mma_fence_before();
             mbar_arrive(&made[j & 1]);   // two: a warp may be a step ahead of another
         }
-        if (ok && j > 0) mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.t.err);
+        if (ok && j > 0) mbar_wait_poll(&done[(j - 1) % N], ((j - 1) / N) & 1, p.t.err);
         mma_fence_after();
         float odd = l * 0.0f;                        // NaN if anything is not finite
         const float inv = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;

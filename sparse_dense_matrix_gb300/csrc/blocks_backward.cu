@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
     // tensor memory: two steps' S and dP, their dS (rounded, remainder), dQ
     constexpr int kTmDp = 64, kTmStep = 128, kTmDs = 256, kTmDq = 384, columns = 512;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t full[N], empty[N], ready[2], made[2], done[2];
+    __shared__ uint64_t full[N], ready[2], made[2], done[N];   // done: dQ, and the stage is free
     __shared__ TileStage<8> info[N];
     __shared__ uint32_t tmem_slot, odd_rows[4];
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -492,12 +492,11 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
     if (threadIdx.x == 0) {
         for (int i = 0; i < N; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ready[i], 2);
             mbar_init(&made[i], 256);
-            mbar_init(&done[i], 1);
         }
         mbar_init_fence();
     }
@@ -531,7 +530,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
 
     if (warp == 8) {
         tile_produce<S, D, KB, 8>(
-            p.t, at, smem, full, empty, info,
+            p.t, at, smem, full, done, info,
             (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_lists));
     } else if (warp == 9) {
         if (lane == 0) {
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
                     // S and dP take the columns that step j - 2's dS was made from,
                     // and its dS those that step j's will: its product comes first
                     if (a_left && mbar_test(&full[st], (j / N) & 1) &&
-                        (j < 2 || mbar_test(&done[j & 1], ((j - 2) >> 1) & 1))) {
+                        (j < 2 || mbar_test(&done[(j - 2) % N], ((j - 2) / N) & 1))) {
                         a_left = false;
                         const int key0 = info[st].key0;
                         more = key0 >= 0;
@@ -587,8 +586,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
                                 mma_f16_ta(tmem + kTmDq, ds + w * 32 + i * 8,
                                            desc_mn(k + i * 2048, KB * 128), sk,
                                            j > 1 || w > 0 || i > 0);
-                        mma_commit(&empty[before]);
-                        mma_commit(&done[(j - 1) & 1]);
+                        mma_commit(&done[before]);
                     }
                     if (spin >= kSpinLimit || ((spin & 255) == 0 && global_ns() - t0 > kWaitLimitNs)) {
                         ok = !a_left && !b_left;
@@ -654,7 +652,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
             mma_fence_before();
             mbar_arrive(&made[j & 1]);   // two: a warp may be a step ahead of another
         }
-        if (ok && j > 0) mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.t.err);
+        if (ok && j > 0) mbar_wait_poll(&done[(j - 1) % N], ((j - 1) / N) & 1, p.t.err);
         mma_fence_after();
         float odd = 0.0f;                            // NaN if anything is not finite
 #pragma unroll
