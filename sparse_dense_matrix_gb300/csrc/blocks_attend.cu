@@ -305,18 +305,18 @@ __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, in
     st_pack<T, E>((T *)p.out + row * D + lane * E, o);
 }
 
-// Variants: kLargeWarps consumer warps take the whole SM (11 and the producer
-// are three per quarter of it, which leaves each 168 registers); kSmallWarps
-// leave room for two CTAs, for problems with too few rows to give every SM two
-// large tiles.
-constexpr int kLargeWarps = 11, kSmallWarps = 4;
-template <int D, int KB, int W>
-using AttendSmem = TileSmem<D, KB, W, 1, (W == kLargeWarps ? 227 : 113) * 1024>;
+// For blocks of 16 and 32 keys; the longer ones go to k_attend_mma. Four consumer
+// warps a CTA, two CTAs to an SM: the consumers wait for one another over the
+// ring, and the other CTA's work while they do (one CTA of 11 warps took 300 us for
+// 277 at 2 x 4096 queries x 4 heads of 64 x 4, and 39 for 28 at 4 x 777).
+constexpr int kTileWarps = 4;
+template <int D, int KB> using AttendSmem = TileSmem<D, KB, kTileWarps, 1, 113 * 1024>;
 
-template <typename T, int D, int KB, int W>
-__global__ void __launch_bounds__(32 * (W + 1), W == kLargeWarps ? 1 : 2)
+template <typename T, int D, int KB>
+__global__ void __launch_bounds__(32 * (kTileWarps + 1), 2)
     k_attend_tile(const __grid_constant__ AttendTileArgs p) {
-    using S = AttendSmem<D, KB, W>;
+    constexpr int W = kTileWarps;
+    using S = AttendSmem<D, KB>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[S::stages], empty[S::stages];
     __shared__ TileStage<W> info[S::stages];
@@ -836,15 +836,15 @@ cudaError_t launch_rows(const RowArgs &p, const RowPlan &rp, cudaStream_t s) {
                       : cudaLaunchKernelEx(&cfg, k_attend_rows<T, D, 2>, p);
 }
 
-template <typename T, int D, int KB, int W>
+template <typename T, int D, int KB>
 cudaError_t launch_tile(AttendTileArgs &p, int64_t B, cudaStream_t s) {
-    constexpr int bytes = AttendSmem<D, KB, W>::bytes;
+    constexpr int bytes = AttendSmem<D, KB>::bytes;
     const cudaError_t e = cudaFuncSetAttribute(
-        k_attend_tile<T, D, KB, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        k_attend_tile<T, D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    p.t.tiles = (int)((p.t.rows + 16 * W - 1) / (16 * W));
-    k_attend_tile<T, D, KB, W><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)),
-                                 32 * (W + 1), bytes, s>>>(p);
+    p.t.tiles = (int)((p.t.rows + 16 * kTileWarps - 1) / (16 * kTileWarps));
+    k_attend_tile<T, D, KB><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)),
+                              32 * (kTileWarps + 1), bytes, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
@@ -862,17 +862,15 @@ template <typename T, int D> cudaError_t launch_mma(AttendTileArgs &p, int64_t B
 }
 
 template <typename T, int D>
-cudaError_t launch_tile(AttendTileArgs &p, bool large, int64_t B, cudaStream_t s) {
-    // on tensor memory: blocks of whole 64-key steps, and a scale that keeps the order
-    if (p.t.a.block % kMmaKeys == 0 && p.t.a.scale > 0.0f) return launch_mma<T, D>(p, B, s);
-    if (large) {
-        if (p.t.a.block == 16) return launch_tile<T, D, 16, kLargeWarps>(p, B, s);
-        if (p.t.a.block == 32) return launch_tile<T, D, 32, kLargeWarps>(p, B, s);
-        return launch_tile<T, D, 64, kLargeWarps>(p, B, s);
-    }
-    if (p.t.a.block == 16) return launch_tile<T, D, 16, kSmallWarps>(p, B, s);
-    if (p.t.a.block == 32) return launch_tile<T, D, 32, kSmallWarps>(p, B, s);
-    return launch_tile<T, D, 64, kSmallWarps>(p, B, s);
+cudaError_t launch_by_tile(AttendTileArgs &p, int64_t B, cudaStream_t s) {
+    if (p.t.a.block == 16) return launch_tile<T, D, 16>(p, B, s);
+    if (p.t.a.block == 32) return launch_tile<T, D, 32>(p, B, s);
+    return launch_mma<T, D>(p, B, s);
+}
+
+// k_attend_mma takes its maxima before the scale: a scale above 0 only.
+bool by_tile(const spmm_blocks_shape *s) {
+    return blocks_by_tile(s) && (s->block < kMmaKeys || s->scale > 0.0f);
 }
 
 }  // namespace
@@ -943,7 +941,7 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
     set_rows(p.a.q, p.a.q_sb, p.a.q_st, p.a.q_sh, q);
     set_rows(p.a.k, p.a.k_sb, p.a.k_st, p.a.k_sh, k);
     set_rows(p.a.v, p.a.v_sb, p.a.v_st, p.a.v_sh, v);
-    if (blocks_by_tile(s)) {
+    if (by_tile(s)) {
         AttendTileArgs t{};
         t.t.a = p.a;
         t.t.rows = s->Tq * p.a.G;
@@ -955,11 +953,11 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
         if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
         if (e == cudaSuccess) {
             if (s->dtype == SPMM_BF16)
-                e = s->D == 64 ? launch_tile<__nv_bfloat16, 64>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs)
-                               : launch_tile<__nv_bfloat16, 128>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs);
+                e = s->D == 64 ? launch_by_tile<__nv_bfloat16, 64>(t, s->B, cs)
+                               : launch_by_tile<__nv_bfloat16, 128>(t, s->B, cs);
             else
-                e = s->D == 64 ? launch_tile<__half, 64>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs)
-                               : launch_tile<__half, 128>(t, blocks_large_tiles(s, 16 * kLargeWarps), s->B, cs);
+                e = s->D == 64 ? launch_by_tile<__half, 64>(t, s->B, cs)
+                               : launch_by_tile<__half, 128>(t, s->B, cs);
         }
         return cuda_status(e);
     }

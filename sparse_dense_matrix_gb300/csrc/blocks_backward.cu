@@ -283,18 +283,18 @@ __device__ __noinline__ void dq_row_alone(const DqTileArgs &p, int b, int h, int
     st_pack<T, E>((T *)p.dq + row * D + lane * E, o);
 }
 
-constexpr int kDqLarge = 8, kDqSmall = 4;
-template <int D, int KB, int W>
-using DqSmem = TileSmem<D, KB, W, 2, (W == kDqLarge ? 227 : 113) * 1024>;
+constexpr int kDqWarps = 4;          // consumers; two CTAs to an SM
+template <int D, int KB> using DqSmem = TileSmem<D, KB, kDqWarps, 2, 113 * 1024>;
 
 // dS is used twice over in bf16, as its rounded value plus what that left out:
 // the rows of dS sum to 0, so dQ = dS K is what remains after the keys' common
 // part cancels, and one rounding of dS to 8 bits would show in it (error 1.5
 // times that of rounding dQ alone; 1.27 times with both parts).
-template <typename T, int D, int KB, int W>
-__global__ void __launch_bounds__(32 * (W + 1), W == kDqLarge ? 1 : 2)
+template <typename T, int D, int KB>
+__global__ void __launch_bounds__(32 * (kDqWarps + 1), 2)
     k_dq_tile(const __grid_constant__ DqTileArgs p) {
-    using S = DqSmem<D, KB, W>;
+    constexpr int W = kDqWarps;
+    using S = DqSmem<D, KB>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[S::stages], empty[S::stages];
     __shared__ TileStage<W> info[S::stages];
@@ -1042,15 +1042,15 @@ template <typename T> cudaError_t launch_keys(BwdArgs &p, const BwdPlan &bp, cud
     return cudaGetLastError();
 }
 
-template <typename T, int D, int KB, int W>
+template <typename T, int D, int KB>
 cudaError_t launch_dq_tile(DqTileArgs &p, int64_t B, cudaStream_t s) {
-    constexpr int bytes = DqSmem<D, KB, W>::bytes;
+    constexpr int bytes = DqSmem<D, KB>::bytes;
     const cudaError_t e = cudaFuncSetAttribute(
-        k_dq_tile<T, D, KB, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        k_dq_tile<T, D, KB>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    p.t.tiles = (int)((p.t.rows + 16 * W - 1) / (16 * W));
-    k_dq_tile<T, D, KB, W><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), 32 * (W + 1),
-                             bytes, s>>>(p);
+    p.t.tiles = (int)((p.t.rows + 16 * kDqWarps - 1) / (16 * kDqWarps));
+    k_dq_tile<T, D, KB><<<dim3((unsigned)p.t.tiles, (unsigned)(B * p.t.a.Hk)), 32 * (kDqWarps + 1),
+                          bytes, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
@@ -1067,18 +1067,11 @@ template <typename T, int D> cudaError_t launch_dq_mma(DqTileArgs &p, int64_t B,
 }
 
 template <typename T, int D>
-cudaError_t launch_dq_tile(DqTileArgs &p, bool large, int64_t B, cudaStream_t s) {
-    if constexpr (!kNarrow<T>) {
-        if (p.t.a.block % kDqKeys == 0) return launch_dq_mma<T, D>(p, B, s);
-    }
-    if (large) {
-        if (p.t.a.block == 16) return launch_dq_tile<T, D, 16, kDqLarge>(p, B, s);
-        if (p.t.a.block == 32) return launch_dq_tile<T, D, 32, kDqLarge>(p, B, s);
-        return launch_dq_tile<T, D, 64, kDqLarge>(p, B, s);
-    }
-    if (p.t.a.block == 16) return launch_dq_tile<T, D, 16, kDqSmall>(p, B, s);
-    if (p.t.a.block == 32) return launch_dq_tile<T, D, 32, kDqSmall>(p, B, s);
-    return launch_dq_tile<T, D, 64, kDqSmall>(p, B, s);
+cudaError_t launch_dq_by_tile(DqTileArgs &p, int64_t B, cudaStream_t s) {
+    if (p.t.a.block == 16) return launch_dq_tile<T, D, 16>(p, B, s);
+    if (p.t.a.block == 32) return launch_dq_tile<T, D, 32>(p, B, s);
+    if constexpr (kNarrow<T>) return launch_dq_tile<T, D, 64>(p, B, s);
+    else return launch_dq_mma<T, D>(p, B, s);
 }
 
 template <typename T, int D>
@@ -1105,7 +1098,7 @@ cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s
         if (e == cudaSuccess) e = encode_rows(k, s, box, &t.t.k_map);
         if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
         if (e == cudaSuccess)
-            e = launch_dq_tile<T, D>(t, blocks_large_tiles(s, 16 * kDqLarge), s->B, cs);
+            e = launch_dq_by_tile<T, D>(t, s->B, cs);
     } else {
         if (p.a.G <= 8) {
             p.gt = 1;

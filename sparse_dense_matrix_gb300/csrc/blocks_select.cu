@@ -382,9 +382,22 @@ __global__ void k_check_lists(BlkArgs a, int64_t rows, int32_t *bad) {
 __global__ void k_zero_word(int32_t *p) { *p = 0; }
 
 // ------------------------------------------------------------------- host
-// From this many queries on, 64-query tiles read each mean once per tile instead
-// of once per query; below it the tile's unused rows cost more.
-constexpr int64_t kTiledQueries = 24;
+// A CTA per row (one launch, scores in shared memory) up to 1024 rows of at most
+// 1024 blocks, and for fewer than 24 queries a sequence, of which a tile of 64
+// would be mostly empty; else tiles, then a warp per row. By row against by tile:
+// 1024 rows (256 queries x 4 heads) of 128 blocks 17 and 26 us, 2048 rows (256 x 8)
+// 20 and 18, 16384 rows (2048 x 8) 42 and 36, 32768 rows (2 x 4096 x 4) 77 and 50.
+// Longer rows of few queries: a warp per 8 blocks, then a warp per row.
+constexpr int64_t kTiledQueries = 24, kTiledRows = 1024, kRowBlocks = 1024;
+
+bool tiled(const spmm_blocks_shape *s) {
+    const int64_t rows = s->B * s->Tq * s->Hk;
+    if (s->Tk <= kRowBlocks * s->block) return s->Tq >= kTiledQueries && rows > kTiledRows;
+    return s->Tq >= kTiledQueries || rows > 65535;
+}
+bool by_row(const spmm_blocks_shape *s) {
+    return s->Tk <= kRowBlocks * s->block && !tiled(s);
+}
 
 template <typename T>
 cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t st) {
@@ -401,9 +414,6 @@ cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t 
     return cudaGetLastError();
 }
 
-// Up to this many blocks a row's scores stay in its CTA.
-constexpr int64_t kRowBlocks = 1024;
-
 template <typename T, int R> void launch_select_row(const SelArgs &s, int threads, cudaStream_t st) {
     if (s.D <= 64) k_select_row<T, R, 8><<<(unsigned)s.rows, threads, 0, st>>>(s);
     else if (s.D <= 128) k_select_row<T, R, 16><<<(unsigned)s.rows, threads, 0, st>>>(s);
@@ -416,13 +426,6 @@ template <typename T> cudaError_t launch_select_row(const SelArgs &s, cudaStream
     else if (s.a.NB <= 512) launch_select_row<T, 16>(s, 512, st);
     else launch_select_row<T, 32>(s, 512, st);
     return cudaGetLastError();
-}
-
-bool tiled(const spmm_blocks_shape *s) {
-    return s->Tq >= kTiledQueries || s->B * s->Tq * s->Hk > 65535;
-}
-bool by_row(const spmm_blocks_shape *s) {
-    return !tiled(s) && s->Tk <= kRowBlocks * s->block;
 }
 
 }  // namespace

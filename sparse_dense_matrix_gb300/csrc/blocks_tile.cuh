@@ -259,12 +259,29 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const T *p, bool live, 
 cudaError_t encode_rows(const spmm_rows &r, const spmm_blocks_shape *s, int box_rows,
                         CUtensorMap *map);
 
-// By tile from 128 rows a kv head on; large tiles when they give every SM two.
+// By query or by tile: the smaller of two estimates, in microseconds.
+// By query, a list costs 12 ns and 0.31 ns per 1000 elements of its keys (on all
+// SMs together). By tile, a CTA walks the union of its queries' lists, of which
+// neighbours share what they share, at worst all blocks, at 1 us a step, two CTAs
+// to an SM. Either takes some 8 us around that. Measured with lists that share
+// nothing, by query against by tile: 16 queries x 8 heads x 4 over a cache of
+// 8192 keys (16 of 64-key blocks, heads of 128) 17 and 112 us, 256 of them 93 and
+// 116; 4 x 777 queries, one head each, 7 of 32-key blocks 190 and 27; 3 x 333
+// queries x 3 heads 71 and 41; 2048 queries x 4 heads x 8, 16 of 32-key blocks
+// 622 and 133.
+constexpr int kTileRows = 128;       // of the tensor-memory kernels; the others' are 64
+
 inline bool blocks_by_tile(const spmm_blocks_shape *s) {
-    return s->Tk > 0 && s->Tq * (s->Hq / s->Hk) >= 128 && s->B * s->Hk <= 65535;
-}
-inline bool blocks_large_tiles(const spmm_blocks_shape *s, int tile_rows) {
-    return s->B * s->Hk * (s->Tq * (s->Hq / s->Hk) / tile_rows) >= 2 * 152;
+    if (s->Tk == 0 || s->B * s->Hk > 65535) return false;
+    const int64_t G = s->Hq / s->Hk, parts = s->block > 64 ? s->block / 64 : 1;
+    const int64_t NB = (s->Tk + s->block - 1) / s->block;
+    const int64_t tiles = s->B * s->Hk * ((s->Tq * G + kTileRows - 1) / kTileRows);
+    const int64_t queries = std::min<int64_t>(s->Tq, (kTileRows + G - 1) / G + 1);
+    const int64_t steps = parts * std::min<int64_t>(NB, queries * std::min<int64_t>(s->n, NB));
+    const double tile_us = (double)steps * (double)((tiles + 303) / 304);
+    const double lists = (double)s->B * s->Tq * s->Hk * ((G + 15) / 16);
+    const double keys = (double)std::min<int64_t>(s->n * s->block, s->Tk);
+    return tile_us < lists * (0.012 + keys * s->D * 0.31e-6);
 }
 
 // Device word that a bounded wait which gave up sets (spmm_dynamic_sync reads it).
