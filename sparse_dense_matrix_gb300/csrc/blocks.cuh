@@ -64,6 +64,19 @@ template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float 
     }
 }
 
+// Two values as the pair of their rounded parts and the pair of what that left out
+// (itself rounded): together 16 bits and more of each.
+template <typename T>
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = pack2<T>(x, y);
+    if constexpr (std::is_same<T, __half>::value) {
+        const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        lo = pack2<T>(x - r.x, y - r.y);
+    } else {
+        lo = pack2<T>(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u));
+    }
+}
+
 // Transpose of an 8x8 matrix of 16-bit elements held two adjacent ones per lane.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     uint32_t y;

@@ -869,8 +869,8 @@ cudaError_t launch_by_tile(AttendTileArgs &p, int64_t B, cudaStream_t s) {
 }
 
 // k_attend_mma takes its maxima before the scale: a scale above 0 only.
-bool by_tile(const spmm_blocks_shape *s) {
-    return blocks_by_tile(s) && (s->block < kMmaKeys || s->scale > 0.0f);
+bool by_tile(const spmm_blocks_shape *s, const spmm_rows &k, const spmm_rows &v) {
+    return blocks_by_tile(s, k, v) && (s->block < kMmaKeys || s->scale > 0.0f);
 }
 
 }  // namespace
@@ -941,7 +941,7 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
     set_rows(p.a.q, p.a.q_sb, p.a.q_st, p.a.q_sh, q);
     set_rows(p.a.k, p.a.k_sb, p.a.k_st, p.a.k_sh, k);
     set_rows(p.a.v, p.a.v_sb, p.a.v_st, p.a.v_sh, v);
-    if (by_tile(s)) {
+    if (by_tile(s, k, v)) {
         AttendTileArgs t{};
         t.t.a = p.a;
         t.t.rows = s->Tq * p.a.G;

@@ -53,6 +53,12 @@ __global__ void k_set_bits(BwdArgs p, int64_t entries) {
 // whenever a tile's largest |dS| would reach 2^15; both are exact powers of two,
 // taken out of the sums at the end. bf16 has fp32's exponent and needs neither.
 template <typename T> constexpr bool kNarrow = std::is_same<T, __half>::value;
+//
+// dS is used twice over, as its rounded value plus what that left out. The rows of
+// dS sum to 0, so dQ = dS K (and, to a degree, dK) is what remains after the keys'
+// common part cancels, and a single rounding of dS shows in it: the error was 1.7
+// times that of rounding dQ alone, and is 1.27 times with both parts (the rest is
+// delta's, from the rounded output).
 template <typename T> constexpr float kPShift = kNarrow<T> ? 14.0f : 0.0f;
 template <typename T> constexpr float kPUnit = kNarrow<T> ? 1.0f / 16384.0f : 1.0f;
 
@@ -198,15 +204,22 @@ __global__ void __launch_bounds__(kRowThreads) k_dq_rows(BwdArgs p) {
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            const uint32_t b0 = movmatrix(pack2<T>(st[i][0], st[i][1]));
-            const uint32_t b1 = movmatrix(pack2<T>(st[i][2], st[i][3]));
+            uint32_t h0, l0, h1, l1;
+            split2<T>(st[i][0], st[i][1], h0, l0);
+            split2<T>(st[i][2], st[i][3], h1, l1);
+            h0 = movmatrix(h0);
+            l0 = movmatrix(l0);
+            h1 = movmatrix(h1);
+            l1 = movmatrix(l1);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 const int u = d / 4, w = d % 4;
                 const uint32_t k0 = (&kt[u][0].x)[w], k1 = (&kt[u][1].x)[w];
                 const uint32_t k8 = (&kt[u][2].x)[w], k9 = (&kt[u][3].x)[w];
-                mma16816<T>(o[d][i], __byte_perm(k0, k1, 0x5410), __byte_perm(k0, k1, 0x7632),
-                            __byte_perm(k8, k9, 0x5410), __byte_perm(k8, k9, 0x7632), b0, b1);
+                const uint32_t a0 = __byte_perm(k0, k1, 0x5410), a1 = __byte_perm(k0, k1, 0x7632);
+                const uint32_t a2 = __byte_perm(k8, k9, 0x5410), a3 = __byte_perm(k8, k9, 0x7632);
+                mma16816<T>(o[d][i], a0, a1, a2, a3, h0, h1);
+                mma16816<T>(o[d][i], a0, a1, a2, a3, l0, l1);
             }
         }
     }
@@ -286,10 +299,6 @@ __device__ __noinline__ void dq_row_alone(const DqTileArgs &p, int b, int h, int
 constexpr int kDqWarps = 4;          // consumers; two CTAs to an SM
 template <int D, int KB> using DqSmem = TileSmem<D, KB, kDqWarps, 2, 113 * 1024>;
 
-// dS is used twice over in bf16, as its rounded value plus what that left out:
-// the rows of dS sum to 0, so dQ = dS K is what remains after the keys' common
-// part cancels, and one rounding of dS to 8 bits would show in it (error 1.5
-// times that of rounding dQ alone; 1.27 times with both parts).
 template <typename T, int D, int KB>
 __global__ void __launch_bounds__(32 * (kDqWarps + 1), 2)
     k_dq_tile(const __grid_constant__ DqTileArgs p) {
@@ -408,10 +417,7 @@ __global__ void __launch_bounds__(32 * (kDqWarps + 1), 2)
                 for (int w = 0; w < 4; ++w) {
                     const float x = s[2 * i + (w >> 1)][2 * (w & 1)];
                     const float y = s[2 * i + (w >> 1)][2 * (w & 1) + 1];
-                    hi[w] = pack2<T>(x, y);
-                    if constexpr (!kNarrow<T>)
-                        lo[w] = pack2<T>(x - __uint_as_float(hi[w] << 16),
-                                         y - __uint_as_float(hi[w] & 0xffff0000u));
+                    split2<T>(x, y, hi[w], lo[w]);
                 }
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
@@ -419,10 +425,8 @@ __global__ void __launch_bounds__(32 * (kDqWarps + 1), 2)
                     ldsm4_t(sk + panel_at<KB>(16 * i + (lane & 15), 2 * n + (lane >> 4)), x);
                     mma16816<T>(o[2 * n], hi[0], hi[1], hi[2], hi[3], x[0], x[1]);
                     mma16816<T>(o[2 * n + 1], hi[0], hi[1], hi[2], hi[3], x[2], x[3]);
-                    if constexpr (!kNarrow<T>) {
-                        mma16816<T>(o[2 * n], lo[0], lo[1], lo[2], lo[3], x[0], x[1]);
-                        mma16816<T>(o[2 * n + 1], lo[0], lo[1], lo[2], lo[3], x[2], x[3]);
-                    }
+                    mma16816<T>(o[2 * n], lo[0], lo[1], lo[2], lo[3], x[0], x[1]);
+                    mma16816<T>(o[2 * n + 1], lo[0], lo[1], lo[2], lo[3], x[2], x[3]);
                 }
             }
             if (key0 + KB > len) fence_proxy_async_shared();   // zeros, then the next copy
@@ -636,10 +640,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
                                 fmaf(__uint_as_float(dp[i + e]), a.scale, ds_off);
                         if (!whole && i + e >= seen) ds[e] = 0.0f;
                     }
-                    const uint32_t x = pack2<T>(ds[0], ds[1]);
-                    hi[i / 2] = x;
-                    lo[i / 2] = pack2<T>(ds[0] - __uint_as_float(x << 16),
-                                         ds[1] - __uint_as_float(x & 0xffff0000u));
+                    split2<T>(ds[0], ds[1], hi[i / 2], lo[i / 2]);
                 }
             } else {
 #pragma unroll
@@ -828,7 +829,7 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
                     mma16816<T>(dp[2 * i + 1], va[0], va[1], va[2], va[3], x[2], x[3]);
                 }
             }
-            uint32_t pa[4][2], da[4][2];         // P^T and dS^T of n-tile i, keys r and r + 8
+            uint32_t pa[4][2], da[4][2], dl[4][2];   // P^T, dS^T, its rest: keys r and r + 8
             float ds_max = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -859,8 +860,8 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                da[i][0] = pack2<T>(st[i][0] * u, st[i][1] * u);
-                da[i][1] = pack2<T>(st[i][2] * u, st[i][3] * u);
+                split2<T>(st[i][0] * u, st[i][1] * u, da[i][0], dl[i][0]);
+                split2<T>(st[i][2] * u, st[i][3] * u, da[i][1], dl[i][1]);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i)          // 16 rows at a time
@@ -879,6 +880,10 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
                                 da[2 * i + 1][1], x[0], x[1]);
                     mma16816<T>(dk[2 * n + 1], da[2 * i][0], da[2 * i][1], da[2 * i + 1][0],
                                 da[2 * i + 1][1], x[2], x[3]);
+                    mma16816<T>(dk[2 * n], dl[2 * i][0], dl[2 * i][1], dl[2 * i + 1][0],
+                                dl[2 * i + 1][1], x[0], x[1]);
+                    mma16816<T>(dk[2 * n + 1], dl[2 * i][0], dl[2 * i][1], dl[2 * i + 1][0],
+                                dl[2 * i + 1][1], x[2], x[3]);
                 }
             __syncthreads();
         }
@@ -1082,7 +1087,7 @@ cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s
     constexpr int per = 128 / (D / 8);
     k_delta<T, D><<<(unsigned)((rows + per - 1) / per), 128, 0, cs>>>(p, rows);
     count_launch();
-    if (blocks_by_tile(s)) {
+    if (blocks_by_tile(s, k, v)) {
         DqTileArgs t{};
         t.t.a = p.a;
         t.t.rows = s->Tq * p.a.G;

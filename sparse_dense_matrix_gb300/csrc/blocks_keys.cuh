@@ -5,6 +5,7 @@
 //   S = Q K^T, dP = dO V^T          128 rows x 64 keys, both operands K-major
 //   P = exp(scale S - lse), dS = scale P (dP - delta)      a thread per row
 //   dV^T += dO^T P, dK^T += Q^T dS  128 elements x 64 keys, summed over the rows
+//                                   (dS as its rounded value and its rest)
 // The gathered rows and P, dS serve as MN-major operands in the second pair of
 // products, so nothing is transposed in memory. Four warps gather rows by
 // asynchronous copies into two stages, one thread issues the products, eight
@@ -102,7 +103,8 @@ constexpr int kKeysPanelK = kKeysN * 128, kKeysPanelR = kKeysRows * 128;   // by
 constexpr int kKeysK = 0, kKeysV = 2 * kKeysPanelK, kKeysStage0 = 4 * kKeysPanelK;
 constexpr int kKeysStage = 4 * kKeysPanelR;                                // Q, dO
 constexpr int kKeysP = kKeysStage0 + 2 * kKeysStage, kKeysDs = kKeysP + kKeysPanelR;
-constexpr int kKeysStats = kKeysDs + kKeysPanelR;                          // [2][3][128] floats
+constexpr int kKeysDl = kKeysDs + kKeysPanelR;                             // dS's rest
+constexpr int kKeysStats = kKeysDl + kKeysPanelR;                          // [2][3][128] floats
 constexpr int kKeysList = kKeysStats + 2 * 3 * kKeysRows * 4;              // the segment's queries
 constexpr int kKeysSmem = kKeysList + kKeysSegment * 4 + 1024;
 // tensor memory columns
@@ -242,6 +244,8 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                             desc_mn(smem + kKeysP + i * 2048, kKeysPanelR), mn, j > 0 || i > 0);
                     mma_f16(tmem + kTmDk, desc_mn(rows_ + i * 2048, kKeysPanelR),
                             desc_mn(smem + kKeysDs + i * 2048, kKeysPanelR), mn, j > 0 || i > 0);
+                    mma_f16(tmem + kTmDk, desc_mn(rows_ + i * 2048, kKeysPanelR),
+                            desc_mn(smem + kKeysDl + i * 2048, kKeysPanelR), mn, true);
                 }
                 mma_commit(&done[j & 1]);
             };
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
             const float lse2 = m[0], delta = m[kKeysRows];
             const int seen = __float_as_int(m[2 * kKeysRows]) - (key0 + half * 32);
             tmem_wait_ld();
-            uint32_t pp[16], dd[16];
+            uint32_t pp[16], dd[16], dl[16];
             const bool whole = __all_sync(0xffffffffu, seen >= 32);
             const float ds_off = -delta * a.scale;
 #pragma unroll
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                     if (!whole && i + e >= seen) pr[e] = ds[e] = 0.0f;
                 }
                 pp[i / 2] = pack2<T>(pr[0], pr[1]);
-                dd[i / 2] = pack2<T>(ds[0], ds[1]);
+                split2<T>(ds[0], ds[1], dd[i / 2], dl[i / 2]);
             }
             // the products of the step before read the buffers that are written now
             if (j > 0) ok = mbar_wait_poll(&done[(j - 1) & 1], ((j - 1) >> 1) & 1, p.err);
@@ -331,6 +335,10 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kKeysDs),
                              "r"(dd[4 * i]), "r"(dd[4 * i + 1]), "r"(dd[4 * i + 2]),
                              "r"(dd[4 * i + 3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + kKeysDl),
+                             "r"(dl[4 * i]), "r"(dl[4 * i + 1]), "r"(dl[4 * i + 2]),
+                             "r"(dl[4 * i + 3])
                              : "memory");
             }
             fence_proxy_async_shared();

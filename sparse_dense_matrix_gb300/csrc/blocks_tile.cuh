@@ -271,8 +271,15 @@ cudaError_t encode_rows(const spmm_rows &r, const spmm_blocks_shape *s, int box_
 // 622 and 133.
 constexpr int kTileRows = 128;       // of the tensor-memory kernels; the others' are 64
 
-inline bool blocks_by_tile(const spmm_blocks_shape *s) {
+inline bool blocks_by_tile(const spmm_blocks_shape *s, const spmm_rows &k, const spmm_rows &v) {
     if (s->Tk == 0 || s->B * s->Hk > 65535) return false;
+    // a tensor map steps forward, by less than 2^40 bytes: a row shared by several
+    // keys, heads or sequences (stride 0) goes by query
+    auto mapped = [&](int64_t n, int64_t stride) {
+        return n <= 1 || (stride > 0 && stride < ((int64_t)1 << 39));
+    };
+    for (const spmm_rows &r : {k, v})
+        if (!mapped(s->Tk, r.st) || !mapped(s->Hk, r.sh) || !mapped(s->B, r.sb)) return false;
     const int64_t G = s->Hq / s->Hk, parts = s->block > 64 ? s->block / 64 : 1;
     const int64_t NB = (s->Tk + s->block - 1) / s->block;
     const int64_t tiles = s->B * s->Hk * ((s->Tq * G + kTileRows - 1) / kTileRows);

@@ -543,3 +543,63 @@ def test_a_row_that_is_not_finite_stays_its_own(sdm, cuda_device, dtype, D):
     assert torch.equal(out2[0, :200, 2:], out[0, :200, 2:]) or \
         (out2[0, :200, 2:] - out[0, :200, 2:]).abs().max() <= 4 * u * out.abs().max()
     assert torch.equal(out2[0, 256:], out[0, 256:]) and torch.equal(out2[:, :, :2], out[:, :, :2])
+
+
+TILES = [  # problems large enough to go by tile; the lists of some do not fit on chip
+    (2, 700, 500, 4, 4, 64, 16, 24, None),
+    (2, 600, 2000, 2, 2, 128, 64, 20, [2000, 777]),
+    (1, 900, 1000, 6, 2, 64, 32, 7, None),
+    (1, 800, 801, 16, 1, 128, 128, 4, None),
+    (2, 512, 640, 4, 2, 64, 64, 5, [640, 100]),
+    (1, 1500, 1500, 1, 1, 128, 32, 9, None),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", TILES)
+def test_attend_and_backward_by_tile(sdm, cuda_device, case, dtype, causal):
+    test_attend_and_backward(sdm, cuda_device, case, dtype, causal)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), "lowest"])
+@pytest.mark.parametrize("case", [TILES[2], TILES[4], (2, 700, 760, 4, 2, 128, 64, 5, [760, 300])])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_masked_places_by_tile(sdm, cuda_device, case, dtype, fill):
+    """Keys past the length and in a block that nobody chose hold anything, and so do
+    the rows of q and of the gradient of queries that see nothing."""
+    B, Tq, Tk, Hq, Hk, D, block, n, lengths = case
+    q, k, v, blocks, L = inputs(cuda_device, case, dtype, seed=21)
+    blocks[blocks == 2] = -1
+    blocks = blocks.masked_fill((blocks < 0).cummax(-1).values, -1)
+    sel = sdm.BlockSelection(blocks, block, Tk, L)
+    grad = randn(cuda_device, 93, *q.shape).to(q.dtype)
+    x = torch.finfo(k.dtype).min if fill == "lowest" else fill
+    k[:, 2 * block:3 * block] = v[:, 2 * block:3 * block] = x
+    for b, m in enumerate(lengths or [Tk] * B):
+        k[b, m:] = v[b, m:] = x
+    blind = ref.limits(L, B, Tq, Tk, True).to(cuda_device) == 0
+    q[blind] = grad[blind] = x
+    out, lse = sel.attend(q, k, v)
+    got = dict(zip(("dq", "dk", "dv"), sel.backward(grad, q, k, v, out, lse)), out=out, lse=lse)
+    want = ref.attend(q, k, v, blocks, block, L, True, grad=grad)
+    for name in got:
+        ref.close(got[name], want[name], want["tol_" + name], name)
+
+
+@pytest.mark.parametrize("Tq", [1, 500])
+def test_shared_caches(sdm, cuda_device, Tq):
+    """One cache for all sequences, one head for all kv heads (strides of 0)."""
+    B, Tk, Hq, Hk, D, block, n = 3, 600, 4, 2, 64, 32, 6
+    q = randn(cuda_device, 1, B, Tq, Hq, D).half()
+    k, v = (randn(cuda_device, i, 1, Tk, 1, D).half() for i in (2, 3))
+    blocks = random_lists(5, B, Tq, Hk, n, -(-Tk // block)).to(cuda_device)
+    sel = sdm.BlockSelection(blocks, block, Tk)
+    grad = randn(cuda_device, 4, *q.shape).half()
+    for shape in ((B, Tk, Hk, D),):
+        ks, vs = k.expand(shape), v.expand(shape)
+        out, lse = sel.attend(q, ks, vs)
+        got = dict(zip(("dq", "dk", "dv"), sel.backward(grad, q, ks, vs, out, lse)), out=out, lse=lse)
+        want = ref.attend(q, ks, vs, blocks, block, None, True, grad=grad)
+        for name in got:
+            ref.close(got[name], want[name], want["tol_" + name], name)
