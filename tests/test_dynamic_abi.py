@@ -97,7 +97,9 @@ def test_blocks_refuse_tensors(dyn):
                                       None) == INVALID
     assert L.spmm_blocks_attend(s, r, r, r, None, PTR, PTR, None) == INVALID
     assert L.spmm_blocks_attend(s, r, r, r, PTR, PTR, None, None) == INVALID
-    assert L.spmm_blocks_select(shape(dyn, Tq=100), r, PTR, PTR, None, 0, None) == INVALID
+    long = shape(dyn, Tk=1 << 20)                # more blocks than a row of one CTA
+    assert L.spmm_blocks_select_workspace(long) > 0
+    assert L.spmm_blocks_select(long, r, PTR, PTR, None, 0, None) == INVALID
     need = L.spmm_blocks_backward_workspace(s)
     assert need > 0
     assert L.spmm_blocks_backward(s, r, r, r, PTR, PTR, PTR, r, PTR, PTR, PTR, PTR, need - 1,
