@@ -497,9 +497,11 @@ __global__ void __launch_bounds__(32 * (kTileWarps + 1), 2)
 // most, and l and O carry the same factor). Two CTAs share an SM: one's products
 // run under the other's exponentials. 291 us for 8192 queries x 32 heads of 128 over
 // 4, 16 of 64-key blocks (126 GFLOP of the rows' own keys, 433 TFLOP/s; the tiles'
-// unions are twice that). Bound by the two products: with N = 64 the first reads
-// its A operand from shared memory at twice the rate that its arithmetic needs,
-// and the tensor pipe computes 39% of the time. By mma.sync it took 511 us.
+// unions are twice that). Bound by the chain of a step (S, the row's weights, O),
+// of which two CTAs and two steps' S overlap a part: the tensor pipe computes 39%
+// of the time. Q in tensor memory, which leaves room for one S only, took 421 us;
+// two threads to a row, whose registers leave room for one CTA only, 531; mma.sync
+// 511.
 constexpr int kMmaRows = 128, kMmaKeys = 64, kMmaThreads = 192;   // 4 + producer + issuer
 template <int D> using MmaSmem = TileSmem<D, kMmaKeys, 8, 1, 113 * 1024>;
 

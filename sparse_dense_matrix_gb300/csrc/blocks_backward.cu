@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(32 * (kDqWarps + 1), 2)
 // (half a row's keys a thread), dQ += dS K with dS in tensor memory, twice over
 // as above. One CTA fills an SM: S and dP of a step run under the dS of the one
 // before. 242 us for 2 x 4096 queries x 16 heads of 128 over 2, 16 of 64-key blocks;
-// bound like the forward by the products' operand reads (the pipe computes 31% of
+// bound like the forward by the chain of a step (the tensor pipe computes 31% of
 // the time). By mma.sync it took 333 us.
 constexpr int kDqRows = 128, kDqKeys = 64, kDqThreads = 320;   // 8 + producer + issuer
 template <int D> using DqMmaSmem = TileSmem<D, kDqKeys, 8, 2, 227 * 1024>;
