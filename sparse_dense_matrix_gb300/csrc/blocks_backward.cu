@@ -701,12 +701,15 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
 }
 
 // ------------------------------------------------------------- dK and dV
-// A CTA per (tile of KT = 16 W keys of one block, kv head, sequence, range of
-// queries), a warp per 16 keys. The range's words are expanded to a list of
-// queries, whose (query, head) rows are taken 32 at a time: Q and dO rows are
-// gathered into shared memory by asynchronous copies, two tiles in flight. For fp16,
-// heads of 64, blocks of 16 and 32 keys and few rows; 27 us for 4 x 777 queries x 4
-// heads of 64 in fp16, bound by the latency of its gathers and barriers.
+// A CTA per (64 keys, kv head, sequence, range of queries), a warp per 16 keys.
+// The range's words are expanded to a list of queries, whose (query, head) rows are
+// taken 32 at a time: Q and dO rows are gathered into shared memory by asynchronous
+// copies, two tiles in flight. 64 keys are NS blocks of 16 or 32: the list is then
+// the union of theirs, a row counts for the warps of the blocks that it chose, and
+// is gathered once for all of them (with a CTA per block of 16 a training step of 5
+// x 784 queries x 6 heads of 128 over 2, 19 of 16-key blocks, took 306 us for 186).
+// For fp16, heads of 64, blocks of 16 and 32 keys and few rows; 23 us for 4 x 777
+// queries x 4 heads of 64 in fp16, bound by the latency of its gathers and barriers.
 constexpr int kRt = 32;             // rows per tile
 constexpr int kSegWords = 32;       // words expanded at a time (1024 queries)
 
@@ -716,27 +719,27 @@ template <int D> __device__ __forceinline__ uint32_t tile_at(int row, int i) {
     return (uint32_t)(row * D * 2 + ((i ^ (row & 7)) << 4));
 }
 
-template <typename T, int D, int W>
-__global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
-    constexpr int KT = 16 * W, C = D / 8, threads = 32 * W;
+template <typename T, int D, int NS>
+__global__ void __launch_bounds__(128) k_dkdv(BwdArgs p) {
+    constexpr int KT = 64, C = D / 8, threads = 128, kPer = kRt / 4;   // rows a warp gathers
     extern __shared__ __align__(128) unsigned char smem[];
-    // K, V [KT][D]; two stages of Q, dO [kRt][D]; then per stage lse, delta, limit [kRt]
+    // K, V [KT][D]; two stages of Q, dO [kRt][D]; then per stage lse, delta, limit and
+    // chosen blocks [kRt]
     const uint32_t sK = smem_addr(smem), sV = sK + KT * D * 2, sQ = sV + KT * D * 2;
     constexpr int stage_bytes = 2 * kRt * D * 2;
-    float *row_f = (float *)(smem + 2 * KT * D * 2 + 2 * stage_bytes);   // [2][3][kRt]
-    int *list = (int *)(row_f + 2 * 3 * kRt);                            // [1024]
+    float *row_f = (float *)(smem + 2 * KT * D * 2 + 2 * stage_bytes);   // [2][4][kRt]
+    int *list = (int *)(row_f + 2 * 4 * kRt);         // [1024] query, chosen blocks << 27
     __shared__ int word_base[kSegWords + 1];
 
     const BlkArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int tiles = a.block / KT;
-    const int tile = blockIdx.x % tiles, blk = blockIdx.x / tiles;
     const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk;
     const int chunk = blockIdx.z;
-    const int key0 = blk * a.block + tile * KT;
+    const int key0 = blockIdx.x * KT, blk = key0 / a.block;
     if (key0 >= a.Tk) return;
     const int len = blk_len(a, b);
     const uint32_t *bits = p.bits + ((int64_t)blockIdx.y * a.NB + blk) * p.words;
+    const int subs = min(NS, a.NB - blk), my_sub = warp * NS / 4;    // of the CTA, of the warp
     const int w_end = min(p.words, (chunk + 1) * p.chunk_words);
     const float scale2 = a.scale * kLog2e, ds_unit = a.scale * kPUnit<T>;
 
@@ -751,12 +754,19 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
     }
     cp_commit();
 
+    const T *qp = (const T *)a.q + b * a.q_sb + (int64_t)h * a.G * a.q_sh;
+    const T *gp = (const T *)p.dout + b * p.do_sb + (int64_t)h * a.G * p.do_sh;
     float dk[D / 8][4] = {}, dv[D / 8][4] = {};
     DsScale ds_scale;
     for (int w0 = chunk * p.chunk_words; w0 < w_end; w0 += kSegWords) {
         __syncthreads();
         if (warp == 0) {                         // counts of the words, then the list
-            const uint32_t x = w0 + lane < w_end ? bits[w0 + lane] : 0u;
+            uint32_t sub[NS], x = 0;
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                sub[i] = i < subs && w0 + lane < w_end ? bits[i * (int64_t)p.words + w0 + lane] : 0u;
+                x |= sub[i];
+            }
             int n = __popc(x), incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -766,39 +776,51 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
             word_base[lane] = incl - n;
             if (lane == 31) word_base[32] = incl;
             int at = incl - n;
-            for (uint32_t m = x; m; m &= m - 1) list[at++] = (w0 + lane) * 32 + __ffs(m) - 1;
+            for (uint32_t m = x; m; m &= m - 1) {
+                const int bit = __ffs(m) - 1;
+                int chosen = 0;
+#pragma unroll
+                for (int i = 0; i < NS; ++i) chosen |= (int)(sub[i] >> bit & 1u) << i;
+                list[at++] = ((w0 + lane) * 32 + bit) | chosen << 27;
+            }
         }
         __syncthreads();
         const int rows = word_base[32] * a.G;
         const int steps = (rows + kRt - 1) / kRt;
         auto fetch = [&](int step) {
             const uint32_t base = sQ + (step & 1) * stage_bytes;
-            for (int i = threadIdx.x; i < kRt * C; i += threads) {
-                const int row = i / C, d = i % C, f = step * kRt + row;
-                const bool live = f < rows;
-                const int t = live ? list[f / a.G] : 0, head = h * a.G + (live ? f % a.G : 0);
-                cp16(base + tile_at<D>(row, d),
-                     (const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + d * 8, live);
-                cp16(base + kRt * D * 2 + tile_at<D>(row, d),
-                     (const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + d * 8, live);
+            // a warp gathers kPer rows; its first lanes know where they are
+            const int row0 = warp * kPer, f = step * kRt + row0 + lane;
+            int64_t q_at = -1, g_at = 0;
+            float lse2 = INFINITY, delta = 0.0f;
+            int limit = 0, chosen = 0;
+            if (lane < kPer && f < rows) {
+                const int q = f / a.G, g = f - q * a.G;
+                const int t = list[q] & ((1 << 27) - 1);
+                chosen = (unsigned)list[q] >> 27;
+                q_at = t * a.q_st + g * a.q_sh;
+                g_at = t * p.do_st + g * p.do_sh;
+                const int64_t i = ((int64_t)b * a.Tq + t) * a.Hq + h * a.G + g;
+                lse2 = p.lse[i] * kLog2e;
+                delta = p.delta[i];
+                limit = blk_limit(a, len, t);
+            }
+#pragma unroll
+            for (int i = 0; i < kPer * C / 32; ++i) {
+                const int row = i * (32 / C) + lane / C, ch = lane % C;
+                const int64_t x = __shfl_sync(0xffffffffu, q_at, row);
+                const int64_t y = __shfl_sync(0xffffffffu, g_at, row);
+                const uint32_t at = base + tile_at<D>(row0 + row, ch);
+                cp16(at, qp + (x < 0 ? 0 : x + ch * 8), x >= 0);
+                cp16(at + kRt * D * 2, gp + (x < 0 ? 0 : y + ch * 8), x >= 0);
             }
             cp_commit();
-            for (int row = threadIdx.x; row < kRt; row += threads) {
-                const int f = step * kRt + row;
-                float x = INFINITY, y = 0.0f;
-                int limit = 0;
-                if (f < rows) {
-                    const int t = list[f / a.G];
-                    const int64_t i = ((int64_t)b * a.Tq + t) * a.Hq + h * a.G + f % a.G;
-                    x = p.lse[i] * kLog2e;
-                    if (x == -INFINITY) x = INFINITY;        // a row without keys: P = 0
-                    y = p.delta[i];
-                    limit = blk_limit(a, len, t);
-                }
-                float *m = row_f + (step & 1) * 3 * kRt;
-                m[row] = x;
-                m[kRt + row] = y;
-                m[2 * kRt + row] = __int_as_float(limit);
+            if (lane < kPer) {
+                float *m = row_f + (step & 1) * 4 * kRt + row0 + lane;
+                m[0] = lse2 == -INFINITY ? INFINITY : lse2;  // a row without keys: P = 0
+                m[kRt] = delta;
+                m[2 * kRt] = __int_as_float(limit);
+                m[3 * kRt] = __int_as_float(chosen);
             }
         };
         if (steps) fetch(0);
@@ -811,7 +833,13 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
             }
             __syncthreads();
             const uint32_t tq = sQ + (step & 1) * stage_bytes, tg = tq + kRt * D * 2;
-            const float *m = row_f + (step & 1) * 3 * kRt;
+            const float *m = row_f + (step & 1) * 4 * kRt;
+            // a warp whose block none of the rows chose goes without
+            if (NS > 1 && !__any_sync(0xffffffffu,
+                                      __float_as_int(m[3 * kRt + lane]) >> my_sub & 1)) {
+                __syncthreads();
+                continue;
+            }
             float st[4][4] = {}, dp[4][4] = {};
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -840,7 +868,12 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
             for (int i = 0; i < 4; ++i) {
                 const int row = 8 * i + 2 * c;
                 const float2 l = *(const float2 *)(m + row), d = *(const float2 *)(m + kRt + row);
-                const int2 lim = *(const int2 *)(m + 2 * kRt + row);
+                int2 lim = *(const int2 *)(m + 2 * kRt + row);
+                if (NS > 1) {
+                    const int2 in = *(const int2 *)(m + 3 * kRt + row);
+                    if (!(in.x >> my_sub & 1)) lim.x = 0;
+                    if (!(in.y >> my_sub & 1)) lim.y = 0;
+                }
                 float pr[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -940,8 +973,9 @@ __global__ void __launch_bounds__(32 * W) k_dkdv(BwdArgs p) {
         dkdv_key_alone<T, D>(
             p, b, h, key,
             [&](auto body) {
+                const uint32_t *mine = bits + my_sub * (int64_t)p.words;
                 for (int w = chunk * p.chunk_words; w < w_end; ++w)
-                    for (uint32_t m = bits[w]; m; m &= m - 1) body(w * 32 + __ffs(m) - 1);
+                    for (uint32_t m = mine[w]; m; m &= m - 1) body(w * 32 + __ffs(m) - 1);
             },
             x, y);
         const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + h) * D + lane * E;
@@ -978,7 +1012,6 @@ template <typename T> __global__ void __launch_bounds__(256) k_dkdv_join(BwdArgs
 struct BwdPlan {
     int64_t words, chunk_words, chunks;
     int64_t bits_bytes, delta_bytes, part_bytes;
-    int W;
     bool keys;               // k_dkdv_keys, over at most so many tiles and items
     int64_t tiles = 0, items = 0;
 };
@@ -996,10 +1029,9 @@ bool by_keys(const spmm_blocks_shape *s) {
 BwdPlan bwd_plan(const spmm_blocks_shape *s) {
     BwdPlan p;
     const int64_t NB = (s->Tk + s->block - 1) / s->block;
-    p.W = s->block == 16 ? 1 : s->block == 32 ? 2 : 4;
     p.words = (s->Tq + 31) / 32;
-    const int64_t ctas = std::max<int64_t>(1, s->B * s->Hk * NB * (s->block / (16 * p.W)));
-    int64_t chunks = std::min<int64_t>((152 * 8 * (4 / p.W) + ctas - 1) / ctas, (p.words + 7) / 8);
+    const int64_t ctas = std::max<int64_t>(1, s->B * s->Hk * ((s->Tk + 63) / 64));
+    int64_t chunks = std::min<int64_t>((152 * 8 + ctas - 1) / ctas, (p.words + 7) / 8);
     chunks = std::max<int64_t>(1, std::min<int64_t>(chunks, 64));
     p.chunk_words = std::max<int64_t>(1, (p.words + chunks - 1) / chunks);
     p.chunks = std::max<int64_t>(1, (p.words + p.chunk_words - 1) / p.chunk_words);
@@ -1018,16 +1050,15 @@ BwdPlan bwd_plan(const spmm_blocks_shape *s) {
     return p;
 }
 
-template <typename T, int D, int W>
-cudaError_t launch_dkdv(const BwdArgs &p, const BwdPlan &bp, int64_t B, cudaStream_t s) {
-    constexpr int KT = 16 * W;
-    const size_t smem = 2 * KT * D * 2 + 4 * kRt * D * 2 + 2 * 3 * kRt * 4 + kSegWords * 32 * 4;
+template <typename T, int D, int NS>
+cudaError_t launch_dkdv(const BwdArgs &p, int64_t B, cudaStream_t s) {
+    const size_t smem = 2 * 64 * D * 2 + 4 * kRt * D * 2 + 2 * 4 * kRt * 4 + kSegWords * 32 * 4;
     const cudaError_t e = cudaFuncSetAttribute(
-        k_dkdv<T, D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        k_dkdv<T, D, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(p.a.NB * (p.a.block / KT)), (unsigned)(B * p.a.Hk),
-                    (unsigned)p.chunks);
-    k_dkdv<T, D, W><<<grid, 32 * W, smem, s>>>(p);
+    k_dkdv<T, D, NS><<<dim3((unsigned)((p.a.Tk + 63) / 64), (unsigned)(B * p.a.Hk),
+                            (unsigned)p.chunks),
+                       128, smem, s>>>(p);
     count_launch();
     return cudaGetLastError();
 }
@@ -1132,9 +1163,9 @@ cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s
         if constexpr (D == kKeysD && !kNarrow<T>) e = launch_keys<T>(p, bp, cs);
         return e;
     }
-    if (bp.W == 1) e = launch_dkdv<T, D, 1>(p, bp, s->B, cs);
-    else if (bp.W == 2) e = launch_dkdv<T, D, 2>(p, bp, s->B, cs);
-    else e = launch_dkdv<T, D, 4>(p, bp, s->B, cs);
+    if (s->block == 16) e = launch_dkdv<T, D, 4>(p, s->B, cs);
+    else if (s->block == 32) e = launch_dkdv<T, D, 2>(p, s->B, cs);
+    else e = launch_dkdv<T, D, 1>(p, s->B, cs);
     if (e != cudaSuccess || p.chunks == 1) return e;
     k_dkdv_join<T><<<(unsigned)((p.part_stride / 8 + 255) / 256), 256, 0, cs>>>(p);
     count_launch();
