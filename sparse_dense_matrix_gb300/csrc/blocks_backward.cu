@@ -47,18 +47,18 @@ __global__ void k_set_bits(BwdArgs p, int64_t entries) {
     atomicOr(p.bits + ((b * a.Hk + h) * a.NB + list[j]) * p.words + (t >> 5), 1u << (t & 31));
 }
 
+// dS is used twice over, as its rounded value plus what that left out. The rows of
+// dS sum to 0, so dQ = dS K (and, to a degree, dK) is what remains after the keys'
+// common part cancels, and a single rounding of dS shows in it: the error was 1.7
+// times that of rounding dQ alone, and is 1.27 times with both parts (the rest is
+// delta's, from the rounded output).
+
 // fp16 has 5 bits of exponent: weights and gradients well below 2^-14 would lose
 // their digits in it. So P is held as P 2^14 (at most 2^14, up to its rounding),
 // and dS as dS 2^e, where a warp lowers its e (and rescales what it has summed)
 // whenever a tile's largest |dS| would reach 2^15; both are exact powers of two,
 // taken out of the sums at the end. bf16 has fp32's exponent and needs neither.
 template <typename T> constexpr bool kNarrow = std::is_same<T, __half>::value;
-//
-// dS is used twice over, as its rounded value plus what that left out. The rows of
-// dS sum to 0, so dQ = dS K (and, to a degree, dK) is what remains after the keys'
-// common part cancels, and a single rounding of dS shows in it: the error was 1.7
-// times that of rounding dQ alone, and is 1.27 times with both parts (the rest is
-// delta's, from the rounded output).
 template <typename T> constexpr float kPShift = kNarrow<T> ? 14.0f : 0.0f;
 template <typename T> constexpr float kPUnit = kNarrow<T> ? 1.0f / 16384.0f : 1.0f;
 
