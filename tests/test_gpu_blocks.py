@@ -603,3 +603,44 @@ def test_shared_caches(sdm, cuda_device, Tq):
         want = ref.attend(q, ks, vs, blocks, block, None, True, grad=grad)
         for name in got:
             ref.close(got[name], want[name], want["tol_" + name], name)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", [TILES[1], TILES[2], TILES[4]])
+def test_scales_by_tile(sdm, cuda_device, case, dtype, scale):
+    B, Tq, Tk, Hq, Hk, D, block, n, lengths = case
+    q, k, v, blocks, L = inputs(cuda_device, case, dtype, seed=31)
+    sel = sdm.BlockSelection(blocks, block, Tk, L)
+    grad = randn(cuda_device, 92, *q.shape).to(q.dtype)
+    out, lse = sel.attend(q, k, v, scale)
+    got = dict(zip(("dq", "dk", "dv"), sel.backward(grad, q, k, v, out, lse, scale)),
+               out=out, lse=lse)
+    want = ref.attend(q, k, v, blocks, block, L, True, scale, grad)
+    for name in got:
+        ref.close(got[name], want[name], want["tol_" + name], name)
+
+
+def test_graph_of_the_tile_kernels(sdm, cuda_device):
+    """A captured training step of tiles replays on new values."""
+    B, T, Hq, Hk, D, block, n = 1, 640, 8, 2, 128, 64, 4
+    q, k, v = (grid(randn(cuda_device, i, B, T, H, D), torch.bfloat16)
+               for i, H in ((0, Hq), (1, Hk), (2, Hk)))
+    grad = randn(cuda_device, 3, *q.shape).bfloat16()
+
+    def step():
+        sel = sdm.select_blocks(q, sdm.block_means(k, block), n, block, T)
+        out, lse = sel.attend(q, k, v)
+        return (sel.blocks, out, lse, *sel.backward(grad, q, k, v, out, lse))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    q.copy_(grid(randn(cuda_device, 8, *q.shape), torch.bfloat16))
+    k.copy_(grid(randn(cuda_device, 9, *k.shape), torch.bfloat16))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, step()))
+    sdm.dynamic_sync()
