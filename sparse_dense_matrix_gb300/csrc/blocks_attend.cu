@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
             const int parts = last ? 1 : a.block / KB;
             for (int s = 0; s < parts && ok; ++s) {
                 const int key0 = last ? -1 : least * a.block + s * KB;
-                if (key0 >= a.Tk) break;             // the second half of a last, short block
+                if (key0 >= len) break;  // nobody sees the second half of a last, short block
                 const int st = j % N;
                 ok = mbar_wait_poll(&ready[st], ((j / N) & 1) ^ 1, p.t.err);
                 if (!ok) break;
@@ -657,11 +657,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                         b_left = false;
                         const uint32_t v = sv + before * S::operand;
                         if (v_key0 + KB > len) {     // values past the length may be anything
-                            for (int i = (len - v_key0) * C; i < KB * C; ++i)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                 v + panel_at<KB>(i / C, i % C)),
-                                             "r"(0)
-                                             : "memory");
+                            zero_tail_one<D, KB>(v, len - v_key0);
                             fence_proxy_async_shared();
                         }
                         mma_fence_after();

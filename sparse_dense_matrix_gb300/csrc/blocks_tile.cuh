@@ -240,6 +240,15 @@ __device__ __forceinline__ void zero_tail(uint32_t operand, int from) {
     __syncwarp();
 }
 
+// The same by one thread, for the threads that issue the products.
+template <int D, int KB> __device__ __forceinline__ void zero_tail_one(uint32_t operand, int from) {
+    for (int i = max(from, 0) * (D / 8); i < KB * (D / 8); ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         operand + panel_at<KB>(i / (D / 8), i % (D / 8))),
+                     "r"(0)
+                     : "memory");
+}
+
 // One warp's 16 rows of a strided tensor into its part of shared memory: lanes
 // 0 to 15 say of rows 0 to 15 where they start; a row that is not live is 0.
 template <typename T, int D>
