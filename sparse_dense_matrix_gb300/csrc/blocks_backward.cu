@@ -564,11 +564,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
                         if (more) {
                             const uint32_t k = smem + st * S::stage, v = k + S::operand;
                             if (key0 + KB > len) {   // keys past the length may be anything
-                                for (int i = (len - key0) * C; i < KB * C; ++i)
-                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                     k + panel_at<KB>(i / C, i % C)),
-                                                 "r"(0)
-                                                 : "memory");
+                                zero_tail_one<D, KB>(k, len - key0);
                                 fence_proxy_async_shared();
                             }
                             const uint32_t tm = tmem + (j & 1) * kTmStep;

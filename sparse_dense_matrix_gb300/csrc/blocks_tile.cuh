@@ -177,7 +177,7 @@ __device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace 
                                              uint32_t smem, uint64_t *full, uint64_t *empty,
                                              TileStage<W> *info, int32_t *lists) {
     const BlkArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, len = blk_len(a, at.b);
     TileMerge<W> merge(p, at, lists, S::lists);
     int stage = 0, issued = 0;
     uint32_t parity = 1;                           // the ring starts empty
@@ -188,7 +188,7 @@ __device__ __forceinline__ void tile_produce(const TileArgs &p, const TilePlace 
         const int parts = last ? 1 : a.block / KB;
         for (int s = 0; s < parts; ++s) {
             const int key0 = last ? -1 : least * a.block + s * KB;
-            if (key0 >= a.Tk) break;               // the second half of a last, short block
+            if (key0 >= len) break;    // nobody sees the second half of a last, short block
             ok = mbar_wait(&empty[stage], parity, p.err);
             if (!ok) break;
             if (lane == 0) {

@@ -45,3 +45,17 @@ def test_forward(sdm, cuda_device, dtype, D, tail, causal):
         ref.close(out, want["out"], want["tol_out"], "out")
         ref.close(lse, want["lse"], want["tol_lse"], "lse")
     sdm.dynamic_sync()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("tail", [1, 20, 63, 64, 65])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", list(DT))
+def test_gradients(sdm, cuda_device, dtype, D, tail, causal):
+    sel, q, k, v, grad, L = problem(sdm, cuda_device, dtype, D, tail, causal)
+    want = ref.attend(q, k, v, sel.blocks, BLOCK, L, causal, grad=grad)
+    out, lse = sel.attend(q, k, v)
+    for _ in range(3):
+        for name, got in zip(("dq", "dk", "dv"), sel.backward(grad, q, k, v, out, lse)):
+            ref.close(got, want[name], want["tol_" + name], name)
+    sdm.dynamic_sync()
