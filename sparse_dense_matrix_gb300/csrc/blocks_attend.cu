@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
     // later step comes in its place while the step's P is still being made
     constexpr int N = S::stages;
     // (S done: ready, which is also when its K may go; P V done: done, and its V)
-    __shared__ uint64_t k_full[N], v_full[N], ready[N], done[N], made[2];
+    __shared__ uint64_t k_full[N], v_full[N], ready[N], done[N], made[2], drained;
     __shared__ TileStage<8> info[N + 2];             // alive from a step's K to its P
     __shared__ uint32_t tmem_slot;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -531,6 +531,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
             mbar_init(&ready[i], 2);
             mbar_init(&done[i], 1);
         }
+        mbar_init(&drained, 1);
         mbar_init(&made[0], kMmaRows);
         mbar_init(&made[1], kMmaRows);
         mbar_init_fence();
@@ -675,6 +676,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
                 }
                 v_key0 = key0;
             }
+            if (!ok) mma_drain(&drained, p.t.err);
         }
         __syncwarp();
     } else {

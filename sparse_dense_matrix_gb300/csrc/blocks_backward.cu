@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
     constexpr int kTmDp = 64, kTmStep = 128, kTmDs = 256, kTmDq = 384, columns = 512;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t full[N], ready[2], made[2], done[N];   // done: dQ, and the stage is free
+    __shared__ uint64_t drained;
     __shared__ TileStage<8> info[N];
     __shared__ uint32_t tmem_slot, odd_rows[4];
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -509,6 +510,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
             mbar_init(&ready[i], 2);
             mbar_init(&made[i], 256);
         }
+        mbar_init(&drained, 1);
         mbar_init_fence();
     }
     if (threadIdx.x < 4) odd_rows[threadIdx.x] = 0;
@@ -602,6 +604,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) k_dq_mma(const __grid_constant_
                     }
                 }
             }
+            if (!ok) mma_drain(&drained, p.t.err);
         }
         __syncwarp();
     } else {

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
     unsigned char *sp = smem_raw + (smem - smem_addr(smem_raw));
     float *stats = (float *)(sp + kKeysStats);
     int32_t *list = (int32_t *)(sp + kKeysList);
-    __shared__ uint64_t full[2], ready[2], made, done[2];
+    __shared__ uint64_t full[2], ready[2], made, done[2], drained;
     __shared__ uint32_t tmem_slot, odd[2];
     __shared__ int n_queries;
 
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                 mbar_init(&done[i], 1);
             }
             mbar_init(&made, 256);
+            mbar_init(&drained, 1);
             mbar_init_fence();
         }
     } else if (warp == kKeysIssuer) {
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                     }
                 }
             }
+            if (!ok) mma_drain(&drained, p.err);
         }
         __syncwarp();
     } else {

@@ -65,6 +65,14 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
         : "memory");
 }
 
+// A thread that gives up waits (within the usual limits) for the MMAs that it has in
+// flight: they read this CTA's shared memory and write its tensor memory, which the
+// next CTA may be given. `bar` is a barrier of its own, for one arrival.
+__device__ __forceinline__ void mma_drain(uint64_t *bar, int32_t *err) {
+    mma_commit(bar);
+    mbar_wait_poll(bar, 0, err);
+}
+
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, int columns) {      // one warp
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(slot)),
