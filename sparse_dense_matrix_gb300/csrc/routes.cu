@@ -298,6 +298,9 @@ int64_t sort_tiles(int64_t P) {
     return std::min<int64_t>(kSortMaxTiles, (P + kSortTile - 1) / kSortTile);
 }
 
+// the warps' counters and the experts' first slots
+size_t sort_smem(int64_t E) { return sizeof(int32_t) * (size_t)(kSortWarps * E + E + 1); }
+
 }  // namespace
 }  // namespace spmm
 
@@ -331,10 +334,12 @@ spmm_status spmm_routes_sort(const int32_t *ids, int64_t T, int64_t k, int64_t E
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_status(e);
     }
-    const size_t smem = sizeof(int32_t) * (size_t)(kSortWarps * E + E + 1);
+    const size_t smem = sort_smem(E);
     if (smem > 48 * 1024) {
+        // the kernel's limit is the process's: always the largest, so that another
+        // thread's call cannot lower it between here and the launch
         e = cudaFuncSetAttribute(k_route_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
+                                 (int)sort_smem(SPMM_ROUTES_MAX_EXPERTS));
         if (e != cudaSuccess) return cuda_status(e);
     }
     k_route_sort<<<(unsigned)tiles, kSortThreads, smem, s>>>(ids, P, (int)E, tile, (int)tiles,
