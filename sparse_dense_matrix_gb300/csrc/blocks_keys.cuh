@@ -87,7 +87,9 @@ __device__ __forceinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, i
                 s += __shfl_xor_sync(0xffffffffu, s, x);
                 d += __shfl_xor_sync(0xffffffffu, d, x);
             }
-            const float pr = ex2(fmaf(s, a.scale * kLog2e, -p.lse[row] * kLog2e));
+            const float lse2 = p.lse[row] * kLog2e;
+            if (lse2 == -INFINITY) continue;     // every score of the row is -infinity: P = 0
+            const float pr = ex2(fmaf(s, a.scale * kLog2e, -lse2));
             const float ds = pr * (d - p.delta[row]) * a.scale;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
