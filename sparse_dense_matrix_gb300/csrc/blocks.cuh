@@ -113,6 +113,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Whether the warp's elements are all NaN: no further term of a sum changes them.
+template <int E> __device__ __forceinline__ bool all_nan(const float (&x)[E]) {
+    bool y = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y = y && isnan(x[e]);
+    return __all_sync(0xffffffffu, y);
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

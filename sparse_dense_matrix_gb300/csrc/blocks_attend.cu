@@ -268,7 +268,8 @@ struct AttendTileArgs {
 // One row, key by key, for rows whose tile gave a result that is not finite: in
 // the tile a value that is infinite or NaN times the weight 0 of a row that does
 // not see it spoils that row's sums too (not its lse); here each row meets the
-// keys it sees only.
+// keys it sees only, until all of it is NaN. (A row whose sum of weights is NaN is NaN
+// throughout as it stands.)
 template <typename T, int D>
 __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, int h, int t, int head) {
     const BlkArgs &a = p.t.a;
@@ -279,10 +280,11 @@ __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, in
     float q[E], o[E] = {}, m = -INFINITY, l = 0.0f;
     ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
     const int32_t *list = a.blocks + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.n;
-    for (int j = 0; j < a.n; ++j) {
+    bool more = true;
+    for (int j = 0; j < a.n && more; ++j) {
         if (!blk_entry_ok(list, j, a.NB)) continue;
         const int k0 = list[j] * a.block, k1 = min(k0 + a.block, limit);
-        for (int key = k0; key < k1; ++key) {
+        for (int key = k0; key < k1 && more; ++key) {
             float x[E], dot = 0.0f;
             ld_pack<T, E>((const T *)a.k + b * a.k_sb + key * a.k_st + h * a.k_sh + lane * E, x);
 #pragma unroll
@@ -298,6 +300,7 @@ __device__ __noinline__ void attend_row_alone(const AttendTileArgs &p, int b, in
             const float pt = to_f32(from_f32<T>(pr));
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = fmaf(pt, x[e], o[e] * corr);
+            more = !all_nan(o);
         }
     }
     const float inv = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(32 * (kTileWarps + 1), 2)
             odd = fmaf(o[n][2 * e], 0.0f, odd);
             odd = fmaf(o[n][2 * e + 1], 0.0f, odd);
         }
-        const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f);
+        const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f && !isnan(l[e]));
         const bool live = at.f0 + warp * 16 + r + 8 * e < p.t.rows;
         redo |= __ballot_sync(0xffffffffu, c == 0 && live && (bad >> (4 * r) & 15u)) << e;
         if (!live) continue;
@@ -787,7 +790,7 @@ __global__ void __launch_bounds__(kMmaThreads, 2) k_attend_mma(const __grid_cons
         }
         if (live)
             p.lse[o_row] = l != 0.0f ? ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2 : -INFINITY;
-        unsigned redo = __ballot_sync(0xffffffffu, live && odd != 0.0f);
+        unsigned redo = __ballot_sync(0xffffffffu, live && odd != 0.0f && !isnan(l));
         for (; redo; redo &= redo - 1) {
             const int64_t g = at.f0 + warp * 32 + __ffs(redo) - 1;
             const int tt = (int)(g / a.G);

@@ -263,7 +263,8 @@ struct DqTileArgs {
 };
 
 // One row, key by key, for rows whose tile gave a result that is not finite (an
-// infinite or NaN key times the weight 0 of a row that does not see it).
+// infinite or NaN key times the weight 0 of a row that does not see it), until all
+// of it is NaN.
 template <typename T, int D>
 __device__ __noinline__ void dq_row_alone(const DqTileArgs &p, int b, int h, int t, int head) {
     const BlkArgs &a = p.t.a;
@@ -276,10 +277,11 @@ __device__ __noinline__ void dq_row_alone(const DqTileArgs &p, int b, int h, int
     ld_pack<T, E>((const T *)a.q + b * a.q_sb + t * a.q_st + head * a.q_sh + lane * E, q);
     ld_pack<T, E>((const T *)p.dout + b * p.do_sb + t * p.do_st + head * p.do_sh + lane * E, g);
     const int32_t *list = a.blocks + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.n;
-    for (int j = 0; j < a.n && lse2 != -INFINITY; ++j) {
+    bool more = lse2 != -INFINITY;
+    for (int j = 0; j < a.n && more; ++j) {
         if (!blk_entry_ok(list, j, a.NB)) continue;
         const int k0 = list[j] * a.block, k1 = min(k0 + a.block, limit);
-        for (int key = k0; key < k1; ++key) {
+        for (int key = k0; key < k1 && more; ++key) {
             float k[E], v[E], sk = 0.0f, sv = 0.0f;
             ld_pack<T, E>((const T *)a.k + b * a.k_sb + key * a.k_st + h * a.k_sh + lane * E, k);
             ld_pack<T, E>((const T *)a.v + b * a.v_sb + key * a.v_st + h * a.v_sh + lane * E, v);
@@ -296,6 +298,7 @@ __device__ __noinline__ void dq_row_alone(const DqTileArgs &p, int b, int h, int
             const float ds = ex2(fmaf(sk, a.scale * kLog2e, -lse2)) * (sv - delta) * a.scale;
 #pragma unroll
             for (int e = 0; e < E; ++e) o[e] = fmaf(ds, k[e], o[e]);
+            more = !all_nan(o);
         }
     }
     st_pack<T, E>((T *)p.dq + row * D + lane * E, o);
@@ -938,16 +941,20 @@ __global__ void __launch_bounds__(128) k_dkdv(BwdArgs p) {
             dk[n][e] *= k_unit;
             dv[n][e] *= v_unit;
         }
-    unsigned redo = 0;                           // bit 4 r + e: key r + 8 e is not finite
+    unsigned redo_k = 0, redo_v = 0;             // bit 4 r + e: key r + 8 e is not finite
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        float odd = 0.0f;
+        float odd_k = 0.0f, odd_v = 0.0f;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-            odd += (dk[n][2 * e] + dk[n][2 * e + 1] + dv[n][2 * e] + dv[n][2 * e + 1]) * 0.0f;
-        const unsigned bad = __ballot_sync(0xffffffffu, odd != 0.0f);
-        const bool live = key0 + warp * 16 + r + 8 * e < a.Tk;
-        redo |= __ballot_sync(0xffffffffu, c == 0 && live && (bad >> (4 * r) & 15u)) << e;
+        for (int n = 0; n < D / 8; ++n) {
+            odd_k += (dk[n][2 * e] + dk[n][2 * e + 1]) * 0.0f;
+            odd_v += (dv[n][2 * e] + dv[n][2 * e + 1]) * 0.0f;
+        }
+        const unsigned bad_k = __ballot_sync(0xffffffffu, odd_k != 0.0f);
+        const unsigned bad_v = __ballot_sync(0xffffffffu, odd_v != 0.0f);
+        const bool live = key0 + warp * 16 + r + 8 * e < a.Tk && c == 0;
+        redo_k |= __ballot_sync(0xffffffffu, live && (bad_k >> (4 * r) & 15u)) << e;
+        redo_v |= __ballot_sync(0xffffffffu, live && (bad_v >> (4 * r) & 15u)) << e;
     }
     // keys r and r + 8 of the warp's 16, elements 8 n + 2 c and the next
 #pragma unroll
@@ -968,27 +975,29 @@ __global__ void __launch_bounds__(128) k_dkdv(BwdArgs p) {
         }
     }
     __syncwarp();
-    for (; redo; redo &= redo - 1) {
+    for (unsigned redo = redo_k | redo_v; redo; redo &= redo - 1) {
         const int bit = __ffs(redo) - 1;
+        const bool want_k = redo_k >> bit & 1u, want_v = redo_v >> bit & 1u;
         constexpr int E = D / 32;
         const int key = key0 + warp * 16 + (bit >> 2) + 8 * (bit & 1);
         float x[E], y[E];
         dkdv_key_alone<T, D>(
-            p, b, h, key,
+            p, b, h, key, want_k, want_v,
             [&](auto body) {
                 const uint32_t *mine = bits + my_sub * (int64_t)p.words;
                 for (int w = chunk * p.chunk_words; w < w_end; ++w)
-                    for (uint32_t m = mine[w]; m; m &= m - 1) body(w * 32 + __ffs(m) - 1);
+                    for (uint32_t m = mine[w]; m; m &= m - 1)
+                        if (!body(w * 32 + __ffs(m) - 1)) return;
             },
             x, y);
         const int64_t at = (((int64_t)b * a.Tk + key) * a.Hk + h) * D + lane * E;
+        float *part = p.part + (int64_t)(2 * chunk) * p.part_stride + at;
         if (p.chunks == 1) {
-            st_pack<T, E>((T *)p.dk + at, x);
-            st_pack<T, E>((T *)p.dv + at, y);
+            if (want_k) st_pack<T, E>((T *)p.dk + at, x);
+            if (want_v) st_pack<T, E>((T *)p.dv + at, y);
         } else {
-            float *part = p.part + (int64_t)(2 * chunk) * p.part_stride + at;
-            st_pack<float, E>(part, x);
-            st_pack<float, E>(part + p.part_stride, y);
+            if (want_k) st_pack<float, E>(part, x);
+            if (want_v) st_pack<float, E>(part + p.part_stride, y);
         }
     }
 }

@@ -54,10 +54,13 @@ struct BwdArgs {
 // One key, row by row, for keys whose tile gave a result that is not finite: in
 // the tile a row of q or of the gradient that is not finite, times the weight 0
 // of a key that it does not see, spoils that key too. `each` calls its argument
-// for every query that chose the key's block; lane l gets elements l E ..
+// for every query that chose the key's block, until it returns false: when all of what
+// is wanted (the gradient that is not finite; the other stands) is NaN. Lane l gets
+// elements l E ..
 template <typename T, int D, typename F>
-__device__ __forceinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, int key, F each,
-                                               float (&dk)[D / 32], float (&dv)[D / 32]) {
+__device__ __forceinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, int key, bool want_k,
+                                               bool want_v, F each, float (&dk)[D / 32],
+                                               float (&dv)[D / 32]) {
     const BlkArgs &a = p.a;
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
@@ -70,7 +73,7 @@ __device__ __forceinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, i
 #pragma unroll
     for (int e = 0; e < E; ++e) dk[e] = dv[e] = 0.0f;
     each([&](int t) {
-        if (key >= blk_limit(a, len, t)) return;
+        if (key >= blk_limit(a, len, t)) return true;
         for (int g = 0; g < a.G; ++g) {
             const int head = h * a.G + g;
             const int64_t row = ((int64_t)b * a.Tq + t) * a.Hq + head;
@@ -97,6 +100,7 @@ __device__ __forceinline__ void dkdv_key_alone(const BwdArgs &p, int b, int h, i
                 dv[e] = fmaf(pr, o[e], dv[e]);
             }
         }
+        return (want_k && !all_nan(dk)) || (want_v && !all_nan(dv));
     });
 }
 
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
     float *stats = (float *)(sp + kKeysStats);
     int32_t *list = (int32_t *)(sp + kKeysList);
     __shared__ uint64_t full[2], ready[2], made, done[2], drained;
-    __shared__ uint32_t tmem_slot, odd[2];
+    __shared__ uint32_t tmem_slot, odd[2][2];        // of dV, of dK: a bit per key
     __shared__ int n_queries;
 
     const BlkArgs &a = p.a;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
         base = max(0, min(base, to) - from);
         if (lane == 0) {
             n_queries = base;
-            odd[0] = odd[1] = 0;
+            odd[0][0] = odd[0][1] = odd[1][0] = odd[1][1] = 0;
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&full[i], 32 * kKeysLoaders);
                 mbar_init(&ready[i], 1);
@@ -388,26 +392,29 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            if (bad[i]) atomicOr(&odd[i], bad[i]);
+            if (bad[i]) atomicOr(&odd[half][i], bad[i]);
         asm volatile("bar.sync 1, 256;" ::: "memory");
         for (int i = warp; i < n; i += 8) {
-            if (!(odd[i >> 5] >> (i & 31) & 1u)) continue;
+            const bool want_v = odd[0][i >> 5] >> (i & 31) & 1u;
+            const bool want_k = odd[1][i >> 5] >> (i & 31) & 1u;
+            if (!want_k && !want_v) continue;
             constexpr int E = D / 32;
             float dk[E], dv[E];
             dkdv_key_alone<T, D>(
-                p, b, h, key0 + i,
+                p, b, h, key0 + i, want_k, want_v,
                 [&](auto body) {
-                    for (int q = 0; q < n_queries; ++q) body(list[q]);
+                    for (int q = 0; q < n_queries; ++q)
+                        if (!body(list[q])) return;
                 },
                 dk, dv);
+            const int64_t at = ((int64_t)b * a.Tk + key0 + i) * step + h * D + lane * E;
+            float *y = p.keys.part + (int64_t)blockIdx.x * 2 * kKeysN * D + i * D + lane * E;
             if (alone) {
-                const int64_t at = ((int64_t)b * a.Tk + key0 + i) * step + h * D + lane * E;
-                st_pack<T, E>((T *)p.dk + at, dk);
-                st_pack<T, E>((T *)p.dv + at, dv);
+                if (want_k) st_pack<T, E>((T *)p.dk + at, dk);
+                if (want_v) st_pack<T, E>((T *)p.dv + at, dv);
             } else {
-                float *y = p.keys.part + (int64_t)blockIdx.x * 2 * kKeysN * D + i * D + lane * E;
-                st_pack<float, E>(y, dk);
-                st_pack<float, E>(y + kKeysN * D, dv);
+                if (want_k) st_pack<float, E>(y, dk);
+                if (want_v) st_pack<float, E>(y + kKeysN * D, dv);
             }
         }
         mma_fence_before();

@@ -1,4 +1,5 @@
-"""Values that are not finite, further: rows whose scores are all -infinity."""
+"""Values that are not finite, further: rows whose scores are all -infinity, and the time
+of a step whose gradients are all NaN."""
 import math
 
 import pytest
@@ -43,4 +44,45 @@ def test_rows_whose_scores_are_all_minus_infinity(sdm, cuda_device, dtype, D, T)
     for a, b in ((dk, dk2), (dv, dv2)):      # alone: rounded once, from unrounded weights
         assert torch.isfinite(b[0, 4:]).all()
         assert (a[0, 4:] - b[0, 4:]).abs().max() <= 4 * u * a.abs().max() + 32 * u
+    sdm.dynamic_sync()
+
+
+def timed(f):
+    for _ in range(2):
+        f()
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    f()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("dtype,D,block", [("bf16", 128, 64), ("bf16", 64, 64), ("fp16", 128, 64),
+                                           ("fp16", 64, 16)])
+@pytest.mark.parametrize("what", ["grad", "v", "q"])
+def test_time_of_a_step_that_is_all_nan(sdm, cuda_device, dtype, D, block, what):
+    """A step whose loss overflowed gives NaN everywhere in a small multiple of its time: the
+    rows that are computed again alone stop once nothing of them can change. (Without
+    that it was a multiple of hundreds.)"""
+    B, T, Hq, Hk, n = 1, 2048, 16, 2, 1024 // block
+    q, k, v, grad = (randn(cuda_device, i, B, T, H, D).to(DT[dtype])
+                     for i, H in ((0, Hq), (1, Hk), (2, Hk), (3, Hq)))
+    sel = sdm.select_blocks(q, sdm.block_means(k, block), n, block, T)
+
+    def step():
+        out, lse = sel.attend(q, k, v)
+        return (out, *sel.backward(grad, q, k, v, out, lse))
+
+    clean = timed(step)
+    {"grad": grad, "v": v, "q": q}[what].fill_(math.nan)
+    odd = timed(step)
+    print(f"clean {clean:.3f} ms, NaN {odd:.3f} ms")
+    out, dq, dk, dv = step()
+    if what != "grad":
+        assert torch.isnan(out).all()
+    assert torch.isnan(dq).all() and torch.isnan(dk).all()
+    assert what == "v" or torch.isnan(dv).all()
+    assert odd <= 12 * clean
     sdm.dynamic_sync()
