@@ -145,6 +145,15 @@ spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const fl
                                int32_t *blocks, void *work, int64_t work_bytes, void *stream);
 
 /*
+ * spmm_blocks_select_kept -- the same, and a copy of lengths as the lists were made
+ * for them: int32 [B] at `kept` (NULL: none; not written without lengths or queries).
+ * A caller that adds to its lengths in place passes the copy to the calls below.
+ */
+spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, const float *means,
+                                    int32_t *blocks, int32_t *kept, void *work, int64_t work_bytes,
+                                    void *stream);
+
+/*
  * spmm_blocks_check -- whether every list is strictly ascending block numbers
  * below ceil(Tk / block), then only -1: writes 0 or 1 (a bad list exists) to
  * the device word *bad. The calls below skip an entry that is out of range or

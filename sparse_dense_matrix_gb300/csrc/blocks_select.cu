@@ -59,6 +59,7 @@ struct SelArgs {
     const float *means;
     float *score;            // [rows, NB]
     int32_t *out;
+    int32_t *kept;           // [B] or NULL: a copy of lengths
 };
 
 // First block that is not a candidate; *own = the block that is always taken, or -1.
@@ -260,6 +261,10 @@ __device__ __forceinline__ void best_of_row(const SelArgs &s, int64_t row, const
     const int lane = threadIdx.x & 31;
     const int want = min(cand, a.n - (own >= 0 ? 1 : 0));
     int32_t *out = s.out + row * a.n;
+    if (s.kept && lane == 0 && row % ((int64_t)a.Tq * a.Hk) == 0) {
+        const int b = (int)(row / ((int64_t)a.Tq * a.Hk));
+        s.kept[b] = a.lengths[b];
+    }
     int done = 0;
     if (want > 0 && want < cand) {
         RowKeys<R> keys;
@@ -470,6 +475,12 @@ int64_t spmm_blocks_select_workspace(const spmm_blocks_shape *s) {
 
 spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const float *means,
                                int32_t *blocks, void *work, int64_t work_bytes, void *stream) {
+    return spmm_blocks_select_kept(s, q, means, blocks, nullptr, work, work_bytes, stream);
+}
+
+spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, const float *means,
+                                    int32_t *blocks, int32_t *kept, void *work, int64_t work_bytes,
+                                    void *stream) {
     using namespace spmm;
     const spmm_status st = blk_check(s, false);
     if (st != SPMM_OK) return st;
@@ -488,6 +499,7 @@ spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const fl
     g.means = means;
     g.score = (float *)work;
     g.out = blocks;
+    g.kept = s->lengths ? kept : nullptr;
     cudaStream_t cs = (cudaStream_t)stream;
     cudaError_t e = cudaSuccess;
     if (by_row(s)) {

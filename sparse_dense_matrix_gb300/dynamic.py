@@ -58,6 +58,7 @@ def _declare():
         "spmm_blocks_means": ([S, _Rows, i64, vp, vp], i32),
         "spmm_blocks_select_workspace": ([S], i64),
         "spmm_blocks_select": ([S, _Rows, vp, vp, vp, i64, vp], i32),
+        "spmm_blocks_select_kept": ([S, _Rows, vp, vp, vp, vp, i64, vp], i32),
         "spmm_blocks_check": ([S, vp, vp, vp], i32),
         "spmm_blocks_attend": ([S, _Rows, _Rows, _Rows, vp, vp, vp, vp], i32),
         "spmm_blocks_backward_workspace": ([S], i64),
@@ -331,16 +332,25 @@ def select_blocks(q, means, n: int, block: int, num_keys: int, lengths=None, cau
     _dense(means, "means", _FLOAT, (B, -(-Tk // block), Hk, D), dev)
     s = _Shape(B, Tq, Tk, Hq, Hk, D, block, n, _DTYPE[q.dtype], 1 if causal else 0, 1.0,
                _lengths_ptr(lengths, B, dev))
-    blocks = q.new_empty((B, Tq, Hk, n), dtype=torch.int32)
+    sel = BlockSelection.__new__(BlockSelection)
+    shape = (B, Tq, Hk, n)
+    if lengths is None or not Tq:
+        sel._set(q.new_empty(shape, dtype=torch.int32), shape, block, Tk, causal)
+        if lengths is not None:
+            sel._keep(lengths)
+    else:
+        # room for the call's copy of lengths behind the lists: a second allocation takes
+        # longer than the views that are made of this one when they are asked for
+        rows_ = B * Tq * Hk
+        sel._set(q.new_empty(rows_ * n + B, dtype=torch.int32), shape, block, Tk, causal)
+        sel._lengths = sel._lists + 4 * rows_ * n
     need = lib.spmm_blocks_select_workspace(s)
     work = _scratch(q, need)
-    st = lib.spmm_blocks_select(s, rows, means.data_ptr() or None, blocks.data_ptr(),
-                                None if work is None else work.data_ptr(), need,
-                                _raw_stream(dev.index))
+    st = lib.spmm_blocks_select_kept(s, rows, means.data_ptr() or None, sel._lists, sel._lengths,
+                                     None if work is None else work.data_ptr(), need,
+                                     _raw_stream(dev.index))
     if st:
         _check(st, "spmm_blocks_select")
-    sel = BlockSelection.__new__(BlockSelection)
-    sel._set(blocks, block, Tk, lengths, causal, s.lengths)
     return sel
 
 
@@ -350,7 +360,10 @@ class BlockSelection:
     ``blocks`` int32 [B, Tq, Hk, n]: strictly ascending block numbers, then -1.
     ``lengths`` int32 [B] (None: num_keys): the valid keys of each sequence, whose Tq
     queries are its last tokens. Causal, a query sees the keys up to its position.
-    ``validate=True`` checks the lists (it synchronises)."""
+    ``validate=True`` checks the lists (it synchronises).
+
+    A selection has a copy of its lengths (a decode loop may add to its own in place);
+    given ``blocks`` are not copied."""
 
     def __init__(self, blocks, block: int, num_keys: int, lengths=None, causal: bool = True,
                  validate: bool = True):
@@ -361,30 +374,52 @@ class BlockSelection:
         num_keys = int(num_keys)
         if Hk < 1 or n < 1 or num_keys < 0:
             raise ValueError(f"blocks must be [B, Tq, Hk >= 1, n >= 1], got {list(blocks.shape)}")
-        self._set(blocks, _block_size(block), num_keys, lengths, causal,
-                  _lengths_ptr(lengths, B, blocks.device))
-        if validate:
-            with torch.cuda.device(self.device):
+        _lengths_ptr(lengths, B, blocks.device)                 # its checks
+        with torch.cuda.device(blocks.device):
+            self._set(blocks, (B, Tq, Hk, n), _block_size(block), num_keys, causal)
+            if lengths is not None:
+                self._keep(lengths)
+            if validate:
                 bad = blocks.new_empty(1)
                 s = _Shape(B, Tq, num_keys, Hk, Hk, 64, self.block, n, 1, int(self.causal), 1.0,
                            self._lengths)
-                _check(lib.spmm_blocks_check(s, blocks.data_ptr() or None, bad.data_ptr(),
+                _check(lib.spmm_blocks_check(s, self._lists or None, bad.data_ptr(),
                                              _raw_stream(self.device.index)), "spmm_blocks_check")
                 if int(bad.item()):
                     raise SpmmError(2, "a list of blocks is not strictly ascending block numbers "
                                        "followed by -1")
 
-    def _set(self, blocks, block, num_keys, lengths, causal, lengths_ptr):
-        self.device, self.blocks, self.block = blocks.device, blocks, block
-        self.num_keys, self.lengths, self.causal = num_keys, lengths, bool(causal)
-        self._lengths = lengths_ptr
+    def _set(self, lists, shape, block, num_keys, causal):
+        """`lists`: the blocks, or one dimension of them with the lengths behind."""
+        self.device, self._mem, self._lists = lists.device, lists, lists.data_ptr()
+        self._shape, self.block, self.num_keys = shape, block, num_keys
+        self.causal, self._lengths, self._kept = bool(causal), None, None
+
+    def _keep(self, lengths):
+        self._kept = lengths.clone()
+        self._lengths = self._kept.data_ptr()
+
+    @property
+    def blocks(self):
+        """int32 [B, Tq, Hk, n]"""
+        if self._mem.dim() == 4:
+            return self._mem
+        B, Tq, Hk, n = self._shape
+        return self._mem.as_strided(self._shape, (Tq * Hk * n, Hk * n, n, 1))
+
+    @property
+    def lengths(self):
+        """int32 [B], or None"""
+        if self._kept is None and self._lengths is not None:
+            self._kept = self._mem[self._mem.numel() - self._shape[0]:]
+        return self._kept
 
     def _problem(self, q, k, v, scale):
         """The call's shape, and the rows of q, k and v."""
         dev = self.device
         rows = (_heads(q, "q", _HALVES, dev), _heads(k, "k", (q.dtype,), dev),
                 _heads(v, "v", (q.dtype,), dev))
-        B, Tq, Hk, n = self.blocks.shape
+        B, Tq, Hk, n = self._shape
         Bq, T, Hq, D = q.shape
         if Bq != B or T != Tq or Hq % Hk or Hq < 1:
             raise ValueError(f"q must be [{B}, {Tq}, a multiple of {Hk}, D], got {list(q.shape)}")
@@ -412,7 +447,7 @@ class BlockSelection:
         s, rows = self._problem(q, k, v, scale)
         out = q.new_empty(q.shape)
         lse = q.new_empty(q.shape[:3], dtype=torch.float32)
-        st = lib.spmm_blocks_attend(s, *rows, self.blocks.data_ptr(), out.data_ptr(),
+        st = lib.spmm_blocks_attend(s, *rows, self._lists, out.data_ptr(),
                                     lse.data_ptr(), _raw_stream(self.device.index))
         if st:
             _check(st, "spmm_blocks_attend")
@@ -434,7 +469,7 @@ class BlockSelection:
         dq, dk, dv = q.new_empty(q.shape), k.new_empty(k.shape), v.new_empty(v.shape)
         need = lib.spmm_blocks_backward_workspace(s)
         work = _scratch(q, need)
-        st = lib.spmm_blocks_backward(s, *rows, self.blocks.data_ptr(), out.data_ptr(),
+        st = lib.spmm_blocks_backward(s, *rows, self._lists, out.data_ptr(),
                                       lse.data_ptr(), g, dq.data_ptr(), dk.data_ptr(),
                                       dv.data_ptr(), None if work is None else work.data_ptr(),
                                       need, _raw_stream(self.device.index))
