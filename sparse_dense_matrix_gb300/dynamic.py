@@ -255,7 +255,9 @@ def _heads(t, name, dtypes, dev=None):
     sb, st, sh, sd = t.stride()
     at, e = t.data_ptr(), t.element_size()
     if ((sb | st | sh) * e | at) % 16 or (sd != 1 and t.shape[3] > 1):
-        if t.numel():
+        # the stride of a dimension of one means nothing, and may be any number
+        sb, st, sh = (0 if n == 1 else x for n, x in zip(t.shape, (sb, st, sh)))
+        if t.numel() and (((sb | st | sh) * e | at) % 16 or (sd != 1 and t.shape[3] > 1)):
             raise ValueError(f"{name} must have adjacent elements in a row and rows at 16-byte "
                              f"boundaries (strides {tuple(t.stride())})")
     return _Rows(at, sb, st, sh)

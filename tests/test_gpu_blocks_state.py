@@ -1,4 +1,4 @@
-"""What a selection keeps: the lengths that it was made for."""
+"""What a selection keeps (the lengths that it was made for), and strides that mean nothing."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +48,27 @@ def test_lengths_without_queries(sdm, cuda_device):
     L += 1
     assert torch.equal(sel.lengths, before) and sel.blocks.shape == (2, 0, 2, 2)
     assert sdm.select_blocks(q, sdm.block_means(k, 16), 2, 16, 12).lengths is None
+
+
+def test_strides_of_dimensions_of_one(sdm, cuda_device):
+    """They mean nothing, and torch gives them any value."""
+    D = 64
+    for dt in (torch.bfloat16, torch.float16):
+        q, k, v, g = (randn(cuda_device, i, D, 1).to(dt).t()[None, None] for i in range(4))
+        assert q.shape == (1, 1, 1, D) and q.stride(2) == 1
+        sel = sdm.select_blocks(q, sdm.block_means(k, 16), 1, 16, 1)
+        out, lse = sel.attend(q, k, v)
+        assert torch.equal(out, v.contiguous())
+        dq, dk, dv = sel.backward(g, q, k, v, out, lse)
+        assert torch.equal(dv, g.contiguous())
+    # one head of many queries, its stride an odd number
+    T = 300
+    q, k, v = (torch.as_strided(randn(cuda_device, i, T * D).half(), (1, T, 1, D), (1, D, 3, 1))
+               for i in range(3))
+    def run(q, k, v):
+        sel = sdm.select_blocks(q, sdm.block_means(k, 32), 4, 32, T)
+        out, lse = sel.attend(q, k, v)
+        return (sel.blocks, out, lse, *sel.backward(q, q, k, v, out, lse))
+    want = run(*(x.contiguous().clone(memory_format=torch.contiguous_format).view(1, T, 1, D)
+                 for x in (q, k, v)))
+    assert all(torch.equal(a, b) for a, b in zip(want, run(q, k, v)))
