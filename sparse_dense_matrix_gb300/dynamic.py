@@ -11,6 +11,9 @@ Like the rest of the binding this marshals arguments only; the computation runs
 in the CUDA library. Calls are asynchronous on ``stream`` (default: the current
 one), on which their outputs and scratch are allocated, and never synchronise,
 except the check of lists that a caller made (``BlockSelection(validate=True)``).
+Ordering streams is the caller's: a call does not wait for the work that made its
+inputs on another one. What a call on a given stream reads, and what routes and
+selections hold, keeps its memory until that stream is done with it.
 """
 from __future__ import annotations
 
@@ -85,6 +88,14 @@ def _elsewhere(dev, stream):
     return torch.cuda.stream(stream)
 
 
+def _lent(dev, *tensors):
+    """The current stream uses them: their memory is not handed out before it is done."""
+    stream = torch.cuda.current_stream(dev)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _tensor(t, name, dtypes, ndim, dev=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -152,9 +163,11 @@ class ExpertRoutes:
         else:
             with ctx:
                 self._sort(ids)
+                _lent(dev, ids)
 
     def _sort(self, ids):
         T, k, E = self.T, self.k, self.num_experts
+        self._stream = stream = _raw_stream(self.device.index)
         self.slots = torch.empty_like(ids)
         self.offsets = ids.new_empty(E + 1)
         need = lib.spmm_routes_workspace(T, k, E)
@@ -162,10 +175,16 @@ class ExpertRoutes:
         # what every product's call begins its list of routes with
         self._routes = (self.slots.data_ptr(), self.offsets.data_ptr(), T, k, E)
         st = lib.spmm_routes_sort(ids.data_ptr(), T, k, E, *self._routes[:2],
-                                  None if work is None else work.data_ptr(), need,
-                                  _raw_stream(self.device.index))
+                                  None if work is None else work.data_ptr(), need, stream)
         if st:
             _check(st, "spmm_routes_sort")
+
+    def _on_stream(self):
+        """The current stream, which the routes' own tensors are now used on."""
+        stream = _raw_stream(self.device.index)
+        if stream != self._stream:
+            _lent(self.device, self.slots, self.offsets)
+        return stream
 
     def _by_token(self, x, name):
         _tensor(x, name, _DTYPE, 2, self.device)
@@ -197,11 +216,13 @@ class ExpertRoutes:
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
-                return self.dispatch(x)
+                xs = self.dispatch(x)
+                _lent(self.device, x)
+                return xs
         H, ld = self._by_token(x, "x")
         xs = x.new_empty((self.T * self.k, H))
         st = lib.spmm_routes_dispatch(_DTYPE[x.dtype], x.data_ptr(), ld, *self._routes, H,
-                                      xs.data_ptr(), _raw_stream(self.device.index))
+                                      xs.data_ptr(), self._on_stream())
         if st:
             _check(st, "spmm_routes_dispatch")
         return xs
@@ -212,12 +233,14 @@ class ExpertRoutes:
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
-                return self.combine(y, weights)
+                out = self.combine(y, weights)
+                _lent(self.device, y, weights)
+                return out
         H = self._by_slot(y, "y")
         w = self._weights(weights)
         out = y.new_empty((self.T, H))
         st = lib.spmm_routes_combine(_DTYPE[y.dtype], y.data_ptr(), w, *self._routes, H,
-                                     out.data_ptr(), _raw_stream(self.device.index))
+                                     out.data_ptr(), self._on_stream())
         if st:
             _check(st, "spmm_routes_combine")
         return out
@@ -232,7 +255,9 @@ class ExpertRoutes:
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
-                return self.combine_backward(grad, y, weights)
+                grads = self.combine_backward(grad, y, weights)
+                _lent(self.device, grad, y, weights)
+                return grads
         H, ld = self._by_token(grad, "grad")
         self._by_slot(y, "y", H)
         if y.dtype != grad.dtype:
@@ -242,7 +267,7 @@ class ExpertRoutes:
         dw = None if w is None else torch.empty_like(weights)
         st = lib.spmm_routes_combine_backward(
             _DTYPE[y.dtype], grad.data_ptr(), ld, y.data_ptr(), w, *self._routes, H, dy.data_ptr(),
-            None if dw is None else dw.data_ptr(), _raw_stream(self.device.index))
+            None if dw is None else dw.data_ptr(), self._on_stream())
         if st:
             _check(st, "spmm_routes_combine_backward")
         return dy, dw
@@ -285,7 +310,9 @@ def block_means(k, block: int = 64, lengths=None, out=None, new_keys: int | None
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return block_means(k, block, lengths, out, new_keys)
+            means = block_means(k, block, lengths, out, new_keys)
+            _lent(dev, k, lengths, out)
+            return means
     B, Tk, Hk, D = k.shape
     block = _block_size(block)
     if D % 8 or not 8 <= D <= 256:
@@ -320,7 +347,9 @@ def select_blocks(q, means, n: int, block: int, num_keys: int, lengths=None, cau
     ctx = _elsewhere(dev, stream)
     if ctx is not None:
         with ctx:
-            return select_blocks(q, means, n, block, num_keys, lengths, causal)
+            sel = select_blocks(q, means, n, block, num_keys, lengths, causal)
+            _lent(dev, q, means, lengths)
+            return sel
     B, Tq, Hq, D = q.shape
     block, n, Tk = _block_size(block), int(n), int(num_keys)
     _tensor(means, "means", _FLOAT, 4, dev)
@@ -396,6 +425,14 @@ class BlockSelection:
         self.device, self._mem, self._lists = lists.device, lists, lists.data_ptr()
         self._shape, self.block, self.num_keys = shape, block, num_keys
         self.causal, self._lengths, self._kept = bool(causal), None, None
+        self._stream = _raw_stream(self.device.index)
+
+    def _on_stream(self):
+        """The current stream, which the selection's own tensors are now used on."""
+        stream = _raw_stream(self.device.index)
+        if stream != self._stream:
+            _lent(self.device, self._mem, self._kept)
+        return stream
 
     def _keep(self, lengths):
         self._kept = lengths.clone()
@@ -445,12 +482,14 @@ class BlockSelection:
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
-                return self.attend(q, k, v, scale)
+                got = self.attend(q, k, v, scale)
+                _lent(self.device, q, k, v)
+                return got
         s, rows = self._problem(q, k, v, scale)
         out = q.new_empty(q.shape)
         lse = q.new_empty(q.shape[:3], dtype=torch.float32)
         st = lib.spmm_blocks_attend(s, *rows, self._lists, out.data_ptr(),
-                                    lse.data_ptr(), _raw_stream(self.device.index))
+                                    lse.data_ptr(), self._on_stream())
         if st:
             _check(st, "spmm_blocks_attend")
         return out, lse
@@ -461,7 +500,9 @@ class BlockSelection:
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
-                return self.backward(grad, q, k, v, out, lse, scale)
+                grads = self.backward(grad, q, k, v, out, lse, scale)
+                _lent(self.device, grad, q, k, v, out, lse)
+                return grads
         s, rows = self._problem(q, k, v, scale)
         g = _heads(grad, "grad", (q.dtype,), self.device)
         if grad.shape != q.shape:
@@ -474,7 +515,7 @@ class BlockSelection:
         st = lib.spmm_blocks_backward(s, *rows, self._lists, out.data_ptr(),
                                       lse.data_ptr(), g, dq.data_ptr(), dk.data_ptr(),
                                       dv.data_ptr(), None if work is None else work.data_ptr(),
-                                      need, _raw_stream(self.device.index))
+                                      need, self._on_stream())
         if st:
             _check(st, "spmm_blocks_backward")
         return dq, dk, dv
