@@ -32,10 +32,20 @@ typedef enum { SPMM_F32 = 0, SPMM_BF16 = 1, SPMM_F16 = 2 } spmm_dtype;
 
 /*
  * spmm_dynamic_sync -- wait for `stream`, then report SPMM_ERR_TIMEOUT if a
- * bounded device-side wait of one of these calls gave up since the last time
- * (its outputs are then incomplete), and clear that. Synchronous.
+ * bounded device-side wait of one of these calls on it gave up since it was last
+ * asked (its outputs are then incomplete), or one in a captured graph, whichever
+ * stream of the current device replayed it: each stream is told of a graph's once.
+ * Synchronous.
  */
 spmm_status spmm_dynamic_sync(void *stream);
+
+/*
+ * spmm_dynamic_check_wait_timeout -- diagnostic of that path, as
+ * spmm_check_wait_timeout is of a plan's: one warp on `stream` waits for an
+ * arrival that nobody makes and gives up after limit_us microseconds (1 to 10^7),
+ * as a broken wait of these calls would. Asynchronous.
+ */
+spmm_status spmm_dynamic_check_wait_timeout(int64_t limit_us, void *stream);
 
 /* ------------------------------------------------------------------ routes */
 

@@ -19,7 +19,6 @@
 namespace spmm {
 namespace {
 
-__device__ int32_t g_dynamic_err[kErrWords];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
 // Warps of a CTA: eight for one n-tile (two CTAs per SM, 128 registers), four for two.
@@ -884,10 +883,6 @@ bool by_tile(const spmm_blocks_shape *s, const spmm_rows &k, const spmm_rows &v)
 
 }  // namespace
 
-cudaError_t dynamic_err(int32_t **err) {
-    return cudaGetSymbolAddress((void **)err, g_dynamic_err);
-}
-
 cudaError_t encode_rows(const spmm_rows &r, const spmm_blocks_shape *s, int box_rows,
                         CUtensorMap *map) {
     if (!g_encode) {
@@ -919,22 +914,6 @@ cudaError_t encode_rows(const spmm_rows &r, const spmm_blocks_shape *s, int box_
 
 extern "C" {
 
-spmm_status spmm_dynamic_sync(void *stream) {
-    using namespace spmm;
-    cudaStream_t s = (cudaStream_t)stream;
-    int32_t *err = nullptr, word = 0;
-    cudaError_t e = dynamic_err(&err);
-    if (e == cudaSuccess)
-        e = cudaMemcpyAsync(&word, err + kErrTimeout, sizeof(word), cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && word) {
-        e = cudaMemsetAsync(err + kErrTimeout, 0, sizeof(word), s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-        if (e == cudaSuccess) return SPMM_ERR_TIMEOUT;
-    }
-    return cuda_status(e);
-}
-
 spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
                                const int32_t *blocks, void *out, float *lse, void *stream) {
     using namespace spmm;
@@ -957,7 +936,7 @@ spmm_status spmm_blocks_attend(const spmm_blocks_shape *s, spmm_rows q, spmm_row
         t.out = out;
         t.lse = lse;
         const int box = (int)std::min<int64_t>(s->block, 64);
-        cudaError_t e = dynamic_err(&t.t.err);
+        cudaError_t e = dynamic_err(cs, &t.t.err);
         if (e == cudaSuccess) e = encode_rows(k, s, box, &t.t.k_map);
         if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
         if (e == cudaSuccess) {

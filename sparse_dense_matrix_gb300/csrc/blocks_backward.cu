@@ -1081,7 +1081,7 @@ template <typename T> cudaError_t launch_keys(BwdArgs &p, const BwdPlan &bp, cud
     p.keys.first = (int32_t *)w;
     p.keys.item = (int2 *)(w + round_up((bp.tiles + 1) * 4, 256));
     p.keys.part = (float *)((char *)p.keys.item + round_up(bp.items * 8, 256));
-    cudaError_t e = dynamic_err(&p.err);
+    cudaError_t e = dynamic_err(s, &p.err);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k_dkdv_keys<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  kKeysSmem);
@@ -1147,7 +1147,7 @@ cudaError_t launch_bwd(BwdArgs &p, const BwdPlan &bp, const spmm_blocks_shape *s
         t.delta = p.delta;
         t.dq = p.dq;
         const int box = (int)std::min<int64_t>(s->block, 64);
-        e = dynamic_err(&t.t.err);
+        e = dynamic_err(cs, &t.t.err);
         if (e == cudaSuccess) e = encode_rows(k, s, box, &t.t.k_map);
         if (e == cudaSuccess) e = encode_rows(v, s, box, &t.t.v_map);
         if (e == cudaSuccess)

@@ -300,7 +300,4 @@ inline bool blocks_by_tile(const spmm_blocks_shape *s, const spmm_rows &k, const
     return tile_us < lists * (0.012 + keys * s->D * 0.31e-6);
 }
 
-// Device word that a bounded wait which gave up sets (spmm_dynamic_sync reads it).
-cudaError_t dynamic_err(int32_t **err);
-
 }  // namespace spmm

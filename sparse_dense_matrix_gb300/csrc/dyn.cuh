@@ -57,4 +57,8 @@ inline spmm_status cuda_status(cudaError_t e) {
     return e == cudaErrorMemoryAllocation ? SPMM_ERR_OOM : SPMM_ERR_CUDA;
 }
 
+// The current device's word that a bounded wait which gave up sets, for a launch on
+// `s` (spmm_dynamic_sync reads it).
+cudaError_t dynamic_err(cudaStream_t s, int32_t **err);
+
 }  // namespace spmm

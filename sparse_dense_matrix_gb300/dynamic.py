@@ -52,6 +52,7 @@ def _declare():
     vp, i64, i32, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.POINTER(_Shape)
     sigs = {
         "spmm_dynamic_sync": ([vp], i32),
+        "spmm_dynamic_check_wait_timeout": ([i64, vp], i32),
         "spmm_routes_workspace": ([i64] * 3, i64),
         "spmm_routes_sort": ([vp, i64, i64, i64, vp, vp, vp, i64, vp], i32),
         "spmm_routes_dispatch": ([i32, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp], i32),
@@ -121,7 +122,10 @@ def _dense(t, name, dtypes, shape, dev):
 
 def dynamic_sync(stream=None) -> None:
     """Wait for the stream; SpmmError (SPMM_ERR_TIMEOUT) if a bounded device-side wait of
-    one of these calls gave up since the last time."""
+    one of these calls on it, or of one in a captured graph, gave up since it was last asked."""
+    if stream is not None and stream.device.index != _current_device():
+        with torch.cuda.device(stream.device):
+            return dynamic_sync(stream)
     handle = _raw_stream(_current_device()) if stream is None else stream.cuda_stream
     _check(lib.spmm_dynamic_sync(handle), "spmm_dynamic_sync")
 
