@@ -121,6 +121,8 @@ typedef struct {
  * up to its position (none if that is negative); otherwise all len_b keys.
  * Keys past those are never used, whatever they hold.
  * Head h of Hq reads the keys and the selection of head h / (Hq / Hk).
+ * Limits, beyond which a call is SPMM_ERR_UNSUPPORTED: Tq and Tk 2^26, n 2^20,
+ * Hq 65535, B Tq Hq < 2^31, B Tk Hk 2^40.
  */
 typedef struct {
     int64_t B, Tq, Tk, Hq, Hk, D;

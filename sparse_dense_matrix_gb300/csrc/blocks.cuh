@@ -143,7 +143,10 @@ inline spmm_status blk_check(const spmm_blocks_shape *s, bool attend) {
     if (s->Tq > (1 << 26) || s->Tk > (1 << 26) || s->Hq > 65535 || s->n > (1 << 20) ||
         s->B > INT32_MAX)
         return SPMM_ERR_UNSUPPORTED;
-    if (s->B && s->Tq && s->Hq * s->Tq > (int64_t)INT32_MAX / s->B) return SPMM_ERR_UNSUPPORTED;
+    // (and sizes that are multiples of all keys' bytes stay far below 2^63)
+    if (s->B * s->Hk > ((int64_t)1 << 40) / std::max<int64_t>(s->Tk, 1)) return SPMM_ERR_UNSUPPORTED;
+    if (s->B && s->Hq * std::max<int64_t>(s->Tq, 1) > (int64_t)INT32_MAX / s->B)
+        return SPMM_ERR_UNSUPPORTED;
     return SPMM_OK;
 }
 
@@ -170,6 +173,10 @@ inline void set_rows(const void *&p, int64_t &sb, int64_t &st, int64_t &sh, cons
     st = r.st;
     sh = r.sh;
 }
+
+// (Sequence, kv head) pairs that one launch takes in its y or z dimension; for more of
+// them there are several launches.
+constexpr int64_t kPairs = 65535;
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 

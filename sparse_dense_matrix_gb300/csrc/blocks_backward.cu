@@ -739,12 +739,12 @@ __global__ void __launch_bounds__(128) k_dkdv(BwdArgs p) {
 
     const BlkArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk;
+    const int pair = p.pair0 + blockIdx.y, b = pair / a.Hk, h = pair % a.Hk;
     const int chunk = blockIdx.z;
     const int key0 = blockIdx.x * KT, blk = key0 / a.block;
     if (key0 >= a.Tk) return;
     const int len = blk_len(a, b);
-    const uint32_t *bits = p.bits + ((int64_t)blockIdx.y * a.NB + blk) * p.words;
+    const uint32_t *bits = p.bits + ((int64_t)pair * a.NB + blk) * p.words;
     const int subs = min(NS, a.NB - blk), my_sub = warp * NS / 4;    // of the CTA, of the warp
     const int w_end = min(p.words, (chunk + 1) * p.chunk_words);
     const float scale2 = a.scale * kLog2e, ds_unit = a.scale * kPUnit<T>;
@@ -1063,15 +1063,19 @@ BwdPlan bwd_plan(const spmm_blocks_shape *s) {
 }
 
 template <typename T, int D, int NS>
-cudaError_t launch_dkdv(const BwdArgs &p, int64_t B, cudaStream_t s) {
+cudaError_t launch_dkdv(BwdArgs &p, int64_t B, cudaStream_t s) {
     const size_t smem = 2 * 64 * D * 2 + 4 * kRt * D * 2 + 2 * 4 * kRt * 4 + kSegWords * 32 * 4;
     const cudaError_t e = cudaFuncSetAttribute(
         k_dkdv<T, D, NS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    k_dkdv<T, D, NS><<<dim3((unsigned)((p.a.Tk + 63) / 64), (unsigned)(B * p.a.Hk),
-                            (unsigned)p.chunks),
-                       128, smem, s>>>(p);
-    count_launch();
+    const int64_t pairs = B * p.a.Hk;
+    for (int64_t i = 0; i < pairs; i += kPairs) {
+        p.pair0 = (int)i;
+        k_dkdv<T, D, NS><<<dim3((unsigned)((p.a.Tk + 63) / 64), (unsigned)std::min(kPairs, pairs - i),
+                                (unsigned)p.chunks),
+                           128, smem, s>>>(p);
+        count_launch();
+    }
     return cudaGetLastError();
 }
 
@@ -1219,7 +1223,9 @@ spmm_status spmm_blocks_backward(const spmm_blocks_shape *s, spmm_rows q, spmm_r
     const BwdPlan bp = bwd_plan(s);
     if (!work || (uintptr_t)work % 16 || work_bytes < bp.bits_bytes + bp.delta_bytes + bp.part_bytes)
         return SPMM_ERR_INVALID_ARG;
-    if (s->B * s->Hk > 65535 || s->B * s->Tq * s->Hk > INT32_MAX / s->n)
+    // launches of 2^31 CTAs: more lists, keys or items than memory holds
+    if ((s->B * s->Tq * s->Hk * s->n + 255) / 256 > INT32_MAX || bp.items > INT32_MAX ||
+        s->B * s->Tk * s->Hk * s->D / 2048 >= INT32_MAX)
         return SPMM_ERR_UNSUPPORTED;
     BwdArgs p{};
     p.a = blk_args(s, blocks);

@@ -46,6 +46,7 @@ struct BwdArgs {
     int chunk_words;
     float *part;             // [chunks][2][B, Tk, Hk, D] when chunks > 1
     int64_t part_stride;     // B Tk Hk D
+    int pair0;               // of the launch's (sequence, kv head) pairs (k_dkdv)
     int gt;
     int32_t *err;
     KeyItems keys;

@@ -14,9 +14,9 @@ constexpr int kMeanThreads = 128;
 
 template <typename T>
 __global__ void __launch_bounds__(kMeanThreads) k_block_means(BlkArgs a, int D, int new_keys,
-                                                             float *__restrict__ means) {
+                                                             int pair0, float *__restrict__ means) {
     __shared__ float part[kMeanThreads * 8];
-    const int b = blockIdx.y / a.Hk, h = blockIdx.y % a.Hk;
+    const int pair = pair0 + blockIdx.y, b = pair / a.Hk, h = pair % a.Hk;
     const int len = blk_len(a, b);
     int c = blockIdx.x;
     if (new_keys >= 0) {
@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(kMeanThreads) k_block_means(BlkArgs a, int D, 
 struct SelArgs {
     BlkArgs a;
     int D;
+    int pair0;               // of the launch's (sequence, kv head) pairs, for the tiles
     int64_t rows;            // B Tq Hk
     const float *means;
     float *score;            // [rows, NB]
@@ -126,7 +127,7 @@ constexpr int kSk = 32;                 // depth of one step
 template <typename T> __global__ void __launch_bounds__(256) k_score_tiles(SelArgs s) {
     __shared__ float qt[kSk][kSt + 4], mt[kSk][kSc + 4];
     const BlkArgs &a = s.a;
-    const int bh = blockIdx.z, b = bh / a.Hk, h = bh % a.Hk;
+    const int pair = s.pair0 + blockIdx.z, b = pair / a.Hk, h = pair % a.Hk;
     const int t0 = blockIdx.y * kSt, c0 = blockIdx.x * kSc;
     int own;
     if (c0 >= candidates(a, b, min(t0 + kSt, a.Tq) - 1, &own)) return;
@@ -416,10 +417,16 @@ cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t 
         k_score_few<T><<<dim3((unsigned)((a.NB + 31) / 32), (unsigned)s.rows), 128, 0, st>>>(s);
         count_launch();
     } else {
-        k_score_tiles<T><<<dim3((unsigned)((a.NB + kSc - 1) / kSc),
-                                (unsigned)((a.Tq + kSt - 1) / kSt), (unsigned)(B * a.Hk)),
-                           256, 0, st>>>(s);
-        count_launch();
+        SelArgs p = s;
+        const int64_t pairs = B * a.Hk;
+        for (int64_t i = 0; i < pairs; i += kPairs) {
+            p.pair0 = (int)i;
+            k_score_tiles<T><<<dim3((unsigned)((a.NB + kSc - 1) / kSc),
+                                    (unsigned)((a.Tq + kSt - 1) / kSt),
+                                    (unsigned)std::min(kPairs, pairs - i)),
+                               256, 0, st>>>(p);
+            count_launch();
+        }
     }
     return cudaGetLastError();
 }
@@ -450,19 +457,22 @@ spmm_status spmm_blocks_means(const spmm_blocks_shape *s, spmm_rows k, int64_t n
     if (st != SPMM_OK) return st;
     if (s->B == 0 || s->Tk == 0 || new_keys == 0) return SPMM_OK;
     if (!means || !rows_ok(k, dtype_bytes(s->dtype))) return SPMM_ERR_INVALID_ARG;
-    if (s->B * s->Hk > 65535) return SPMM_ERR_UNSUPPORTED;
     BlkArgs a = blk_args(s, nullptr);
     set_rows(a.k, a.k_sb, a.k_st, a.k_sh, k);
     const int64_t most = new_keys < 0 ? a.NB : std::min<int64_t>(a.NB, new_keys / s->block + 2);
     const int nk = (int)std::min<int64_t>(new_keys, INT32_MAX);
-    const dim3 grid((unsigned)most, (unsigned)(s->B * s->Hk));
     cudaStream_t cs = (cudaStream_t)stream;
     const int D = (int)s->D;
-    if (s->dtype == SPMM_F32) k_block_means<float><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, means);
-    else if (s->dtype == SPMM_BF16)
-        k_block_means<__nv_bfloat16><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, means);
-    else k_block_means<__half><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, means);
-    count_launch();
+    const int64_t pairs = s->B * s->Hk;
+    for (int64_t i = 0; i < pairs; i += kPairs) {
+        const dim3 grid((unsigned)most, (unsigned)std::min(kPairs, pairs - i));
+        if (s->dtype == SPMM_F32)
+            k_block_means<float><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, (int)i, means);
+        else if (s->dtype == SPMM_BF16)
+            k_block_means<__nv_bfloat16><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, (int)i, means);
+        else k_block_means<__half><<<grid, kMeanThreads, 0, cs>>>(a, D, nk, (int)i, means);
+        count_launch();
+    }
     return cuda_status(cudaGetLastError());
 }
 
@@ -489,8 +499,7 @@ spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, con
     if (s->Tk > 0 && (!means || (uintptr_t)means % 16)) return SPMM_ERR_INVALID_ARG;
     const int64_t need = spmm_blocks_select_workspace(s);
     if (need && (!work || work_bytes < need)) return SPMM_ERR_INVALID_ARG;
-    if (tiled(s) && (s->B * s->Hk > 65535 || (s->Tq + kSt - 1) / kSt > 65535))
-        return SPMM_ERR_UNSUPPORTED;
+    if (tiled(s) && (s->Tq + kSt - 1) / kSt > 65535) return SPMM_ERR_UNSUPPORTED;
     SelArgs g{};
     g.a = blk_args(s, nullptr);
     set_rows(g.a.q, g.a.q_sb, g.a.q_st, g.a.q_sh, q);
