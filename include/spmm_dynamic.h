@@ -151,6 +151,8 @@ spmm_status spmm_blocks_means(const spmm_blocks_shape *s, spmm_rows k, int64_t n
  * Causal: the block of the query's own position, and the n - 1 blocks before it
  * with the largest scores. Otherwise the n largest of all blocks that hold a
  * key. Equal scores go to the lowest block; NaN is below every number.
+ * Prompts are taken in strips of queries: the scratch is at most 1 GB or, if that is
+ * more, the scores of 64 queries of each sequence (of fewer than 24: of all of them).
  */
 int64_t spmm_blocks_select_workspace(const spmm_blocks_shape *s);
 spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const float *means,

@@ -49,14 +49,15 @@ __global__ void __launch_bounds__(kMeanThreads) k_block_means(BlkArgs a, int D, 
 }
 
 // ----------------------------------------------------------------- scores
-// score[row, c], row = (b, t, h) in that order, written for the candidates only:
+// score[row, c], row = (b, t - t0, h) in that order, written for the candidates only:
 // causal c < position / block (the block of the position itself is always
 // taken), else c < blocks that hold a key.
 struct SelArgs {
     BlkArgs a;
     int D;
     int pair0;               // of the launch's (sequence, kv head) pairs, for the tiles
-    int64_t rows;            // B Tq Hk
+    int t0, nt;              // the strip's queries: t0 .. t0 + nt - 1 of each sequence
+    int64_t rows;            // B nt Hk
     const float *means;
     float *score;            // [rows, NB]
     int32_t *out;
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(128) k_score_few(SelArgs s) {
     const int64_t row = blockIdx.y;
     const int h = (int)(row % a.Hk);
     const int64_t bt = row / a.Hk;
-    const int t = (int)(bt % a.Tq), b = (int)(bt / a.Tq);
+    const int t = s.t0 + (int)(bt % s.nt), b = (int)(bt / s.nt);
     int own;
     const int cand = candidates(a, b, t, &own);
     const int c0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 8;
@@ -128,12 +129,12 @@ template <typename T> __global__ void __launch_bounds__(256) k_score_tiles(SelAr
     __shared__ float qt[kSk][kSt + 4], mt[kSk][kSc + 4];
     const BlkArgs &a = s.a;
     const int pair = s.pair0 + blockIdx.z, b = pair / a.Hk, h = pair % a.Hk;
-    const int t0 = blockIdx.y * kSt, c0 = blockIdx.x * kSc;
+    const int t0 = s.t0 + blockIdx.y * kSt, t1 = s.t0 + s.nt, c0 = blockIdx.x * kSc;
     int own;
-    if (c0 >= candidates(a, b, min(t0 + kSt, a.Tq) - 1, &own)) return;
+    if (c0 >= candidates(a, b, min(t0 + kSt, t1) - 1, &own)) return;
     const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
     const int qr = threadIdx.x / 4, qd = threadIdx.x % 4 * 8;     // row and elements it loads
-    const T *qp = (const T *)a.q + b * a.q_sb + min(t0 + qr, a.Tq - 1) * a.q_st +
+    const T *qp = (const T *)a.q + b * a.q_sb + min(t0 + qr, t1 - 1) * a.q_st +
                   (int64_t)h * a.G * a.q_sh + qd;
     float acc[4][8] = {};
     for (int d0 = 0; d0 < s.D; d0 += kSk) {
@@ -183,8 +184,8 @@ template <typename T> __global__ void __launch_bounds__(256) k_score_tiles(SelAr
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = t0 + ty * 4 + i;
-        if (t >= a.Tq) continue;
-        float *p = s.score + (((int64_t)b * a.Tq + t) * a.Hk + h) * a.NB;
+        if (t >= t1) continue;
+        float *p = s.score + (((int64_t)b * s.nt + t - s.t0) * a.Hk + h) * a.NB;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = c0 + (j >> 2) * 64 + tx * 4 + (j & 3);
@@ -319,10 +320,11 @@ __device__ __forceinline__ void best_of_row(const SelArgs &s, int64_t row, const
 template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
     const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= s.rows) return;
-    const int64_t bt = row / s.a.Hk;
+    const int64_t bt = row / s.a.Hk, b = bt / s.nt;
+    const int t = s.t0 + (int)(bt % s.nt);
     int own;
-    const int cand = candidates(s.a, (int)(bt / s.a.Tq), (int)(bt % s.a.Tq), &own);
-    best_of_row<R>(s, row, s.score + row * s.a.NB, cand, own);
+    const int cand = candidates(s.a, (int)b, t, &own);
+    best_of_row<R>(s, (b * s.a.Tq + t) * s.a.Hk + row % s.a.Hk, s.score + row * s.a.NB, cand, own);
 }
 
 // Few queries over at most 32 R blocks: a CTA per row, scores in shared memory,
@@ -410,6 +412,19 @@ bool by_row(const spmm_blocks_shape *s) {
     return s->Tk <= kRowBlocks * s->block && !tiled(s);
 }
 
+// Queries of each sequence whose scores are held at a time: the scores of a prompt grow
+// with the square of its length, so tiles take it in strips of at most 1 GB of them (of
+// kSt queries at least, and no more than a launch takes). Each strip's last CTAs leave
+// SMs idle: 65536 queries x 8 kv heads of 1024 blocks (2 GB) took 4.06 ms whole, 4.27 in
+// strips of 256 MB and 4.51 in strips of 64 MB.
+constexpr int64_t kStripBytes = 1 << 30;
+int64_t strip(const spmm_blocks_shape *s) {
+    if (!tiled(s)) return s->Tq;
+    const int64_t query = s->B * s->Hk * ((s->Tk + s->block - 1) / s->block) * 4;
+    const int64_t tiles = std::min<int64_t>(kStripBytes / std::max<int64_t>(query, 1) / kSt, 65535);
+    return std::min(s->Tq, std::max<int64_t>(tiles, 1) * kSt);
+}
+
 template <typename T>
 cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t st) {
     const BlkArgs &a = s.a;
@@ -422,12 +437,30 @@ cudaError_t launch_scores(const SelArgs &s, int64_t B, bool tiles, cudaStream_t 
         for (int64_t i = 0; i < pairs; i += kPairs) {
             p.pair0 = (int)i;
             k_score_tiles<T><<<dim3((unsigned)((a.NB + kSc - 1) / kSc),
-                                    (unsigned)((a.Tq + kSt - 1) / kSt),
+                                    (unsigned)((s.nt + kSt - 1) / kSt),
                                     (unsigned)std::min(kPairs, pairs - i)),
                                256, 0, st>>>(p);
             count_launch();
         }
     }
+    return cudaGetLastError();
+}
+
+// A strip's scores, and the lists that they give.
+template <typename T>
+cudaError_t launch_lists(const SelArgs &s, int64_t B, bool tiles, cudaStream_t st) {
+    const int NB = s.a.NB;
+    if (NB > 0) {
+        const cudaError_t e = launch_scores<T>(s, B, tiles, st);
+        if (e != cudaSuccess) return e;
+    }
+    const unsigned grid = (unsigned)((s.rows + 3) / 4);
+    if (NB <= 32) k_best<1><<<grid, 128, 0, st>>>(s);
+    else if (NB <= 128) k_best<4><<<grid, 128, 0, st>>>(s);
+    else if (NB <= 512) k_best<16><<<grid, 128, 0, st>>>(s);
+    else if (NB <= 1024) k_best<32><<<grid, 128, 0, st>>>(s);
+    else k_best<0><<<grid, 128, 0, st>>>(s);
+    count_launch();
     return cudaGetLastError();
 }
 
@@ -479,8 +512,8 @@ spmm_status spmm_blocks_means(const spmm_blocks_shape *s, spmm_rows k, int64_t n
 int64_t spmm_blocks_select_workspace(const spmm_blocks_shape *s) {
     using namespace spmm;
     if (blk_check(s, false) != SPMM_OK || by_row(s)) return 0;
-    const int64_t NB = (s->Tk + s->block - 1) / s->block, rows = s->B * s->Tq * s->Hk;
-    return rows * NB * 4;
+    const int64_t NB = (s->Tk + s->block - 1) / s->block;
+    return s->B * strip(s) * s->Hk * NB * 4;
 }
 
 spmm_status spmm_blocks_select(const spmm_blocks_shape *s, spmm_rows q, const float *means,
@@ -499,11 +532,11 @@ spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, con
     if (s->Tk > 0 && (!means || (uintptr_t)means % 16)) return SPMM_ERR_INVALID_ARG;
     const int64_t need = spmm_blocks_select_workspace(s);
     if (need && (!work || work_bytes < need)) return SPMM_ERR_INVALID_ARG;
-    if (tiled(s) && (s->Tq + kSt - 1) / kSt > 65535) return SPMM_ERR_UNSUPPORTED;
     SelArgs g{};
     g.a = blk_args(s, nullptr);
     set_rows(g.a.q, g.a.q_sb, g.a.q_st, g.a.q_sh, q);
     g.D = (int)s->D;
+    g.nt = (int)s->Tq;
     g.rows = s->B * s->Tq * s->Hk;
     g.means = means;
     g.score = (float *)work;
@@ -517,21 +550,16 @@ spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, con
         else e = launch_select_row<__half>(g, cs);
         return cuda_status(e);
     }
-    if (g.a.NB > 0) {
-        if (s->dtype == SPMM_F32) e = launch_scores<float>(g, s->B, tiled(s), cs);
-        else if (s->dtype == SPMM_BF16) e = launch_scores<__nv_bfloat16>(g, s->B, tiled(s), cs);
-        else e = launch_scores<__half>(g, s->B, tiled(s), cs);
-        if (e != cudaSuccess) return cuda_status(e);
+    for (int64_t t0 = 0, step = strip(s); t0 < s->Tq; t0 += step) {
+        g.t0 = (int)t0;
+        g.nt = (int)std::min(step, s->Tq - t0);
+        g.rows = s->B * g.nt * s->Hk;
+        if (s->dtype == SPMM_F32) e = launch_lists<float>(g, s->B, tiled(s), cs);
+        else if (s->dtype == SPMM_BF16) e = launch_lists<__nv_bfloat16>(g, s->B, tiled(s), cs);
+        else e = launch_lists<__half>(g, s->B, tiled(s), cs);
+        if (e != cudaSuccess) break;
     }
-    const unsigned grid = (unsigned)((g.rows + 3) / 4);
-    const int NB = g.a.NB;
-    if (NB <= 32) k_best<1><<<grid, 128, 0, cs>>>(g);
-    else if (NB <= 128) k_best<4><<<grid, 128, 0, cs>>>(g);
-    else if (NB <= 512) k_best<16><<<grid, 128, 0, cs>>>(g);
-    else if (NB <= 1024) k_best<32><<<grid, 128, 0, cs>>>(g);
-    else k_best<0><<<grid, 128, 0, cs>>>(g);
-    count_launch();
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }
 
 spmm_status spmm_blocks_check(const spmm_blocks_shape *s, const int32_t *blocks, int32_t *bad,

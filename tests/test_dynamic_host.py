@@ -26,3 +26,18 @@ def test_sync_asks_the_streams_device(monkeypatch):
                                              cuda_stream=7 + index))
     m.dynamic_sync()
     assert asked == [(0, 7), (1, 8), (0, 100)] and current == [0]
+
+
+def test_selection_scratch_is_bounded():
+    """The scores of a prompt grow with the square of its length; the scratch does not."""
+    import sparse_dense_matrix_gb300.dynamic as m
+
+    def need(B, Tq, Tk, Hk, block):
+        return m.lib.spmm_blocks_select_workspace(
+            m._Shape(B, Tq, Tk, 8 * Hk, Hk, 128, block, 16, 1, 1, 1.0, None))
+
+    for block in (16, 64):
+        for T in (1 << 15, 1 << 17, 1 << 20):
+            one = 8 * (T // block) * 4                       # the scores of one query
+            assert one <= need(1, T, T, 8, block) <= max(1 << 30, 64 * one)
+    assert need(1, 8192, 8192, 4, 64) == 8192 * 4 * 128 * 4  # a whole prompt that fits
