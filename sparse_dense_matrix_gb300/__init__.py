@@ -20,7 +20,9 @@ None (unweighted), ``mat`` float32 [K, N] row-major; all on the same CUDA device
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import sys
 
 from ._build import LIB as _LIB_PATH
 from ._build import build as build_library
@@ -34,8 +36,23 @@ __all__ = [
     "spmm_check_wait_timeout", "spmm_plan_create_range", "spmm_partition_rows",
     "spmm_plan_prepare_blocks",
     "PlanInfo", "REDUCE", "FAMILY", "lib", "build_library",
-    "ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync",
 ]
+# the products whose sparse matrix the model chooses: imported when first asked for, as
+# their binding needs torch and the rest of the package can do without
+_DYNAMIC = ("ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync")
+
+
+def _has_torch() -> bool:
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ImportError:
+        return False
+    except ValueError:                           # sys.modules holds a None or a stand-in
+        return sys.modules.get("torch") is not None
+
+
+if _has_torch():                                 # `import *` fetches every name here
+    __all__ += _DYNAMIC
 
 REDUCE = {"sum": 0, "mean": 1, "max": 2}
 ACT = {None: 0, "none": 0, "relu": 1}
@@ -505,8 +522,7 @@ def spmm_max(rowptr, col, val, mat):
 
 
 def __getattr__(name):
-    """The products whose sparse matrix the model chooses (they import torch)."""
-    if name in ("ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync"):
+    if name in _DYNAMIC:
         from . import dynamic
         return getattr(dynamic, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

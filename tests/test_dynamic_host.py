@@ -1,5 +1,13 @@
-"""The binding's host side without a GPU: devices of streams."""
+"""The binding's host side without a GPU: devices of streams, scratch, and the package
+without torch."""
+import os
+import subprocess
+import sys
 import types
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def test_sync_asks_the_streams_device(monkeypatch):
@@ -41,3 +49,32 @@ def test_selection_scratch_is_bounded():
             one = 8 * (T // block) * 4                       # the scores of one query
             assert one <= need(1, T, T, 8, block) <= max(1 << 30, 64 * one)
     assert need(1, 8192, 8192, 4, 64) == 8192 * 4 * 128 * 4  # a whole prompt that fits
+
+
+NO_TORCH = {
+    "absent": """
+import importlib.abc, sys
+class NoTorch(importlib.abc.MetaPathFinder):
+    def find_spec(self, name, path, target=None):
+        if name.partition(".")[0] == "torch":
+            raise ModuleNotFoundError("No module named 'torch'", name="torch")
+sys.meta_path.insert(0, NoTorch())
+""",
+    "blocked": "import sys\nsys.modules['torch'] = None\n"}
+
+
+@pytest.mark.parametrize("how", list(NO_TORCH))
+def test_star_import_without_torch(how):
+    """The package and all of its names that need no torch come without it."""
+    code = NO_TORCH[how] + """
+from sparse_dense_matrix_gb300 import *
+assert spmm_default_t_split(100, 1000, 50) >= 0 and "ExpertRoutes" not in globals()
+"""
+    got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert got.returncode == 0, got.stderr
+
+
+def test_star_import_with_torch():
+    code = "from sparse_dense_matrix_gb300 import *\nassert ExpertRoutes and dynamic_sync and spmm\n"
+    got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert got.returncode == 0, got.stderr
