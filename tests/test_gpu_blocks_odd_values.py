@@ -48,15 +48,16 @@ def test_rows_whose_scores_are_all_minus_infinity(sdm, cuda_device, dtype, D, T)
 
 
 def timed(f):
-    for _ in range(2):
+    """ms, the best of seven: the launches are the host's, which may be held up."""
+    best = math.inf
+    for _ in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
         f()
-    torch.cuda.synchronize()
-    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-    a.record()
-    f()
-    b.record()
-    torch.cuda.synchronize()
-    return a.elapsed_time(b)
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b))
+    return best
 
 
 @pytest.mark.parametrize("dtype,D,block", [("bf16", 128, 64), ("bf16", 64, 64), ("fp16", 128, 64),
