@@ -57,7 +57,7 @@ struct SelArgs {
     int D;
     int pair0;               // of the launch's (sequence, kv head) pairs, for the tiles
     int t0, nt;              // the strip's queries: t0 .. t0 + nt - 1 of each sequence
-    int64_t rows;            // B nt Hk
+    uint32_t rows;           // B nt Hk (below 2^31)
     const float *means;
     float *score;            // [rows, NB]
     int32_t *out;
@@ -263,10 +263,6 @@ __device__ __forceinline__ void best_of_row(const SelArgs &s, int64_t row, const
     const int lane = threadIdx.x & 31;
     const int want = min(cand, a.n - (own >= 0 ? 1 : 0));
     int32_t *out = s.out + row * a.n;
-    if (s.kept && lane == 0 && row % ((int64_t)a.Tq * a.Hk) == 0) {
-        const int b = (int)(row / ((int64_t)a.Tq * a.Hk));
-        s.kept[b] = a.lengths[b];
-    }
     int done = 0;
     if (want > 0 && want < cand) {
         RowKeys<R> keys;
@@ -317,14 +313,22 @@ __device__ __forceinline__ void best_of_row(const SelArgs &s, int64_t row, const
     for (int j = done + lane; j < a.n; j += 32) out[j] = -1;
 }
 
+// The copy of a sequence's length, by the warp of its first list.
+__device__ __forceinline__ void keep_length(const SelArgs &s, int b, int t, int h) {
+    if (s.kept && (threadIdx.x & 31) == 0 && t == 0 && h == 0) s.kept[b] = s.a.lengths[b];
+}
+
 template <int R> __global__ void __launch_bounds__(128) k_best(SelArgs s) {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const uint32_t row = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (row >= s.rows) return;
-    const int64_t bt = row / s.a.Hk, b = bt / s.nt;
-    const int t = s.t0 + (int)(bt % s.nt);
+    const uint32_t bt = row / (uint32_t)s.a.Hk, b = bt / (uint32_t)s.nt;
+    const int t = s.t0 + (int)(bt - b * s.nt);
     int own;
     const int cand = candidates(s.a, (int)b, t, &own);
-    best_of_row<R>(s, (b * s.a.Tq + t) * s.a.Hk + row % s.a.Hk, s.score + row * s.a.NB, cand, own);
+    const int h = (int)(row - bt * s.a.Hk);
+    keep_length(s, (int)b, t, h);
+    best_of_row<R>(s, ((int64_t)b * s.a.Tq + t) * s.a.Hk + h, s.score + (int64_t)row * s.a.NB, cand,
+                   own);
 }
 
 // Few queries over at most 32 R blocks: a CTA per row, scores in shared memory,
@@ -379,7 +383,10 @@ __global__ void __launch_bounds__(512) k_select_row(SelArgs s) {
         }
     }
     __syncthreads();
-    if (warp == 0) best_of_row<R>(s, row, score, cand, own);
+    if (warp == 0) {
+        keep_length(s, b, t, h);
+        best_of_row<R>(s, row, score, cand, own);
+    }
 }
 
 __global__ void k_check_lists(BlkArgs a, int64_t rows, int32_t *bad) {
@@ -454,7 +461,7 @@ cudaError_t launch_lists(const SelArgs &s, int64_t B, bool tiles, cudaStream_t s
         const cudaError_t e = launch_scores<T>(s, B, tiles, st);
         if (e != cudaSuccess) return e;
     }
-    const unsigned grid = (unsigned)((s.rows + 3) / 4);
+    const unsigned grid = s.rows / 4 + (s.rows % 4 != 0);
     if (NB <= 32) k_best<1><<<grid, 128, 0, st>>>(s);
     else if (NB <= 128) k_best<4><<<grid, 128, 0, st>>>(s);
     else if (NB <= 512) k_best<16><<<grid, 128, 0, st>>>(s);
@@ -537,7 +544,7 @@ spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, con
     set_rows(g.a.q, g.a.q_sb, g.a.q_st, g.a.q_sh, q);
     g.D = (int)s->D;
     g.nt = (int)s->Tq;
-    g.rows = s->B * s->Tq * s->Hk;
+    g.rows = (uint32_t)(s->B * s->Tq * s->Hk);
     g.means = means;
     g.score = (float *)work;
     g.out = blocks;
@@ -553,7 +560,7 @@ spmm_status spmm_blocks_select_kept(const spmm_blocks_shape *s, spmm_rows q, con
     for (int64_t t0 = 0, step = strip(s); t0 < s->Tq; t0 += step) {
         g.t0 = (int)t0;
         g.nt = (int)std::min(step, s->Tq - t0);
-        g.rows = s->B * g.nt * s->Hk;
+        g.rows = (uint32_t)(s->B * g.nt * s->Hk);
         if (s->dtype == SPMM_F32) e = launch_lists<float>(g, s->B, tiled(s), cs);
         else if (s->dtype == SPMM_BF16) e = launch_lists<__nv_bfloat16>(g, s->B, tiled(s), cs);
         else e = launch_lists<__half>(g, s->B, tiled(s), cs);
