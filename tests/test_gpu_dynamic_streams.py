@@ -125,3 +125,32 @@ def test_selections_on_another_stream_keep_their_memory(sdm, cuda_device):
         torch.cuda.synchronize()
         del got, sel
     sdm.dynamic_sync()
+
+
+def test_made_outside_and_captured(sdm, cuda_device):
+    """Routes and selections made on another stream before a capture, used in it and
+    dropped when the graph is done: its results are those of the calls."""
+    B, T, H, block, n = 1, 600, 2, 64, 4
+    q, k, v = (randn(cuda_device, i, B, T, H, 128).bfloat16() for i in range(3))
+    sel = sdm.select_blocks(q, sdm.block_means(k, block), n, block, T,
+                            torch.tensor([580], dtype=torch.int32, device=cuda_device))
+    routes = sdm.ExpertRoutes(torch.arange(T, dtype=torch.int32, device=cuda_device)[:, None] % 7, 7)
+    x = randn(cuda_device, 5, T, 64)
+    out, lse = sel.attend(q, k, v)
+    want = (out, lse, *sel.backward(q, q, k, v, out, lse), routes.dispatch(x))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = sel.attend(q, k, v)
+        got = (out, lse, *sel.backward(q, q, k, v, out, lse), routes.dispatch(x))
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    torch.cuda.synchronize()
+    torch.empty(1 << 20, device=cuda_device)             # the allocator is whole
+    del sel, routes
+    torch.cuda.empty_cache()
+    assert torch.ones(8, device=cuda_device).sum() == 8
