@@ -15,8 +15,11 @@
  *     scratch, the caller passes `work` of at least the bytes that the matching
  *     *_workspace function returns (16-byte aligned); the scratch holds nothing
  *     between calls.
- *   - Elements are fp32, bf16 or fp16 (spmm_dtype). Sums, softmax statistics
- *     and weights are fp32; an output is rounded to its type once.
+ *   - Elements are fp32, bf16 or fp16 (spmm_dtype). Sums, scores, softmax
+ *     statistics and the routes' weights are fp32; an output is rounded to its
+ *     type once. Attention's weights are rounded to the inputs' type where they
+ *     enter a matrix product; dS enters it as two such parts; the gradients'
+ *     <dO, O> is formed from the rounded output.
  *   - Results are bitwise reproducible run to run: no floating-point atomics.
  */
 #ifndef GB300_SPMM_DYNAMIC_H

@@ -10,7 +10,9 @@ namespace spmm {
 namespace {
 
 // delta, and the bits cleared for k_set_bits. Bound by memory: 14 us for 2 x 4096 x
-// 16 rows of 128 (67 MB).
+// 16 rows of 128 (67 MB). It is summed in fp32 from the rounded output, the only one that
+// a caller has (an fp32 copy would be twice its bytes to write and read): it is off by
+// what that rounding left out, which dQ shows.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) k_delta(BwdArgs p, int64_t rows, int64_t words) {
     constexpr int U = D / 8;
@@ -55,7 +57,8 @@ __global__ void k_set_bits(BwdArgs p, int64_t entries) {
 // dS sum to 0, so dQ = dS K (and, to a degree, dK) is what remains after the keys'
 // common part cancels, and a single rounding of dS shows in it: the error was 1.7
 // times that of rounding dQ alone, and is 1.27 times with both parts (the rest is
-// delta's, from the rounded output).
+// delta's, from the rounded output: given that output it is 1.00 times, where one part
+// alone gives 8 on keys whose common part is 8 times the rest).
 
 // fp16 has 5 bits of exponent: weights and gradients well below 2^-14 would lose
 // their digits in it. So P is held as P 2^14 (at most 2^14, up to its rounding),
@@ -889,6 +892,8 @@ __global__ void __launch_bounds__(128) k_dkdv(BwdArgs p) {
                     st[i][e] = seen ? pr[e] * (dp[i][e] - (e & 1 ? d.y : d.x)) * ds_unit : 0.0f;
                     if constexpr (kNarrow<T>) ds_max = finite_max(ds_max, st[i][e]);
                 }
+                // one part: dV = P^T dO does not cancel as dQ does, and is off by no more
+                // than the output is by its P
                 pa[i][0] = pack2<T>(pr[0], pr[1]);
                 pa[i][1] = pack2<T>(pr[2], pr[3]);
             }

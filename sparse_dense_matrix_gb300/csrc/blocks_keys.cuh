@@ -7,7 +7,7 @@
 //   dV^T += dO^T P, dK^T += Q^T dS  128 elements x 64 keys, summed over the rows
 //                                   (dS as its rounded value and its rest)
 // The gathered rows and P, dS serve as MN-major operands in the second pair of
-// products, so nothing is transposed in memory. Four warps gather rows by
+// products, so nothing is transposed in memory. Eight warps gather rows by
 // asynchronous copies into two stages, one thread issues the products, eight
 // warps make P and dS, each half of a row's keys. 245 us for 2 x 4096 queries x 16
 // heads of 128 over 2, 16 of 64-key blocks (mma.sync 852 us). Bound by the chain of
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kKeysThreads, 1) k_dkdv_keys(const BwdArgs p) 
                     ds[e] = pr[e] * fmaf(__uint_as_float(dp[i + e]), a.scale, ds_off);
                     if (!whole && i + e >= seen) pr[e] = ds[e] = 0.0f;
                 }
-                pp[i / 2] = pack2<T>(pr[0], pr[1]);
+                pp[i / 2] = pack2<T>(pr[0], pr[1]);          // one part, as in k_dkdv
                 split2<T>(ds[0], ds[1], dd[i / 2], dl[i / 2]);
             }
             // the products of the step before read the buffers that are written now
