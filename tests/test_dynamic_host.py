@@ -78,3 +78,27 @@ def test_star_import_with_torch():
     code = "from sparse_dense_matrix_gb300 import *\nassert ExpertRoutes and dynamic_sync and spmm\n"
     got = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert got.returncode == 0, got.stderr
+
+
+def test_limits_and_refusals_of_the_later_calls():
+    import ctypes
+
+    import sparse_dense_matrix_gb300.dynamic as m
+    ptr, L = ctypes.c_void_p(4096), m.lib        # never dereferenced: the checks come first
+    rows = m._Rows(4096, 8192, 256, 64)
+
+    def shape(B=1, Tq=4, Tk=64, Hq=4, Hk=2):
+        return m._Shape(B, Tq, Tk, Hq, Hk, 64, 16, 2, 1, 1, 0.125, None)
+
+    for limit in (0, -5, 10 ** 7 + 1):
+        assert L.spmm_dynamic_check_wait_timeout(limit, None) == 1
+    assert L.spmm_blocks_select_kept(shape(), rows, ptr, None, None, None, 0, None) == 1
+    assert L.spmm_blocks_select_kept(shape(), rows, None, ptr, ptr, None, 0, None) == 1
+    # more keys or rows than the limits: the means as the gradient
+    for s in (shape(B=1 << 12, Tk=1 << 26, Hq=8, Hk=8), shape(B=1 << 20, Tq=1 << 10)):
+        assert L.spmm_blocks_means(s, rows, -1, ptr, None) == 5
+        assert L.spmm_blocks_backward(s, rows, rows, rows, ptr, ptr, ptr, rows, ptr, ptr, ptr, ptr,
+                                      1 << 62, None) == 5
+        assert L.spmm_blocks_backward_workspace(s) == 0
+    # what the forward takes, the gradient takes: scratch for more pairs than 65535
+    assert L.spmm_blocks_backward_workspace(shape(B=70000)) > 0
