@@ -2,11 +2,15 @@
  * spmm_dynamic.h -- C ABI of the products whose sparse matrix a model chooses
  * anew in every call (libspmm.so; spmm.h holds the products with a fixed A).
  *
- *   routes  tokens x slots: tokens sorted by expert, gathered, and the experts'
- *           rows weighted and added back per token, with every gradient.
+ *   routes  tokens x slots: tokens sorted by expert, gathered, each expert's rows
+ *           times its matrix, and the experts' rows weighted and added back per
+ *           token, with every gradient.
  *   blocks  queries x key blocks: each query attends to the key blocks that a
  *           cheap score selects for it; forward, single tokens over a cache,
  *           and backward (through the transpose of the selection).
+ *   heads   what comes before the blocks: queries and keys, each head normed and
+ *           its pairs of elements turned by the token's position (a block-diagonal
+ *           matrix of 2 x 2 rotations), also written into a cache, and the gradient.
  *
  * Conventions are spmm.h's: device pointers of the current device, `stream` a
  * cudaStream_t as void*, argument checks on the host before any CUDA call, no
@@ -107,6 +111,33 @@ spmm_status spmm_routes_combine_backward(int dtype, const void *dout, int64_t ld
                                          const int32_t *offsets, int64_t T, int64_t k, int64_t E,
                                          int64_t H, void *dy, float *dw, void *stream);
 
+/*
+ * spmm_routes_product -- each expert's rows times its matrix:
+ *   ys[s, f] = sum_h xs[s, h] w[e, h, f] for the slots s of expert e;
+ * rows offsets[E] .. P - 1 of ys are set to 0, those of xs do not matter.
+ *   xs : device, [P, H], contiguous (P = T k slots). ys : device, [P, F], contiguous, written.
+ *   w  : device, [E, H, F], element strides w_se, w_sh, w_sf. One of w_sh and w_sf
+ *        is 1; the other and w_se are multiples of 8 (w_se may be 0: one matrix
+ *        for every expert).
+ * With w transposed (w_sh and w_sf, H and F exchanged) it is the gradient of xs.
+ * dtype is SPMM_BF16 or SPMM_F16, H and F multiples of 8 up to 2^20, E at most
+ * SPMM_ROUTES_MAX_EXPERTS, P < 2^31 (else SPMM_ERR_UNSUPPORTED); pointers are
+ * 16-byte aligned.
+ */
+spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_t w_se,
+                                int64_t w_sh, int64_t w_sf, const int32_t *offsets, int64_t P,
+                                int64_t E, int64_t H, int64_t F, void *ys, void *stream);
+
+/*
+ * spmm_routes_product_weights -- the gradient of the matrices:
+ *   dw[e, h, f] = sum over the slots s of e of xs[s, h] dys[s, f]; 0 without slots.
+ *   dw : device, written whole, strides as w's above (but dw_se > 0 for E > 1).
+ */
+spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *dys,
+                                        const int32_t *offsets, int64_t P, int64_t E, int64_t H,
+                                        int64_t F, void *dw, int64_t dw_se, int64_t dw_sh,
+                                        int64_t dw_sf, void *stream);
+
 /* ------------------------------------------------------------------ blocks */
 
 /* A [B, T, heads, D] tensor: element strides of the first three dimensions; the
@@ -199,6 +230,61 @@ spmm_status spmm_blocks_backward(const spmm_blocks_shape *s, spmm_rows q, spmm_r
                                  spmm_rows v, const int32_t *blocks, const void *out,
                                  const float *lse, spmm_rows dout, void *dq, void *dk, void *dv,
                                  void *work, int64_t work_bytes, void *stream);
+
+/* ------------------------------------------------------------------- heads */
+
+/*
+ * What the calls on heads share. A token's heads [H, D] of queries (Hq) and keys
+ * (Hk, may be 0) become, with a weight [D] for the tensor, z = x w / sqrt(mean(x^2) + eps),
+ * else z = x; then the first R elements are turned in pairs by the angle
+ * 2 pi 2^-64 turns[i] p, p the token's position (an integer product mod 2^64:
+ * exact at any position):
+ *   y1 = magnitude (z1 cos - z2 sin), y2 = magnitude (z2 cos + z1 sin),
+ * pairs being (i, i + R / 2) or, interleaved, (2 i, 2 i + 1); elements from R on are z.
+ * Token t of sequence b is at positions[b p_sb + t p_st], else, with lengths, at
+ * lengths[b] - T + t, else at t. Positions may be negative.
+ * Sums and angles are fp32 or better; results are rounded once.
+ * D and R are multiples of 16, D at most 256, R at most D; tensors are spmm_rows
+ * of fp32, bf16 or fp16. Limits, else SPMM_ERR_UNSUPPORTED: T 2^26, Hq and Hk 65535,
+ * B T (Hq + Hk) < 2^31.
+ */
+typedef struct {
+    int64_t B, T, Hq, Hk, D, R;
+    int32_t dtype;               /* of the tensors                                   */
+    int32_t weight_dtype;        /* of the weights: SPMM_F32 or dtype                */
+    int32_t interleaved;
+    float eps, magnitude;
+    const uint64_t *turns;       /* device, [R / 2]                                  */
+    const int32_t *positions;    /* device, or NULL                                  */
+    int64_t p_sb, p_st;
+    const int32_t *lengths;      /* device, int32 [B], or NULL                       */
+    const void *wq, *wk;         /* device, [D], 16-byte aligned, or NULL            */
+} spmm_heads_shape;
+
+/* spmm_heads_rotate -- q_out [B, T, Hq, D] and k_out [B, T, Hk, D], contiguous, written. */
+spmm_status spmm_heads_rotate(const spmm_heads_shape *s, spmm_rows q, spmm_rows k, void *q_out,
+                              void *k_out, void *stream);
+
+/*
+ * spmm_heads_append -- the same, the new keys going into a cache [B, Tk, Hk, D] at
+ * their positions and the values v [B, T, Hk, D] as they are into another. Needs
+ * lengths (those after the new tokens) and no positions. Keys at positions outside
+ * [0, Tk) are not written; every other row of the caches stays as it is.
+ */
+spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
+                              void *q_out, spmm_rows cache_k, spmm_rows cache_v, int64_t Tk,
+                              void *stream);
+
+/*
+ * spmm_heads_rotate_backward -- the gradients of q, k and the weights, given those of
+ * rotate's results. dq, dk contiguous, dwq, dwk [D] of weight_dtype (NULL where there is no
+ * weight), all written. q and k are read for tensors with a weight only.
+ */
+int64_t spmm_heads_backward_workspace(const spmm_heads_shape *s);
+spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad_q,
+                                       spmm_rows grad_k, spmm_rows q, spmm_rows k, void *dq,
+                                       void *dk, void *dwq, void *dwk, void *work,
+                                       int64_t work_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,8 @@ __all__ = [
 ]
 # the products whose sparse matrix the model chooses: imported when first asked for, as
 # their binding needs torch and the rest of the package can do without
-_DYNAMIC = ("ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync")
+_DYNAMIC = ("ExpertRoutes", "BlockSelection", "block_means", "select_blocks", "dynamic_sync",
+            "HeadRotation")
 
 
 def _has_torch() -> bool:
@@ -522,6 +523,9 @@ def spmm_max(rowptr, col, val, mat):
 
 
 def __getattr__(name):
+    if name == "HeadRotation":
+        from . import heads
+        return heads.HeadRotation
     if name in _DYNAMIC:
         from . import dynamic
         return getattr(dynamic, name)

@@ -1,8 +1,9 @@
 """Products whose sparse matrix a model chooses anew in every call (include/spmm_dynamic.h).
 
 * :class:`ExpertRoutes` -- the tokens x slots matrix of a router: tokens sorted
-  by expert and gathered (``dispatch``), the experts' rows weighted and added
-  back per token (``combine``), and every gradient.
+  by expert and gathered (``dispatch``), each expert's rows times its matrix
+  (``product``), the experts' rows weighted and added back per token
+  (``combine``), and every gradient.
 * :func:`block_means`, :func:`select_blocks`, :class:`BlockSelection` -- the
   queries x key-blocks matrix of a cheap score, attention over the selected
   blocks (many queries, or single tokens over a cache) and its gradient.
@@ -59,6 +60,9 @@ def _declare():
         "spmm_routes_combine": ([i32, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp], i32),
         "spmm_routes_combine_backward": ([i32, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp,
                                           vp], i32),
+        "spmm_routes_product": ([i32, vp, vp, i64, i64, i64, vp, i64, i64, i64, i64, vp, vp], i32),
+        "spmm_routes_product_weights": ([i32, vp, vp, vp, i64, i64, i64, i64, vp, i64, i64, i64,
+                                         vp], i32),
         "spmm_blocks_means": ([S, _Rows, i64, vp, vp], i32),
         "spmm_blocks_select_workspace": ([S], i64),
         "spmm_blocks_select": ([S, _Rows, vp, vp, vp, i64, vp], i32),
@@ -275,6 +279,82 @@ class ExpertRoutes:
         if st:
             _check(st, "spmm_routes_combine_backward")
         return dy, dw
+
+    def _matrices(self, w, xs):
+        """w [E, H, F] for rows xs [T * k, H]: F, and w's address and strides."""
+        H = self._by_slot(xs, "xs")
+        _tensor(w, "w", (xs.dtype,), 3, self.device)
+        E, Hw, F = w.shape
+        if E != self.num_experts or Hw != H:
+            raise ValueError(f"w must be [{self.num_experts}, {H}, F], got {list(w.shape)}")
+        if xs.dtype not in _HALVES or H % 8 or F % 8:
+            raise ValueError("a product takes bfloat16 or float16 and widths that are multiples "
+                             f"of 8, got {xs.dtype}, {H} and {F}")
+        return (F, *_matrix_strides(w, "w"))
+
+    def product(self, xs, w, stream=None):
+        """ys [T * k, F]: each expert's rows of xs [T * k, H] times its w[e], in fp32, rounded
+        once; rows of no pair are written as 0.
+
+        ``w`` [E, H, F]: H or F adjacent (a linear layer's [E, F, H], transposed, is), rows
+        and experts at 16-byte boundaries; an expanded w is one matrix for every expert.
+        bfloat16 or float16, H and F multiples of 8."""
+        ctx = _elsewhere(self.device, stream)
+        if ctx is not None:
+            with ctx:
+                ys = self.product(xs, w)
+                _lent(self.device, xs, w)
+                return ys
+        F, at, se, sh, sf = self._matrices(w, xs)
+        P, H = xs.shape
+        ys = xs.new_empty((P, F))
+        st = lib.spmm_routes_product(_DTYPE[xs.dtype], xs.data_ptr(), at, se, sh, sf,
+                                     self._routes[1], P, self.num_experts, H, F, ys.data_ptr(),
+                                     self._on_stream())
+        if st:
+            _check(st, "spmm_routes_product")
+        return ys
+
+    def product_backward(self, grad, xs, w, stream=None):
+        """(dxs [T * k, H], dw [E, H, F]) of ``product(xs, w)``, given the gradient [T * k, F] of
+        its result. dw has w's strides where those are dense; an expert without rows gets 0."""
+        ctx = _elsewhere(self.device, stream)
+        if ctx is not None:
+            with ctx:
+                grads = self.product_backward(grad, xs, w)
+                _lent(self.device, grad, xs, w)
+                return grads
+        F, at, se, sh, sf = self._matrices(w, xs)
+        self._by_slot(grad, "grad", F)
+        if grad.dtype != xs.dtype:
+            raise TypeError(f"grad must be {xs.dtype}, got {grad.dtype}")
+        P, H = xs.shape
+        E, dt, offsets, handle = self.num_experts, _DTYPE[xs.dtype], self._routes[1], self._on_stream()
+        dxs = torch.empty_like(xs)
+        dw = torch.empty_like(w)
+        st = lib.spmm_routes_product(dt, grad.data_ptr(), at, se, sf, sh, offsets, P, E, F, H,
+                                     dxs.data_ptr(), handle)
+        if st:
+            _check(st, "spmm_routes_product")
+        st = lib.spmm_routes_product_weights(dt, xs.data_ptr(), grad.data_ptr(), offsets, P, E, H, F,
+                                             *_matrix_strides(dw, "dw"), handle)
+        if st:
+            _check(st, "spmm_routes_product_weights")
+        return dxs, dw
+
+
+def _matrix_strides(w, name):
+    """Address and strides of [E, H, F] matrices with H or F adjacent."""
+    E, H, F = w.shape
+    se, sh, sf = w.stride()
+    at = w.data_ptr()
+    if E <= 1:
+        se = 0                                   # the stride of a dimension of one may be any
+    if w.numel() and (at % 16 or se % 8 or not ((sf == 1 and sh % 8 == 0 and sh > 0) or
+                                                (sh == 1 and sf % 8 == 0 and sf > 0))):
+        raise ValueError(f"{name} must have H or F adjacent, and rows and experts at 16-byte "
+                         f"boundaries (strides {tuple(w.stride())})")
+    return at, se, sh, sf
 
 
 # -------------------------------------------------------------------- blocks
