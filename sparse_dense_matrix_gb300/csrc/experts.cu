@@ -1,115 +1,397 @@
 // Products grouped by expert: the slots of expert e, rows offsets[e] .. offsets[e + 1]
 // of xs [P, H], times w[e] [H, F], and the gradient of w:
 //   ys[s, f] = sum_h xs[s, h] w[e, h, f],   dw[e, h, f] = sum_s xs[s, h] dys[s, f].
-// The simplest form: 64 x 64 outputs a CTA, 4 x 4 a thread, operands in shared memory
-// as fp32.
-#include "blocks.cuh"
+// One kernel does both, as D[m, n] = sum_k A[m, k] B[n, k] on the tensor cores (tcgen05),
+// m being the index that is adjacent in the result:
+//   product    m = f, n = a slot, k = h: A = w[e]^T, B = xs. The ragged index is the
+//              instruction's N, which comes in steps of 16: an expert with few slots
+//              costs little, and w is read once per 256 of its slots.
+//   gradient   m = f (h where h is adjacent in dw), n = h (f), k = a slot: A = dys^T,
+//              B = xs^T, both MN-major. The ragged index is the summed one: rows past
+//              the expert's last are the next expert's, and are set to 0 in shared
+//              memory before they are used (0 times a NaN is none of this expert's).
+// CTAs stay and take tiles of 128 x up to 256 in turn. A warp's thread copies the
+// operands' tiles of 64 of k into a ring of stages (tensor copies), another issues
+// the products into one of two accumulators in tensor memory, and four warps
+// write the other one out meanwhile.
+#include <cudaTypedefs.h>
+
+#include "umma.cuh"
 
 namespace spmm {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kThreads = 256;
+constexpr int kSms = 152;
+constexpr int kDepth = 64;           // of k in a stage: a row of 128 bytes
+constexpr int kRowsM = 128;          // of m in a tile
+constexpr int kThreads = 192;        // copies, products, four warps of results
+constexpr int kSmemMax = 227 * 1024;
 
 struct ExpertArgs {
-    const void *a, *b;               // xs and w, or xs and dys
-    void *out;
+    CUtensorMap a_map, b_map;
     const int32_t *offsets;
-    int64_t se, sh, sf;              // strides of w or dw
+    void *out;
+    int64_t o_se, o_ld;              // strides of e (gradient) and of n in the result
     int64_t P;
-    int E, H, F;
+    int E, M, N, K;                  // N: gradient; K: product
+    int a_step;                      // 0: one matrix for every expert
+    int tiles_m, tiles_n;
+    int32_t *err;
 };
 
-struct Segment {
-    int64_t begin, end;
+// NT: largest n of a tile. BOX: rows of B that one copy brings.
+template <int NT_> struct ExpertShape {
+    static constexpr int NT = NT_, BOX = NT / 4;
+    static constexpr int a_bytes = kRowsM * kDepth * 2, b_bytes = NT * kDepth * 2;
+    static constexpr int stage = a_bytes + b_bytes;
+    static constexpr int stages = NT == 256 ? 4 : 8;
+    static constexpr int columns = 2 * NT;
+    // results: 32 rows of 64 bytes for each of four warps, the rows 80 bytes apart, so
+    // that eight of them fall in different banks
+    static constexpr int out_pitch = 80, out_bytes = 4 * 32 * out_pitch;
+    static constexpr int at_out = stages * stage, at_offsets = at_out + out_bytes;
+    static size_t bytes(int E) { return 1024 + at_offsets + sizeof(int32_t) * 2 * ((size_t)E + 1); }
 };
-__device__ __forceinline__ Segment segment(const ExpertArgs &p, int e) {
-    Segment s;
-    s.begin = min(max((int64_t)p.offsets[e], (int64_t)0), p.P);
-    s.end = min(max((int64_t)p.offsets[e + 1], s.begin), p.P);
-    return s;
-}
 
-// c[4][4] += the tile's product over `n` of the summed index; at(i, j) and bt(i, j) give
-// the elements (summed index, row) and (summed index, column).
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(float (&c)[4][4], int64_t n, FA at, FB bt) {
-    __shared__ float sa[kDepth][kTile + 4], sb[kDepth][kTile + 4];
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int64_t k0 = 0; k0 < n; k0 += kDepth) {
-        for (int i = threadIdx.x; i < kDepth * kTile; i += kThreads) {
-            const int64_t k = k0 + i / kTile;
-            sa[i / kTile][i % kTile] = k < n ? at(k, i % kTile) : 0.0f;
-            sb[i / kTile][i % kTile] = k < n ? bt(k, i % kTile) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    c[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], c[i][j]);
-        __syncthreads();
+struct ExpertTile {
+    int e, n, m0, n0;                // m0, n0: first of m, of n (gradient)
+    int64_t r0;                      // first slot: of n (product), of k (gradient)
+    int k;                           // length of k
+};
+
+// Shared memory's view of the experts: first slots, and (product) the tiles of slots before
+// each expert.
+struct ExpertList {
+    const int32_t *first, *before;
+    template <int NT, bool GRAD>
+    __device__ __forceinline__ int tiles(const ExpertArgs &p) const {
+        return (GRAD ? p.E * p.tiles_n : before[p.E]) * p.tiles_m;
     }
-}
-
-// CTA y takes the y-th tile of 64 slots of the experts in turn, then of the rows behind.
-template <typename T> __global__ void __launch_bounds__(kThreads) k_product(const ExpertArgs p) {
-    __shared__ int which;
-    __shared__ int64_t first;
-    if (threadIdx.x == 0) {
-        int64_t left = blockIdx.y;
-        int e = 0;
-        for (; e < p.E; ++e) {
-            const Segment s = segment(p, e);
-            const int64_t tiles = (s.end - s.begin + kTile - 1) / kTile;
-            if (left < tiles) break;
-            left -= tiles;
+    template <int NT, bool GRAD>
+    __device__ __forceinline__ ExpertTile tile(const ExpertArgs &p, int t) const {
+        ExpertTile x;
+        x.m0 = t % p.tiles_m * kRowsM;
+        const int u = t / p.tiles_m;
+        if (GRAD) {
+            x.e = u / p.tiles_n;
+            x.n0 = u % p.tiles_n * NT;
+            x.n = min(NT, p.N - x.n0);
+            x.r0 = first[x.e];
+            x.k = first[x.e + 1] - first[x.e];
+        } else {
+            int lo = 0, hi = p.E - 1;            // the last expert with before[e] <= u
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (before[mid] <= u) lo = mid;
+                else hi = mid - 1;
+            }
+            x.e = lo;
+            x.n0 = 0;
+            // an expert's slots in equal parts
+            const int rows = first[lo + 1] - first[lo], parts = before[lo + 1] - before[lo];
+            const int per = (((rows + parts - 1) / parts) + 15) & ~15, at = (u - before[lo]) * per;
+            x.r0 = (int64_t)first[lo] + at;
+            x.n = min(per, rows - at);
+            x.k = p.K;
         }
-        which = e;
-        first = (e < p.E ? segment(p, e).begin : min(max((int64_t)p.offsets[p.E], (int64_t)0), p.P)) +
-                left * kTile;
+        return x;
+    }
+};
+
+template <int NT, bool GRAD>
+__device__ __forceinline__ ExpertList expert_list(const ExpertArgs &p, int32_t *smem) {
+    int32_t *first = smem, *before = smem + p.E + 1;
+    for (int e = threadIdx.x; e <= p.E; e += kThreads)
+        first[e] = (int)min(max((int64_t)p.offsets[e], (int64_t)0), p.P);
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        // a first slot below the one before it leaves the expert without any
+        int most = 0, sum = 0;
+        for (int e0 = 0; e0 <= p.E; e0 += 32) {
+            const int e = e0 + (int)threadIdx.x;
+            int x = e <= p.E ? first[e] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if ((int)threadIdx.x >= o) x = max(x, y);
+            }
+            x = max(x, most);
+            if (e <= p.E) first[e] = x;
+            most = __shfl_sync(0xffffffffu, x, 31);
+        }
+        __syncwarp();
+        if (!GRAD) {
+            for (int e0 = 0; e0 <= p.E; e0 += 32) {
+                const int e = e0 + (int)threadIdx.x;
+                const int mine = e < p.E ? (first[e + 1] - first[e] + NT - 1) / NT : 0;
+                int x = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if ((int)threadIdx.x >= o) x += y;
+                }
+                if (e <= p.E) before[e] = sum + x - mine;
+                sum += __shfl_sync(0xffffffffu, x, 31);
+            }
+        }
     }
     __syncthreads();
-    const int e = which;
-    const int64_t r0 = first, r1 = min(e < p.E ? segment(p, e).end : p.P, r0 + kTile);
-    const int f0 = blockIdx.x * kTile;
-    if (r0 >= r1) return;
-    const T *xs = (const T *)p.a, *w = (const T *)p.b + e * p.se;
-    float c[4][4] = {};
-    if (e < p.E)
-        tile_product(
-            c, p.H,
-            [&](int64_t k, int i) { return r0 + i < r1 ? to_f32(xs[(r0 + i) * p.H + k]) : 0.0f; },
-            [&](int64_t k, int j) {
-                return f0 + j < p.F ? to_f32(w[k * p.sh + (f0 + j) * p.sf]) : 0.0f;
-            });
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + ty * 4 + i;
-            const int f = f0 + tx * 4 + j;
-            if (r < r1 && f < p.F) ((T *)p.out)[r * p.F + f] = from_f32<T>(c[i][j]);
-        }
+    return ExpertList{first, before};
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) k_weights(const ExpertArgs p) {
-    const int e = blockIdx.z;
-    const Segment s = segment(p, e);
-    const int h0 = blockIdx.y * kTile, f0 = blockIdx.x * kTile;
-    const T *xs = (const T *)p.a + s.begin * p.H, *dys = (const T *)p.b + s.begin * p.F;
-    float c[4][4] = {};
-    tile_product(
-        c, s.end - s.begin,
-        [&](int64_t k, int i) { return h0 + i < p.H ? to_f32(xs[k * p.H + h0 + i]) : 0.0f; },
-        [&](int64_t k, int j) { return f0 + j < p.F ? to_f32(dys[k * p.F + f0 + j]) : 0.0f; });
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int h = h0 + ty * 4 + i, f = f0 + tx * 4 + j;
-            if (h < p.H && f < p.F)
-                ((T *)p.out)[e * p.se + h * p.sh + f * p.sf] = from_f32<T>(c[i][j]);
+__device__ __forceinline__ void tensor3d_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                             int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tensor2d_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                             uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// 16 lanes x 32 columns: with r = lane / 4 and c = lane % 4, registers 4 i and 4 i + 1
+// hold row r, columns 8 i + 2 c and + 1; 4 i + 2 and 4 i + 3 those of row r + 8.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t addr, uint32_t (&x)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+        "%15}, [%16];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]),
+          "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]),
+          "=r"(x[14]), "=r"(x[15])
+        : "r"(addr)
+        : "memory");
+}
+
+// Four 8x8 matrices, held as the matrix instruction's results are, to shared memory
+// transposed: lane l gives the address of column l % 8 of matrix l / 8.
+__device__ __forceinline__ void stsm4_t(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                        uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(addr));
+    return x;
+}
+
+// mbar_wait by a whole warp, whose lanes then go the same way.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+}
+
+// Rows [from, to) of `panels` panels of 64 rows set to 0, by one warp.
+__device__ __forceinline__ void zero_rows(uint32_t operand, int panels, int from, int to) {
+    const int lane = threadIdx.x & 31, n = (to - from) * 8;
+    for (int q = 0; q < panels; ++q)
+        for (int i = lane; i < n; i += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             operand + q * 8192 + from * 128 + i * 16),
+                         "r"(0)
+                         : "memory");
+}
+
+// A_MN: A's elements adjacent in m (else in k). B is adjacent in k, in the gradient in n.
+template <typename T, int NT, bool A_MN, bool GRAD>
+__global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__ ExpertArgs p) {
+    using S = ExpertShape<NT>;
+    static_assert(A_MN || !GRAD, "the gradient's operands are both adjacent in m and n");
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t full[S::stages], empty[S::stages], ready[2], taken[2], drained;
+    __shared__ uint32_t tmem_slot;
+    const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ready[i], 1);
+            mbar_init(&taken[i], 4);
+        }
+        mbar_init(&drained, 1);
+        mbar_init_fence();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, S::columns);
+        mma_fence_before();
+    }
+    const ExpertList list = expert_list<NT, GRAD>(
+        p, (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_offsets));
+    mma_fence_after();                           // (the list's barriers came between)
+    const uint32_t tmem = tmem_slot;
+    const int tiles = list.template tiles<NT, GRAD>(p);
+
+    if (warp == 0) {
+        // ------------------------------------------------------ operands' tiles
+        if (lane == 0) {
+            int stage = 0;
+            int64_t issued = 0;
+            uint32_t parity = 1;                 // the ring starts empty
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                const ExpertTile x = list.template tile<NT, GRAD>(p, t);
+                const int boxes = GRAD ? (x.n + 63) / 64 : (x.n + S::BOX - 1) / S::BOX;
+                const uint32_t bytes =
+                    S::a_bytes + (uint32_t)boxes * (GRAD ? 8192 : S::BOX * kDepth * 2);
+                for (int k0 = 0; k0 < x.k; k0 += kDepth) {
+                    ok = mbar_wait(&empty[stage], parity, p.err);
+                    if (!ok) break;
+                    uint64_t *bar = &full[stage];
+                    const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    if (GRAD) {
+                        const int r = (int)(x.r0 + k0);
+                        tensor3d_g2s(a, &p.a_map, x.m0, r, 0, bar);
+                        tensor3d_g2s(a + 8192, &p.a_map, x.m0 + 64, r, 0, bar);
+                        for (int i = 0; i < boxes; ++i)
+                            tensor2d_g2s(b + i * 8192, &p.b_map, x.n0 + 64 * i, r, bar);
+                    } else {
+                        const int z = x.e * p.a_step;
+                        if (A_MN) {
+                            tensor3d_g2s(a, &p.a_map, x.m0, k0, z, bar);
+                            tensor3d_g2s(a + 8192, &p.a_map, x.m0 + 64, k0, z, bar);
+                        } else {
+                            tensor3d_g2s(a, &p.a_map, k0, x.m0, z, bar);
+                        }
+                        for (int i = 0; i < boxes; ++i)
+                            tensor2d_g2s(b + i * S::BOX * 128, &p.b_map, k0,
+                                         (int)(x.r0 + i * S::BOX), bar);
+                    }
+                    ++issued;
+                    if (++stage == S::stages) {
+                        stage = 0;
+                        parity ^= 1;
+                    }
+                }
+            }
+            // another thread gave up: see the copies in flight land before the CTA ends
+            for (int64_t i = 0; !ok && i < S::stages && i < issued; ++i) {
+                const int64_t last = issued - 1 - i;
+                mbar_wait(&full[last % S::stages], (uint32_t)(last / S::stages) & 1, p.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------ products
+        int stage = 0, acc = 0;
+        uint32_t parity = 0, free_parity = 1;    // both accumulators start free
+        bool ok = true;
+        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+            const ExpertTile x = list.template tile<NT, GRAD>(p, t);
+            if (x.k == 0) continue;
+            ok = warp_wait(&taken[acc], free_parity, p.err);
+            if (!ok) break;
+            mma_fence_after();
+            const uint32_t d = tmem + acc * NT;
+            const uint32_t instr = instr_f16<T>(kRowsM, (x.n + 15) & ~15, A_MN, GRAD);
+            for (int k0 = 0; k0 < x.k; k0 += kDepth) {
+                ok = warp_wait(&full[stage], parity, p.err);
+                if (!ok) break;
+                mma_fence_after();
+                const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+                const int left = min(kDepth, x.k - k0), steps = (left + 15) / 16;
+                if (GRAD && left % 16) {
+                    zero_rows(a, 2, left, steps * 16);
+                    zero_rows(b, (x.n + 63) / 64, left, steps * 16);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    for (int i = 0; i < steps; ++i) {
+                        const uint64_t da = A_MN ? desc_mn(a + i * 2048, 8192) : desc_k(a + i * 32);
+                        const uint64_t db = GRAD ? desc_mn(b + i * 2048, 8192) : desc_k(b + i * 32);
+                        mma_f16(d, da, db, instr, k0 > 0 || i > 0);
+                    }
+                    mma_commit(&empty[stage]);
+                }
+                if (++stage == S::stages) {
+                    stage = 0;
+                    parity ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) mma_commit(&ready[acc]);
+            acc ^= 1;
+            free_parity ^= acc == 0;
+        }
+        if (!ok && lane == 0) mma_drain(&drained, p.err);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------ results
+        const int quarter = warp & 3;            // the lanes of tensor memory it may read
+        const uint32_t out_smem = smem + S::at_out + quarter * 32 * S::out_pitch;
+        // where this lane's column of a transposed store lies, and its part of a row to write
+        const uint32_t put = out_smem + ((lane >> 4) * 8 + (lane & 7)) * S::out_pitch +
+                             ((lane >> 3) & 1) * 16;
+        const uint32_t get = out_smem + (lane >> 2) * S::out_pitch + (lane & 3) * 16;
+        int acc = 0;
+        uint32_t parity = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const ExpertTile x = list.template tile<NT, GRAD>(p, t);
+            const int m = x.m0 + quarter * 32 + (lane & 3) * 8;
+            T *out = (T *)p.out + (GRAD ? x.e * p.o_se + x.n0 * p.o_ld : x.r0 * p.o_ld) + m;
+            if (x.k == 0) {
+                for (int n = lane >> 2; m < p.M && n < x.n; n += 8)
+                    *(uint4 *)(out + n * p.o_ld) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            if (!warp_wait(&ready[acc], parity, p.err)) break;
+            mma_fence_after();
+            const uint32_t d = tmem + acc * NT + ((uint32_t)quarter << 21);
+            for (int c = 0; c < x.n; c += 32) {
+                uint32_t v[2][16];
+                tmem_ld16x32(d + c, v[0]);
+                tmem_ld16x32(d + (16u << 16) + c, v[1]);
+                tmem_wait_ld();
+                __syncwarp();                    // the rows before are written out
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            y[j] = pack2<T>(__uint_as_float(v[h][4 * i + 2 * j]),
+                                            __uint_as_float(v[h][4 * i + 2 * j + 1]));
+                        stsm4_t(put + i * 8 * S::out_pitch + h * 32, y[0], y[1], y[2], y[3]);
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n = c + i * 8 + (lane >> 2);
+                    const uint4 y = lds16(get + i * 8 * S::out_pitch);
+                    if (m < p.M && n < x.n) *(uint4 *)(out + n * p.o_ld) = y;
+                }
+            }
+            mma_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&taken[acc]);
+            acc ^= 1;
+            parity ^= acc == 0;
+        }
+        if (!GRAD) {                             // the rows of no pair
+            const int64_t kept = list.first[p.E];
+            uint4 *out = (uint4 *)((T *)p.out + kept * p.o_ld);
+            const int64_t n = (p.P - kept) * p.o_ld / 8;
+            for (int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x - 64; i < n;
+                 i += (int64_t)gridDim.x * 128)
+                out[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    __syncthreads();
+    if (warp == 1) tmem_free(tmem, S::columns);
 }
 
 // ------------------------------------------------------------------- host
@@ -130,6 +412,76 @@ bool strides_ok(int64_t se, int64_t sh, int64_t sf) {
     if (se < 0 || se % 8) return false;
     return (sf == 1 && sh > 0 && sh % 8 == 0) || (sh == 1 && sf > 0 && sf % 8 == 0);
 }
+bool strides_far(int64_t se, int64_t sh, int64_t sf) {
+    return std::max(se, std::max(sh, sf)) >= (int64_t)1 << 38;   // a tensor map's are below 2^40 bytes
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                               cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess
+                   ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f)
+                   : nullptr;
+    }();
+    return fn;
+}
+
+// [n2, n1, n0] elements with adjacent n0; copies of box1 rows of 64.
+cudaError_t encode(CUtensorMap *map, int dtype, int rank, const void *p, int64_t n0, int64_t n1,
+                   int64_t n2, int64_t s1, int64_t s2, int box1) {
+    if (!encoder()) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)s2 * 2};
+    const cuuint32_t box[3] = {kDepth, (cuuint32_t)box1, 1}, step[3] = {1, 1, 1};
+    const CUresult e = encoder()(
+        map, dtype == SPMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+        (cuuint32_t)rank, const_cast<void *>(p), dims, strides, box, step,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename T, int NT, bool A_MN, bool GRAD>
+cudaError_t launch(const ExpertArgs &p, int64_t most, cudaStream_t s) {
+    using S = ExpertShape<NT>;
+    // the kernel's limit is the process's: always the largest, as another thread may set it
+    static_assert(S::at_offsets + 1024 + 8 * (SPMM_ROUTES_MAX_EXPERTS + 1) <= kSmemMax, "fits");
+    cudaError_t e = cudaFuncSetAttribute(k_experts<T, NT, A_MN, GRAD>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)S::bytes(SPMM_ROUTES_MAX_EXPERTS));
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, kSms));
+    k_experts<T, NT, A_MN, GRAD><<<grid, kThreads, S::bytes(p.E), s>>>(p);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <int NT, bool A_MN, bool GRAD>
+cudaError_t launch(int dtype, const ExpertArgs &p, int64_t most, cudaStream_t s) {
+    return dtype == SPMM_BF16 ? launch<__nv_bfloat16, NT, A_MN, GRAD>(p, most, s)
+                              : launch<__half, NT, A_MN, GRAD>(p, most, s);
+}
+
+// Tiles of up to 64 slots while the experts have no more than that on average: eight
+// stages of copies in flight instead of four.
+bool few_slots(int64_t P, int64_t E) { return P <= 64 * E; }
+
+template <int NT>
+cudaError_t product(int dtype, ExpertArgs &p, const void *xs, const void *w, int64_t se,
+                    int64_t sh, int64_t sf, cudaStream_t s) {
+    const int64_t n2 = p.a_step ? p.E : 1, s2 = p.a_step ? se : 8;
+    const bool mn = sf == 1;
+    cudaError_t e = mn ? encode(&p.a_map, dtype, 3, w, p.M, p.K, n2, sh, s2, 64)
+                       : encode(&p.a_map, dtype, 3, w, p.K, p.M, n2, sf, s2, kRowsM);
+    if (e == cudaSuccess)
+        e = encode(&p.b_map, dtype, 2, xs, p.K, p.P, 1, p.K, 8, ExpertShape<NT>::BOX);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (p.P / NT + std::min<int64_t>(p.E, p.P)) * p.tiles_m;
+    return mn ? launch<NT, true, false>(dtype, p, most, s) : launch<NT, false, false>(dtype, p, most, s);
+}
 
 }  // namespace
 }  // namespace spmm
@@ -143,16 +495,28 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
     const spmm_status st = check_sizes(dtype, offsets, P, E, H, F);
     if (st != SPMM_OK) return st;
     if (P == 0 || F == 0) return SPMM_OK;
-    if (!aligned(ys) || (H && (!aligned(xs) || (E && (!aligned(w) || !strides_ok(w_se, w_sh, w_sf))))))
-        return SPMM_ERR_INVALID_ARG;
-    const ExpertArgs p{xs, w, ys, offsets, w_se, w_sh, w_sf, P, (int)E, (int)H, (int)F};
-    const dim3 grid((unsigned)((F + kTile - 1) / kTile), (unsigned)(P / kTile + E + 1));
-    if (dtype == SPMM_BF16)
-        k_product<__nv_bfloat16><<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-    else
-        k_product<__half><<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-    count_launch();
-    return cuda_status(cudaGetLastError());
+    if (!aligned(ys)) return SPMM_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    if (E == 0 || H == 0)                        // nothing to add up
+        return cuda_status(cudaMemsetAsync(ys, 0, (size_t)P * F * 2, s));
+    if (!aligned(xs) || !aligned(w) || !strides_ok(w_se, w_sh, w_sf)) return SPMM_ERR_INVALID_ARG;
+    ExpertArgs p{};
+    p.tiles_m = (int)((F + kRowsM - 1) / kRowsM);
+    if (strides_far(w_se, w_sh, w_sf) || (P / 64 + E) * p.tiles_m > INT32_MAX)
+        return SPMM_ERR_UNSUPPORTED;
+    p.offsets = offsets;
+    p.out = ys;
+    p.o_ld = F;
+    p.P = P;
+    p.E = (int)E;
+    p.M = (int)F;
+    p.K = (int)H;
+    p.a_step = E > 1 && w_se > 0;
+    cudaError_t e = dynamic_err(s, &p.err);
+    if (e == cudaSuccess)
+        e = few_slots(P, E) ? product<64>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
+                            : product<256>(dtype, p, xs, w, w_se, w_sh, w_sf, s);
+    return cuda_status(e);
 }
 
 spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *dys,
@@ -166,15 +530,30 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
     if (!aligned(dw) || !strides_ok(dw_se, dw_sh, dw_sf) || (E > 1 && dw_se == 0))
         return SPMM_ERR_INVALID_ARG;
     if (P && (!aligned(xs) || !aligned(dys))) return SPMM_ERR_INVALID_ARG;
-    const ExpertArgs p{xs, dys, dw, offsets, dw_se, dw_sh, dw_sf, P, (int)E, (int)H, (int)F};
-    const dim3 grid((unsigned)((F + kTile - 1) / kTile), (unsigned)((H + kTile - 1) / kTile),
-                    (unsigned)E);
-    if (dtype == SPMM_BF16)
-        k_weights<__nv_bfloat16><<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-    else
-        k_weights<__half><<<grid, kThreads, 0, (cudaStream_t)stream>>>(p);
-    count_launch();
-    return cuda_status(cudaGetLastError());
+    constexpr int NT = 256;
+    const bool by_f = dw_sf == 1;                // m = f, else m = h
+    ExpertArgs p{};
+    p.M = (int)(by_f ? F : H);
+    p.N = (int)(by_f ? H : F);
+    p.tiles_m = (p.M + kRowsM - 1) / kRowsM;
+    p.tiles_n = (p.N + NT - 1) / NT;
+    if (E * p.tiles_m * p.tiles_n > INT32_MAX) return SPMM_ERR_UNSUPPORTED;
+    p.offsets = offsets;
+    p.out = dw;
+    p.o_se = dw_se;
+    p.o_ld = by_f ? dw_sh : dw_sf;
+    p.P = P;
+    p.E = (int)E;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = dynamic_err(s, &p.err);
+    const void *a = by_f ? dys : xs, *b = by_f ? xs : dys;
+    if (e == cudaSuccess && P) {
+        e = encode(&p.a_map, dtype, 3, a, p.M, P, 1, p.M, 8, kDepth);
+        if (e == cudaSuccess) e = encode(&p.b_map, dtype, 2, b, p.N, P, 1, p.N, 8, kDepth);
+    }
+    if (e == cudaSuccess)
+        e = launch<NT, true, true>(dtype, p, (int64_t)p.E * p.tiles_m * p.tiles_n, s);
+    return cuda_status(e);
 }
 
 }  // extern "C"
