@@ -10,10 +10,11 @@
 //              B = xs^T, both MN-major. The ragged index is the summed one: rows past
 //              the expert's last are the next expert's, and are set to 0 in shared
 //              memory before they are used (0 times a NaN is none of this expert's).
-// CTAs stay and take tiles of 128 x up to 256 in turn. A warp's thread copies the
-// operands' tiles of 64 of k into a ring of stages (tensor copies), another issues
-// the products into one of two accumulators in tensor memory, and four warps
-// write the other one out meanwhile.
+// CTAs stay and take tiles of 128 x up to 256 in turn, or pairs of CTAs tiles of 256 x
+// up to 256, of which each holds half of either operand and 128 of m of the result. A
+// warp's thread copies the operands' tiles of 64 of k into a ring of stages (tensor
+// copies), another (of the pair's first CTA) issues the products into one of two
+// accumulators in tensor memory, and four warps write the other one out meanwhile.
 #include <cudaTypedefs.h>
 
 #include "umma.cuh"
@@ -23,7 +24,7 @@ namespace {
 
 constexpr int kSms = 152;
 constexpr int kDepth = 64;           // of k in a stage: a row of 128 bytes
-constexpr int kRowsM = 128;          // of m in a tile
+constexpr int kRowsM = 128;          // of m in a CTA's tile
 constexpr int kThreads = 192;        // copies, products, four warps of results
 constexpr int kSmemMax = 227 * 1024;
 
@@ -39,12 +40,12 @@ struct ExpertArgs {
     int32_t *err;
 };
 
-// NT: largest n of a tile. BOX: rows of B that one copy brings.
-template <int NT_> struct ExpertShape {
-    static constexpr int NT = NT_, BOX = NT / 4;
-    static constexpr int a_bytes = kRowsM * kDepth * 2, b_bytes = NT * kDepth * 2;
+// NT: largest n of a tile. NC: CTAs of a tile. BOX: rows of B that one copy brings.
+template <int NT_, int NC_> struct ExpertShape {
+    static constexpr int NT = NT_, NC = NC_, BOX = NT / NC / 4, STEP = 16 * NC;   // of n
+    static constexpr int a_bytes = kRowsM * kDepth * 2, b_bytes = NT / NC * kDepth * 2;
     static constexpr int stage = a_bytes + b_bytes;
-    static constexpr int stages = NT == 256 ? 4 : 8;
+    static constexpr int stages = 192 * 1024 / stage;
     static constexpr int columns = 2 * NT;
     // results: 32 rows of 64 bytes for each of four warps, the rows 80 bytes apart, so
     // that eight of them fall in different banks
@@ -54,7 +55,7 @@ template <int NT_> struct ExpertShape {
 };
 
 struct ExpertTile {
-    int e, n, m0, n0;                // m0, n0: first of m, of n (gradient)
+    int e, n, m0, n0;                // m0, n0: first of m (of the pair's), of n (gradient)
     int64_t r0;                      // first slot: of n (product), of k (gradient)
     int k;                           // length of k
 };
@@ -63,14 +64,15 @@ struct ExpertTile {
 // each expert.
 struct ExpertList {
     const int32_t *first, *before;
-    template <int NT, bool GRAD>
+    template <bool GRAD>
     __device__ __forceinline__ int tiles(const ExpertArgs &p) const {
         return (GRAD ? p.E * p.tiles_n : before[p.E]) * p.tiles_m;
     }
-    template <int NT, bool GRAD>
+    template <typename S, bool GRAD>
     __device__ __forceinline__ ExpertTile tile(const ExpertArgs &p, int t) const {
+        constexpr int NT = S::NT;
         ExpertTile x;
-        x.m0 = t % p.tiles_m * kRowsM;
+        x.m0 = t % p.tiles_m * (kRowsM * S::NC);
         const int u = t / p.tiles_m;
         if (GRAD) {
             x.e = u / p.tiles_n;
@@ -89,7 +91,8 @@ struct ExpertList {
             x.n0 = 0;
             // an expert's slots in equal parts
             const int rows = first[lo + 1] - first[lo], parts = before[lo + 1] - before[lo];
-            const int per = (((rows + parts - 1) / parts) + 15) & ~15, at = (u - before[lo]) * per;
+            const int per = ((rows + parts - 1) / parts + S::STEP - 1) / S::STEP * S::STEP;
+            const int at = (u - before[lo]) * per;
             x.r0 = (int64_t)first[lo] + at;
             x.n = min(per, rows - at);
             x.k = p.K;
@@ -139,21 +142,39 @@ __device__ __forceinline__ ExpertList expert_list(const ExpertArgs &p, int32_t *
     return ExpertList{first, before};
 }
 
-__device__ __forceinline__ void tensor3d_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                             int z, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-        : "memory");
+// Tensor copies into this CTA's shared memory; of a pair, `bar` may be the other's barrier
+// (its address in the cluster's shared memory).
+template <int NC>
+__device__ __forceinline__ void copy3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                       uint32_t bar) {
+    if constexpr (NC == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::"
+            "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
 }
-__device__ __forceinline__ void tensor2d_g2s(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                             uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
-        : "memory");
+template <int NC>
+__device__ __forceinline__ void copy2d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                       uint32_t bar) {
+    if constexpr (NC == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::"
+            "complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 
 // 16 lanes x 32 columns: with r = lane / 4 and c = lane % 4, registers 4 i and 4 i + 1
@@ -189,6 +210,79 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
+// The same for arrivals of the pair's other CTA: what that did before is seen. (An
+// acquire of the cluster's costs a microsecond, so only once a tile.)
+__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
+    const bool ok = warp_wait(bar, parity, err);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    return ok;
+}
+
+// Address of the pair's first CTA's variable.
+__device__ __forceinline__ uint32_t of_first(const void *p) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(at) : "r"(smem_addr(p)));
+    return at;
+}
+
+// One arrival at the barrier of the pair's first CTA.
+__device__ __forceinline__ void arrive_first(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first(bar))
+                 : "memory");
+}
+
+// The instructions of one CTA (umma.cuh) or of a pair.
+template <int NC>
+__device__ __forceinline__ void product_step(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
+                                             bool accumulate) {
+    if constexpr (NC == 1) {
+        mma_f16(d, a, b, instr, accumulate);
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(instr), "r"((uint32_t)accumulate)
+            : "memory");
+    }
+}
+// The barrier (of both CTAs) receives one arrival when the products issued so far are done.
+template <int NC> __device__ __forceinline__ void commit_products(uint64_t *bar) {
+    if constexpr (NC == 1) {
+        mma_commit(bar);
+    } else {
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+            ".b64 [%0], %1;" ::"r"(smem_addr(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+    }
+}
+template <int NC> __device__ __forceinline__ void alloc_columns(uint32_t *slot, int columns) {
+    if constexpr (NC == 1) {
+        tmem_alloc(slot, columns);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(slot)),
+                     "r"(columns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int NC> __device__ __forceinline__ void free_columns(uint32_t tmem, int columns) {
+    if constexpr (NC == 1)
+        tmem_free(tmem, columns);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(columns)
+                     : "memory");
+}
+// All threads of the CTA, or of the pair.
+template <int NC> __device__ __forceinline__ void pair_barrier() {
+    if constexpr (NC == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 
 // Rows [from, to) of `panels` panels of 64 rows set to 0, by one warp.
 __device__ __forceinline__ void zero_rows(uint32_t operand, int panels, int from, int to) {
@@ -202,36 +296,42 @@ __device__ __forceinline__ void zero_rows(uint32_t operand, int panels, int from
 }
 
 // A_MN: A's elements adjacent in m (else in k). B is adjacent in k, in the gradient in n.
-template <typename T, int NT, bool A_MN, bool GRAD>
+template <typename T, int NT, int NC, bool A_MN, bool GRAD>
 __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__ ExpertArgs p) {
-    using S = ExpertShape<NT>;
+    using S = ExpertShape<NT, NC>;
     static_assert(A_MN || !GRAD, "the gradient's operands are both adjacent in m and n");
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t full[S::stages], empty[S::stages], ready[2], taken[2], drained;
+    // other: (first CTA of a pair) the second one's part of a stage is mended
+    __shared__ uint64_t full[S::stages], empty[S::stages], other[S::stages], ready[2], taken[2];
+    __shared__ uint64_t drained;
     __shared__ uint32_t tmem_slot;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = NC == 1 ? 0 : blockIdx.x & 1;   // in the pair
+    const int first_tile = blockIdx.x / NC, step = gridDim.x / NC;
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
+            mbar_init(&other[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ready[i], 1);
-            mbar_init(&taken[i], 4);
+            mbar_init(&taken[i], 4 * NC);
         }
         mbar_init(&drained, 1);
         mbar_init_fence();
     }
     if (warp == 1) {
-        tmem_alloc(&tmem_slot, S::columns);
+        alloc_columns<NC>(&tmem_slot, S::columns);
         mma_fence_before();
     }
     const ExpertList list = expert_list<NT, GRAD>(
         p, (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_offsets));
-    mma_fence_after();                           // (the list's barriers came between)
+    pair_barrier<NC>();
+    mma_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int tiles = list.template tiles<NT, GRAD>(p);
+    const int tiles = list.template tiles<GRAD>(p);
 
     if (warp == 0) {
         // ------------------------------------------------------ operands' tiles
@@ -240,34 +340,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             int64_t issued = 0;
             uint32_t parity = 1;                 // the ring starts empty
             bool ok = true;
-            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-                const ExpertTile x = list.template tile<NT, GRAD>(p, t);
-                const int boxes = GRAD ? (x.n + 63) / 64 : (x.n + S::BOX - 1) / S::BOX;
+            for (int t = first_tile; ok && t < tiles; t += step) {
+                const ExpertTile x = list.template tile<S, GRAD>(p, t);
+                const int m0 = x.m0 + rank * kRowsM;
+                const int mine = (x.n + S::STEP - 1) / S::STEP * 16, n0 = rank * mine;   // of n
+                const int boxes = GRAD ? (mine + 63) / 64 : (mine + S::BOX - 1) / S::BOX;
                 const uint32_t bytes =
                     S::a_bytes + (uint32_t)boxes * (GRAD ? 8192 : S::BOX * kDepth * 2);
                 for (int k0 = 0; k0 < x.k; k0 += kDepth) {
                     ok = mbar_wait(&empty[stage], parity, p.err);
                     if (!ok) break;
-                    uint64_t *bar = &full[stage];
+                    // a pair's copies are counted by its first CTA, but for a stage that
+                    // each mends first
+                    const bool apart = GRAD && (x.k - k0) % 16 && x.k - k0 < kDepth;
+                    const bool joint = NC == 2 && !apart;
+                    if (rank == 0 || !joint)
+                        mbar_arrive_expect_tx(&full[stage], joint ? NC * bytes : bytes);
+                    const uint32_t bar =
+                        rank == 0 || !joint ? smem_addr(&full[stage]) : of_first(&full[stage]);
                     const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
-                    mbar_arrive_expect_tx(bar, bytes);
                     if (GRAD) {
                         const int r = (int)(x.r0 + k0);
-                        tensor3d_g2s(a, &p.a_map, x.m0, r, 0, bar);
-                        tensor3d_g2s(a + 8192, &p.a_map, x.m0 + 64, r, 0, bar);
+                        copy3d<NC>(a, &p.a_map, m0, r, 0, bar);
+                        copy3d<NC>(a + 8192, &p.a_map, m0 + 64, r, 0, bar);
                         for (int i = 0; i < boxes; ++i)
-                            tensor2d_g2s(b + i * 8192, &p.b_map, x.n0 + 64 * i, r, bar);
+                            copy2d<NC>(b + i * 8192, &p.b_map, x.n0 + n0 + 64 * i, r, bar);
                     } else {
                         const int z = x.e * p.a_step;
                         if (A_MN) {
-                            tensor3d_g2s(a, &p.a_map, x.m0, k0, z, bar);
-                            tensor3d_g2s(a + 8192, &p.a_map, x.m0 + 64, k0, z, bar);
+                            copy3d<NC>(a, &p.a_map, m0, k0, z, bar);
+                            copy3d<NC>(a + 8192, &p.a_map, m0 + 64, k0, z, bar);
                         } else {
-                            tensor3d_g2s(a, &p.a_map, k0, x.m0, z, bar);
+                            copy3d<NC>(a, &p.a_map, k0, m0, z, bar);
                         }
                         for (int i = 0; i < boxes; ++i)
-                            tensor2d_g2s(b + i * S::BOX * 128, &p.b_map, k0,
-                                         (int)(x.r0 + i * S::BOX), bar);
+                            copy2d<NC>(b + i * S::BOX * 128, &p.b_map, k0,
+                                       (int)(x.r0 + n0 + i * S::BOX), bar);
                     }
                     ++issued;
                     if (++stage == S::stages) {
@@ -277,7 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                 }
             }
             // another thread gave up: see the copies in flight land before the CTA ends
-            for (int64_t i = 0; !ok && i < S::stages && i < issued; ++i) {
+            // (those of a pair's second CTA are counted by the first: it waits for a while)
+            if (!ok && rank == 1) mbar_wait(&drained, 0, p.err);
+            for (int64_t i = 0; !ok && rank == 0 && i < S::stages && i < issued; ++i) {
                 const int64_t last = issued - 1 - i;
                 mbar_wait(&full[last % S::stages], (uint32_t)(last / S::stages) & 1, p.err);
             }
@@ -287,34 +397,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         // ------------------------------------------------------ products
         int stage = 0, acc = 0;
         uint32_t parity = 0, free_parity = 1;    // both accumulators start free
+        uint32_t mended = 0;                     // a bit per stage: how often, mod 2
         bool ok = true;
-        for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-            const ExpertTile x = list.template tile<NT, GRAD>(p, t);
+        for (int t = first_tile; ok && t < tiles; t += step) {
+            const ExpertTile x = list.template tile<S, GRAD>(p, t);
             if (x.k == 0) continue;
-            ok = warp_wait(&taken[acc], free_parity, p.err);
-            if (!ok) break;
-            mma_fence_after();
-            const uint32_t d = tmem + acc * NT;
-            const uint32_t instr = instr_f16<T>(kRowsM, (x.n + 15) & ~15, A_MN, GRAD);
-            for (int k0 = 0; k0 < x.k; k0 += kDepth) {
-                ok = warp_wait(&full[stage], parity, p.err);
+            const int mine = (x.n + S::STEP - 1) / S::STEP * 16;
+            if (rank == 0) {
+                ok = NC == 1 ? warp_wait(&taken[acc], free_parity, p.err)
+                             : pair_wait(&taken[acc], free_parity, p.err);
                 if (!ok) break;
                 mma_fence_after();
-                const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+            }
+            const uint32_t d = tmem + acc * NT;
+            const uint32_t instr = instr_f16<T>(kRowsM * NC, mine * NC, A_MN, GRAD);
+            for (int k0 = 0; k0 < x.k; k0 += kDepth) {
                 const int left = min(kDepth, x.k - k0), steps = (left + 15) / 16;
-                if (GRAD && left % 16) {
+                const bool mend = GRAD && left % 16;
+                const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+                if (rank == 0) {
+                    ok = warp_wait(&full[stage], parity, p.err);
+                    if (!ok) break;
+                }
+                if (mend) {
+                    const uint32_t times = mended >> stage & 1;
+                    if (rank == 1) {
+                        ok = warp_wait(&full[stage], times, p.err);
+                        if (!ok) break;
+                    }
                     zero_rows(a, 2, left, steps * 16);
-                    zero_rows(b, (x.n + 63) / 64, left, steps * 16);
+                    zero_rows(b, (mine + 63) / 64, left, steps * 16);
                     fence_proxy_async_shared();
                     __syncwarp();
-                }
-                if (lane == 0) {
-                    for (int i = 0; i < steps; ++i) {
-                        const uint64_t da = A_MN ? desc_mn(a + i * 2048, 8192) : desc_k(a + i * 32);
-                        const uint64_t db = GRAD ? desc_mn(b + i * 2048, 8192) : desc_k(b + i * 32);
-                        mma_f16(d, da, db, instr, k0 > 0 || i > 0);
+                    if (NC == 2 && rank == 0) {
+                        ok = pair_wait(&other[stage], times, p.err);
+                        if (!ok) break;
+                    } else if (NC == 2 && lane == 0) {
+                        arrive_first(&other[stage]);
                     }
-                    mma_commit(&empty[stage]);
+                    mended ^= 1u << stage;
+                }
+                if (rank == 0) {
+                    mma_fence_after();
+                    if (lane == 0) {
+                        for (int i = 0; i < steps; ++i) {
+                            const uint64_t da =
+                                A_MN ? desc_mn(a + i * 2048, 8192) : desc_k(a + i * 32);
+                            const uint64_t db =
+                                GRAD ? desc_mn(b + i * 2048, 8192) : desc_k(b + i * 32);
+                            product_step<NC>(d, da, db, instr, k0 > 0 || i > 0);
+                        }
+                        commit_products<NC>(&empty[stage]);
+                    }
                 }
                 if (++stage == S::stages) {
                     stage = 0;
@@ -322,11 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                 }
             }
             if (!ok) break;
-            if (lane == 0) mma_commit(&ready[acc]);
+            if (rank == 0 && lane == 0) commit_products<NC>(&ready[acc]);
             acc ^= 1;
             free_parity ^= acc == 0;
         }
-        if (!ok && lane == 0) mma_drain(&drained, p.err);
+        if (!ok && rank == 0 && lane == 0) {
+            commit_products<NC>(&drained);
+            mbar_wait_poll(&drained, 0, p.err);
+        }
         __syncwarp();
     } else {
         // ------------------------------------------------------ results
@@ -338,9 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         const uint32_t get = out_smem + (lane >> 2) * S::out_pitch + (lane & 3) * 16;
         int acc = 0;
         uint32_t parity = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-            const ExpertTile x = list.template tile<NT, GRAD>(p, t);
-            const int m = x.m0 + quarter * 32 + (lane & 3) * 8;
+        for (int t = first_tile; t < tiles; t += step) {
+            const ExpertTile x = list.template tile<S, GRAD>(p, t);
+            const int m = x.m0 + rank * kRowsM + quarter * 32 + (lane & 3) * 8;
             T *out = (T *)p.out + (GRAD ? x.e * p.o_se + x.n0 * p.o_ld : x.r0 * p.o_ld) + m;
             if (x.k == 0) {
                 for (int n = lane >> 2; m < p.M && n < x.n; n += 8)
@@ -377,7 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             }
             mma_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&taken[acc]);
+            if (lane == 0) {
+                if (rank == 0) mbar_arrive(&taken[acc]);
+                else arrive_first(&taken[acc]);
+            }
             acc ^= 1;
             parity ^= acc == 0;
         }
@@ -389,9 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                  i += (int64_t)gridDim.x * 128)
                 out[i] = make_uint4(0, 0, 0, 0);
         }
+        __syncwarp();
     }
-    __syncthreads();
-    if (warp == 1) tmem_free(tmem, S::columns);
+    // (of a pair: neither leaves, or gives its tensor memory back, before both are done)
+    pair_barrier<NC>();
+    if (warp == 1) free_columns<NC>(tmem, S::columns);
 }
 
 // ------------------------------------------------------------------- host
@@ -444,43 +586,63 @@ cudaError_t encode(CUtensorMap *map, int dtype, int rank, const void *p, int64_t
     return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename T, int NT, bool A_MN, bool GRAD>
+template <typename T, int NT, int NC, bool A_MN, bool GRAD>
 cudaError_t launch(const ExpertArgs &p, int64_t most, cudaStream_t s) {
-    using S = ExpertShape<NT>;
+    using S = ExpertShape<NT, NC>;
     // the kernel's limit is the process's: always the largest, as another thread may set it
     static_assert(S::at_offsets + 1024 + 8 * (SPMM_ROUTES_MAX_EXPERTS + 1) <= kSmemMax, "fits");
-    cudaError_t e = cudaFuncSetAttribute(k_experts<T, NT, A_MN, GRAD>,
+    cudaError_t e = cudaFuncSetAttribute(k_experts<T, NT, NC, A_MN, GRAD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)S::bytes(SPMM_ROUTES_MAX_EXPERTS));
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(most, kSms));
-    k_experts<T, NT, A_MN, GRAD><<<grid, kThreads, S::bytes(p.E), s>>>(p);
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = NC;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    c.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min<int64_t>(most, kSms / NC)) * NC);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = S::bytes(p.E);
+    c.stream = s;
+    c.attrs = &attr;
+    c.numAttrs = NC > 1;
+    e = cudaLaunchKernelEx(&c, k_experts<T, NT, NC, A_MN, GRAD>, p);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
-template <int NT, bool A_MN, bool GRAD>
+template <int NT, int NC, bool A_MN, bool GRAD>
 cudaError_t launch(int dtype, const ExpertArgs &p, int64_t most, cudaStream_t s) {
-    return dtype == SPMM_BF16 ? launch<__nv_bfloat16, NT, A_MN, GRAD>(p, most, s)
-                              : launch<__half, NT, A_MN, GRAD>(p, most, s);
+    return dtype == SPMM_BF16 ? launch<__nv_bfloat16, NT, NC, A_MN, GRAD>(p, most, s)
+                              : launch<__half, NT, NC, A_MN, GRAD>(p, most, s);
 }
 
 // Tiles of up to 64 slots while the experts have no more than that on average: eight
 // stages of copies in flight instead of four.
 bool few_slots(int64_t P, int64_t E) { return P <= 64 * E; }
 
-template <int NT>
+template <int NT, int NC>
 cudaError_t product(int dtype, ExpertArgs &p, const void *xs, const void *w, int64_t se,
                     int64_t sh, int64_t sf, cudaStream_t s) {
+    using S = ExpertShape<NT, NC>;
     const int64_t n2 = p.a_step ? p.E : 1, s2 = p.a_step ? se : 8;
     const bool mn = sf == 1;
     cudaError_t e = mn ? encode(&p.a_map, dtype, 3, w, p.M, p.K, n2, sh, s2, 64)
                        : encode(&p.a_map, dtype, 3, w, p.K, p.M, n2, sf, s2, kRowsM);
-    if (e == cudaSuccess)
-        e = encode(&p.b_map, dtype, 2, xs, p.K, p.P, 1, p.K, 8, ExpertShape<NT>::BOX);
+    if (e == cudaSuccess) e = encode(&p.b_map, dtype, 2, xs, p.K, p.P, 1, p.K, 8, S::BOX);
     if (e != cudaSuccess) return e;
+    p.tiles_m = (p.M + kRowsM * NC - 1) / (kRowsM * NC);
     const int64_t most = (p.P / NT + std::min<int64_t>(p.E, p.P)) * p.tiles_m;
-    return mn ? launch<NT, true, false>(dtype, p, most, s) : launch<NT, false, false>(dtype, p, most, s);
+    return mn ? launch<NT, NC, true, false>(dtype, p, most, s)
+              : launch<NT, NC, false, false>(dtype, p, most, s);
+}
+
+template <int NC>
+cudaError_t weights(int dtype, ExpertArgs &p, cudaStream_t s) {
+    constexpr int NT = 256;
+    p.tiles_m = (p.M + kRowsM * NC - 1) / (kRowsM * NC);
+    p.tiles_n = (p.N + NT - 1) / NT;
+    return launch<NT, NC, true, true>(dtype, p, (int64_t)p.E * p.tiles_m * p.tiles_n, s);
 }
 
 }  // namespace
@@ -501,8 +663,7 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
         return cuda_status(cudaMemsetAsync(ys, 0, (size_t)P * F * 2, s));
     if (!aligned(xs) || !aligned(w) || !strides_ok(w_se, w_sh, w_sf)) return SPMM_ERR_INVALID_ARG;
     ExpertArgs p{};
-    p.tiles_m = (int)((F + kRowsM - 1) / kRowsM);
-    if (strides_far(w_se, w_sh, w_sf) || (P / 64 + E) * p.tiles_m > INT32_MAX)
+    if (strides_far(w_se, w_sh, w_sf) || (P / 64 + E) * ((F + kRowsM - 1) / kRowsM) > INT32_MAX)
         return SPMM_ERR_UNSUPPORTED;
     p.offsets = offsets;
     p.out = ys;
@@ -514,8 +675,10 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
     p.a_step = E > 1 && w_se > 0;
     cudaError_t e = dynamic_err(s, &p.err);
     if (e == cudaSuccess)
-        e = few_slots(P, E) ? product<64>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
-                            : product<256>(dtype, p, xs, w, w_se, w_sh, w_sf, s);
+        e = few_slots(P, E)
+                ? product<64, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
+            : F > kRowsM ? product<256, 2>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
+                         : product<256, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s);
     return cuda_status(e);
 }
 
@@ -530,14 +693,11 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
     if (!aligned(dw) || !strides_ok(dw_se, dw_sh, dw_sf) || (E > 1 && dw_se == 0))
         return SPMM_ERR_INVALID_ARG;
     if (P && (!aligned(xs) || !aligned(dys))) return SPMM_ERR_INVALID_ARG;
-    constexpr int NT = 256;
     const bool by_f = dw_sf == 1;                // m = f, else m = h
     ExpertArgs p{};
     p.M = (int)(by_f ? F : H);
     p.N = (int)(by_f ? H : F);
-    p.tiles_m = (p.M + kRowsM - 1) / kRowsM;
-    p.tiles_n = (p.N + NT - 1) / NT;
-    if (E * p.tiles_m * p.tiles_n > INT32_MAX) return SPMM_ERR_UNSUPPORTED;
+    if (E * ((p.M + kRowsM - 1) / kRowsM) * ((p.N + 255) / 256) > INT32_MAX) return SPMM_ERR_UNSUPPORTED;
     p.offsets = offsets;
     p.out = dw;
     p.o_se = dw_se;
@@ -552,7 +712,7 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
         if (e == cudaSuccess) e = encode(&p.b_map, dtype, 2, b, p.N, P, 1, p.N, 8, kDepth);
     }
     if (e == cudaSuccess)
-        e = launch<NT, true, true>(dtype, p, (int64_t)p.E * p.tiles_m * p.tiles_n, s);
+        e = p.M > kRowsM ? weights<2>(dtype, p, s) : weights<1>(dtype, p, s);
     return cuda_status(e);
 }
 
