@@ -42,7 +42,7 @@ struct ExpertArgs {
 
 // NT: largest n of a tile. NC: CTAs of a tile. BOX: rows of B that one copy brings.
 template <int NT_, int NC_> struct ExpertShape {
-    static constexpr int NT = NT_, NC = NC_, BOX = NT / NC / 4, STEP = 16 * NC;   // of n
+    static constexpr int NT = NT_, NC = NC_, BOX = NT == 64 ? 16 : NT / NC, STEP = 16 * NC;   // of n
     static constexpr int a_bytes = kRowsM * kDepth * 2, b_bytes = NT / NC * kDepth * 2;
     static constexpr int stage = a_bytes + b_bytes;
     static constexpr int stages = 192 * 1024 / stage;
@@ -411,22 +411,52 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             }
             const uint32_t d = tmem + acc * NT;
             const uint32_t instr = instr_f16<T>(kRowsM * NC, mine * NC, A_MN, GRAD);
-            for (int k0 = 0; k0 < x.k; k0 += kDepth) {
-                const int left = min(kDepth, x.k - k0), steps = (left + 15) / 16;
-                const bool mend = GRAD && left % 16;
+            // whole stages, by one thread
+            const int whole = x.k / kDepth, rest = x.k % kDepth;
+            if (rank == 0) {
+                if (lane == 0) {
+                    for (int i = 0; i < whole; ++i) {
+                        ok = mbar_wait(&full[stage], parity, p.err);
+                        if (!ok) break;
+                        mma_fence_after();
+                        const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+                        uint64_t da = A_MN ? desc_mn(a, 8192) : desc_k(a);
+                        uint64_t db = GRAD ? desc_mn(b, 8192) : desc_k(b);
+#pragma unroll
+                        for (int j = 0; j < kDepth / 16; ++j) {
+                            product_step<NC>(d, da, db, instr, i > 0 || j > 0);
+                            da += (A_MN ? 2048 : 32) >> 4;
+                            db += (GRAD ? 2048 : 32) >> 4;
+                        }
+                        commit_products<NC>(&empty[stage]);
+                        if (++stage == S::stages) {
+                            stage = 0;
+                            parity ^= 1;
+                        }
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                stage = __shfl_sync(0xffffffffu, stage, 0);
+                parity = __shfl_sync(0xffffffffu, parity, 0);
+                if (!ok) break;
+            } else {
+                stage = (stage + whole) % S::stages;
+            }
+            if (rest) {                          // (rank 1 has no use for its parity)
+                const int steps = (rest + 15) / 16;
                 const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
                 if (rank == 0) {
                     ok = warp_wait(&full[stage], parity, p.err);
                     if (!ok) break;
                 }
-                if (mend) {
+                if (GRAD && rest % 16) {
                     const uint32_t times = mended >> stage & 1;
                     if (rank == 1) {
                         ok = warp_wait(&full[stage], times, p.err);
                         if (!ok) break;
                     }
-                    zero_rows(a, 2, left, steps * 16);
-                    zero_rows(b, (mine + 63) / 64, left, steps * 16);
+                    zero_rows(a, 2, rest, steps * 16);
+                    zero_rows(b, (mine + 63) / 64, rest, steps * 16);
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (NC == 2 && rank == 0) {
@@ -437,18 +467,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                     }
                     mended ^= 1u << stage;
                 }
-                if (rank == 0) {
+                if (rank == 0 && lane == 0) {
                     mma_fence_after();
-                    if (lane == 0) {
-                        for (int i = 0; i < steps; ++i) {
-                            const uint64_t da =
-                                A_MN ? desc_mn(a + i * 2048, 8192) : desc_k(a + i * 32);
-                            const uint64_t db =
-                                GRAD ? desc_mn(b + i * 2048, 8192) : desc_k(b + i * 32);
-                            product_step<NC>(d, da, db, instr, k0 > 0 || i > 0);
-                        }
-                        commit_products<NC>(&empty[stage]);
-                    }
+                    for (int i = 0; i < steps; ++i)
+                        product_step<NC>(d, A_MN ? desc_mn(a + i * 2048, 8192) : desc_k(a + i * 32),
+                                         GRAD ? desc_mn(b + i * 2048, 8192) : desc_k(b + i * 32),
+                                         instr, whole > 0 || i > 0);
+                    commit_products<NC>(&empty[stage]);
                 }
                 if (++stage == S::stages) {
                     stage = 0;
