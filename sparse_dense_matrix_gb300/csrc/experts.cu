@@ -231,6 +231,11 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {
                  : "memory");
 }
 
+__device__ __forceinline__ void arrive_first_relaxed(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first(bar))
+                 : "memory");
+}
+
 // The instructions of one CTA (umma.cuh) or of a pair.
 template <int NC>
 __device__ __forceinline__ void product_step(uint32_t d, uint64_t a, uint64_t b, uint32_t instr,
@@ -404,8 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             if (x.k == 0) continue;
             const int mine = (x.n + S::STEP - 1) / S::STEP * 16;
             if (rank == 0) {
-                ok = NC == 1 ? warp_wait(&taken[acc], free_parity, p.err)
-                             : pair_wait(&taken[acc], free_parity, p.err);
+                ok = warp_wait(&taken[acc], free_parity, p.err);
                 if (!ok) break;
                 mma_fence_after();
             }
@@ -540,8 +544,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             mma_fence_before();
             __syncwarp();
             if (lane == 0) {
+                // no memory is handed over (a release would wait for the stores above)
                 if (rank == 0) mbar_arrive(&taken[acc]);
-                else arrive_first(&taken[acc]);
+                else arrive_first_relaxed(&taken[acc]);
             }
             acc ^= 1;
             parity ^= acc == 0;
