@@ -25,7 +25,8 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kDepth = 64;           // of k in a stage: a row of 128 bytes
 constexpr int kRowsM = 128;          // of m in a CTA's tile
-constexpr int kThreads = 192;        // copies, products, four warps of results
+constexpr int kThreads = 224;        // copies, products, four warps of results, the tiles' list
+constexpr int kTilesAhead = 4;
 constexpr int kSmemMax = 227 * 1024;
 
 struct ExpertArgs {
@@ -56,7 +57,7 @@ template <int NT_, int NC_> struct ExpertShape {
 
 struct ExpertTile {
     int e, n, m0, n0;                // m0, n0: first of m (of the pair's), of n (gradient)
-    int64_t r0;                      // first slot: of n (product), of k (gradient)
+    int r0;                          // first slot: of n (product), of k (gradient)
     int k;                           // length of k
 };
 
@@ -93,7 +94,7 @@ struct ExpertList {
             const int rows = first[lo + 1] - first[lo], parts = before[lo + 1] - before[lo];
             const int per = ((rows + parts - 1) / parts + S::STEP - 1) / S::STEP * S::STEP;
             const int at = (u - before[lo]) * per;
-            x.r0 = (int64_t)first[lo] + at;
+            x.r0 = first[lo] + at;
             x.n = min(per, rows - at);
             x.k = p.K;
         }
@@ -225,6 +226,40 @@ __device__ __forceinline__ uint32_t of_first(const void *p) {
     return at;
 }
 
+// The CTA's tiles in turn, worked out by a warp of their own: a search and four divisions
+// take half a microsecond, in which the thread that issues the products would leave the
+// tensor cores idle (they hold a product or two ahead, no more).
+struct TileRing {
+    ExpertTile *tile;
+    uint64_t *full, *empty;
+    int at;
+    uint32_t parity;
+    __device__ __forceinline__ void next() {
+        if (++at == kTilesAhead) {
+            at = 0;
+            parity ^= 1;
+        }
+    }
+    // The next tile, or false after the last; ok is false if the wait gave up.
+    __device__ __forceinline__ bool take(ExpertTile &x, bool &ok, int32_t *err) {
+        ok = mbar_wait(&full[at], parity, err);
+        if (!ok) return false;
+        x = tile[at];
+        mbar_arrive(&empty[at]);
+        next();
+        return x.e >= 0;
+    }
+    __device__ __forceinline__ bool take_warp(ExpertTile &x, bool &ok, int32_t *err) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[at], parity, err));
+        if (!ok) return false;
+        x = tile[at];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[at]);
+        next();
+        return x.e >= 0;
+    }
+};
+
 // One arrival at the barrier of the pair's first CTA.
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(of_first(bar))
@@ -308,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     extern __shared__ unsigned char smem_raw[];
     // other: (first CTA of a pair) the second one's part of a stage is mended
     __shared__ uint64_t full[S::stages], empty[S::stages], other[S::stages], ready[2], taken[2];
-    __shared__ uint64_t drained;
+    __shared__ uint64_t drained, listed[kTilesAhead], read[kTilesAhead];
+    __shared__ ExpertTile tile_ring[kTilesAhead];
     __shared__ uint32_t tmem_slot;
     const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,6 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             mbar_init(&ready[i], 1);
             mbar_init(&taken[i], 4 * NC);
         }
+        for (int i = 0; i < kTilesAhead; ++i) {
+            mbar_init(&listed[i], 1);
+            mbar_init(&read[i], 6);              // a thread of copies, five warps
+        }
         mbar_init(&drained, 1);
         mbar_init_fence();
     }
@@ -336,17 +376,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     pair_barrier<NC>();
     mma_fence_after();
     const uint32_t tmem = tmem_slot;
-    const int tiles = list.template tiles<GRAD>(p);
+    TileRing ring{tile_ring, listed, read, 0, 0};
+    ExpertTile x;
 
-    if (warp == 0) {
+    if (warp == 6) {
+        // ------------------------------------------------------ the tiles' list
+        if (lane == 0) {
+            const int tiles = list.template tiles<GRAD>(p);
+            ring.parity = 1;
+            for (int t = first_tile;; t += step) {
+                if (!mbar_wait(&read[ring.at], ring.parity, p.err)) break;
+                const bool more = t < tiles;
+                if (more) tile_ring[ring.at] = list.template tile<S, GRAD>(p, t);
+                else tile_ring[ring.at].e = -1;
+                mbar_arrive(&listed[ring.at]);
+                ring.next();
+                if (!more) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 0) {
         // ------------------------------------------------------ operands' tiles
         if (lane == 0) {
             int stage = 0;
             int64_t issued = 0;
             uint32_t parity = 1;                 // the ring starts empty
             bool ok = true;
-            for (int t = first_tile; ok && t < tiles; t += step) {
-                const ExpertTile x = list.template tile<S, GRAD>(p, t);
+            while (ok && ring.take(x, ok, p.err)) {
                 const int m0 = x.m0 + rank * kRowsM;
                 const int mine = (x.n + S::STEP - 1) / S::STEP * 16, n0 = rank * mine;   // of n
                 const int boxes = GRAD ? (mine + 63) / 64 : (mine + S::BOX - 1) / S::BOX;
@@ -365,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                         rank == 0 || !joint ? smem_addr(&full[stage]) : of_first(&full[stage]);
                     const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
                     if (GRAD) {
-                        const int r = (int)(x.r0 + k0);
+                        const int r = (int)((int64_t)x.r0 + k0);
                         copy3d<NC>(a, &p.a_map, m0, r, 0, bar);
                         copy3d<NC>(a + 8192, &p.a_map, m0 + 64, r, 0, bar);
                         for (int i = 0; i < boxes; ++i)
@@ -380,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                         }
                         for (int i = 0; i < boxes; ++i)
                             copy2d<NC>(b + i * S::BOX * 128, &p.b_map, k0,
-                                       (int)(x.r0 + n0 + i * S::BOX), bar);
+                                       (int)((int64_t)x.r0 + n0 + i * S::BOX), bar);
                     }
                     ++issued;
                     if (++stage == S::stages) {
@@ -404,8 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         uint32_t parity = 0, free_parity = 1;    // both accumulators start free
         uint32_t mended = 0;                     // a bit per stage: how often, mod 2
         bool ok = true;
-        for (int t = first_tile; ok && t < tiles; t += step) {
-            const ExpertTile x = list.template tile<S, GRAD>(p, t);
+        while (ok && ring.take_warp(x, ok, p.err)) {
             if (x.k == 0) continue;
             const int mine = (x.n + S::STEP - 1) / S::STEP * 16;
             if (rank == 0) {
@@ -504,10 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         const uint32_t get = out_smem + (lane >> 2) * S::out_pitch + (lane & 3) * 16;
         int acc = 0;
         uint32_t parity = 0;
-        for (int t = first_tile; t < tiles; t += step) {
-            const ExpertTile x = list.template tile<S, GRAD>(p, t);
+        bool ok = true;
+        while (ring.take_warp(x, ok, p.err)) {
             const int m = x.m0 + rank * kRowsM + quarter * 32 + (lane & 3) * 8;
-            T *out = (T *)p.out + (GRAD ? x.e * p.o_se + x.n0 * p.o_ld : x.r0 * p.o_ld) + m;
+            T *out = (T *)p.out + (GRAD ? x.e * p.o_se + x.n0 * p.o_ld : (int64_t)x.r0 * p.o_ld) + m;
             if (x.k == 0) {
                 for (int n = lane >> 2; m < p.M && n < x.n; n += 8)
                     *(uint4 *)(out + n * p.o_ld) = make_uint4(0, 0, 0, 0);
