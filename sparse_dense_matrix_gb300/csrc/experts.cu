@@ -25,7 +25,8 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kDepth = 64;           // of k in a stage: a row of 128 bytes
 constexpr int kRowsM = 128;          // of m in a CTA's tile
-constexpr int kThreads = 224;        // copies, products, four warps of results, the tiles' list
+constexpr int kThreads = 256;        // copies, products, four warps of results, the tiles' list,
+                                     // ends of segments
 constexpr int kTilesAhead = 4;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -211,14 +212,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
-// The same for arrivals of the pair's other CTA: what that did before is seen. (An
-// acquire of the cluster's costs a microsecond, so only once a tile.)
-__device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
-    const bool ok = warp_wait(bar, parity, err);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-    return ok;
-}
-
 // Address of the pair's first CTA's variable.
 __device__ __forceinline__ uint32_t of_first(const void *p) {
     uint32_t at;
@@ -341,8 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     using S = ExpertShape<NT, NC>;
     static_assert(A_MN || !GRAD, "the gradient's operands are both adjacent in m and n");
     extern __shared__ unsigned char smem_raw[];
-    // other: (first CTA of a pair) the second one's part of a stage is mended
-    __shared__ uint64_t full[S::stages], empty[S::stages], other[S::stages], ready[2], taken[2];
+    // last: a segment's last stage is there; mended: its rows past the end are 0, in both
+    // CTAs of a pair. (These have barriers of their own, as who waits for them does not
+    // follow the phases of the others.)
+    __shared__ uint64_t full[S::stages], empty[S::stages], last[S::stages], mended[S::stages];
+    __shared__ uint64_t ready[2], taken[2];
     __shared__ uint64_t drained, listed[kTilesAhead], read[kTilesAhead];
     __shared__ ExpertTile tile_ring[kTilesAhead];
     __shared__ uint32_t tmem_slot;
@@ -354,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         for (int i = 0; i < S::stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
-            mbar_init(&other[i], 1);
+            mbar_init(&last[i], 1);
+            mbar_init(&mended[i], NC);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ready[i], 1);
@@ -362,7 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         for (int i = 0; i < kTilesAhead; ++i) {
             mbar_init(&listed[i], 1);
-            mbar_init(&read[i], 6);              // a thread of copies, five warps
+            // a thread of copies, one of products, four warps of results, ends of segments
+            mbar_init(&read[i], 5 + (rank == 0) + GRAD);
         }
         mbar_init(&drained, 1);
         mbar_init_fence();
@@ -401,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             int stage = 0;
             int64_t issued = 0;
             uint32_t parity = 1;                 // the ring starts empty
+            uint32_t ends = 0;                   // a bit per stage: ends so far, mod 2
             bool ok = true;
             while (ok && ring.take(x, ok, p.err)) {
                 const int m0 = x.m0 + rank * kRowsM;
@@ -411,14 +410,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                 for (int k0 = 0; k0 < x.k; k0 += kDepth) {
                     ok = mbar_wait(&empty[stage], parity, p.err);
                     if (!ok) break;
-                    // a pair's copies are counted by its first CTA, but for a stage that
-                    // each mends first
-                    const bool apart = GRAD && (x.k - k0) % 16 && x.k - k0 < kDepth;
-                    const bool joint = NC == 2 && !apart;
-                    if (rank == 0 || !joint)
-                        mbar_arrive_expect_tx(&full[stage], joint ? NC * bytes : bytes);
-                    const uint32_t bar =
-                        rank == 0 || !joint ? smem_addr(&full[stage]) : of_first(&full[stage]);
+                    // a pair's copies are counted by its first CTA, but for a segment's end
+                    const bool end = GRAD && (x.k - k0) % 16 && x.k - k0 < kDepth;
+                    uint32_t bar = smem_addr(&full[stage]);
+                    if (end) {
+                        mbar_arrive_expect_tx(&last[stage], bytes);
+                        if (rank == 0) mbar_arrive(&full[stage]);
+                        bar = smem_addr(&last[stage]);
+                        ends ^= 1u << stage;
+                    } else if (rank == 0) {
+                        mbar_arrive_expect_tx(&full[stage], NC * bytes);
+                    } else {
+                        bar = of_first(&full[stage]);
+                    }
                     const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
                     if (GRAD) {
                         const int r = (int)((int64_t)x.r0 + k0);
@@ -448,105 +452,112 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             // another thread gave up: see the copies in flight land before the CTA ends
             // (those of a pair's second CTA are counted by the first: it waits for a while)
             if (!ok && rank == 1) mbar_wait(&drained, 0, p.err);
-            for (int64_t i = 0; !ok && rank == 0 && i < S::stages && i < issued; ++i) {
-                const int64_t last = issued - 1 - i;
-                mbar_wait(&full[last % S::stages], (uint32_t)(last / S::stages) & 1, p.err);
+            for (int64_t i = 0; !ok && i < S::stages; ++i) {
+                const int64_t at = issued - 1 - i;
+                if (rank == 0 && at >= 0)
+                    mbar_wait(&full[at % S::stages], (uint32_t)(at / S::stages) & 1, p.err);
+                if (GRAD) mbar_wait(&last[i], (ends >> i & 1) ^ 1, p.err);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------ products
-        int stage = 0, acc = 0;
-        uint32_t parity = 0, free_parity = 1;    // both accumulators start free
-        uint32_t mended = 0;                     // a bit per stage: how often, mod 2
-        bool ok = true;
-        while (ok && ring.take_warp(x, ok, p.err)) {
-            if (x.k == 0) continue;
-            const int mine = (x.n + S::STEP - 1) / S::STEP * 16;
-            if (rank == 0) {
-                ok = warp_wait(&taken[acc], free_parity, p.err);
-                if (!ok) break;
-                mma_fence_after();
-            }
-            const uint32_t d = tmem + acc * NT;
-            const uint32_t instr = instr_f16<T>(kRowsM * NC, mine * NC, A_MN, GRAD);
-            // whole stages, by one thread
-            const int whole = x.k / kDepth, rest = x.k % kDepth;
-            if (rank == 0) {
-                if (lane == 0) {
-                    for (int i = 0; i < whole; ++i) {
-                        ok = mbar_wait(&full[stage], parity, p.err);
-                        if (!ok) break;
-                        mma_fence_after();
-                        const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
-                        uint64_t da = A_MN ? desc_mn(a, 8192) : desc_k(a);
-                        uint64_t db = GRAD ? desc_mn(b, 8192) : desc_k(b);
-#pragma unroll
-                        for (int j = 0; j < kDepth / 16; ++j) {
-                            product_step<NC>(d, da, db, instr, i > 0 || j > 0);
-                            da += (A_MN ? 2048 : 32) >> 4;
-                            db += (GRAD ? 2048 : 32) >> 4;
-                        }
-                        commit_products<NC>(&empty[stage]);
-                        if (++stage == S::stages) {
-                            stage = 0;
-                            parity ^= 1;
-                        }
-                    }
+        if (lane == 0 && rank == 0) {
+            int stage = 0, acc = 0;
+            uint32_t parity = 0, free_parity = 1;    // both accumulators start free
+            uint32_t ends = 0;                       // a bit per stage: ends so far, mod 2
+            bool ok = true, more = ring.take(x, ok, p.err);
+            while (more) {
+                ExpertTile y;                    // the next tile, taken while this one's products run
+                if (x.k == 0) {
+                    more = ring.take(x, ok, p.err);
+                    continue;
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                stage = __shfl_sync(0xffffffffu, stage, 0);
-                parity = __shfl_sync(0xffffffffu, parity, 0);
+                ok = mbar_wait(&taken[acc], free_parity, p.err);
                 if (!ok) break;
-            } else {
-                stage = (stage + whole) % S::stages;
-            }
-            if (rest) {                          // (rank 1 has no use for its parity)
-                const int steps = (rest + 15) / 16;
-                const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
-                if (rank == 0) {
-                    ok = warp_wait(&full[stage], parity, p.err);
+                const int mine = (x.n + S::STEP - 1) / S::STEP * 16;
+                const uint32_t d = tmem + acc * NT;
+                const uint32_t instr = instr_f16<T>(kRowsM * NC, mine * NC, A_MN, GRAD);
+                const int whole = x.k / kDepth, rest = x.k % kDepth;
+                for (int i = 0; i < whole; ++i) {
+                    ok = mbar_wait(&full[stage], parity, p.err);
+                    if (!ok) break;
+                    mma_fence_after();
+                    const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+                    uint64_t da = A_MN ? desc_mn(a, 8192) : desc_k(a);
+                    uint64_t db = GRAD ? desc_mn(b, 8192) : desc_k(b);
+#pragma unroll
+                    for (int j = 0; j < kDepth / 16; ++j) {
+                        product_step<NC>(d, da, db, instr, i > 0 || j > 0);
+                        da += (A_MN ? 2048 : 32) >> 4;
+                        db += (GRAD ? 2048 : 32) >> 4;
+                    }
+                    commit_products<NC>(&empty[stage]);
+                    if (++stage == S::stages) {
+                        stage = 0;
+                        parity ^= 1;
+                    }
+                    if (i == 0) more = ring.take(y, ok, p.err);
                     if (!ok) break;
                 }
-                if (GRAD && rest % 16) {
-                    const uint32_t times = mended >> stage & 1;
-                    if (rank == 1) {
-                        ok = warp_wait(&full[stage], times, p.err);
-                        if (!ok) break;
+                if (!ok) break;
+                if (rest) {
+                    const int steps = (rest + 15) / 16;
+                    const uint32_t a = smem + stage * S::stage, b = a + S::a_bytes;
+                    ok = mbar_wait(&full[stage], parity, p.err);
+                    if (ok && GRAD && rest % 16) {
+                        ok = mbar_wait(&mended[stage], ends >> stage & 1, p.err);
+                        if (NC == 2) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        ends ^= 1u << stage;
                     }
-                    zero_rows(a, 2, rest, steps * 16);
-                    zero_rows(b, (mine + 63) / 64, rest, steps * 16);
-                    fence_proxy_async_shared();
-                    __syncwarp();
-                    if (NC == 2 && rank == 0) {
-                        ok = pair_wait(&other[stage], times, p.err);
-                        if (!ok) break;
-                    } else if (NC == 2 && lane == 0) {
-                        arrive_first(&other[stage]);
-                    }
-                    mended ^= 1u << stage;
-                }
-                if (rank == 0 && lane == 0) {
+                    if (!ok) break;
                     mma_fence_after();
                     for (int i = 0; i < steps; ++i)
                         product_step<NC>(d, A_MN ? desc_mn(a + i * 2048, 8192) : desc_k(a + i * 32),
                                          GRAD ? desc_mn(b + i * 2048, 8192) : desc_k(b + i * 32),
                                          instr, whole > 0 || i > 0);
                     commit_products<NC>(&empty[stage]);
+                    if (++stage == S::stages) {
+                        stage = 0;
+                        parity ^= 1;
+                    }
                 }
-                if (++stage == S::stages) {
-                    stage = 0;
-                    parity ^= 1;
+                commit_products<NC>(&ready[acc]);
+                acc ^= 1;
+                free_parity ^= acc == 0;
+                if (whole == 0) more = ring.take(y, ok, p.err);
+                x = y;
+            }
+            if (!ok) {
+                commit_products<NC>(&drained);
+                mbar_wait_poll(&drained, 0, p.err);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ------------------------------------------------------ ends of segments
+        // rows of k past the expert's last, up to a step of products, are set to 0
+        uint32_t count = 0, ends = 0;            // stages so far
+        bool ok = true;
+        while (GRAD && ok && ring.take_warp(x, ok, p.err)) {
+            count += x.k / kDepth;
+            const int rest = x.k % kDepth, stage = count % S::stages;
+            if (rest % 16) {
+                ok = warp_wait(&last[stage], ends >> stage & 1, p.err);
+                if (!ok) break;
+                ends ^= 1u << stage;
+                const int to = (rest + 15) & ~15, mine = (x.n + S::STEP - 1) / S::STEP * 16;
+                const uint32_t a = smem + stage * S::stage;
+                zero_rows(a, 2, rest, to);
+                zero_rows(a + S::a_bytes, (mine + 63) / 64, rest, to);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&mended[stage]);
+                    else arrive_first(&mended[stage]);
                 }
             }
-            if (!ok) break;
-            if (rank == 0 && lane == 0) commit_products<NC>(&ready[acc]);
-            acc ^= 1;
-            free_parity ^= acc == 0;
-        }
-        if (!ok && rank == 0 && lane == 0) {
-            commit_products<NC>(&drained);
-            mbar_wait_poll(&drained, 0, p.err);
+            count += rest > 0;
         }
         __syncwarp();
     } else {
