@@ -254,7 +254,7 @@ typedef struct {
     int32_t weight_dtype;        /* of the weights: SPMM_F32 or dtype                */
     int32_t interleaved;
     float eps, magnitude;
-    const uint64_t *turns;       /* device, [R / 2]                                  */
+    const uint64_t *turns;       /* device, [R / 2], 16-byte aligned                 */
     const int32_t *positions;    /* device, or NULL                                  */
     int64_t p_sb, p_st;
     const int32_t *lengths;      /* device, int32 [B], or NULL                       */

@@ -7,11 +7,12 @@
 // The angle of position p is p f turns, f < 1 in units of 2^-64: one 64-bit integer
 // product, whose wrap is the reduction mod a turn, so a far position costs no accuracy.
 //
-// A lane holds 16 elements of a row, eight pairs: two wide loads each 8 elements
+// A lane holds 16 elements of a row, eight pairs: two wide loads of 8 elements
 // (the lanes of a row read adjacent ones), no exchange for the rotation, and a
-// shuffle over the row's lanes for the norm's sum. A warp takes a token: the eight
-// sines and cosines of a lane are formed once for all of the token's heads of
-// queries and keys. One pass: every element is read once and written once.
+// shuffle over the row's lanes for the norm's sum. A warp takes a few heads of a token
+// (of several where a token has few), UN rows for each of its groups of lanes: it asks for
+// all of them first and works out the angles, the same for all, while they come. One
+// pass: every element is read once and written once.
 #include "blocks.cuh"
 
 namespace spmm {
@@ -26,56 +27,74 @@ struct HeadTensor {                  // one [B, T, heads, D] tensor and what bec
     const void *w;
     void *out;                       // results, or gradients of the inputs
     int64_t o_sb, o_st, o_sh;
-    int heads;
+    int heads, at_once, tokens;      // heads of a token, and tokens, that a warp's rows are of
+    unsigned chunks, items;          // warps' items per (group of tokens), in all
 };
 
 struct HeadArgs {
-    HeadTensor q, k, v;              // v: copied (append)
-    int64_t tokens;                  // B T
-    int T, D, R, lanes, splits;      // lanes of a row; warps per token
+    HeadTensor t[2];                 // queries, keys
+    const void *v;                   // append: the values, copied by the keys' warps
+    void *v_out;
+    int64_t v_sb, v_st, v_sh, vo_sb, vo_st, vo_sh;
+    unsigned q_ctas;                 // the first CTAs are the queries'
+    int all, T, D, R, lanes;         // B T; lanes of a row
     int w32;                         // weights are fp32
     float eps, magnitude;
     const uint64_t *turns;
     const int32_t *positions, *lengths;
     int64_t p_sb, p_st;
     int Tk;                          // rows of the caches that k and v go to, or -1
-    float *parts;                    // backward: [CTAs][2][D] parts of the weights' gradients
+    float *parts;                    // backward: [CTAs][D] parts of the weights' gradients
 };
 
-template <typename T> __device__ __forceinline__ void load8(const T *p, float *x) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = *(const float4 *)p, b = *(const float4 *)(p + 4);
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-        x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-        float y[8];
-        ld_pack<T, 8>(p, y);
+// 16 elements as they lie in memory: 8 from one place and 8 from another.
+template <typename T> struct Raw {
+    static constexpr int N = sizeof(T) / 2;        // 16-byte words of 8 elements
+    uint4 w[2 * N];
+    __device__ __forceinline__ void load(const T *lo, const T *hi) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i];
+        for (int i = 0; i < N; ++i) {
+            w[i] = __ldg((const uint4 *)lo + i);
+            w[N + i] = __ldg((const uint4 *)hi + i);
+        }
     }
-}
-
-template <typename T> __device__ __forceinline__ void store8(T *p, const float *x) {
-    if constexpr (sizeof(T) == 4) {
-        *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
-        *(float4 *)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-        float y[8];
+    __device__ __forceinline__ void store(T *lo, T *hi) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i];
-        st_pack<T, 8>(p, y);
+        for (int i = 0; i < N; ++i) {
+            ((uint4 *)lo)[i] = w[i];
+            ((uint4 *)hi)[i] = w[N + i];
+        }
     }
-}
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) w[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&x)[16]) const {
+        const T *e = reinterpret_cast<const T *>(w);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = to_f32(e[i]);
+    }
+    __device__ __forceinline__ void set(const float (&x)[16]) {
+        if constexpr (sizeof(T) == 4) {
+            float *e = reinterpret_cast<float *>(w);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) e[i] = x[i];
+        } else {
+            uint32_t *e = reinterpret_cast<uint32_t *>(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+        }
+    }
+};
 
 // A lane's place: row `row` of the warp's rows at a time, and in it the 8 elements
 // from `lo` and the 8 from `hi`. D and R are multiples of 16, so a lane's elements
 // are all turned (its eight pairs) or none is.
 struct HeadLane {
-    int row, rows, lo, hi;
+    int row, lo, hi;
     bool live, turned;
     __device__ __forceinline__ HeadLane(const HeadArgs &a, bool interleaved) {
         const int lane = threadIdx.x & 31, u = lane & (a.lanes - 1);
-        rows = 32 / a.lanes;
         row = lane / a.lanes;
         live = u * 16 < a.D;
         turned = u * 16 < a.R;
@@ -84,9 +103,31 @@ struct HeadLane {
     }
 };
 
-// Sines and cosines of the lane's pairs. The turn is cut to the nearest quarter
-// (exactly, in integers) before it becomes a float: the rest, at most an eighth of a
-// turn, is off by 2^-27 of pi at most.
+// Which token and first head the lane's rows are of; its u-th is at_once heads further.
+struct HeadPlace {
+    int64_t b;
+    int t, head;
+    bool live;
+    __device__ __forceinline__ HeadPlace(const HeadArgs &a, const HeadTensor &h, const HeadLane &l,
+                                         unsigned item, int un) {
+        const unsigned group = item / h.chunks, chunk = item % h.chunks;
+        const int64_t token = (int64_t)group * h.tokens + l.row / h.at_once;
+        live = l.live && l.row < h.tokens * h.at_once && token < a.all;
+        b = live ? (unsigned)token / (unsigned)a.T : 0;
+        t = live ? (int)((unsigned)token % (unsigned)a.T) : 0;
+        head = (int)chunk * un * h.at_once + l.row % h.at_once;
+    }
+    __device__ __forceinline__ int64_t position(const HeadArgs &a) const {
+        if (!live) return 0;
+        if (a.positions) return a.positions[b * a.p_sb + t * a.p_st];
+        return (a.lengths ? (int64_t)a.lengths[b] - a.T : 0) + t;
+    }
+};
+
+// Sines and cosines of the lane's pairs, times the magnitude. The turn is cut to the
+// nearest quarter (exactly, in integers) before it becomes a float. What is left, x
+// of at most pi / 4, is off by 2^-26 and goes into the two functions' power series, whose
+// first terms left out, x^11 / 11! and x^10 / 10!, are below 2^-25.
 __device__ __forceinline__ void angles(const HeadArgs &a, const HeadLane &l, bool interleaved,
                                        int64_t pos, float (&c)[8], float (&s)[8]) {
 #pragma unroll
@@ -95,14 +136,23 @@ __device__ __forceinline__ void angles(const HeadArgs &a, const HeadLane &l, boo
         s[i] = 0.0f;
     }
     if (!l.turned) return;
-    const uint64_t *f = a.turns + (interleaved ? l.lo / 2 : l.lo);
+    const ulonglong2 *f = (const ulonglong2 *)(a.turns + (interleaved ? l.lo / 2 : l.lo));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t t = (uint32_t)(((uint64_t)pos * __ldg(f + i)) >> 32);
+        const ulonglong2 two = __ldg(f + i / 2);
+        const uint32_t t = (uint32_t)(((uint64_t)pos * (i & 1 ? two.y : two.x)) >> 32);
         const uint32_t quarter = (t + (1u << 29)) >> 30;
-        float x, y;
-        sincospif((float)(int32_t)(t - (quarter << 30)) * 0x1p-31f, &y, &x);
-        const float cc = quarter & 1 ? y : x, ss = quarter & 1 ? x : y;
+        const float x = (float)(int32_t)(t - (quarter << 30)) * 1.46291807926716e-9f;   // 2 pi / 2^32
+        const float y = x * x;
+        float sx = fmaf(y, 1.0f / 362880, -1.0f / 5040);
+        sx = fmaf(y, sx, 1.0f / 120);
+        sx = fmaf(y, sx, -1.0f / 6);
+        sx = fmaf(x * y, sx, x);
+        float cx = fmaf(y, 1.0f / 40320, -1.0f / 720);
+        cx = fmaf(y, cx, 1.0f / 24);
+        cx = fmaf(y, cx, -0.5f);
+        cx = fmaf(y, cx, 1.0f);
+        const float cc = quarter & 1 ? sx : cx, ss = quarter & 1 ? cx : sx;
         c[i] = ((quarter + 1) & 2 ? -cc : cc) * a.magnitude;
         s[i] = (quarter & 2 ? -ss : ss) * a.magnitude;
     }
@@ -131,35 +181,49 @@ __device__ __forceinline__ void load_weight(const HeadArgs &a, const HeadLane &l
                                             float (&x)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-    if (!l.live || !w) return;
+    if (!l.live) return;
     if (a.w32) {
-        load8((const float *)w + l.lo, x);
-        load8((const float *)w + l.hi, x + 8);
+        Raw<float> r;
+        r.load((const float *)w + l.lo, (const float *)w + l.hi);
+        r.get(x);
     } else {
-        load8((const T *)w + l.lo, x);
-        load8((const T *)w + l.hi, x + 8);
+        Raw<T> r;
+        r.load((const T *)w + l.lo, (const T *)w + l.hi);
+        r.get(x);
     }
 }
 
-// Heads of one token: rows split * rows + row, then splits * rows further.
-template <typename T, bool INTER, bool NORM>
-__device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadTensor &h,
-                                              const HeadLane &l, int split, const T *x, T *out,
-                                              const float (&c)[8], const float (&s)[8]) {
-    float w[16];
-    if (NORM) load_weight<T>(a, l, h.w, w);
-    const int step = a.splits * l.rows;
-    for (int base = split * l.rows; base < h.heads; base += step) {
-        const int at = base + l.row;
-        const bool live = l.live && at < h.heads;
-        float z[16];
+template <typename T, bool INTER, int UN>
+__global__ void __launch_bounds__(kThreads, 2) k_heads_rotate(const __grid_constant__ HeadArgs a) {
+    const HeadLane l(a, INTER);
+    const bool keys = blockIdx.x >= a.q_ctas;
+    const HeadTensor &h = a.t[keys];
+    const unsigned item = (blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + threadIdx.x / 32;
+    if (item >= h.items) return;
+    const HeadPlace at(a, h, l, item, UN);
+    Raw<T> x[UN];
+    bool live[UN];
+    const T *from = (const T *)h.x + at.b * h.sb + at.t * h.st + at.head * h.sh;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-        if (live) {
-            load8(x + at * h.sh + l.lo, z);
-            load8(x + at * h.sh + l.hi, z + 8);
-        }
-        if (NORM) {
+    for (int u = 0; u < UN; ++u) {
+        live[u] = at.live && at.head + u * h.at_once < h.heads;
+        const T *p = from + u * h.at_once * h.sh;
+        if (live[u]) x[u].load(p + l.lo, p + l.hi);
+        else x[u].zero();
+    }
+    const int64_t pos = at.position(a);
+    const bool cached = keys && a.Tk >= 0, put = !cached || (pos >= 0 && pos < a.Tk);
+    const int64_t row = cached ? pos : at.t;
+    float c[8], s[8], w[16];
+    if (h.w) load_weight<T>(a, l, h.w, w);
+    angles(a, l, INTER, pos, c, s);
+    T *to = (T *)h.out + at.b * h.o_sb + row * h.o_st + at.head * h.o_sh;
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+        if (u * h.at_once >= h.heads) break;     // no lane has one more
+        float z[16];
+        x[u].get(z);
+        if (h.w) {
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum = fmaf(z[i], z[i], sum);
@@ -168,168 +232,131 @@ __device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadTenso
             for (int i = 0; i < 16; ++i) z[i] = z[i] * r * w[i];
         }
         if (l.turned) turn<INTER>(z, c, s, false);
-        if (live) {
-            store8(out + at * h.o_sh + l.lo, z);
-            store8(out + at * h.o_sh + l.hi, z + 8);
-        }
+        x[u].set(z);
+        T *p = to + u * h.at_once * h.o_sh;
+        if (live[u] && put) x[u].store(p + l.lo, p + l.hi);
     }
-}
-
-__device__ __forceinline__ int64_t position(const HeadArgs &a, int64_t b, int t) {
-    if (a.positions) return a.positions[b * a.p_sb + t * a.p_st];
-    return (a.lengths ? (int64_t)a.lengths[b] - a.T : 0) + t;
-}
-
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads) k_heads_rotate(const HeadArgs a) {
-    const HeadLane l(a, INTER);
-    const int64_t items = a.tokens * a.splits;
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; i < items;
-         i += (int64_t)gridDim.x * kWarps) {
-        const int64_t token = i / a.splits, b = token / a.T;
-        const int split = (int)(i % a.splits), t = (int)(token % a.T);
-        const int64_t pos = position(a, b, t);
-        float c[8], s[8];
-        angles(a, l, INTER, pos, c, s);
-        auto heads = [&](const HeadTensor &h, int64_t row) {
-            const T *x = (const T *)h.x + b * h.sb + t * h.st;
-            T *out = (T *)h.out + b * h.o_sb + row * h.o_st;
-            if (h.w) forward_heads<T, INTER, true>(a, h, l, split, x, out, c, s);
-            else forward_heads<T, INTER, false>(a, h, l, split, x, out, c, s);
-        };
-        heads(a.q, t);
-        if (a.Tk < 0) {
-            heads(a.k, t);
-        } else if (pos >= 0 && pos < a.Tk) {
-            heads(a.k, pos);
-            const T *x = (const T *)a.v.x + b * a.v.sb + t * a.v.st;
-            T *out = (T *)a.v.out + b * a.v.o_sb + pos * a.v.o_st;
-            constexpr int V = 16 / sizeof(T);
-            const int n = a.D / V;
-            for (int j = split * 32 + (threadIdx.x & 31); j < a.v.heads * n; j += a.splits * 32)
-                *(uint4 *)(out + j / n * a.v.o_sh + j % n * V) =
-                    *(const uint4 *)(x + j / n * a.v.sh + j % n * V);
-        }
+    if (!cached || !put) return;
+    const T *v = (const T *)a.v + at.b * a.v_sb + at.t * a.v_st + at.head * a.v_sh;
+    T *v_to = (T *)a.v_out + at.b * a.vo_sb + pos * a.vo_st + at.head * a.vo_sh;
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+        const T *p = v + u * h.at_once * a.v_sh;
+        if (live[u]) x[u].load(p + l.lo, p + l.hi);
     }
-}
-
-template <typename T, bool INTER, bool NORM>
-__device__ __forceinline__ void backward_heads(const HeadArgs &a, const HeadTensor &h,
-                                               const HeadLane &l, int split, const T *g, const T *x,
-                                               T *out, const float (&c)[8], const float (&s)[8],
-                                               float (&dw)[16]) {
-    float w[16];
-    if (NORM) load_weight<T>(a, l, h.w, w);
-    const int step = a.splits * l.rows;
-    for (int base = split * l.rows; base < h.heads; base += step) {
-        const int at = base + l.row;
-        const bool live = l.live && at < h.heads;
-        float u[16], z[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = z[i] = 0.0f;
-        if (live) {
-            load8(g + at * h.g_sh + l.lo, u);
-            load8(g + at * h.g_sh + l.hi, u + 8);
-            if (NORM) {
-                load8(x + at * h.sh + l.lo, z);
-                load8(x + at * h.sh + l.hi, z + 8);
-            }
-        }
-        if (l.turned) turn<INTER>(u, c, s, true);
-        if (NORM) {
-            float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                sum = fmaf(z[i], z[i], sum);
-                dot = fmaf(u[i] * w[i], z[i], dot);
-            }
-            const float r = rsqrtf(row_sum(sum, a.lanes) / (float)a.D + a.eps);
-            const float m = row_sum(dot, a.lanes) * r / (float)a.D;    // mean(u n)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float n = z[i] * r;
-                dw[i] = fmaf(u[i], n, dw[i]);
-                u[i] = r * (u[i] * w[i] - n * m);
-            }
-        }
-        if (live) {
-            store8(out + at * h.o_sh + l.lo, u);
-            store8(out + at * h.o_sh + l.hi, u + 8);
-        }
+    for (int u = 0; u < UN; ++u) {
+        T *p = v_to + u * h.at_once * a.vo_sh;
+        if (live[u]) x[u].store(p + l.lo, p + l.hi);
     }
 }
 
 // The weights' gradients: a lane's sums over its rows, then over the rows of the
 // warp, the warps of the CTA and, by a second kernel, the CTAs, each in a fixed order.
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads) k_heads_backward(const HeadArgs a) {
+template <typename T, bool INTER, int UN>
+__global__ void __launch_bounds__(kThreads, 2) k_heads_backward(const __grid_constant__ HeadArgs a) {
     __shared__ float sums[kWarps][256];
     const HeadLane l(a, INTER);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    float dwq[16], dwk[16];
+    const bool keys = blockIdx.x >= a.q_ctas;
+    const HeadTensor &h = a.t[keys];
+    const unsigned ctas = keys ? gridDim.x - a.q_ctas : a.q_ctas;
+    float w[16], dw[16];
+    if (h.w) load_weight<T>(a, l, h.w, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dwq[i] = dwk[i] = 0.0f;
-    const int64_t items = a.tokens * a.splits;
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + warp; i < items;
-         i += (int64_t)gridDim.x * kWarps) {
-        const int64_t token = i / a.splits, b = token / a.T;
-        const int split = (int)(i % a.splits), t = (int)(token % a.T);
+    for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+    for (uint64_t item = (uint64_t)(blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + warp;
+         item < h.items; item += (uint64_t)ctas * kWarps) {
+        const HeadPlace at(a, h, l, (unsigned)item, UN);
+        Raw<T> g[UN], x[UN];
+        bool live[UN];
+        const T *gs = (const T *)h.g + at.b * h.g_sb + at.t * h.g_st + at.head * h.g_sh;
+        const T *xs = (const T *)h.x + at.b * h.sb + at.t * h.st + at.head * h.sh;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            live[u] = at.live && at.head + u * h.at_once < h.heads;
+            g[u].zero();
+            x[u].zero();
+            if (!live[u]) continue;
+            const T *p = gs + u * h.at_once * h.g_sh;
+            g[u].load(p + l.lo, p + l.hi);
+            p = xs + u * h.at_once * h.sh;
+            if (h.w) x[u].load(p + l.lo, p + l.hi);
+        }
         float c[8], s[8];
-        angles(a, l, INTER, position(a, b, t), c, s);
-        auto heads = [&](const HeadTensor &h, float (&dw)[16]) {
-            const T *g = (const T *)h.g + b * h.g_sb + t * h.g_st;
-            const T *x = (const T *)h.x + b * h.sb + t * h.st;
-            T *out = (T *)h.out + b * h.o_sb + t * h.o_st;
-            if (h.w) backward_heads<T, INTER, true>(a, h, l, split, g, x, out, c, s, dw);
-            else backward_heads<T, INTER, false>(a, h, l, split, g, x, out, c, s, dw);
-        };
-        heads(a.q, dwq);
-        heads(a.k, dwk);
+        angles(a, l, INTER, at.position(a), c, s);
+        T *to = (T *)h.out + at.b * h.o_sb + at.t * h.o_st + at.head * h.o_sh;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            if (u * h.at_once >= h.heads) break;
+            float y[16];
+            g[u].get(y);
+            if (l.turned) turn<INTER>(y, c, s, true);
+            if (h.w) {
+                float z[16], sum = 0.0f, dot = 0.0f;
+                x[u].get(z);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sum = fmaf(z[i], z[i], sum);
+                    dot = fmaf(y[i] * w[i], z[i], dot);
+                }
+                for (int o = 1; o < a.lanes; o <<= 1) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                }
+                const float r = rsqrtf(sum / (float)a.D + a.eps);
+                const float m = dot * r / (float)a.D;      // mean(u n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float n = z[i] * r;
+                    dw[i] = fmaf(y[i], n, dw[i]);
+                    y[i] = r * (y[i] * w[i] - n * m);
+                }
+            }
+            g[u].set(y);
+            T *p = to + u * h.at_once * h.o_sh;
+            if (live[u]) g[u].store(p + l.lo, p + l.hi);
+        }
     }
-    if (!a.parts) return;
-    auto total = [&](float (&dw)[16], float *out) {
+    if (!h.w) return;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            for (int o = a.lanes; o < 32; o <<= 1)
-                dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-        __syncthreads();
-        if (lane < a.lanes && l.live) {
+    for (int i = 0; i < 16; ++i)
+        for (int o = a.lanes; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+    if (lane < a.lanes && l.live) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sums[warp][i < 8 ? l.lo + i : l.hi + i - 8] = dw[i];
-        }
-        __syncthreads();
-        if ((int)threadIdx.x < a.D) {
-            float x = 0.0f;
-            for (int w = 0; w < kWarps; ++w) x += sums[w][threadIdx.x];
-            out[threadIdx.x] = x;
-        }
-    };
-    float *out = a.parts + (int64_t)blockIdx.x * 2 * a.D;
-    total(dwq, out);
-    total(dwk, out + a.D);
+        for (int i = 0; i < 16; ++i) sums[warp][i < 8 ? l.lo + i : l.hi + i - 8] = dw[i];
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.D) {
+        float x = 0.0f;
+        for (int i = 0; i < kWarps; ++i) x += sums[i][threadIdx.x];
+        a.parts[(int64_t)blockIdx.x * a.D + threadIdx.x] = x;
+    }
 }
 
-// dw[j] = the sum of n parts `pitch` apart: 32 columns a CTA, its warps in turn over the parts.
-__global__ void __launch_bounds__(1024) k_heads_weights(const float *parts, int n, int D, int w32,
-                                                        int half, void *dwq, void *dwk) {
+// A weight's gradient is the sum of its tensor's CTAs' parts: 32 columns a CTA, its warps
+// in turn over the parts; CTAs y = 0 for the queries', 1 for the keys'.
+__global__ void __launch_bounds__(1024) k_heads_weights(const float *parts, int q_ctas, int ctas,
+                                                        int D, int w32, int half, void *dwq,
+                                                        void *dwk) {
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + lane;
+    void *out = blockIdx.y ? dwk : dwq;
+    if (!out) return;
+    const int end = blockIdx.y ? ctas : q_ctas;
     float x = 0.0f;
-    if (j < 2 * D)
-        for (int i = warp; i < n; i += 32) x += parts[(int64_t)i * 2 * D + j];
+    if (j < D)
+        for (int i = (blockIdx.y ? q_ctas : 0) + warp; i < end; i += 32) x += parts[(int64_t)i * D + j];
     sums[warp][lane] = x;
     __syncthreads();
-    if (warp || j >= 2 * D) return;
+    if (warp || j >= D) return;
     x = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) x += sums[i][lane];
-    void *out = j < D ? dwq : dwk;
-    const int at = j < D ? j : j - D;
-    if (!out) return;
-    if (w32) ((float *)out)[at] = x;
-    else if (half) ((__half *)out)[at] = from_f32<__half>(x);
-    else ((__nv_bfloat16 *)out)[at] = from_f32<__nv_bfloat16>(x);
+    if (w32) ((float *)out)[j] = x;
+    else if (half) ((__half *)out)[j] = from_f32<__half>(x);
+    else ((__nv_bfloat16 *)out)[j] = from_f32<__nv_bfloat16>(x);
 }
 
 // ------------------------------------------------------------------- host
@@ -345,18 +372,11 @@ spmm_status heads_check(const spmm_heads_shape *s) {
         return SPMM_ERR_UNSUPPORTED;
     if (s->B && (s->Hq + s->Hk) * std::max<int64_t>(s->T, 1) > (int64_t)INT32_MAX / s->B)
         return SPMM_ERR_UNSUPPORTED;
-    if (s->R && !s->turns) return SPMM_ERR_INVALID_ARG;
+    if (s->R && (!s->turns || (uintptr_t)s->turns % 16)) return SPMM_ERR_INVALID_ARG;
     return SPMM_OK;
 }
 
 bool heads_empty(const spmm_heads_shape *s) { return !s->B || !s->T || !(s->Hq + s->Hk); }
-
-HeadTensor tensor(int64_t heads, const void *w) {
-    HeadTensor h{};
-    h.heads = (int)heads;
-    h.w = w;
-    return h;
-}
 
 void contiguous_out(HeadTensor &h, void *out, const spmm_heads_shape *s) {
     h.out = out;
@@ -365,12 +385,12 @@ void contiguous_out(HeadTensor &h, void *out, const spmm_heads_shape *s) {
     h.o_sb = s->T * h.o_st;
 }
 
-HeadArgs heads_args(const spmm_heads_shape *s) {
+// Rows of 16-byte words that a lane asks for at a time: 128 bytes of them.
+constexpr int kForwardRows = 8, kBackwardRows = 4;   // over the element's bytes
+
+HeadArgs heads_args(const spmm_heads_shape *s, int rows) {
     HeadArgs a{};
-    a.q = tensor(s->Hq, s->wq);
-    a.k = tensor(s->Hk, s->wk);
-    a.v = tensor(0, nullptr);
-    a.tokens = s->B * s->T;
+    a.all = (int)(s->B * s->T);
     a.T = (int)s->T;
     a.D = (int)s->D;
     a.R = (int)s->R;
@@ -385,19 +405,33 @@ HeadArgs heads_args(const spmm_heads_shape *s) {
     a.p_st = s->p_st;
     a.lengths = s->lengths;
     a.Tk = -1;
-    // few tokens: a warp takes a part of a token's heads only
-    const int64_t rows = 32 / a.lanes, most = (std::max(s->Hq, s->Hk) + rows - 1) / rows;
-    const int64_t want = (kSms * 16 + a.tokens - 1) / std::max<int64_t>(a.tokens, 1);
-    a.splits = (int)std::max<int64_t>(1, std::min(most, want));
+    const int groups = 32 / a.lanes, un = rows / dtype_bytes(s->dtype);
+    for (int i = 0; i < 2; ++i) {
+        HeadTensor &h = a.t[i];
+        h.heads = (int)(i ? s->Hk : s->Hq);
+        h.w = i ? s->wk : s->wq;
+        h.at_once = std::max(1, std::min(h.heads, groups));
+        h.tokens = groups / h.at_once;
+        h.chunks = (unsigned)((h.heads + un * h.at_once - 1) / (un * h.at_once));
+        h.items = (unsigned)(((int64_t)a.all + h.tokens - 1) / h.tokens) * h.chunks;
+    }
     return a;
 }
 
-unsigned heads_grid(const HeadArgs &a, int per_sm) {
-    const int64_t ctas = (a.tokens * a.splits + kWarps - 1) / kWarps;
-    return (unsigned)std::min<int64_t>(ctas, kSms * per_sm);
-}
+unsigned warps_ctas(unsigned items) { return items / kWarps + (items % kWarps > 0); }
 
-constexpr int kForwardCtas = 8, kBackwardCtas = 4;     // per SM
+// Two CTAs to an SM stay (their sums do), in proportion to the tensors' elements.
+void backward_grid(HeadArgs &a, unsigned &grid) {
+    const double q = (double)a.t[0].heads, k = (double)a.t[1].heads;
+    const unsigned most = 2 * kSms;
+    unsigned n[2] = {(unsigned)(most * q / (q + k) + 0.5), 0};
+    if (k > 0) n[0] = std::min(n[0], most - 1);
+    if (q > 0) n[0] = std::max(n[0], 1u);
+    n[1] = most - n[0];
+    for (int i = 0; i < 2; ++i) n[i] = std::min(n[i], warps_ctas(a.t[i].items));
+    a.q_ctas = n[0];
+    grid = n[0] + n[1];
+}
 
 template <template <typename, bool> class K>
 cudaError_t launch_heads(const spmm_heads_shape *s, const HeadArgs &a, unsigned grid,
@@ -414,14 +448,19 @@ cudaError_t launch_heads(const spmm_heads_shape *s, const HeadArgs &a, unsigned 
 }
 template <typename T, bool INTER> struct Rotate {
     static void go(const HeadArgs &a, unsigned grid, cudaStream_t cs) {
-        k_heads_rotate<T, INTER><<<grid, kThreads, 0, cs>>>(a);
+        k_heads_rotate<T, INTER, kForwardRows / (int)sizeof(T)><<<grid, kThreads, 0, cs>>>(a);
     }
 };
 template <typename T, bool INTER> struct Backward {
     static void go(const HeadArgs &a, unsigned grid, cudaStream_t cs) {
-        k_heads_backward<T, INTER><<<grid, kThreads, 0, cs>>>(a);
+        k_heads_backward<T, INTER, kBackwardRows / (int)sizeof(T)><<<grid, kThreads, 0, cs>>>(a);
     }
 };
+
+cudaError_t rotate(const spmm_heads_shape *s, HeadArgs &a, void *stream) {
+    a.q_ctas = warps_ctas(a.t[0].items);
+    return launch_heads<Rotate>(s, a, a.q_ctas + warps_ctas(a.t[1].items), (cudaStream_t)stream);
+}
 
 bool written_ok(const spmm_rows &r, int64_t e, const spmm_heads_shape *s, int64_t Tk) {
     // rows that two tokens share (stride 0) would be written twice
@@ -443,12 +482,12 @@ spmm_status spmm_heads_rotate(const spmm_heads_shape *s, spmm_rows q, spmm_rows 
     const int e = dtype_bytes(s->dtype);
     if (s->Hq && (!rows_ok(q, e) || !q_out || (uintptr_t)q_out % 16)) return SPMM_ERR_INVALID_ARG;
     if (s->Hk && (!rows_ok(k, e) || !k_out || (uintptr_t)k_out % 16)) return SPMM_ERR_INVALID_ARG;
-    HeadArgs a = heads_args(s);
-    set_rows(a.q.x, a.q.sb, a.q.st, a.q.sh, q);
-    set_rows(a.k.x, a.k.sb, a.k.st, a.k.sh, k);
-    contiguous_out(a.q, q_out, s);
-    contiguous_out(a.k, k_out, s);
-    return cuda_status(launch_heads<Rotate>(s, a, heads_grid(a, kForwardCtas), (cudaStream_t)stream));
+    HeadArgs a = heads_args(s, kForwardRows);
+    set_rows(a.t[0].x, a.t[0].sb, a.t[0].st, a.t[0].sh, q);
+    set_rows(a.t[1].x, a.t[1].sb, a.t[1].st, a.t[1].sh, k);
+    contiguous_out(a.t[0], q_out, s);
+    contiguous_out(a.t[1], k_out, s);
+    return cuda_status(rotate(s, a, stream));
 }
 
 spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
@@ -465,24 +504,26 @@ spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows 
     if (!rows_ok(k, e) || !rows_ok(v, e)) return SPMM_ERR_INVALID_ARG;
     if (Tk && (!written_ok(cache_k, e, s, Tk) || !written_ok(cache_v, e, s, Tk)))
         return SPMM_ERR_INVALID_ARG;
-    HeadArgs a = heads_args(s);
-    set_rows(a.q.x, a.q.sb, a.q.st, a.q.sh, q);
-    set_rows(a.k.x, a.k.sb, a.k.st, a.k.sh, k);
-    contiguous_out(a.q, q_out, s);
-    a.v = tensor(s->Hk, nullptr);
-    set_rows(a.v.x, a.v.sb, a.v.st, a.v.sh, v);
+    HeadArgs a = heads_args(s, kForwardRows);
+    set_rows(a.t[0].x, a.t[0].sb, a.t[0].st, a.t[0].sh, q);
+    set_rows(a.t[1].x, a.t[1].sb, a.t[1].st, a.t[1].sh, k);
+    contiguous_out(a.t[0], q_out, s);
+    set_rows(a.v, a.v_sb, a.v_st, a.v_sh, v);
     a.Tk = (int)Tk;
-    a.k.out = const_cast<void *>(cache_k.data);
-    a.k.o_sb = cache_k.sb, a.k.o_st = cache_k.st, a.k.o_sh = cache_k.sh;
-    a.v.out = const_cast<void *>(cache_v.data);
-    a.v.o_sb = cache_v.sb, a.v.o_st = cache_v.st, a.v.o_sh = cache_v.sh;
-    return cuda_status(launch_heads<Rotate>(s, a, heads_grid(a, kForwardCtas), (cudaStream_t)stream));
+    a.t[1].out = const_cast<void *>(cache_k.data);
+    a.t[1].o_sb = cache_k.sb, a.t[1].o_st = cache_k.st, a.t[1].o_sh = cache_k.sh;
+    a.v_out = const_cast<void *>(cache_v.data);
+    a.vo_sb = cache_v.sb, a.vo_st = cache_v.st, a.vo_sh = cache_v.sh;
+    return cuda_status(rotate(s, a, stream));
 }
 
 int64_t spmm_heads_backward_workspace(const spmm_heads_shape *s) {
     using namespace spmm;
     if (heads_check(s) != SPMM_OK || heads_empty(s) || (!s->wq && !s->wk)) return 0;
-    return heads_grid(heads_args(s), kBackwardCtas) * 2 * s->D * (int64_t)sizeof(float);
+    HeadArgs a = heads_args(s, kBackwardRows);
+    unsigned grid;
+    backward_grid(a, grid);
+    return grid * s->D * (int64_t)sizeof(float);
 }
 
 spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad_q,
@@ -508,19 +549,20 @@ spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad
         return SPMM_ERR_INVALID_ARG;
     const int64_t need = spmm_heads_backward_workspace(s);
     if (need && (!work || work_bytes < need || (uintptr_t)work % 16)) return SPMM_ERR_INVALID_ARG;
-    HeadArgs a = heads_args(s);
-    set_rows(a.q.x, a.q.sb, a.q.st, a.q.sh, q);
-    set_rows(a.k.x, a.k.sb, a.k.st, a.k.sh, k);
-    set_rows(a.q.g, a.q.g_sb, a.q.g_st, a.q.g_sh, grad_q);
-    set_rows(a.k.g, a.k.g_sb, a.k.g_st, a.k.g_sh, grad_k);
-    contiguous_out(a.q, dq, s);
-    contiguous_out(a.k, dk, s);
+    HeadArgs a = heads_args(s, kBackwardRows);
+    set_rows(a.t[0].x, a.t[0].sb, a.t[0].st, a.t[0].sh, q);
+    set_rows(a.t[1].x, a.t[1].sb, a.t[1].st, a.t[1].sh, k);
+    set_rows(a.t[0].g, a.t[0].g_sb, a.t[0].g_st, a.t[0].g_sh, grad_q);
+    set_rows(a.t[1].g, a.t[1].g_sb, a.t[1].g_st, a.t[1].g_sh, grad_k);
+    contiguous_out(a.t[0], dq, s);
+    contiguous_out(a.t[1], dk, s);
     a.parts = need ? (float *)work : nullptr;
-    const unsigned grid = heads_grid(a, kBackwardCtas);
+    unsigned grid;
+    backward_grid(a, grid);
     cudaError_t err = launch_heads<Backward>(s, a, grid, cs);
     if (err == cudaSuccess && need) {
-        k_heads_weights<<<(unsigned)((2 * s->D + 31) / 32), 1024, 0, cs>>>(
-            a.parts, (int)grid, a.D, a.w32, s->dtype == SPMM_F16, s->wq ? dwq : nullptr,
+        k_heads_weights<<<dim3((unsigned)((s->D + 31) / 32), 2), 1024, 0, cs>>>(
+            a.parts, (int)a.q_ctas, (int)grid, a.D, a.w32, s->dtype == SPMM_F16, s->wq ? dwq : nullptr,
             s->wk ? dwk : nullptr);
         count_launch();
         err = cudaGetLastError();
