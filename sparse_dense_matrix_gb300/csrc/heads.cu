@@ -39,7 +39,7 @@ struct HeadArgs {
     unsigned q_ctas;                 // the first CTAs are the queries'
     int all, T, D, R, lanes;         // B T; lanes of a row
     int w32;                         // weights are fp32
-    float eps, magnitude;
+    float eps, magnitude, inv_D;
     const uint64_t *turns;
     const int32_t *positions, *lengths;
     int64_t p_sb, p_st;
@@ -47,7 +47,36 @@ struct HeadArgs {
     float *parts;                    // backward: [CTAs][D] parts of the weights' gradients
 };
 
-// 16 elements as they lie in memory: 8 from one place and 8 from another.
+// Two floats to an instruction: the arithmetic of a row would else take longer to issue
+// than the row takes to come.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 two(float lo, float hi) {
+    F2 x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
+    return x;
+}
+__device__ __forceinline__ float2 both(F2 x) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(x));
+    return y;
+}
+__device__ __forceinline__ F2 swap(F2 x) {
+    const float2 y = both(x);
+    return two(y.y, y.x);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 x;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(a), "l"(b), "l"(c));
+    return x;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 x;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(a), "l"(b));
+    return x;
+}
+
+// 16 elements as they lie in memory: 8 from one place and 8 from another. As floats,
+// number i holds elements 2 i and 2 i + 1.
 template <typename T> struct Raw {
     static constexpr int N = sizeof(T) / 2;        // 16-byte words of 8 elements
     uint4 w[2 * N];
@@ -69,20 +98,19 @@ template <typename T> struct Raw {
 #pragma unroll
         for (int i = 0; i < 2 * N; ++i) w[i] = make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void get(float (&x)[16]) const {
+    __device__ __forceinline__ void get(F2 (&x)[8]) const {
         const T *e = reinterpret_cast<const T *>(w);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f32(e[i]);
+        for (int i = 0; i < 8; ++i) x[i] = two(to_f32(e[2 * i]), to_f32(e[2 * i + 1]));
     }
-    __device__ __forceinline__ void set(const float (&x)[16]) {
-        if constexpr (sizeof(T) == 4) {
-            float *e = reinterpret_cast<float *>(w);
+    __device__ __forceinline__ void set(const F2 (&x)[8]) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = x[i];
-        } else {
-            uint32_t *e = reinterpret_cast<uint32_t *>(w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = pack2<T>(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 8; ++i) {
+            const float2 y = both(x[i]);
+            if constexpr (sizeof(T) == 4)
+                reinterpret_cast<float2 *>(w)[i] = y;
+            else
+                reinterpret_cast<uint32_t *>(w)[i] = pack2<T>(y.x, y.y);
         }
     }
 };
@@ -124,50 +152,79 @@ struct HeadPlace {
     }
 };
 
-// Sines and cosines of the lane's pairs, times the magnitude. The turn is cut to the
-// nearest quarter (exactly, in integers) before it becomes a float. What is left, x
-// of at most pi / 4, is off by 2^-26 and goes into the two functions' power series, whose
-// first terms left out, x^11 / 11! and x^10 / 10!, are below 2^-25.
+// Sines and cosines of the lane's pairs, times the magnitude (of pairs 2 i and 2 i + 1 in
+// number i). The turn is cut to the nearest half (exactly, in integers) before it
+// becomes a float. What is left, x of at most pi / 2, is off by 2^-24 of itself and goes
+// into the two functions' power series, whose first terms left out, x^13 / 13! and
+// x^14 / 14!, are below 2^-24.
 __device__ __forceinline__ void angles(const HeadArgs &a, const HeadLane &l, bool interleaved,
-                                       int64_t pos, float (&c)[8], float (&s)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = 1.0f;
-        s[i] = 0.0f;
-    }
-    if (!l.turned) return;
+                                       int64_t pos, F2 (&c)[4], F2 (&s)[4]) {
     const ulonglong2 *f = (const ulonglong2 *)(a.turns + (interleaved ? l.lo / 2 : l.lo));
+    auto all = [](float x) { return two(x, x); };
+    const F2 unit = all(1.46291807926716e-9f), size = all(a.magnitude);      // 2 pi / 2^32
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const ulonglong2 two = __ldg(f + i / 2);
-        const uint32_t t = (uint32_t)(((uint64_t)pos * (i & 1 ? two.y : two.x)) >> 32);
-        const uint32_t quarter = (t + (1u << 29)) >> 30;
-        const float x = (float)(int32_t)(t - (quarter << 30)) * 1.46291807926716e-9f;   // 2 pi / 2^32
-        const float y = x * x;
-        float sx = fmaf(y, 1.0f / 362880, -1.0f / 5040);
-        sx = fmaf(y, sx, 1.0f / 120);
-        sx = fmaf(y, sx, -1.0f / 6);
-        sx = fmaf(x * y, sx, x);
-        float cx = fmaf(y, 1.0f / 40320, -1.0f / 720);
-        cx = fmaf(y, cx, 1.0f / 24);
-        cx = fmaf(y, cx, -0.5f);
-        cx = fmaf(y, cx, 1.0f);
-        const float cc = quarter & 1 ? sx : cx, ss = quarter & 1 ? cx : sx;
-        c[i] = ((quarter + 1) & 2 ? -cc : cc) * a.magnitude;
-        s[i] = (quarter & 2 ? -ss : ss) * a.magnitude;
+    for (int i = 0; i < 4; ++i) {
+        const ulonglong2 t2 = __ldg(f + i);
+        const uint32_t t0 = (uint32_t)(((uint64_t)pos * t2.x) >> 32);
+        const uint32_t t1 = (uint32_t)(((uint64_t)pos * t2.y) >> 32);
+        // the sign of both functions: whether the nearest half turn is an odd one
+        const uint32_t odd0 = (t0 + (1u << 30)) & (1u << 31), odd1 = (t1 + (1u << 30)) & (1u << 31);
+        const F2 x = mul2(two((float)(int32_t)(t0 ^ odd0), (float)(int32_t)(t1 ^ odd1)), unit);
+        const F2 y = mul2(x, x);
+        F2 sx = fma2(y, all(-1.0f / 39916800), all(1.0f / 362880));
+        sx = fma2(y, sx, all(-1.0f / 5040));
+        sx = fma2(y, sx, all(1.0f / 120));
+        sx = fma2(y, sx, all(-1.0f / 6));
+        sx = fma2(mul2(x, y), sx, x);
+        F2 cx = fma2(y, all(1.0f / 479001600), all(-1.0f / 3628800));
+        cx = fma2(y, cx, all(1.0f / 40320));
+        cx = fma2(y, cx, all(-1.0f / 720));
+        cx = fma2(y, cx, all(1.0f / 24));
+        cx = fma2(y, cx, all(-0.5f));
+        cx = fma2(y, cx, all(1.0f));
+        const F2 odd = (F2)odd1 << 32 | odd0;
+        s[i] = mul2(sx, size) ^ odd;
+        c[i] = mul2(cx, size) ^ odd;
     }
 }
 
-// Turned by the angles (back: by their negatives).
+// z by its matrix: element i of a pair times a, and its partner times b.
 template <bool INTER>
-__device__ __forceinline__ void turn(float (&z)[16], const float (&c)[8], const float (&s)[8],
-                                     bool back) {
+__device__ __forceinline__ void by_matrix(F2 (&z)[8], const F2 (&a)[8], const F2 (&b)[8]) {
+    if constexpr (INTER) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float &p = z[INTER ? 2 * i : i], &q = z[INTER ? 2 * i + 1 : 8 + i];
-        const float sn = back ? -s[i] : s[i], x = p, y = q;
-        p = x * c[i] - y * sn;
-        q = y * c[i] + x * sn;
+        for (int i = 0; i < 8; ++i) z[i] = fma2(swap(z[i]), b[i], mul2(z[i], a[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 x = z[i], y = z[4 + i];
+            z[i] = fma2(y, b[i], mul2(x, a[i]));
+            z[4 + i] = fma2(x, b[4 + i], mul2(y, a[4 + i]));
+        }
+    }
+}
+
+// That matrix for w, then the turn by the angles; w of 1 and back: the transposed turn.
+template <bool INTER>
+__device__ __forceinline__ void matrix(const F2 (&c)[4], const F2 (&s)[4], const F2 (&w)[8],
+                                       bool back, F2 (&a)[8], F2 (&b)[8]) {
+    const float minus = back ? 1.0f : -1.0f;
+    if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 cc = both(c[i / 2]), ss = both(s[i / 2]), ww = both(w[i]);
+            const float ci = i & 1 ? cc.y : cc.x, si = i & 1 ? ss.y : ss.x;
+            a[i] = two(ww.x * ci, ww.y * ci);
+            b[i] = two(minus * ww.y * si, -minus * ww.x * si);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = mul2(w[i], c[i]);
+            a[4 + i] = mul2(w[4 + i], c[i]);
+            b[i] = mul2(mul2(w[4 + i], s[i]), two(minus, minus));
+            b[4 + i] = mul2(mul2(w[i], s[i]), two(-minus, -minus));
+        }
     }
 }
 
@@ -176,12 +233,13 @@ __device__ __forceinline__ float row_sum(float x, int lanes) {
     return x;
 }
 
+// The lane's part of a weight; 1 without one.
 template <typename T>
 __device__ __forceinline__ void load_weight(const HeadArgs &a, const HeadLane &l, const void *w,
-                                            float (&x)[16]) {
+                                            F2 (&x)[8]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-    if (!l.live) return;
+    for (int i = 0; i < 8; ++i) x[i] = two(1.0f, 1.0f);
+    if (!l.live || !w) return;
     if (a.w32) {
         Raw<float> r;
         r.load((const float *)w + l.lo, (const float *)w + l.hi);
@@ -214,24 +272,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_heads_rotate(const __grid_const
     const int64_t pos = at.position(a);
     const bool cached = keys && a.Tk >= 0, put = !cached || (pos >= 0 && pos < a.Tk);
     const int64_t row = cached ? pos : at.t;
-    float c[8], s[8], w[16];
-    if (h.w) load_weight<T>(a, l, h.w, w);
-    angles(a, l, INTER, pos, c, s);
+    F2 w[8], ma[8], mb[8];
+    load_weight<T>(a, l, h.w, w);
+    if (l.turned) {
+        F2 c[4], s[4];
+        angles(a, l, INTER, pos, c, s);
+        matrix<INTER>(c, s, w, false, ma, mb);
+    }
     T *to = (T *)h.out + at.b * h.o_sb + row * h.o_st + at.head * h.o_sh;
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
         if (u * h.at_once >= h.heads) break;     // no lane has one more
-        float z[16];
+        F2 z[8];
         x[u].get(z);
         if (h.w) {
-            float sum = 0.0f;
+            F2 sum = mul2(z[0], z[0]);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) sum = fmaf(z[i], z[i], sum);
-            const float r = rsqrtf(row_sum(sum, a.lanes) / (float)a.D + a.eps);
+            for (int i = 1; i < 8; ++i) sum = fma2(z[i], z[i], sum);
+            const float2 t = both(sum);
+            const float r = rsqrtf(fmaf(row_sum(t.x + t.y, a.lanes), a.inv_D, a.eps));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = z[i] * r * w[i];
+            for (int i = 0; i < 8; ++i) z[i] = mul2(z[i], two(r, r));
         }
-        if (l.turned) turn<INTER>(z, c, s, false);
+        if (l.turned) {
+            by_matrix<INTER>(z, ma, mb);
+        } else if (h.w) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = mul2(z[i], w[i]);
+        }
         x[u].set(z);
         T *p = to + u * h.at_once * h.o_sh;
         if (live[u] && put) x[u].store(p + l.lo, p + l.hi);
@@ -261,10 +329,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_heads_backward(const __grid_con
     const bool keys = blockIdx.x >= a.q_ctas;
     const HeadTensor &h = a.t[keys];
     const unsigned ctas = keys ? gridDim.x - a.q_ctas : a.q_ctas;
-    float w[16], dw[16];
-    if (h.w) load_weight<T>(a, l, h.w, w);
+    F2 w[8], dw[8];
+    load_weight<T>(a, l, h.w, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) dw[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) dw[i] = two(0.0f, 0.0f);
     for (uint64_t item = (uint64_t)(blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + warp;
          item < h.items; item += (uint64_t)ctas * kWarps) {
         const HeadPlace at(a, h, l, (unsigned)item, UN);
@@ -283,34 +351,44 @@ __global__ void __launch_bounds__(kThreads, 2) k_heads_backward(const __grid_con
             p = xs + u * h.at_once * h.sh;
             if (h.w) x[u].load(p + l.lo, p + l.hi);
         }
-        float c[8], s[8];
-        angles(a, l, INTER, at.position(a), c, s);
+        F2 ma[8], mb[8];
+        if (l.turned) {
+            F2 c[4], s[4], ones[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ones[i] = two(1.0f, 1.0f);
+            angles(a, l, INTER, at.position(a), c, s);
+            matrix<INTER>(c, s, ones, true, ma, mb);
+        }
         T *to = (T *)h.out + at.b * h.o_sb + at.t * h.o_st + at.head * h.o_sh;
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             if (u * h.at_once >= h.heads) break;
-            float y[16];
+            F2 y[8];
             g[u].get(y);
-            if (l.turned) turn<INTER>(y, c, s, true);
+            if (l.turned) by_matrix<INTER>(y, ma, mb);
             if (h.w) {
-                float z[16], sum = 0.0f, dot = 0.0f;
+                F2 z[8], sums = two(0.0f, 0.0f), dots = sums;
                 x[u].get(z);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    sum = fmaf(z[i], z[i], sum);
-                    dot = fmaf(y[i] * w[i], z[i], dot);
+                for (int i = 0; i < 8; ++i) {
+                    sums = fma2(z[i], z[i], sums);
+                    dots = fma2(mul2(y[i], w[i]), z[i], dots);
                 }
+                float2 t = both(sums);
+                float sum = t.x + t.y;
+                t = both(dots);
+                float dot = t.x + t.y;
                 for (int o = 1; o < a.lanes; o <<= 1) {
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     dot += __shfl_xor_sync(0xffffffffu, dot, o);
                 }
-                const float r = rsqrtf(sum / (float)a.D + a.eps);
-                const float m = dot * r / (float)a.D;      // mean(u n)
+                const float r = rsqrtf(fmaf(sum, a.inv_D, a.eps));
+                const float m = -dot * r * a.inv_D;        // -mean(u n)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float n = z[i] * r;
-                    dw[i] = fmaf(y[i], n, dw[i]);
-                    y[i] = r * (y[i] * w[i] - n * m);
+                for (int i = 0; i < 8; ++i) {
+                    const F2 n = mul2(z[i], two(r, r));
+                    dw[i] = fma2(y[i], n, dw[i]);
+                    y[i] = mul2(two(r, r), fma2(n, two(m, m), mul2(y[i], w[i])));
                 }
             }
             g[u].set(y);
@@ -320,11 +398,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_heads_backward(const __grid_con
     }
     if (!h.w) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        for (int o = a.lanes; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
-    if (lane < a.lanes && l.live) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sums[warp][i < 8 ? l.lo + i : l.hi + i - 8] = dw[i];
+    for (int i = 0; i < 8; ++i) {
+        float2 t = both(dw[i]);
+        for (int o = a.lanes; o < 32; o <<= 1) {
+            t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
+            t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+        }
+        if (lane < a.lanes && l.live) {
+            const int at = (i < 4 ? l.lo : l.hi) + 2 * (i & 3);
+            sums[warp][at] = t.x;
+            sums[warp][at + 1] = t.y;
+        }
     }
     __syncthreads();
     if ((int)threadIdx.x < a.D) {
@@ -399,6 +483,7 @@ HeadArgs heads_args(const spmm_heads_shape *s, int rows) {
     a.w32 = s->weight_dtype == SPMM_F32;
     a.eps = s->eps;
     a.magnitude = s->magnitude;
+    a.inv_D = 1.0f / (float)s->D;
     a.turns = s->turns;
     a.positions = s->positions;
     a.p_sb = s->p_sb;
