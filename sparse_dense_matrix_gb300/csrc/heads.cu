@@ -7,49 +7,60 @@
 // The angle of position p is p f turns, f < 1 in units of 2^-64: one 64-bit integer
 // product, whose wrap is the reduction mod a turn, so a far position costs no accuracy.
 //
-// A lane holds 16 elements of a row, eight pairs: two wide loads of 8 elements
+// A lane holds 8 elements of a row, four pairs: two loads of 4 elements
 // (the lanes of a row read adjacent ones), no exchange for the rotation, and a
-// shuffle over the row's lanes for the norm's sum. A warp takes a few heads of a token
-// (of several where a token has few), UN rows for each of its groups of lanes: it asks for
-// all of them first and works out the angles, the same for all, while they come. One
-// pass: every element is read once and written once.
+// shuffle over the row's lanes for the norm's sum. A warp takes a token (several where
+// they have few heads) and walks its heads of queries and keys: the angles are the same
+// for all of them. One pass: every element is read once and written once.
+// A warp works the angles out once, a pair to a lane, and hands them round in shared memory.
+// Two rows are worked on side by side, as one row's chain (its sum over the lanes, the
+// root, the products) leaves the pipes idle, and four more are on their way meanwhile.
 #include "blocks.cuh"
 
 namespace spmm {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kSms = 152;
+constexpr int kSms = 152, kCtas = 3 * kSms;
 
-struct HeadTensor {                  // one [B, T, heads, D] tensor and what becomes of it
-    const void *x, *g;               // inputs; gradients of the results (backward)
-    int64_t sb, st, sh, g_sb, g_st, g_sh;
-    const void *w;
-    void *out;                       // results, or gradients of the inputs
-    int64_t o_sb, o_st, o_sh;
-    int heads, at_once, tokens;      // heads of a token, and tokens, that a warp's rows are of
-    unsigned chunks, items;          // warps' items per (group of tokens), in all
+// Strided [B, T, heads, D] tensors: what is read, with its weight, and what is written.
+struct HeadFrom {
+    const void *x, *w;
+    int64_t sb, st, sh;
+    int heads;
+};
+struct HeadTo {
+    void *out;
+    int64_t sb, st, sh;
+};
+
+// How warps share the tokens: their rows at a time are of at_once heads of `tokens` tokens;
+// `splits` warps share a token's heads; `items` shares in all.
+struct HeadWalk {
+    int at_once, tokens;
+    unsigned splits, items;
 };
 
 struct HeadArgs {
-    HeadTensor t[2];                 // queries, keys
-    const void *v;                   // append: the values, copied by the keys' warps
-    void *v_out;
-    int64_t v_sb, v_st, v_sh, vo_sb, vo_st, vo_sh;
-    unsigned q_ctas;                 // the first CTAs are the queries'
     int all, T, D, R, lanes;         // B T; lanes of a row
     int w32;                         // weights are fp32
     float eps, magnitude, inv_D;
     const uint64_t *turns;
     const int32_t *positions, *lengths;
     int64_t p_sb, p_st;
+    HeadFrom from[3];                // queries, keys, values (append); backward: the gradients
+    HeadTo to[3];
+    HeadFrom x[2];                   // backward: queries, keys
+    HeadWalk walk[2];                // forward: the first; backward: queries', keys'
     int Tk;                          // rows of the caches that k and v go to, or -1
+    unsigned q_ctas;                 // backward: the first CTAs are the queries'
     float *parts;                    // backward: [CTAs][D] parts of the weights' gradients
 };
 
 // Two floats to an instruction: the arithmetic of a row would else take longer to issue
 // than the row takes to come.
 using F2 = unsigned long long;
+constexpr F2 kMinus2 = 0x8000000080000000ull;
 __device__ __forceinline__ F2 two(float lo, float hi) {
     F2 x;
     asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(lo), "f"(hi));
@@ -75,37 +86,28 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
     return x;
 }
 
-// 16 elements as they lie in memory: 8 from one place and 8 from another. As floats,
+// 8 elements as they lie in memory: 4 from one place and 4 from another. As floats,
 // number i holds elements 2 i and 2 i + 1.
 template <typename T> struct Raw {
-    static constexpr int N = sizeof(T) / 2;        // 16-byte words of 8 elements
-    uint4 w[2 * N];
+    using V = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
+    V w[2];
     __device__ __forceinline__ void load(const T *lo, const T *hi) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            w[i] = __ldg((const uint4 *)lo + i);
-            w[N + i] = __ldg((const uint4 *)hi + i);
-        }
+        w[0] = __ldg((const V *)lo);
+        w[1] = __ldg((const V *)hi);
     }
     __device__ __forceinline__ void store(T *lo, T *hi) const {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            ((uint4 *)lo)[i] = w[i];
-            ((uint4 *)hi)[i] = w[N + i];
-        }
+        *(V *)lo = w[0];
+        *(V *)hi = w[1];
     }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < 2 * N; ++i) w[i] = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void get(F2 (&x)[8]) const {
+    __device__ __forceinline__ void zero() { w[0] = w[1] = V{}; }
+    __device__ __forceinline__ void get(F2 (&x)[4]) const {
         const T *e = reinterpret_cast<const T *>(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = two(to_f32(e[2 * i]), to_f32(e[2 * i + 1]));
+        for (int i = 0; i < 4; ++i) x[i] = two(to_f32(e[2 * i]), to_f32(e[2 * i + 1]));
     }
-    __device__ __forceinline__ void set(const F2 (&x)[8]) {
+    __device__ __forceinline__ void set(const F2 (&x)[4]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float2 y = both(x[i]);
             if constexpr (sizeof(T) == 4)
                 reinterpret_cast<float2 *>(w)[i] = y;
@@ -115,130 +117,155 @@ template <typename T> struct Raw {
     }
 };
 
-// A lane's place: row `row` of the warp's rows at a time, and in it the 8 elements
-// from `lo` and the 8 from `hi`. D and R are multiples of 16, so a lane's elements
-// are all turned (its eight pairs) or none is.
+// A lane's place: row `row` of the warp's rows at a time, and in it the 4 elements
+// from `lo` and the 4 from `hi`. D and R are multiples of 16, so a lane's elements
+// are all turned (its four pairs) or none is.
 struct HeadLane {
     int row, lo, hi;
     bool live, turned;
     __device__ __forceinline__ HeadLane(const HeadArgs &a, bool interleaved) {
         const int lane = threadIdx.x & 31, u = lane & (a.lanes - 1);
         row = lane / a.lanes;
-        live = u * 16 < a.D;
-        turned = u * 16 < a.R;
-        lo = turned && !interleaved ? 8 * u : 16 * u;
-        hi = turned && !interleaved ? a.R / 2 + 8 * u : 16 * u + 8;
+        live = u * 8 < a.D;
+        turned = u * 8 < a.R;
+        lo = turned && !interleaved ? 4 * u : 8 * u;
+        hi = turned && !interleaved ? a.R / 2 + 4 * u : 8 * u + 4;
     }
 };
 
-// Which token and first head the lane's rows are of; its u-th is at_once heads further.
+// One token of each of the warp's groups of lanes, and where among its heads the lane begins.
 struct HeadPlace {
-    int64_t b;
-    int t, head;
+    int64_t b, pos;
+    int t, first;
     bool live;
-    __device__ __forceinline__ HeadPlace(const HeadArgs &a, const HeadTensor &h, const HeadLane &l,
-                                         unsigned item, int un) {
-        const unsigned group = item / h.chunks, chunk = item % h.chunks;
-        const int64_t token = (int64_t)group * h.tokens + l.row / h.at_once;
-        live = l.live && l.row < h.tokens * h.at_once && token < a.all;
+    __device__ __forceinline__ HeadPlace(const HeadArgs &a, const HeadWalk &w, const HeadLane &l,
+                                         unsigned item) {
+        const int which = w.tokens == 1 ? 0 : l.row / w.at_once;
+        const int64_t token = (int64_t)(item / w.splits) * w.tokens + which;
+        live = l.live && which < w.tokens && token < a.all;
         b = live ? (unsigned)token / (unsigned)a.T : 0;
-        t = live ? (int)((unsigned)token % (unsigned)a.T) : 0;
-        head = (int)chunk * un * h.at_once + l.row % h.at_once;
-    }
-    __device__ __forceinline__ int64_t position(const HeadArgs &a) const {
-        if (!live) return 0;
-        if (a.positions) return a.positions[b * a.p_sb + t * a.p_st];
-        return (a.lengths ? (int64_t)a.lengths[b] - a.T : 0) + t;
+        t = live ? (int)((unsigned)token - (unsigned)b * (unsigned)a.T) : 0;
+        first = l.row - which * w.at_once;
+        pos = t;
+        if (a.positions) pos = live ? a.positions[b * a.p_sb + t * a.p_st] : 0;
+        else if (a.lengths) pos = live ? (int64_t)a.lengths[b] - a.T + t : 0;
     }
 };
 
-// Sines and cosines of the lane's pairs, times the magnitude (of pairs 2 i and 2 i + 1 in
-// number i). The turn is cut to the nearest half (exactly, in integers) before it
-// becomes a float. What is left, x of at most pi / 2, is off by 2^-24 of itself and goes
-// into the two functions' power series, whose first terms left out, x^13 / 13! and
-// x^14 / 14!, are below 2^-24.
-__device__ __forceinline__ void angles(const HeadArgs &a, const HeadLane &l, bool interleaved,
-                                       int64_t pos, F2 (&c)[4], F2 (&s)[4]) {
-    const ulonglong2 *f = (const ulonglong2 *)(a.turns + (interleaved ? l.lo / 2 : l.lo));
-    auto all = [](float x) { return two(x, x); };
-    const F2 unit = all(1.46291807926716e-9f), size = all(a.magnitude);      // 2 pi / 2^32
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const ulonglong2 t2 = __ldg(f + i);
-        const uint32_t t0 = (uint32_t)(((uint64_t)pos * t2.x) >> 32);
-        const uint32_t t1 = (uint32_t)(((uint64_t)pos * t2.y) >> 32);
+// Sines and cosines of the warp's tokens' pairs, times the magnitude. The turn is cut to the
+// nearest half (exactly, in integers) before it becomes a float. What is left, x of at
+// most pi / 2, is off by 2^-24 of itself and goes into the two functions' power series,
+// whose first terms left out, x^13 / 13! and x^14 / 14!, are below 2^-24.
+struct HeadAngles {
+    float c[128], s[128];            // of a warp: tokens x R / 2, at most 32 / lanes x 4 lanes
+};
+__device__ __forceinline__ void angles(const HeadArgs &a, const HeadWalk &w, int64_t pos,
+                                       HeadAngles &to) {
+    const int pairs = a.R / 2, lane = threadIdx.x & 31;
+    for (int i0 = 0; i0 < pairs * w.tokens; i0 += 32) {
+        const int i = i0 + lane, token = w.tokens == 1 ? 0 : i / pairs;
+        const int64_t p =
+            __shfl_sync(0xffffffffu, pos, (w.tokens == 1 ? 0 : token * w.at_once * a.lanes) & 31);
+        if (i >= pairs * w.tokens) continue;
+        const uint32_t t = (uint32_t)(((uint64_t)p * __ldg(a.turns + (i - token * pairs))) >> 32);
         // the sign of both functions: whether the nearest half turn is an odd one
-        const uint32_t odd0 = (t0 + (1u << 30)) & (1u << 31), odd1 = (t1 + (1u << 30)) & (1u << 31);
-        const F2 x = mul2(two((float)(int32_t)(t0 ^ odd0), (float)(int32_t)(t1 ^ odd1)), unit);
-        const F2 y = mul2(x, x);
-        F2 sx = fma2(y, all(-1.0f / 39916800), all(1.0f / 362880));
-        sx = fma2(y, sx, all(-1.0f / 5040));
-        sx = fma2(y, sx, all(1.0f / 120));
-        sx = fma2(y, sx, all(-1.0f / 6));
-        sx = fma2(mul2(x, y), sx, x);
-        F2 cx = fma2(y, all(1.0f / 479001600), all(-1.0f / 3628800));
-        cx = fma2(y, cx, all(1.0f / 40320));
-        cx = fma2(y, cx, all(-1.0f / 720));
-        cx = fma2(y, cx, all(1.0f / 24));
-        cx = fma2(y, cx, all(-0.5f));
-        cx = fma2(y, cx, all(1.0f));
-        const F2 odd = (F2)odd1 << 32 | odd0;
-        s[i] = mul2(sx, size) ^ odd;
-        c[i] = mul2(cx, size) ^ odd;
+        const uint32_t odd = (t + (1u << 30)) & (1u << 31);
+        const float x = (float)(int32_t)(t ^ odd) * 1.46291807926716e-9f;    // 2 pi / 2^32
+        const float y = x * x;
+        float sx = fmaf(y, -1.0f / 39916800, 1.0f / 362880);
+        sx = fmaf(y, sx, -1.0f / 5040);
+        sx = fmaf(y, sx, 1.0f / 120);
+        sx = fmaf(y, sx, -1.0f / 6);
+        sx = fmaf(x * y, sx, x);
+        float cx = fmaf(y, 1.0f / 479001600, -1.0f / 3628800);
+        cx = fmaf(y, cx, 1.0f / 40320);
+        cx = fmaf(y, cx, -1.0f / 720);
+        cx = fmaf(y, cx, 1.0f / 24);
+        cx = fmaf(y, cx, -0.5f);
+        cx = fmaf(y, cx, 1.0f);
+        to.c[i] = __uint_as_float(__float_as_uint(cx * a.magnitude) ^ odd);
+        to.s[i] = __uint_as_float(__float_as_uint(sx * a.magnitude) ^ odd);
+    }
+    __syncwarp();
+}
+// The lane's: of pairs 2 i and 2 i + 1 in number i.
+__device__ __forceinline__ void take_angles(const HeadArgs &a, const HeadWalk &w, const HeadLane &l,
+                                            const HeadAngles &from, F2 (&c)[2], F2 (&s)[2]) {
+    if (!l.turned) return;
+    const int which = w.tokens == 1 ? 0 : min(l.row / w.at_once, w.tokens - 1);
+    const int at = which * (a.R / 2) + ((threadIdx.x & 31) & (a.lanes - 1)) * 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        c[i] = two(from.c[at + 2 * i], from.c[at + 2 * i + 1]);
+        s[i] = two(from.s[at + 2 * i], from.s[at + 2 * i + 1]);
     }
 }
 
 // z by its matrix: element i of a pair times a, and its partner times b.
 template <bool INTER>
-__device__ __forceinline__ void by_matrix(F2 (&z)[8], const F2 (&a)[8], const F2 (&b)[8]) {
+__device__ __forceinline__ void by_matrix(F2 (&z)[4], const F2 (&a)[4], const F2 (&b)[4]) {
     if constexpr (INTER) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = fma2(swap(z[i]), b[i], mul2(z[i], a[i]));
+        for (int i = 0; i < 4; ++i) z[i] = fma2(swap(z[i]), b[i], mul2(z[i], a[i]));
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const F2 x = z[i], y = z[4 + i];
+        for (int i = 0; i < 2; ++i) {
+            const F2 x = z[i], y = z[2 + i];
             z[i] = fma2(y, b[i], mul2(x, a[i]));
-            z[4 + i] = fma2(x, b[4 + i], mul2(y, a[4 + i]));
+            z[2 + i] = fma2(x, b[2 + i], mul2(y, a[2 + i]));
         }
     }
 }
 
-// That matrix for w, then the turn by the angles; w of 1 and back: the transposed turn.
+// That matrix for the product with w and then the turn by the angles.
 template <bool INTER>
-__device__ __forceinline__ void matrix(const F2 (&c)[4], const F2 (&s)[4], const F2 (&w)[8],
-                                       bool back, F2 (&a)[8], F2 (&b)[8]) {
-    const float minus = back ? 1.0f : -1.0f;
+__device__ __forceinline__ void matrix(const F2 (&c)[2], const F2 (&s)[2], const F2 (&w)[4],
+                                       F2 (&a)[4], F2 (&b)[4]) {
     if constexpr (INTER) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const float2 cc = both(c[i / 2]), ss = both(s[i / 2]), ww = both(w[i]);
             const float ci = i & 1 ? cc.y : cc.x, si = i & 1 ? ss.y : ss.x;
             a[i] = two(ww.x * ci, ww.y * ci);
-            b[i] = two(minus * ww.y * si, -minus * ww.x * si);
+            b[i] = two(-ww.y * si, ww.x * si);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             a[i] = mul2(w[i], c[i]);
-            a[4 + i] = mul2(w[4 + i], c[i]);
-            b[i] = mul2(mul2(w[4 + i], s[i]), two(minus, minus));
-            b[4 + i] = mul2(mul2(w[i], s[i]), two(-minus, -minus));
+            a[2 + i] = mul2(w[2 + i], c[i]);
+            b[i] = mul2(w[2 + i], s[i]) ^ kMinus2;
+            b[2 + i] = mul2(w[i], s[i]);
         }
     }
 }
 
-__device__ __forceinline__ float row_sum(float x, int lanes) {
-    for (int o = 1; o < lanes; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+// Turned by the negatives of the angles.
+template <bool INTER>
+__device__ __forceinline__ void turn_back(F2 (&z)[4], const F2 (&c)[2], const F2 (&s)[2]) {
+    if constexpr (INTER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 cc = both(c[i / 2]), ss = both(s[i / 2]), x = both(z[i]);
+            const float ci = i & 1 ? cc.y : cc.x, si = i & 1 ? ss.y : ss.x;
+            z[i] = two(fmaf(x.y, si, x.x * ci), fmaf(-x.x, si, x.y * ci));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const F2 x = z[i], y = z[2 + i];
+            z[i] = fma2(y, s[i], mul2(x, c[i]));
+            z[2 + i] = fma2(x, s[i] ^ kMinus2, mul2(y, c[i]));
+        }
+    }
 }
 
 // The lane's part of a weight; 1 without one.
 template <typename T>
 __device__ __forceinline__ void load_weight(const HeadArgs &a, const HeadLane &l, const void *w,
-                                            F2 (&x)[8]) {
+                                            F2 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = two(1.0f, 1.0f);
+    for (int i = 0; i < 4; ++i) x[i] = two(1.0f, 1.0f);
     if (!l.live || !w) return;
     if (a.w32) {
         Raw<float> r;
@@ -251,170 +278,238 @@ __device__ __forceinline__ void load_weight(const HeadArgs &a, const HeadLane &l
     }
 }
 
-template <typename T, bool INTER, int UN>
-__global__ void __launch_bounds__(kThreads, 2) k_heads_rotate(const __grid_constant__ HeadArgs a) {
-    const HeadLane l(a, INTER);
-    const bool keys = blockIdx.x >= a.q_ctas;
-    const HeadTensor &h = a.t[keys];
-    const unsigned item = (blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + threadIdx.x / 32;
-    if (item >= h.items) return;
-    const HeadPlace at(a, h, l, item, UN);
-    Raw<T> x[UN];
-    bool live[UN];
-    const T *from = (const T *)h.x + at.b * h.sb + at.t * h.st + at.head * h.sh;
+// Rows asked for ahead of the work, of a lane.
+template <typename T> constexpr int kForwardRows = 8 / (int)sizeof(T);
+template <typename T> constexpr int kBackwardRows = 4 / (int)sizeof(T);
+
+// Heads split * at_once + first of a token, then splits * at_once further. COPY: as they are.
+template <typename T, bool INTER, bool COPY>
+__device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadWalk &w,
+                                              const HeadLane &l, const HeadPlace &at, int split,
+                                              const HeadFrom &h, const HeadTo &o, int64_t row,
+                                              bool put, const HeadAngles *told) {
+    constexpr int AHEAD = kForwardRows<T>;
+    static_assert(AHEAD % 2 == 0, "rows come in twos");
+    const int step = (int)w.splits * w.at_once;
+    const int left = h.heads - split * w.at_once, n = left > 0 ? (left + step - 1) / step : 0;
+    if (n == 0) return;
+    const int off = l.hi - l.lo;
+    const int64_t from_step = step * h.sh, to_step = step * o.sh;
+    int head = split * w.at_once + at.first;
+    const T *from = (const T *)h.x + at.b * h.sb + at.t * h.st + head * h.sh + l.lo;
+    T *to = (T *)o.out + at.b * o.sb + row * o.st + head * o.sh + l.lo;
+    Raw<T> x[AHEAD];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-        live[u] = at.live && at.head + u * h.at_once < h.heads;
-        const T *p = from + u * h.at_once * h.sh;
-        if (live[u]) x[u].load(p + l.lo, p + l.hi);
-        else x[u].zero();
+    for (int u = 0; u < AHEAD; ++u) {
+        x[u].zero();                             // (lanes without a part of a row add 0 to it)
+        if (at.live && head + u * step < h.heads) x[u].load(from, from + off);
+        from += from_step;
     }
-    const int64_t pos = at.position(a);
-    const bool cached = keys && a.Tk >= 0, put = !cached || (pos >= 0 && pos < a.Tk);
-    const int64_t row = cached ? pos : at.t;
-    F2 w[8], ma[8], mb[8];
-    load_weight<T>(a, l, h.w, w);
-    if (l.turned) {
-        F2 c[4], s[4];
-        angles(a, l, INTER, pos, c, s);
-        matrix<INTER>(c, s, w, false, ma, mb);
-    }
-    T *to = (T *)h.out + at.b * h.o_sb + row * h.o_st + at.head * h.o_sh;
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-        if (u * h.at_once >= h.heads) break;     // no lane has one more
-        F2 z[8];
-        x[u].get(z);
-        if (h.w) {
-            F2 sum = mul2(z[0], z[0]);
-#pragma unroll
-            for (int i = 1; i < 8; ++i) sum = fma2(z[i], z[i], sum);
-            const float2 t = both(sum);
-            const float r = rsqrtf(fmaf(row_sum(t.x + t.y, a.lanes), a.inv_D, a.eps));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = mul2(z[i], two(r, r));
-        }
+    const bool norm = !COPY && h.w;
+    F2 ma[4], mb[4];                             // (ma: of lanes that are not turned, the weight)
+    if (!COPY) {
+        load_weight<T>(a, l, h.w, ma);
         if (l.turned) {
-            by_matrix<INTER>(z, ma, mb);
-        } else if (h.w) {
+            F2 c[2], s[2], weight[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = mul2(z[i], w[i]);
+            for (int j = 0; j < 4; ++j) weight[j] = ma[j];
+            take_angles(a, w, l, *told, c, s);
+            matrix<INTER>(c, s, weight, ma, mb);
         }
-        x[u].set(z);
-        T *p = to + u * h.at_once * h.o_sh;
-        if (live[u] && put) x[u].store(p + l.lo, p + l.hi);
     }
-    if (!cached || !put) return;
-    const T *v = (const T *)a.v + at.b * a.v_sb + at.t * a.v_st + at.head * a.v_sh;
-    T *v_to = (T *)a.v_out + at.b * a.vo_sb + pos * a.vo_st + at.head * a.vo_sh;
+    for (int i = 0; i < n; i += AHEAD) {
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-        const T *p = v + u * h.at_once * a.v_sh;
-        if (live[u]) x[u].load(p + l.lo, p + l.hi);
-    }
+        for (int u = 0; u < AHEAD; u += 2) {
+            if (i + u >= n) break;
+            Raw<T> y[2];
+            if (COPY) {
+                y[0] = x[u];
+                y[1] = x[u + 1];
+            } else {
+                F2 z[2][4];
+                x[u].get(z[0]);
+                x[u + 1].get(z[1]);
+                if (norm) {
+                    float sum[2];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-        T *p = v_to + u * h.at_once * a.vo_sh;
-        if (live[u]) x[u].store(p + l.lo, p + l.hi);
+                    for (int v = 0; v < 2; ++v) {
+                        F2 sq = mul2(z[v][0], z[v][0]);
+#pragma unroll
+                        for (int j = 1; j < 4; ++j) sq = fma2(z[v][j], z[v][j], sq);
+                        const float2 t = both(sq);
+                        sum[v] = t.x + t.y;
+                    }
+                    for (int d = 1; d < a.lanes; d <<= 1) {
+                        const float s0 = __shfl_xor_sync(0xffffffffu, sum[0], d);
+                        const float s1 = __shfl_xor_sync(0xffffffffu, sum[1], d);
+                        sum[0] += s0;
+                        sum[1] += s1;
+                    }
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const float r = rsqrtf(fmaf(sum[v], a.inv_D, a.eps));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) z[v][j] = mul2(z[v][j], two(r, r));
+                    }
+                }
+                if (l.turned) {
+                    by_matrix<INTER>(z[0], ma, mb);
+                    by_matrix<INTER>(z[1], ma, mb);
+                } else if (norm) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        z[0][j] = mul2(z[0][j], ma[j]);
+                        z[1][j] = mul2(z[1][j], ma[j]);
+                    }
+                }
+                y[0].set(z[0]);
+                y[1].set(z[1]);
+            }
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                if (at.live && put && head < h.heads) y[v].store(to, to + off);
+                to += to_step;
+                if (at.live && head + AHEAD * step < h.heads) x[u + v].load(from, from + off);
+                from += from_step;
+                head += step;
+            }
+        }
     }
+}
+
+// A warp takes a token's queries, keys and (append) values, or every splits-th of their rows.
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) k_heads_rotate(const __grid_constant__ HeadArgs a) {
+    __shared__ HeadAngles told[kWarps];
+    const HeadLane l(a, INTER);
+    const HeadWalk &w = a.walk[0];
+    const int warp = threadIdx.x / 32;
+    const unsigned item = blockIdx.x * kWarps + warp;
+    if (item >= w.items) return;
+    const int split = w.splits == 1 ? 0 : (int)(item % w.splits);
+    const HeadPlace at(a, w, l, item);
+    angles(a, w, at.pos, told[warp]);
+    const bool cached = a.Tk >= 0, put = !cached || (at.pos >= 0 && at.pos < a.Tk);
+    const int64_t row = cached ? at.pos : at.t;
+    forward_heads<T, INTER, false>(a, w, l, at, split, a.from[0], a.to[0], at.t, true, &told[warp]);
+    forward_heads<T, INTER, false>(a, w, l, at, split, a.from[1], a.to[1], row, put, &told[warp]);
+    if (cached)
+        forward_heads<T, INTER, true>(a, w, l, at, split, a.from[2], a.to[2], row, put, nullptr);
 }
 
 // The weights' gradients: a lane's sums over its rows, then over the rows of the
 // warp, the warps of the CTA and, by a second kernel, the CTAs, each in a fixed order.
-template <typename T, bool INTER, int UN>
-__global__ void __launch_bounds__(kThreads, 2) k_heads_backward(const __grid_constant__ HeadArgs a) {
-    __shared__ float sums[kWarps][256];
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3)
+    k_heads_backward(const __grid_constant__ HeadArgs a) {
+    __shared__ HeadAngles told[kWarps];
+    constexpr int AHEAD = kBackwardRows<T>;
     const HeadLane l(a, INTER);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, off = l.hi - l.lo;
     const bool keys = blockIdx.x >= a.q_ctas;
-    const HeadTensor &h = a.t[keys];
+    const HeadWalk &w = a.walk[keys];
+    const HeadFrom &g = a.from[keys], &x = a.x[keys];
+    const HeadTo &o = a.to[keys];
+    const bool norm = x.w != nullptr;
     const unsigned ctas = keys ? gridDim.x - a.q_ctas : a.q_ctas;
-    F2 w[8], dw[8];
-    load_weight<T>(a, l, h.w, w);
+    const int n = (g.heads + w.at_once - 1) / w.at_once;
+    const int64_t g_step = w.at_once * g.sh, x_step = w.at_once * x.sh, o_step = w.at_once * o.sh;
+    F2 weight[4], dw[4];
+    load_weight<T>(a, l, x.w, weight);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[i] = two(0.0f, 0.0f);
-    for (uint64_t item = (uint64_t)(blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + warp;
-         item < h.items; item += (uint64_t)ctas * kWarps) {
-        const HeadPlace at(a, h, l, (unsigned)item, UN);
-        Raw<T> g[UN], x[UN];
-        bool live[UN];
-        const T *gs = (const T *)h.g + at.b * h.g_sb + at.t * h.g_st + at.head * h.g_sh;
-        const T *xs = (const T *)h.x + at.b * h.sb + at.t * h.st + at.head * h.sh;
+    for (int i = 0; i < 4; ++i) dw[i] = two(0.0f, 0.0f);
+    for (unsigned item = (blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + warp; item < w.items;
+         item += ctas * kWarps) {
+        const HeadPlace at(a, w, l, item);
+        int head = at.first;
+        const T *gs = (const T *)g.x + at.b * g.sb + at.t * g.st + head * g.sh + l.lo;
+        const T *xs = (const T *)x.x + at.b * x.sb + at.t * x.st + head * x.sh + l.lo;
+        T *to = (T *)o.out + at.b * o.sb + at.t * o.st + head * o.sh + l.lo;
+        Raw<T> rg[AHEAD], rx[AHEAD];
 #pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            live[u] = at.live && at.head + u * h.at_once < h.heads;
-            g[u].zero();
-            x[u].zero();
-            if (!live[u]) continue;
-            const T *p = gs + u * h.at_once * h.g_sh;
-            g[u].load(p + l.lo, p + l.hi);
-            p = xs + u * h.at_once * h.sh;
-            if (h.w) x[u].load(p + l.lo, p + l.hi);
+        for (int u = 0; u < AHEAD; ++u) {
+            rg[u].zero();
+            rx[u].zero();
+            const bool live = at.live && head + u * w.at_once < g.heads;
+            if (live) rg[u].load(gs, gs + off);
+            if (live && norm) rx[u].load(xs, xs + off);
+            gs += g_step;
+            xs += x_step;
         }
-        F2 ma[8], mb[8];
-        if (l.turned) {
-            F2 c[4], s[4], ones[8];
+        F2 c[2], s[2];
+        __syncwarp();                            // (the angles before are read)
+        angles(a, w, at.pos, told[warp]);
+        take_angles(a, w, l, told[warp], c, s);
+        for (int i = 0; i < n; i += AHEAD) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ones[i] = two(1.0f, 1.0f);
-            angles(a, l, INTER, at.position(a), c, s);
-            matrix<INTER>(c, s, ones, true, ma, mb);
-        }
-        T *to = (T *)h.out + at.b * h.o_sb + at.t * h.o_st + at.head * h.o_sh;
-#pragma unroll
-        for (int u = 0; u < UN; ++u) {
-            if (u * h.at_once >= h.heads) break;
-            F2 y[8];
-            g[u].get(y);
-            if (l.turned) by_matrix<INTER>(y, ma, mb);
-            if (h.w) {
-                F2 z[8], sums = two(0.0f, 0.0f), dots = sums;
-                x[u].get(z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sums = fma2(z[i], z[i], sums);
-                    dots = fma2(mul2(y[i], w[i]), z[i], dots);
+            for (int u = 0; u < AHEAD; ++u) {
+                if (i + u >= n) break;
+                const bool live = at.live && head < g.heads;
+                F2 y[4], z[4];
+                rg[u].get(y);
+                rx[u].get(z);
+                if (at.live && head + AHEAD * w.at_once < g.heads) {
+                    rg[u].load(gs, gs + off);
+                    if (norm) rx[u].load(xs, xs + off);
                 }
-                float2 t = both(sums);
-                float sum = t.x + t.y;
-                t = both(dots);
-                float dot = t.x + t.y;
-                for (int o = 1; o < a.lanes; o <<= 1) {
-                    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                }
-                const float r = rsqrtf(fmaf(sum, a.inv_D, a.eps));
-                const float m = -dot * r * a.inv_D;        // -mean(u n)
+                gs += g_step;
+                xs += x_step;
+                if (l.turned) turn_back<INTER>(y, c, s);
+                if (norm) {
+                    F2 sq = mul2(z[0], z[0]), dots = mul2(mul2(y[0], weight[0]), z[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const F2 n = mul2(z[i], two(r, r));
-                    dw[i] = fma2(y[i], n, dw[i]);
-                    y[i] = mul2(two(r, r), fma2(n, two(m, m), mul2(y[i], w[i])));
+                    for (int j = 1; j < 4; ++j) {
+                        sq = fma2(z[j], z[j], sq);
+                        dots = fma2(mul2(y[j], weight[j]), z[j], dots);
+                    }
+                    float2 v = both(sq);
+                    float sum = v.x + v.y;
+                    v = both(dots);
+                    float dot = v.x + v.y;
+                    for (int d = 1; d < a.lanes; d <<= 1) {
+                        const float s0 = __shfl_xor_sync(0xffffffffu, sum, d);
+                        const float s1 = __shfl_xor_sync(0xffffffffu, dot, d);
+                        sum += s0;
+                        dot += s1;
+                    }
+                    const float q = rsqrtf(fmaf(sum, a.inv_D, a.eps));
+                    const float m = -dot * q * a.inv_D;    // -mean(u n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const F2 nj = mul2(z[j], two(q, q));
+                        if (live) dw[j] = fma2(y[j], nj, dw[j]);
+                        y[j] = mul2(two(q, q), fma2(nj, two(m, m), mul2(y[j], weight[j])));
+                    }
                 }
+                Raw<T> r;
+                r.set(y);
+                if (live) r.store(to, to + off);
+                to += o_step;
+                head += w.at_once;
             }
-            g[u].set(y);
-            T *p = to + u * h.at_once * h.o_sh;
-            if (live[u]) g[u].store(p + l.lo, p + l.hi);
         }
     }
-    if (!h.w) return;
+    if (!norm) return;
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(told);         // [kWarps][256]
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float2 t = both(dw[i]);
-        for (int o = a.lanes; o < 32; o <<= 1) {
-            t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-            t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+    for (int i = 0; i < 4; ++i) {
+        float2 v = both(dw[i]);
+        for (int j = a.lanes; j < 32; j <<= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, j);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, j);
         }
         if (lane < a.lanes && l.live) {
-            const int at = (i < 4 ? l.lo : l.hi) + 2 * (i & 3);
-            sums[warp][at] = t.x;
-            sums[warp][at + 1] = t.y;
+            const int j = warp * 256 + (i < 2 ? l.lo : l.hi) + 2 * (i & 1);
+            sums[j] = v.x;
+            sums[j + 1] = v.y;
         }
     }
     __syncthreads();
     if ((int)threadIdx.x < a.D) {
-        float x = 0.0f;
-        for (int i = 0; i < kWarps; ++i) x += sums[i][threadIdx.x];
-        a.parts[(int64_t)blockIdx.x * a.D + threadIdx.x] = x;
+        float v = 0.0f;
+        for (int i = 0; i < kWarps; ++i) v += sums[i * 256 + threadIdx.x];
+        a.parts[(int64_t)blockIdx.x * a.D + threadIdx.x] = v;
     }
 }
 
@@ -462,24 +557,30 @@ spmm_status heads_check(const spmm_heads_shape *s) {
 
 bool heads_empty(const spmm_heads_shape *s) { return !s->B || !s->T || !(s->Hq + s->Hk); }
 
-void contiguous_out(HeadTensor &h, void *out, const spmm_heads_shape *s) {
-    h.out = out;
-    h.o_sh = s->D;
-    h.o_st = h.heads * s->D;
-    h.o_sb = s->T * h.o_st;
+HeadFrom from(const spmm_rows &r, int64_t heads, const void *w) {
+    HeadFrom h{};
+    set_rows(h.x, h.sb, h.st, h.sh, r);
+    h.w = w;
+    h.heads = (int)heads;
+    return h;
+}
+HeadTo to(const spmm_rows &r) {
+    return HeadTo{const_cast<void *>(r.data), r.sb, r.st, r.sh};
+}
+HeadTo contiguous(void *out, int64_t heads, const spmm_heads_shape *s) {
+    return HeadTo{out, s->T * heads * s->D, heads * s->D, s->D};
 }
 
-// Rows of 16-byte words that a lane asks for at a time: 128 bytes of them.
-constexpr int kForwardRows = 8, kBackwardRows = 4;   // over the element's bytes
+unsigned warps_ctas(unsigned items) { return items / kWarps + (items % kWarps > 0); }
 
-HeadArgs heads_args(const spmm_heads_shape *s, int rows) {
+HeadArgs shared_args(const spmm_heads_shape *s) {
     HeadArgs a{};
     a.all = (int)(s->B * s->T);
     a.T = (int)s->T;
     a.D = (int)s->D;
     a.R = (int)s->R;
     a.lanes = 1;
-    while (a.lanes * 16 < a.D) a.lanes *= 2;
+    while (a.lanes * 8 < a.D) a.lanes *= 2;
     a.w32 = s->weight_dtype == SPMM_F32;
     a.eps = s->eps;
     a.magnitude = s->magnitude;
@@ -490,61 +591,75 @@ HeadArgs heads_args(const spmm_heads_shape *s, int rows) {
     a.p_st = s->p_st;
     a.lengths = s->lengths;
     a.Tk = -1;
-    const int groups = 32 / a.lanes, un = rows / dtype_bytes(s->dtype);
-    for (int i = 0; i < 2; ++i) {
-        HeadTensor &h = a.t[i];
-        h.heads = (int)(i ? s->Hk : s->Hq);
-        h.w = i ? s->wk : s->wq;
-        h.at_once = std::max(1, std::min(h.heads, groups));
-        h.tokens = groups / h.at_once;
-        h.chunks = (unsigned)((h.heads + un * h.at_once - 1) / (un * h.at_once));
-        h.items = (unsigned)(((int64_t)a.all + h.tokens - 1) / h.tokens) * h.chunks;
-    }
     return a;
 }
 
-unsigned warps_ctas(unsigned items) { return items / kWarps + (items % kWarps > 0); }
-
-// Two CTAs to an SM stay (their sums do), in proportion to the tensors' elements.
-void backward_grid(HeadArgs &a, unsigned &grid) {
-    const double q = (double)a.t[0].heads, k = (double)a.t[1].heads;
-    const unsigned most = 2 * kSms;
-    unsigned n[2] = {(unsigned)(most * q / (q + k) + 0.5), 0};
-    if (k > 0) n[0] = std::min(n[0], most - 1);
-    if (q > 0) n[0] = std::max(n[0], 1u);
-    n[1] = most - n[0];
-    for (int i = 0; i < 2; ++i) n[i] = std::min(n[i], warps_ctas(a.t[i].items));
-    a.q_ctas = n[0];
-    grid = n[0] + n[1];
+constexpr int64_t kWaves = 2;
+// For tokens of up to `heads` heads. Few tokens: a warp takes a part of a token's heads only.
+HeadWalk walk(const HeadArgs &a, int64_t heads, bool split) {
+    HeadWalk w{};
+    const int groups = 32 / a.lanes;
+    w.at_once = (int)std::max<int64_t>(1, std::min<int64_t>(heads, groups));
+    w.tokens = groups / w.at_once;
+    w.splits = 1;
+    const int64_t warps = heads ? ((int64_t)a.all + w.tokens - 1) / w.tokens : 0;
+    if (split && warps)
+        w.splits = (unsigned)std::max<int64_t>(
+            1, std::min<int64_t>((heads + w.at_once - 1) / w.at_once, kWaves * kCtas * kWarps / warps));
+    w.items = (unsigned)(warps * w.splits);
+    return w;
 }
 
-template <template <typename, bool> class K>
-cudaError_t launch_heads(const spmm_heads_shape *s, const HeadArgs &a, unsigned grid,
-                         cudaStream_t cs) {
-    if (s->dtype == SPMM_F32)
-        s->interleaved ? K<float, true>::go(a, grid, cs) : K<float, false>::go(a, grid, cs);
-    else if (s->dtype == SPMM_BF16)
-        s->interleaved ? K<__nv_bfloat16, true>::go(a, grid, cs)
-                       : K<__nv_bfloat16, false>::go(a, grid, cs);
-    else
-        s->interleaved ? K<__half, true>::go(a, grid, cs) : K<__half, false>::go(a, grid, cs);
+HeadArgs forward_args(const spmm_heads_shape *s, const spmm_rows &q, const spmm_rows &k, void *q_out,
+                      void *k_out) {
+    HeadArgs a = shared_args(s);
+    a.from[0] = from(q, s->Hq, s->wq);
+    a.from[1] = from(k, s->Hk, s->wk);
+    a.to[0] = contiguous(q_out, s->Hq, s);
+    a.to[1] = contiguous(k_out, s->Hk, s);
+    a.walk[0] = walk(a, std::max(s->Hq, s->Hk), true);
+    return a;
+}
+
+// Three CTAs to an SM, which stay, in proportion to the tensors' elements.
+HeadArgs backward_args(const spmm_heads_shape *s, unsigned &grid) {
+    HeadArgs a = shared_args(s);
+    const double q = (double)s->Hq, k = (double)s->Hk;
+    unsigned n[2] = {(unsigned)(kCtas * q / (q + k) + 0.5), 0};
+    if (k > 0) n[0] = std::min<unsigned>(n[0], kCtas - 1);
+    if (q > 0) n[0] = std::max(n[0], 1u);
+    n[1] = kCtas - n[0];
+    for (int i = 0; i < 2; ++i) {
+        a.walk[i] = walk(a, i ? s->Hk : s->Hq, false);
+        n[i] = std::min(n[i], warps_ctas(a.walk[i].items));
+    }
+    a.q_ctas = n[0];
+    grid = n[0] + n[1];
+    return a;
+}
+
+// f(element, std::bool_constant: interleaved) for the call's.
+template <typename F> cudaError_t by_kind(const spmm_heads_shape *s, F f) {
+    auto type = [&](auto inter) {
+        if (s->dtype == SPMM_F32) return f(float{}, inter);
+        if (s->dtype == SPMM_BF16) return f(__nv_bfloat16{}, inter);
+        return f(__half{}, inter);
+    };
+    return s->interleaved ? type(std::true_type{}) : type(std::false_type{});
+}
+
+template <typename K>
+cudaError_t launch(K kernel, const HeadArgs &a, unsigned grid, cudaStream_t cs) {
+    kernel<<<grid, kThreads, 0, cs>>>(a);
     count_launch();
     return cudaGetLastError();
 }
-template <typename T, bool INTER> struct Rotate {
-    static void go(const HeadArgs &a, unsigned grid, cudaStream_t cs) {
-        k_heads_rotate<T, INTER, kForwardRows / (int)sizeof(T)><<<grid, kThreads, 0, cs>>>(a);
-    }
-};
-template <typename T, bool INTER> struct Backward {
-    static void go(const HeadArgs &a, unsigned grid, cudaStream_t cs) {
-        k_heads_backward<T, INTER, kBackwardRows / (int)sizeof(T)><<<grid, kThreads, 0, cs>>>(a);
-    }
-};
 
-cudaError_t rotate(const spmm_heads_shape *s, HeadArgs &a, void *stream) {
-    a.q_ctas = warps_ctas(a.t[0].items);
-    return launch_heads<Rotate>(s, a, a.q_ctas + warps_ctas(a.t[1].items), (cudaStream_t)stream);
+cudaError_t rotate(const spmm_heads_shape *s, const HeadArgs &a, cudaStream_t cs) {
+    return by_kind(s, [&](auto t, auto inter) {
+        using T = decltype(t);
+        return launch(k_heads_rotate<T, decltype(inter)::value>, a, warps_ctas(a.walk[0].items), cs);
+    });
 }
 
 bool written_ok(const spmm_rows &r, int64_t e, const spmm_heads_shape *s, int64_t Tk) {
@@ -567,12 +682,7 @@ spmm_status spmm_heads_rotate(const spmm_heads_shape *s, spmm_rows q, spmm_rows 
     const int e = dtype_bytes(s->dtype);
     if (s->Hq && (!rows_ok(q, e) || !q_out || (uintptr_t)q_out % 16)) return SPMM_ERR_INVALID_ARG;
     if (s->Hk && (!rows_ok(k, e) || !k_out || (uintptr_t)k_out % 16)) return SPMM_ERR_INVALID_ARG;
-    HeadArgs a = heads_args(s, kForwardRows);
-    set_rows(a.t[0].x, a.t[0].sb, a.t[0].st, a.t[0].sh, q);
-    set_rows(a.t[1].x, a.t[1].sb, a.t[1].st, a.t[1].sh, k);
-    contiguous_out(a.t[0], q_out, s);
-    contiguous_out(a.t[1], k_out, s);
-    return cuda_status(rotate(s, a, stream));
+    return cuda_status(rotate(s, forward_args(s, q, k, q_out, k_out), (cudaStream_t)stream));
 }
 
 spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
@@ -589,25 +699,19 @@ spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows 
     if (!rows_ok(k, e) || !rows_ok(v, e)) return SPMM_ERR_INVALID_ARG;
     if (Tk && (!written_ok(cache_k, e, s, Tk) || !written_ok(cache_v, e, s, Tk)))
         return SPMM_ERR_INVALID_ARG;
-    HeadArgs a = heads_args(s, kForwardRows);
-    set_rows(a.t[0].x, a.t[0].sb, a.t[0].st, a.t[0].sh, q);
-    set_rows(a.t[1].x, a.t[1].sb, a.t[1].st, a.t[1].sh, k);
-    contiguous_out(a.t[0], q_out, s);
-    set_rows(a.v, a.v_sb, a.v_st, a.v_sh, v);
+    HeadArgs a = forward_args(s, q, k, q_out, nullptr);
+    a.from[2] = from(v, s->Hk, nullptr);
+    a.to[1] = to(cache_k);
+    a.to[2] = to(cache_v);
     a.Tk = (int)Tk;
-    a.t[1].out = const_cast<void *>(cache_k.data);
-    a.t[1].o_sb = cache_k.sb, a.t[1].o_st = cache_k.st, a.t[1].o_sh = cache_k.sh;
-    a.v_out = const_cast<void *>(cache_v.data);
-    a.vo_sb = cache_v.sb, a.vo_st = cache_v.st, a.vo_sh = cache_v.sh;
-    return cuda_status(rotate(s, a, stream));
+    return cuda_status(rotate(s, a, (cudaStream_t)stream));
 }
 
 int64_t spmm_heads_backward_workspace(const spmm_heads_shape *s) {
     using namespace spmm;
     if (heads_check(s) != SPMM_OK || heads_empty(s) || (!s->wq && !s->wk)) return 0;
-    HeadArgs a = heads_args(s, kBackwardRows);
     unsigned grid;
-    backward_grid(a, grid);
+    backward_args(s, grid);
     return grid * s->D * (int64_t)sizeof(float);
 }
 
@@ -632,20 +736,23 @@ spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad
         return SPMM_ERR_INVALID_ARG;
     if (s->Hk && (!rows_ok(grad_k, e) || !dk || (uintptr_t)dk % 16 || (s->wk && !rows_ok(k, e))))
         return SPMM_ERR_INVALID_ARG;
-    const int64_t need = spmm_heads_backward_workspace(s);
-    if (need && (!work || work_bytes < need || (uintptr_t)work % 16)) return SPMM_ERR_INVALID_ARG;
-    HeadArgs a = heads_args(s, kBackwardRows);
-    set_rows(a.t[0].x, a.t[0].sb, a.t[0].st, a.t[0].sh, q);
-    set_rows(a.t[1].x, a.t[1].sb, a.t[1].st, a.t[1].sh, k);
-    set_rows(a.t[0].g, a.t[0].g_sb, a.t[0].g_st, a.t[0].g_sh, grad_q);
-    set_rows(a.t[1].g, a.t[1].g_sb, a.t[1].g_st, a.t[1].g_sh, grad_k);
-    contiguous_out(a.t[0], dq, s);
-    contiguous_out(a.t[1], dk, s);
-    a.parts = need ? (float *)work : nullptr;
     unsigned grid;
-    backward_grid(a, grid);
-    cudaError_t err = launch_heads<Backward>(s, a, grid, cs);
-    if (err == cudaSuccess && need) {
+    HeadArgs a = backward_args(s, grid);
+    const bool sums = s->wq || s->wk;
+    if (sums && (!work || work_bytes < grid * s->D * (int64_t)sizeof(float) || (uintptr_t)work % 16))
+        return SPMM_ERR_INVALID_ARG;
+    a.from[0] = from(grad_q, s->Hq, nullptr);
+    a.from[1] = from(grad_k, s->Hk, nullptr);
+    a.x[0] = from(q, s->Hq, s->wq);
+    a.x[1] = from(k, s->Hk, s->wk);
+    a.to[0] = contiguous(dq, s->Hq, s);
+    a.to[1] = contiguous(dk, s->Hk, s);
+    a.parts = (float *)work;
+    cudaError_t err = by_kind(s, [&](auto t, auto inter) {
+        using T = decltype(t);
+        return launch(k_heads_backward<T, decltype(inter)::value>, a, grid, cs);
+    });
+    if (err == cudaSuccess && sums) {
         k_heads_weights<<<dim3((unsigned)((s->D + 31) / 32), 2), 1024, 0, cs>>>(
             a.parts, (int)a.q_ctas, (int)grid, a.D, a.w32, s->dtype == SPMM_F16, s->wq ? dwq : nullptr,
             s->wk ? dwk : nullptr);
