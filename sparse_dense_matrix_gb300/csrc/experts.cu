@@ -687,9 +687,17 @@ cudaError_t launch(const ExpertArgs &p, int64_t most, cudaStream_t s) {
     using S = ExpertShape<NT, NC>;
     // the kernel's limit is the process's: always the largest, as another thread may set it
     static_assert(S::at_offsets + 1024 + 8 * (SPMM_ROUTES_MAX_EXPERTS + 1) <= kSmemMax, "fits");
-    cudaError_t e = cudaFuncSetAttribute(k_experts<T, NT, NC, A_MN, GRAD>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)S::bytes(SPMM_ROUTES_MAX_EXPERTS));
+    // (and once for each device)
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e == cudaSuccess && (dev > 63 || !(done.load(std::memory_order_relaxed) & bit))) {
+        e = cudaFuncSetAttribute(k_experts<T, NT, NC, A_MN, GRAD>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)S::bytes(SPMM_ROUTES_MAX_EXPERTS));
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c{};
     cudaLaunchAttribute attr{};

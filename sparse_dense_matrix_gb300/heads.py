@@ -17,8 +17,8 @@ import math
 import torch
 
 from . import _check, lib
-from .dynamic import (_DTYPE, _INT, _Rows, _dense, _elsewhere, _heads, _lent, _raw_stream,
-                      _scratch, _tensor)
+from .dynamic import (_DTYPE, _INT, _Rows, _dense, _elsewhere, _heads, _lent, _like, _raw_stream,
+                      _tensor)
 
 __all__ = ["HeadRotation"]
 
@@ -47,7 +47,19 @@ def _declare():
 
 
 _declare()
+_BYTES = {torch.float32: 4, torch.bfloat16: 2, torch.float16: 2}
 _NONE = _Rows(None, 0, 0, 0)
+_Tensor = torch.Tensor
+
+
+def _rows(t, name, dt, dev):
+    """``_heads`` for a tensor of one type, on one device; the usual case at half the time."""
+    if type(t) is _Tensor and t.dtype is dt and t.device == dev and t.dim() == 4:
+        sb, st, sh, sd = t.stride()
+        at = t.data_ptr()
+        if sd == 1 and not ((sb | st | sh) * _BYTES[dt] | at) % 16:
+            return _Rows(at, sb, st, sh)
+    return _heads(t, name, (dt,), dev)
 
 
 def _frequencies(R, base, scaling):
@@ -155,6 +167,8 @@ class HeadRotation:
             self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
             self.device = self.turns.device
             self._stream = _raw_stream(self.device.index)
+        self._turns = self.turns.data_ptr() or None
+        self._interleaved = 1 if layout == "interleaved" else 0
 
     def _on_stream(self):
         """The current stream, which the frequencies are now used on."""
@@ -166,7 +180,10 @@ class HeadRotation:
     def _weight(self, w, name, dtype):
         if w is None:
             return None, None
-        _dense(w, name, (dtype, torch.float32), (self.dim,), self.device)
+        dt = w.dtype if type(w) is _Tensor else None
+        if not (dt is dtype or dt is torch.float32) or w.shape != (self.dim,) or \
+                w.device != self.device or not w.is_contiguous():
+            _dense(w, name, (dtype, torch.float32), (self.dim,), self.device)
         at = w.data_ptr()
         if at % 16:
             raise ValueError(f"{name} must start at a 16-byte boundary")
@@ -175,13 +192,14 @@ class HeadRotation:
     def _problem(self, q, k, positions, lengths, q_weight, k_weight, eps):
         """The call's shape, and the rows of q and k."""
         dev = self.device
-        rows = _heads(q, "q", _DTYPE, dev)
+        dtype = getattr(q, "dtype", None)
+        rows = _rows(q, "q", dtype, dev) if dtype in _DTYPE else _heads(q, "q", _DTYPE, dev)
         B, T, Hq, D = q.shape
         Hk, krows = 0, _NONE
         if k is not None:
-            krows = _heads(k, "k", (q.dtype,), dev)
-            Hk = k.shape[2]
-            if k.shape[0] != B or k.shape[1] != T or k.shape[3] != D:
+            krows = _rows(k, "k", dtype, dev)
+            Bk, Tk, Hk, Dk = k.shape
+            if Bk != B or Tk != T or Dk != D:
                 raise ValueError(f"k must be [{B}, {T}, heads, {D}], got {list(k.shape)}")
         elif k_weight is not None:
             raise ValueError("k_weight is given without k")
@@ -192,7 +210,7 @@ class HeadRotation:
         if positions is not None:
             if lengths is not None:
                 raise ValueError("give positions or lengths, not both")
-            if not isinstance(positions, torch.Tensor):
+            if not isinstance(positions, _Tensor):
                 raise TypeError("positions must be a torch.Tensor")
             _tensor(positions, "positions", _INT, 1 if positions.dim() == 1 else 2, dev)
             if positions.shape != (T,) and positions.shape != (B, T):
@@ -203,15 +221,16 @@ class HeadRotation:
             at = positions.data_ptr() or None
         elif lengths is not None:
             lat = _dense(lengths, "lengths", _INT, (B,), dev).data_ptr() or None
-        wq, tq = self._weight(q_weight, "q_weight", q.dtype)
-        wk, tk = self._weight(k_weight, "k_weight", q.dtype)
-        if tq is not None and tk is not None and tq != tk:
-            raise TypeError(f"q_weight and k_weight must have one type, got {tq} and {tk}")
-        dt = _DTYPE[q.dtype]
-        wt = tq or tk
-        return _HeadsShape(B, T, Hq, Hk, D, self.rotary_dim, dt, dt if wt is None else _DTYPE[wt],
-                           1 if self.layout == "interleaved" else 0, eps, self.magnitude,
-                           self.turns.data_ptr() or None, at, sb, st, lat, wq, wk), rows, krows
+        dt = wt = _DTYPE[dtype]
+        wq = wk = None
+        if q_weight is not None or k_weight is not None:
+            wq, tq = self._weight(q_weight, "q_weight", dtype)
+            wk, tk = self._weight(k_weight, "k_weight", dtype)
+            if tq is not tk and tq is not None and tk is not None:
+                raise TypeError(f"q_weight and k_weight must have one type, got {tq} and {tk}")
+            wt = _DTYPE[tq or tk]
+        return _HeadsShape(B, T, Hq, Hk, D, self.rotary_dim, dt, wt, self._interleaved, eps,
+                           self.magnitude, self._turns, at, sb, st, lat, wq, wk), rows, krows
 
     def rotate(self, q, k=None, positions=None, lengths=None, q_weight=None, k_weight=None,
                eps: float = 1e-6, stream=None):
@@ -223,8 +242,8 @@ class HeadRotation:
                 _lent(self.device, q, k, positions, lengths, q_weight, k_weight)
                 return got
         s, rows, krows = self._problem(q, k, positions, lengths, q_weight, k_weight, eps)
-        q2 = q.new_empty(q.shape)
-        k2 = None if k is None else k.new_empty(k.shape)
+        q2 = _like(q)
+        k2 = None if k is None else _like(k)
         st = lib.spmm_heads_rotate(s, rows, krows, q2.data_ptr(),
                                    None if k2 is None else k2.data_ptr(), self._on_stream())
         if st:
@@ -245,27 +264,38 @@ class HeadRotation:
                 got = self.append(q, k, v, cache_k, cache_v, lengths, q_weight, k_weight, eps)
                 _lent(self.device, q, k, v, cache_k, cache_v, lengths, q_weight, k_weight)
                 return got
-        dev, dt = self.device, (q.dtype,)
         if k is None or lengths is None:
             raise ValueError("append needs k and lengths")
         s, rows, krows = self._problem(q, k, None, lengths, q_weight, k_weight, eps)
-        vrows = _heads(v, "v", dt, dev)
-        if v.shape != k.shape:
-            raise ValueError(f"v must be {list(k.shape)}, got {list(v.shape)}")
-        ck, cv = _heads(cache_k, "cache_k", dt, dev), _heads(cache_v, "cache_v", dt, dev)
-        B, Tk, Hk, D = cache_k.shape
-        if (B, Hk, D) != (s.B, s.Hk, s.D) or cache_v.shape != cache_k.shape:
+        dev, dt, shape = self.device, q.dtype, k.shape
+        vrows = _rows(v, "v", dt, dev)
+        if v.shape != shape:
+            raise ValueError(f"v must be {list(shape)}, got {list(v.shape)}")
+        ck, cv = _rows(cache_k, "cache_k", dt, dev), _rows(cache_v, "cache_v", dt, dev)
+        want = cache_k.shape
+        B, Tk, Hk, D = want
+        if cache_v.shape != want or (B, Hk, D) != (shape[0], shape[2], shape[3]):
             raise ValueError(f"cache_k and cache_v must be [{s.B}, rows, {s.Hk}, {s.D}], got "
-                             f"{list(cache_k.shape)} and {list(cache_v.shape)}")
+                             f"{list(want)} and {list(cache_v.shape)}")
         for c, name in ((cache_k, "cache_k"), (cache_v, "cache_v")):
-            if any(n > 1 and x == 0 for n, x in zip(c.shape, c.stride())):
-                raise ValueError(f"{name} has rows that share memory (strides {c.stride()})")
-        q2 = q.new_empty(q.shape)
+            strides = c.stride()
+            if 0 in strides and any(n > 1 and x == 0 for n, x in zip(want, strides)):
+                raise ValueError(f"{name} has rows that share memory (strides {strides})")
+        q2 = _like(q)
         st = lib.spmm_heads_append(s, rows, krows, vrows, q2.data_ptr(), ck, cv, Tk,
                                    self._on_stream())
         if st:
             _check(st, "spmm_heads_append")
         return q2
+
+    def _input(self, x, grad, name):
+        """The rows of the forward's input for its weight's gradient."""
+        if x is None:
+            raise ValueError(f"the gradient of {name}_weight needs {name}")
+        rows = _rows(x, name, grad.dtype, self.device)
+        if x.shape != grad.shape:
+            raise ValueError(f"{name} must be {list(grad.shape)}, got {list(x.shape)}")
+        return rows
 
     def rotate_backward(self, grad_q, grad_k, q=None, k=None, positions=None, lengths=None,
                         q_weight=None, k_weight=None, eps: float = 1e-6, stream=None):
@@ -280,26 +310,25 @@ class HeadRotation:
                 _lent(self.device, grad_q, grad_k, q, k, positions, lengths, q_weight, k_weight)
                 return grads
         s, gq, gk = self._problem(grad_q, grad_k, positions, lengths, q_weight, k_weight, eps)
-        dt, dev = (grad_q.dtype,), self.device
-        rows = []
-        for x, w, g, name in ((q, q_weight, grad_q, "q"), (k, k_weight, grad_k, "k")):
-            if w is None:
-                rows.append(_NONE)
-                continue
-            if x is None:
-                raise ValueError(f"the gradient of {name}_weight needs {name}")
-            rows.append(_heads(x, name, dt, dev))
-            if x.shape != g.shape:
-                raise ValueError(f"{name} must be {list(g.shape)}, got {list(x.shape)}")
-        dq = grad_q.new_empty(grad_q.shape)
-        dk = None if grad_k is None else grad_k.new_empty(grad_k.shape)
-        dwq = None if q_weight is None else torch.empty_like(q_weight)
-        dwk = None if k_weight is None else torch.empty_like(k_weight)
-        need = lib.spmm_heads_backward_workspace(s)
-        work = _scratch(grad_q, need)
+        xq = xk = _NONE
+        dk = dwq = dwk = work = None
+        need = 0
+        if q_weight is not None:
+            xq = self._input(q, grad_q, "q")
+            dwq = torch.empty_like(q_weight)
+        if k_weight is not None:
+            xk = self._input(k, grad_k, "k")
+            dwk = torch.empty_like(k_weight)
+        dq = _like(grad_q)
+        if grad_k is not None:
+            dk = _like(grad_k)
+        if dwq is not None or dwk is not None:
+            need = lib.spmm_heads_backward_workspace(s)
+            work = torch.empty(need, dtype=torch.uint8, device=self.device)
         st = lib.spmm_heads_rotate_backward(
-            s, gq, gk, *rows, *(None if t is None else t.data_ptr()
-                                for t in (dq, dk, dwq, dwk, work)), need, self._on_stream())
+            s, gq, gk, xq, xk, dq.data_ptr(), None if dk is None else dk.data_ptr(),
+            None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(),
+            None if work is None else work.data_ptr(), need, self._on_stream())
         if st:
             _check(st, "spmm_heads_rotate_backward")
         return dq, dk, dwq, dwk
