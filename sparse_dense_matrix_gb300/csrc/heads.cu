@@ -51,10 +51,9 @@ struct HeadArgs {
     HeadFrom from[3];                // queries, keys, values (append); backward: the gradients
     HeadTo to[3];
     HeadFrom x[2];                   // backward: queries, keys
-    HeadWalk walk[2];                // forward: the first; backward: queries', keys'
+    HeadWalk walk;
     int Tk;                          // rows of the caches that k and v go to, or -1
-    unsigned q_ctas;                 // backward: the first CTAs are the queries'
-    float *parts;                    // backward: [CTAs][D] parts of the weights' gradients
+    float *parts;                    // backward: [CTAs][2][D] parts of the weights' gradients
 };
 
 // Two floats to an instruction: the arithmetic of a row would else take longer to issue
@@ -260,6 +259,18 @@ __device__ __forceinline__ void turn_back(F2 (&z)[4], const F2 (&c)[2], const F2
     }
 }
 
+// Two sums over the lanes of a row (LANES: their number, where it is a constant).
+template <int LANES> __device__ __forceinline__ void row_sums(float &x, float &y, int lanes) {
+    const int n = LANES ? LANES : lanes;
+#pragma unroll
+    for (int d = 1; d < (LANES ? LANES : 32); d <<= 1) {
+        if (!LANES && d >= n) break;
+        const float u = __shfl_xor_sync(0xffffffffu, x, d), v = __shfl_xor_sync(0xffffffffu, y, d);
+        x += u;
+        y += v;
+    }
+}
+
 // The lane's part of a weight; 1 without one.
 template <typename T>
 __device__ __forceinline__ void load_weight(const HeadArgs &a, const HeadLane &l, const void *w,
@@ -280,10 +291,9 @@ __device__ __forceinline__ void load_weight(const HeadArgs &a, const HeadLane &l
 
 // Rows asked for ahead of the work, of a lane.
 template <typename T> constexpr int kForwardRows = 8 / (int)sizeof(T);
-template <typename T> constexpr int kBackwardRows = 4 / (int)sizeof(T);
 
 // Heads split * at_once + first of a token, then splits * at_once further. COPY: as they are.
-template <typename T, bool INTER, bool COPY>
+template <typename T, bool INTER, int LANES, bool COPY>
 __device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadWalk &w,
                                               const HeadLane &l, const HeadPlace &at, int split,
                                               const HeadFrom &h, const HeadTo &o, int64_t row,
@@ -339,12 +349,7 @@ __device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadWalk 
                         const float2 t = both(sq);
                         sum[v] = t.x + t.y;
                     }
-                    for (int d = 1; d < a.lanes; d <<= 1) {
-                        const float s0 = __shfl_xor_sync(0xffffffffu, sum[0], d);
-                        const float s1 = __shfl_xor_sync(0xffffffffu, sum[1], d);
-                        sum[0] += s0;
-                        sum[1] += s1;
-                    }
+                    row_sums<LANES>(sum[0], sum[1], a.lanes);
 #pragma unroll
                     for (int v = 0; v < 2; ++v) {
                         const float r = rsqrtf(fmaf(sum[v], a.inv_D, a.eps));
@@ -378,11 +383,11 @@ __device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadWalk 
 }
 
 // A warp takes a token's queries, keys and (append) values, or every splits-th of their rows.
-template <typename T, bool INTER>
+template <typename T, bool INTER, int LANES>
 __global__ void __launch_bounds__(kThreads, 3) k_heads_rotate(const __grid_constant__ HeadArgs a) {
     __shared__ HeadAngles told[kWarps];
     const HeadLane l(a, INTER);
-    const HeadWalk &w = a.walk[0];
+    const HeadWalk &w = a.walk;
     const int warp = threadIdx.x / 32;
     const unsigned item = blockIdx.x * kWarps + warp;
     if (item >= w.items) return;
@@ -391,142 +396,169 @@ __global__ void __launch_bounds__(kThreads, 3) k_heads_rotate(const __grid_const
     angles(a, w, at.pos, told[warp]);
     const bool cached = a.Tk >= 0, put = !cached || (at.pos >= 0 && at.pos < a.Tk);
     const int64_t row = cached ? at.pos : at.t;
-    forward_heads<T, INTER, false>(a, w, l, at, split, a.from[0], a.to[0], at.t, true, &told[warp]);
-    forward_heads<T, INTER, false>(a, w, l, at, split, a.from[1], a.to[1], row, put, &told[warp]);
+    forward_heads<T, INTER, LANES, false>(a, w, l, at, split, a.from[0], a.to[0], at.t, true, &told[warp]);
+    forward_heads<T, INTER, LANES, false>(a, w, l, at, split, a.from[1], a.to[1], row, put, &told[warp]);
     if (cached)
-        forward_heads<T, INTER, true>(a, w, l, at, split, a.from[2], a.to[2], row, put, nullptr);
+        forward_heads<T, INTER, LANES, true>(a, w, l, at, split, a.from[2], a.to[2], row, put, nullptr);
+}
+
+// The same heads' gradients; dw: the lane's part of the weight's, added to.
+template <typename T, bool INTER, int LANES>
+__device__ __forceinline__ void backward_heads(const HeadArgs &a, const HeadWalk &w,
+                                               const HeadLane &l, const HeadPlace &at, int split,
+                                               const HeadFrom &g, const HeadFrom &x,
+                                               const HeadTo &o, const HeadAngles &told,
+                                               F2 (&dw)[4]) {
+    const int step = (int)w.splits * w.at_once;
+    const int left = g.heads - split * w.at_once, n = left > 0 ? (left + step - 1) / step : 0;
+    if (n == 0) return;
+    const bool norm = x.w != nullptr;
+    const int off = l.hi - l.lo;
+    const int64_t g_step = step * g.sh, x_step = step * x.sh, o_step = step * o.sh;
+    int head = split * w.at_once + at.first;
+    const T *gs = (const T *)g.x + at.b * g.sb + at.t * g.st + head * g.sh + l.lo;
+    const T *xs = (const T *)x.x + at.b * x.sb + at.t * x.st + head * x.sh + l.lo;
+    T *to = (T *)o.out + at.b * o.sb + at.t * o.st + head * o.sh + l.lo;
+    Raw<T> rg[2], rx[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        rg[u].zero();
+        rx[u].zero();
+        const bool live = at.live && head + u * step < g.heads;
+        if (live) rg[u].load(gs, gs + off);
+        if (live && norm) rx[u].load(xs, xs + off);
+        gs += g_step;
+        xs += x_step;
+    }
+    F2 c[2], s[2], weight[4];
+    load_weight<T>(a, l, x.w, weight);
+    take_angles(a, w, l, told, c, s);
+    for (int i = 0; i < n; i += 2) {
+        F2 y[2][4], z[2][4];
+        bool live[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            live[u] = at.live && head + u * step < g.heads;
+            rg[u].get(y[u]);
+            rx[u].get(z[u]);
+            if (at.live && head + (u + 2) * step < g.heads) {
+                rg[u].load(gs, gs + off);
+                if (norm) rx[u].load(xs, xs + off);
+            }
+            gs += g_step;
+            xs += x_step;
+        }
+        if (l.turned) {
+            turn_back<INTER>(y[0], c, s);
+            turn_back<INTER>(y[1], c, s);
+        }
+        if (norm) {
+            float sum[2], dot[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                F2 sq = mul2(z[u][0], z[u][0]);
+                F2 dots = mul2(mul2(y[u][0], weight[0]), z[u][0]);
+#pragma unroll
+                for (int j = 1; j < 4; ++j) {
+                    sq = fma2(z[u][j], z[u][j], sq);
+                    dots = fma2(mul2(y[u][j], weight[j]), z[u][j], dots);
+                }
+                float2 v = both(sq);
+                sum[u] = v.x + v.y;
+                v = both(dots);
+                dot[u] = v.x + v.y;
+            }
+            row_sums<LANES>(sum[0], sum[1], a.lanes);
+            row_sums<LANES>(dot[0], dot[1], a.lanes);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float q = rsqrtf(fmaf(sum[u], a.inv_D, a.eps));
+                const float m = -dot[u] * q * a.inv_D;     // -mean(u n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const F2 nj = mul2(z[u][j], two(q, q));
+                    if (live[u]) dw[j] = fma2(y[u][j], nj, dw[j]);
+                    y[u][j] = mul2(two(q, q), fma2(nj, two(m, m), mul2(y[u][j], weight[j])));
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            Raw<T> r;
+            r.set(y[u]);
+            if (live[u]) r.store(to, to + off);
+            to += o_step;
+        }
+        head += 2 * step;
+    }
 }
 
 // The weights' gradients: a lane's sums over its rows, then over the rows of the
 // warp, the warps of the CTA and, by a second kernel, the CTAs, each in a fixed order.
-template <typename T, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3)
+template <typename T, bool INTER, int LANES>
+__global__ void __launch_bounds__(kThreads, 2)
     k_heads_backward(const __grid_constant__ HeadArgs a) {
     __shared__ HeadAngles told[kWarps];
-    constexpr int AHEAD = kBackwardRows<T>;
     const HeadLane l(a, INTER);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, off = l.hi - l.lo;
-    const bool keys = blockIdx.x >= a.q_ctas;
-    const HeadWalk &w = a.walk[keys];
-    const HeadFrom &g = a.from[keys], &x = a.x[keys];
-    const HeadTo &o = a.to[keys];
-    const bool norm = x.w != nullptr;
-    const unsigned ctas = keys ? gridDim.x - a.q_ctas : a.q_ctas;
-    const int n = (g.heads + w.at_once - 1) / w.at_once;
-    const int64_t g_step = w.at_once * g.sh, x_step = w.at_once * x.sh, o_step = w.at_once * o.sh;
-    F2 weight[4], dw[4];
-    load_weight<T>(a, l, x.w, weight);
+    const HeadWalk &w = a.walk;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    F2 dwq[4], dwk[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dw[i] = two(0.0f, 0.0f);
-    for (unsigned item = (blockIdx.x - (keys ? a.q_ctas : 0)) * kWarps + warp; item < w.items;
-         item += ctas * kWarps) {
+    for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = two(0.0f, 0.0f);
+    for (unsigned item = blockIdx.x * kWarps + warp; item < w.items; item += gridDim.x * kWarps) {
+        const int split = w.splits == 1 ? 0 : (int)(item % w.splits);
         const HeadPlace at(a, w, l, item);
-        int head = at.first;
-        const T *gs = (const T *)g.x + at.b * g.sb + at.t * g.st + head * g.sh + l.lo;
-        const T *xs = (const T *)x.x + at.b * x.sb + at.t * x.st + head * x.sh + l.lo;
-        T *to = (T *)o.out + at.b * o.sb + at.t * o.st + head * o.sh + l.lo;
-        Raw<T> rg[AHEAD], rx[AHEAD];
-#pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-            rg[u].zero();
-            rx[u].zero();
-            const bool live = at.live && head + u * w.at_once < g.heads;
-            if (live) rg[u].load(gs, gs + off);
-            if (live && norm) rx[u].load(xs, xs + off);
-            gs += g_step;
-            xs += x_step;
-        }
-        F2 c[2], s[2];
         __syncwarp();                            // (the angles before are read)
         angles(a, w, at.pos, told[warp]);
-        take_angles(a, w, l, told[warp], c, s);
-        for (int i = 0; i < n; i += AHEAD) {
+        backward_heads<T, INTER, LANES>(a, w, l, at, split, a.from[0], a.x[0], a.to[0], told[warp],
+                                        dwq);
+        backward_heads<T, INTER, LANES>(a, w, l, at, split, a.from[1], a.x[1], a.to[1], told[warp],
+                                        dwk);
+    }
+    if (!a.parts) return;
+    float *sums = reinterpret_cast<float *>(told);         // [kWarps][256]
+    auto total = [&](const F2 (&dw)[4], float *out) {
+        __syncthreads();
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                if (i + u >= n) break;
-                const bool live = at.live && head < g.heads;
-                F2 y[4], z[4];
-                rg[u].get(y);
-                rx[u].get(z);
-                if (at.live && head + AHEAD * w.at_once < g.heads) {
-                    rg[u].load(gs, gs + off);
-                    if (norm) rx[u].load(xs, xs + off);
-                }
-                gs += g_step;
-                xs += x_step;
-                if (l.turned) turn_back<INTER>(y, c, s);
-                if (norm) {
-                    F2 sq = mul2(z[0], z[0]), dots = mul2(mul2(y[0], weight[0]), z[0]);
-#pragma unroll
-                    for (int j = 1; j < 4; ++j) {
-                        sq = fma2(z[j], z[j], sq);
-                        dots = fma2(mul2(y[j], weight[j]), z[j], dots);
-                    }
-                    float2 v = both(sq);
-                    float sum = v.x + v.y;
-                    v = both(dots);
-                    float dot = v.x + v.y;
-                    for (int d = 1; d < a.lanes; d <<= 1) {
-                        const float s0 = __shfl_xor_sync(0xffffffffu, sum, d);
-                        const float s1 = __shfl_xor_sync(0xffffffffu, dot, d);
-                        sum += s0;
-                        dot += s1;
-                    }
-                    const float q = rsqrtf(fmaf(sum, a.inv_D, a.eps));
-                    const float m = -dot * q * a.inv_D;    // -mean(u n)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const F2 nj = mul2(z[j], two(q, q));
-                        if (live) dw[j] = fma2(y[j], nj, dw[j]);
-                        y[j] = mul2(two(q, q), fma2(nj, two(m, m), mul2(y[j], weight[j])));
-                    }
-                }
-                Raw<T> r;
-                r.set(y);
-                if (live) r.store(to, to + off);
-                to += o_step;
-                head += w.at_once;
+        for (int i = 0; i < 4; ++i) {
+            float2 v = both(dw[i]);
+            for (int j = a.lanes; j < 32; j <<= 1) {
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, j);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, j);
+            }
+            if (lane < a.lanes && l.live) {
+                const int j = warp * 256 + (i < 2 ? l.lo : l.hi) + 2 * (i & 1);
+                sums[j] = v.x;
+                sums[j + 1] = v.y;
             }
         }
-    }
-    if (!norm) return;
-    __syncthreads();
-    float *sums = reinterpret_cast<float *>(told);         // [kWarps][256]
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float2 v = both(dw[i]);
-        for (int j = a.lanes; j < 32; j <<= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, j);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, j);
+        __syncthreads();
+        if ((int)threadIdx.x < a.D) {
+            float v = 0.0f;
+            for (int i = 0; i < kWarps; ++i) v += sums[i * 256 + threadIdx.x];
+            out[threadIdx.x] = v;
         }
-        if (lane < a.lanes && l.live) {
-            const int j = warp * 256 + (i < 2 ? l.lo : l.hi) + 2 * (i & 1);
-            sums[j] = v.x;
-            sums[j + 1] = v.y;
-        }
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < a.D) {
-        float v = 0.0f;
-        for (int i = 0; i < kWarps; ++i) v += sums[i * 256 + threadIdx.x];
-        a.parts[(int64_t)blockIdx.x * a.D + threadIdx.x] = v;
-    }
+    };
+    float *out = a.parts + (int64_t)blockIdx.x * 2 * a.D;
+    if (a.x[0].w) total(dwq, out);
+    if (a.x[1].w) total(dwk, out + a.D);
 }
 
-// A weight's gradient is the sum of its tensor's CTAs' parts: 32 columns a CTA, its warps
-// in turn over the parts; CTAs y = 0 for the queries', 1 for the keys'.
-__global__ void __launch_bounds__(1024) k_heads_weights(const float *parts, int q_ctas, int ctas,
-                                                        int D, int w32, int half, void *dwq,
-                                                        void *dwk) {
+// A weight's gradient is the sum of the CTAs' parts: 32 columns a CTA, its warps in turn over
+// the parts; CTAs y = 0 for the queries', 1 for the keys'.
+__global__ void __launch_bounds__(1024) k_heads_weights(const float *parts, int n, int D, int w32,
+                                                        int half, void *dwq, void *dwk) {
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int j = blockIdx.x * 32 + lane;
     void *out = blockIdx.y ? dwk : dwq;
     if (!out) return;
-    const int end = blockIdx.y ? ctas : q_ctas;
     float x = 0.0f;
-    if (j < D)
-        for (int i = (blockIdx.y ? q_ctas : 0) + warp; i < end; i += 32) x += parts[(int64_t)i * D + j];
+    if (j < D) {
+        parts += blockIdx.y * D + j;
+#pragma unroll 8
+        for (int i = warp; i < n; i += 32) x += parts[(int64_t)i * 2 * D];
+    }
     sums[warp][lane] = x;
     __syncthreads();
     if (warp || j >= D) return;
@@ -596,14 +628,14 @@ HeadArgs shared_args(const spmm_heads_shape *s) {
 
 constexpr int64_t kWaves = 2;
 // For tokens of up to `heads` heads. Few tokens: a warp takes a part of a token's heads only.
-HeadWalk walk(const HeadArgs &a, int64_t heads, bool split) {
+HeadWalk walk(const HeadArgs &a, int64_t heads) {
     HeadWalk w{};
     const int groups = 32 / a.lanes;
     w.at_once = (int)std::max<int64_t>(1, std::min<int64_t>(heads, groups));
     w.tokens = groups / w.at_once;
     w.splits = 1;
     const int64_t warps = heads ? ((int64_t)a.all + w.tokens - 1) / w.tokens : 0;
-    if (split && warps)
+    if (warps)
         w.splits = (unsigned)std::max<int64_t>(
             1, std::min<int64_t>((heads + w.at_once - 1) / w.at_once, kWaves * kCtas * kWarps / warps));
     w.items = (unsigned)(warps * w.splits);
@@ -617,33 +649,33 @@ HeadArgs forward_args(const spmm_heads_shape *s, const spmm_rows &q, const spmm_
     a.from[1] = from(k, s->Hk, s->wk);
     a.to[0] = contiguous(q_out, s->Hq, s);
     a.to[1] = contiguous(k_out, s->Hk, s);
-    a.walk[0] = walk(a, std::max(s->Hq, s->Hk), true);
+    a.walk = walk(a, std::max(s->Hq, s->Hk));
     return a;
 }
 
-// Three CTAs to an SM, which stay, in proportion to the tensors' elements.
+// Backward: CTAs that each add up a part of the weights' gradients. (With two to an SM, which
+// stay for all tokens, a training step of 2 x 4096 took 82 us, with 8 times as many 66.)
+constexpr unsigned kParts = 16 * kSms;
 HeadArgs backward_args(const spmm_heads_shape *s, unsigned &grid) {
     HeadArgs a = shared_args(s);
-    const double q = (double)s->Hq, k = (double)s->Hk;
-    unsigned n[2] = {(unsigned)(kCtas * q / (q + k) + 0.5), 0};
-    if (k > 0) n[0] = std::min<unsigned>(n[0], kCtas - 1);
-    if (q > 0) n[0] = std::max(n[0], 1u);
-    n[1] = kCtas - n[0];
-    for (int i = 0; i < 2; ++i) {
-        a.walk[i] = walk(a, i ? s->Hk : s->Hq, false);
-        n[i] = std::min(n[i], warps_ctas(a.walk[i].items));
-    }
-    a.q_ctas = n[0];
-    grid = n[0] + n[1];
+    a.walk = walk(a, std::max(s->Hq, s->Hk));
+    grid = std::min(kParts, warps_ctas(a.walk.items));
     return a;
 }
 
-// f(element, std::bool_constant: interleaved) for the call's.
+// f(element, interleaved, lanes) for the call's: lanes of heads of 64 and 128, the widths that
+// the attention takes, are constants (two sums over 16 lanes then take 16 instructions,
+// with a loop 40, of some 110 that a row takes in all); those of other widths 0.
 template <typename F> cudaError_t by_kind(const spmm_heads_shape *s, F f) {
+    auto lanes = [&](auto t, auto inter) {
+        if (s->D == 64) return f(t, inter, std::integral_constant<int, 8>{});
+        if (s->D == 128) return f(t, inter, std::integral_constant<int, 16>{});
+        return f(t, inter, std::integral_constant<int, 0>{});
+    };
     auto type = [&](auto inter) {
-        if (s->dtype == SPMM_F32) return f(float{}, inter);
-        if (s->dtype == SPMM_BF16) return f(__nv_bfloat16{}, inter);
-        return f(__half{}, inter);
+        if (s->dtype == SPMM_F32) return lanes(float{}, inter);
+        if (s->dtype == SPMM_BF16) return lanes(__nv_bfloat16{}, inter);
+        return lanes(__half{}, inter);
     };
     return s->interleaved ? type(std::true_type{}) : type(std::false_type{});
 }
@@ -656,9 +688,9 @@ cudaError_t launch(K kernel, const HeadArgs &a, unsigned grid, cudaStream_t cs) 
 }
 
 cudaError_t rotate(const spmm_heads_shape *s, const HeadArgs &a, cudaStream_t cs) {
-    return by_kind(s, [&](auto t, auto inter) {
+    return by_kind(s, [&](auto t, auto inter, auto lanes) {
         using T = decltype(t);
-        return launch(k_heads_rotate<T, decltype(inter)::value>, a, warps_ctas(a.walk[0].items), cs);
+        return launch(k_heads_rotate<T, decltype(inter)::value, decltype(lanes)::value>, a, warps_ctas(a.walk.items), cs);
     });
 }
 
@@ -712,7 +744,7 @@ int64_t spmm_heads_backward_workspace(const spmm_heads_shape *s) {
     if (heads_check(s) != SPMM_OK || heads_empty(s) || (!s->wq && !s->wk)) return 0;
     unsigned grid;
     backward_args(s, grid);
-    return grid * s->D * (int64_t)sizeof(float);
+    return grid * 2 * s->D * (int64_t)sizeof(float);
 }
 
 spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad_q,
@@ -739,7 +771,7 @@ spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad
     unsigned grid;
     HeadArgs a = backward_args(s, grid);
     const bool sums = s->wq || s->wk;
-    if (sums && (!work || work_bytes < grid * s->D * (int64_t)sizeof(float) || (uintptr_t)work % 16))
+    if (sums && (!work || work_bytes < grid * 2 * s->D * (int64_t)sizeof(float) || (uintptr_t)work % 16))
         return SPMM_ERR_INVALID_ARG;
     a.from[0] = from(grad_q, s->Hq, nullptr);
     a.from[1] = from(grad_k, s->Hk, nullptr);
@@ -747,14 +779,15 @@ spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad
     a.x[1] = from(k, s->Hk, s->wk);
     a.to[0] = contiguous(dq, s->Hq, s);
     a.to[1] = contiguous(dk, s->Hk, s);
-    a.parts = (float *)work;
-    cudaError_t err = by_kind(s, [&](auto t, auto inter) {
+    a.parts = sums ? (float *)work : nullptr;
+    cudaError_t err = by_kind(s, [&](auto t, auto inter, auto lanes) {
         using T = decltype(t);
-        return launch(k_heads_backward<T, decltype(inter)::value>, a, grid, cs);
+        return launch(k_heads_backward<T, decltype(inter)::value, decltype(lanes)::value>, a, grid,
+                      cs);
     });
     if (err == cudaSuccess && sums) {
         k_heads_weights<<<dim3((unsigned)((s->D + 31) / 32), 2), 1024, 0, cs>>>(
-            a.parts, (int)a.q_ctas, (int)grid, a.D, a.w32, s->dtype == SPMM_F16, s->wq ? dwq : nullptr,
+            a.parts, (int)grid, a.D, a.w32, s->dtype == SPMM_F16, s->wq ? dwq : nullptr,
             s->wk ? dwk : nullptr);
         count_launch();
         err = cudaGetLastError();
