@@ -62,8 +62,8 @@ struct ExpertTile {
     int k;                           // length of k
 };
 
-// Shared memory's view of the experts: first slots, and (product) the tiles of slots before
-// each expert.
+// Shared memory's view of the experts: first slots, and the tiles of slots before each expert
+// (product) or the experts in order of their slots, most first (gradient).
 struct ExpertList {
     const int32_t *first, *before;
     template <bool GRAD>
@@ -77,7 +77,7 @@ struct ExpertList {
         x.m0 = t % p.tiles_m * (kRowsM * S::NC);
         const int u = t / p.tiles_m;
         if (GRAD) {
-            x.e = u / p.tiles_n;
+            x.e = before[u / p.tiles_n];
             x.n0 = u % p.tiles_n * NT;
             x.n = min(NT, p.N - x.n0);
             x.r0 = first[x.e];
@@ -125,7 +125,45 @@ __device__ __forceinline__ ExpertList expert_list(const ExpertArgs &p, int32_t *
             most = __shfl_sync(0xffffffffu, x, 31);
         }
         __syncwarp();
-        if (!GRAD) {
+        if (GRAD) {
+            // A counting sort by the slots' number, to two bits behind its first: tiles of
+            // like length follow one another, and CTAs that take them in turn, there and
+            // back, end at about the same time (65536 slots of 64 experts, most of which
+            // have between half and twice as many as the mean: 260 us without it, 190 with).
+            constexpr int kKeys = 128;
+            __shared__ int32_t keys[kKeys];
+            auto key = [&](int e) {
+                return kKeys - 1 - (__float_as_int((float)(first[e + 1] - first[e])) + 0x200000 -
+                                    __float_as_int(1.0f)) / 0x200000;
+            };
+            for (int i = threadIdx.x; i < kKeys; i += 32) keys[i] = 0;
+            __syncwarp();
+            for (int e = threadIdx.x; e < p.E; e += 32)
+                atomicAdd(&keys[min(max(key(e), 0), kKeys - 1)], 1);
+            __syncwarp();
+            for (int i0 = 0; i0 < kKeys; i0 += 32) {
+                const int mine = keys[i0 + threadIdx.x];
+                int x = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if ((int)threadIdx.x >= o) x += y;
+                }
+                keys[i0 + threadIdx.x] = sum + x - mine;
+                sum += __shfl_sync(0xffffffffu, x, 31);
+            }
+            __syncwarp();
+            for (int e0 = 0; e0 < p.E; e0 += 32) {
+                const int e = e0 + (int)threadIdx.x;
+                const int k = e < p.E ? min(max(key(e), 0), kKeys - 1) : kKeys;
+                const uint32_t same = __match_any_sync(0xffffffffu, k);
+                const int rank = __popc(same & ((1u << threadIdx.x) - 1));
+                if (e < p.E) before[keys[k] + rank] = e;
+                __syncwarp();
+                if (e < p.E && rank == 0) keys[k] += __popc(same);
+                __syncwarp();
+            }
+        } else {
             for (int e0 = 0; e0 <= p.E; e0 += 32) {
                 const int e = e0 + (int)threadIdx.x;
                 const int mine = e < p.E ? (first[e + 1] - first[e] + NT - 1) / NT : 0;
@@ -382,11 +420,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         if (lane == 0) {
             const int tiles = list.template tiles<GRAD>(p);
             ring.parity = 1;
-            for (int t = first_tile;; t += step) {
+            for (int turn = 0;; ++turn) {
                 if (!mbar_wait(&read[ring.at], ring.parity, p.err)) break;
-                const bool more = t < tiles;
-                if (more) tile_ring[ring.at] = list.template tile<S, GRAD>(p, t);
-                else tile_ring[ring.at].e = -1;
+                // there and back
+                const int t = turn * step + (turn & 1 ? step - 1 - first_tile : first_tile);
+                // (a turn that has none here may have been the last, or the one before it)
+                const bool more = turn * (int64_t)step < tiles;
+                ExpertTile &to = tile_ring[ring.at];
+                if (more && t < tiles) {
+                    to = list.template tile<S, GRAD>(p, t);
+                } else if (more) {
+                    continue;
+                } else {
+                    to.e = -1;
+                }
                 mbar_arrive(&listed[ring.at]);
                 ring.next();
                 if (!more) break;
@@ -582,37 +629,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             if (!warp_wait(&ready[acc], parity, p.err)) break;
             mma_fence_after();
             const uint32_t d = tmem + acc * NT + ((uint32_t)quarter << 21);
+            uint32_t v[2][16];
+            tmem_ld16x32(d, v[0]);
+            tmem_ld16x32(d + (16u << 16), v[1]);
             for (int c = 0; c < x.n; c += 32) {
-                uint32_t v[2][16];
-                tmem_ld16x32(d + c, v[0]);
-                tmem_ld16x32(d + (16u << 16) + c, v[1]);
                 tmem_wait_ld();
-                __syncwarp();                    // the rows before are written out
+                uint32_t y[2][8];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < 4; i += 2) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            y[j] = pack2<T>(__uint_as_float(v[h][4 * i + 2 * j]),
-                                            __uint_as_float(v[h][4 * i + 2 * j + 1]));
-                        stsm4_t(put + i * 8 * S::out_pitch + h * 32, y[0], y[1], y[2], y[3]);
+                    for (int i = 0; i < 8; ++i)
+                        y[h][i] = pack2<T>(__uint_as_float(v[h][2 * i]),
+                                           __uint_as_float(v[h][2 * i + 1]));
+                if (c + 32 < x.n) {              // on their way while these are written
+                    tmem_ld16x32(d + c + 32, v[0]);
+                    tmem_ld16x32(d + (16u << 16) + c + 32, v[1]);
+                } else {
+                    mma_fence_before();
+                    __syncwarp();
+                    // no memory is handed over (a release would wait for the stores)
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(&taken[acc]);
+                        else arrive_first_relaxed(&taken[acc]);
                     }
+                }
+                __syncwarp();                    // the rows before are read
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        stsm4_t(put + i * 8 * S::out_pitch + h * 32, y[h][2 * i], y[h][2 * i + 1],
+                                y[h][2 * i + 2], y[h][2 * i + 3]);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int n = c + i * 8 + (lane >> 2);
-                    const uint4 y = lds16(get + i * 8 * S::out_pitch);
-                    if (m < p.M && n < x.n) *(uint4 *)(out + n * p.o_ld) = y;
+                    const uint4 z = lds16(get + i * 8 * S::out_pitch);
+                    if (m < p.M && n < x.n) *(uint4 *)(out + n * p.o_ld) = z;
                 }
-            }
-            mma_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                // no memory is handed over (a release would wait for the stores above)
-                if (rank == 0) mbar_arrive(&taken[acc]);
-                else arrive_first_relaxed(&taken[acc]);
             }
             acc ^= 1;
             parity ^= acc == 0;
@@ -767,7 +821,7 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
         return cuda_status(cudaMemsetAsync(ys, 0, (size_t)P * F * 2, s));
     if (!aligned(xs) || !aligned(w) || !strides_ok(w_se, w_sh, w_sf)) return SPMM_ERR_INVALID_ARG;
     ExpertArgs p{};
-    if (strides_far(w_se, w_sh, w_sf) || (P / 64 + E) * ((F + kRowsM - 1) / kRowsM) > INT32_MAX)
+    if (strides_far(w_se, w_sh, w_sf) || (P / 64 + E) * ((F + kRowsM - 1) / kRowsM) > (1 << 30))
         return SPMM_ERR_UNSUPPORTED;
     p.offsets = offsets;
     p.out = ys;
@@ -779,10 +833,9 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
     p.a_step = E > 1 && w_se > 0;
     cudaError_t e = dynamic_err(s, &p.err);
     if (e == cudaSuccess)
-        e = few_slots(P, E)
-                ? product<64, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
-            : F > kRowsM ? product<256, 2>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
-                         : product<256, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s);
+        e = few_slots(P, E) ? product<64, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
+            : F > kRowsM    ? product<256, 2>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
+                            : product<256, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s);
     return cuda_status(e);
 }
 
@@ -801,7 +854,7 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
     ExpertArgs p{};
     p.M = (int)(by_f ? F : H);
     p.N = (int)(by_f ? H : F);
-    if (E * ((p.M + kRowsM - 1) / kRowsM) * ((p.N + 255) / 256) > INT32_MAX) return SPMM_ERR_UNSUPPORTED;
+    if (E * ((p.M + kRowsM - 1) / kRowsM) * ((p.N + 255) / 256) > (1 << 30)) return SPMM_ERR_UNSUPPORTED;
     p.offsets = offsets;
     p.out = dw;
     p.o_se = dw_se;

@@ -161,6 +161,7 @@ struct HeadAngles {
 __device__ __forceinline__ void angles(const HeadArgs &a, const HeadWalk &w, int64_t pos,
                                        HeadAngles &to) {
     const int pairs = a.R / 2, lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int i0 = 0; i0 < pairs * w.tokens; i0 += 32) {
         const int i = i0 + lane, token = w.tokens == 1 ? 0 : i / pairs;
         const int64_t p =
@@ -327,6 +328,7 @@ __device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadWalk 
             matrix<INTER>(c, s, weight, ma, mb);
         }
     }
+#pragma unroll 1
     for (int i = 0; i < n; i += AHEAD) {
 #pragma unroll
         for (int u = 0; u < AHEAD; u += 2) {
@@ -433,6 +435,7 @@ __device__ __forceinline__ void backward_heads(const HeadArgs &a, const HeadWalk
     F2 c[2], s[2], weight[4];
     load_weight<T>(a, l, x.w, weight);
     take_angles(a, w, l, told, c, s);
+#pragma unroll 1
     for (int i = 0; i < n; i += 2) {
         F2 y[2][4], z[2][4];
         bool live[2];
