@@ -44,7 +44,7 @@ struct ExpertArgs {
 
 // NT: largest n of a tile. NC: CTAs of a tile. BOX: rows of B that one copy brings.
 template <int NT_, int NC_> struct ExpertShape {
-    static constexpr int NT = NT_, NC = NC_, BOX = NT == 64 ? 16 : NT / NC, STEP = 16 * NC;   // of n
+    static constexpr int NT = NT_, NC = NC_, BOX = NT == 32 ? 16 : NT / NC, STEP = 16 * NC;   // of n
     static constexpr int a_bytes = kRowsM * kDepth * 2, b_bytes = NT / NC * kDepth * 2;
     static constexpr int stage = a_bytes + b_bytes;
     static constexpr int stages = 192 * 1024 / stage;
@@ -250,6 +250,16 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *err) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
 }
+// One thread of the warp, always the same. (Told so, the compiler keeps the thread's
+// addresses and descriptors where the copies and products take them from.)
+__device__ __forceinline__ bool elected() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // Address of the pair's first CTA's variable.
 __device__ __forceinline__ uint32_t of_first(const void *p) {
     uint32_t at;
@@ -442,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
     } else if (warp == 0) {
         // ------------------------------------------------------ operands' tiles
-        if (lane == 0) {
+        if (elected()) {
             int stage = 0;
             int64_t issued = 0;
             uint32_t parity = 1;                 // the ring starts empty
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------ products
-        if (lane == 0 && rank == 0) {
+        if (rank == 0 && elected()) {
             int stage = 0, acc = 0;
             uint32_t parity = 0, free_parity = 1;    // both accumulators start free
             uint32_t ends = 0;                       // a bit per stage: ends so far, mod 2
@@ -775,9 +785,12 @@ cudaError_t launch(int dtype, const ExpertArgs &p, int64_t most, cudaStream_t s)
                               : launch<__half, NT, NC, A_MN, GRAD>(p, most, s);
 }
 
-// Tiles of up to 64 slots while the experts have no more than that on average: eight
-// stages of copies in flight instead of four.
-bool few_slots(int64_t P, int64_t E) { return P <= 64 * E; }
+// Tiles of up to 32 slots while the experts have no more than 8 on average. A product is then
+// bound by the matrices' bytes and by the latency of its copies, of which such tiles have nine
+// stages in flight instead of six. Measured, in microseconds, against the pairs' tiles
+// of 256: 8 slots of 64 experts, 2048 x 1024, SMALL1 and 13.7; 512 of 64 SMALL2 and 37.6; 16 on average,
+// 2048 of 128, 2048 x 768, 56 and 52.
+bool few_slots(int64_t P, int64_t E) { return P <= 8 * E; }
 
 template <int NT, int NC>
 cudaError_t product(int dtype, ExpertArgs &p, const void *xs, const void *w, int64_t se,
@@ -821,7 +834,7 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
         return cuda_status(cudaMemsetAsync(ys, 0, (size_t)P * F * 2, s));
     if (!aligned(xs) || !aligned(w) || !strides_ok(w_se, w_sh, w_sf)) return SPMM_ERR_INVALID_ARG;
     ExpertArgs p{};
-    if (strides_far(w_se, w_sh, w_sf) || (P / 64 + E) * ((F + kRowsM - 1) / kRowsM) > (1 << 30))
+    if (strides_far(w_se, w_sh, w_sf) || (P / 32 + E) * ((F + kRowsM - 1) / kRowsM) > (1 << 30))
         return SPMM_ERR_UNSUPPORTED;
     p.offsets = offsets;
     p.out = ys;
@@ -833,7 +846,7 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
     p.a_step = E > 1 && w_se > 0;
     cudaError_t e = dynamic_err(s, &p.err);
     if (e == cudaSuccess)
-        e = few_slots(P, E) ? product<64, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
+        e = few_slots(P, E) ? product<32, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
             : F > kRowsM    ? product<256, 2>(dtype, p, xs, w, w_se, w_sh, w_sf, s)
                             : product<256, 1>(dtype, p, xs, w, w_se, w_sh, w_sf, s);
     return cuda_status(e);
