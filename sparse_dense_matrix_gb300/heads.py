@@ -54,11 +54,13 @@ _Tensor = torch.Tensor
 
 def _rows(t, name, dt, dev):
     """``_heads`` for a tensor of one type, on one device; the usual case at half the time."""
-    if type(t) is _Tensor and t.dtype is dt and t.device == dev and t.dim() == 4:
-        sb, st, sh, sd = t.stride()
-        at = t.data_ptr()
-        if sd == 1 and not ((sb | st | sh) * _BYTES[dt] | at) % 16:
-            return _Rows(at, sb, st, sh)
+    if type(t) is _Tensor and t.dtype is dt and t.device == dev:
+        strides = t.stride()
+        if len(strides) == 4:
+            sb, st, sh, sd = strides
+            at = t.data_ptr()
+            if sd == 1 and not ((sb | st | sh) * _BYTES[dt] | at) & 15:
+                return _Rows(at, sb, st, sh)
     return _heads(t, name, (dt,), dev)
 
 
@@ -169,6 +171,7 @@ class HeadRotation:
             self._stream = _raw_stream(self.device.index)
         self._turns = self.turns.data_ptr() or None
         self._interleaved = 1 if layout == "interleaved" else 0
+        self._weight_shape = (self.dim,)
 
     def _on_stream(self):
         """The current stream, which the frequencies are now used on."""
@@ -178,16 +181,14 @@ class HeadRotation:
         return stream
 
     def _weight(self, w, name, dtype):
-        if w is None:
-            return None, None
-        dt = w.dtype if type(w) is _Tensor else None
-        if not (dt is dtype or dt is torch.float32) or w.shape != (self.dim,) or \
-                w.device != self.device or not w.is_contiguous():
-            _dense(w, name, (dtype, torch.float32), (self.dim,), self.device)
+        """A weight's address."""
+        if type(w) is not _Tensor or not (w.dtype is dtype or w.dtype is torch.float32) or \
+                w.shape != self._weight_shape or w.device != self.device or not w.is_contiguous():
+            _dense(w, name, (dtype, torch.float32), self._weight_shape, self.device)
         at = w.data_ptr()
-        if at % 16:
+        if at & 15:
             raise ValueError(f"{name} must start at a 16-byte boundary")
-        return at, w.dtype
+        return at
 
     def _problem(self, q, k, positions, lengths, q_weight, k_weight, eps):
         """The call's shape, and the rows of q and k."""
@@ -205,30 +206,38 @@ class HeadRotation:
             raise ValueError("k_weight is given without k")
         if D != self.dim:
             raise ValueError(f"the width of a head must be {self.dim}, got {D}")
-        at = lat = None
+        at = lat = wq = wk = None
         sb = st = 0
-        if positions is not None:
-            if lengths is not None:
+        if lengths is not None:
+            if positions is not None:
                 raise ValueError("give positions or lengths, not both")
+            if type(lengths) is not _Tensor or lengths.dtype is not torch.int32 or \
+                    lengths.shape != (B,) or lengths.device != dev or not lengths.is_contiguous():
+                _dense(lengths, "lengths", _INT, (B,), dev)
+            lat = lengths.data_ptr() or None
+        elif positions is not None:
             if not isinstance(positions, _Tensor):
                 raise TypeError("positions must be a torch.Tensor")
-            _tensor(positions, "positions", _INT, 1 if positions.dim() == 1 else 2, dev)
-            if positions.shape != (T,) and positions.shape != (B, T):
+            n = positions.dim()
+            _tensor(positions, "positions", _INT, 1 if n == 1 else 2, dev)
+            if positions.shape != ((T,) if n == 1 else (B, T)):
                 raise ValueError(f"positions must be [{B}, {T}] or [{T}], got "
                                  f"{list(positions.shape)}")
-            st = positions.stride(-1)
-            sb = positions.stride(0) if positions.dim() == 2 else 0
+            strides = positions.stride()
+            st = strides[-1]
+            if n == 2:
+                sb = strides[0]
             at = positions.data_ptr() or None
-        elif lengths is not None:
-            lat = _dense(lengths, "lengths", _INT, (B,), dev).data_ptr() or None
         dt = wt = _DTYPE[dtype]
-        wq = wk = None
-        if q_weight is not None or k_weight is not None:
-            wq, tq = self._weight(q_weight, "q_weight", dtype)
-            wk, tk = self._weight(k_weight, "k_weight", dtype)
-            if tq is not tk and tq is not None and tk is not None:
-                raise TypeError(f"q_weight and k_weight must have one type, got {tq} and {tk}")
-            wt = _DTYPE[tq or tk]
+        if q_weight is not None:
+            wq = self._weight(q_weight, "q_weight", dtype)
+            wt = _DTYPE[q_weight.dtype]
+        if k_weight is not None:
+            wk = self._weight(k_weight, "k_weight", dtype)
+            if wq is not None and k_weight.dtype is not q_weight.dtype:
+                raise TypeError("q_weight and k_weight must have one type, got "
+                                f"{q_weight.dtype} and {k_weight.dtype}")
+            wt = _DTYPE[k_weight.dtype]
         return _HeadsShape(B, T, Hq, Hk, D, self.rotary_dim, dt, wt, self._interleaved, eps,
                            self.magnitude, self._turns, at, sb, st, lat, wq, wk), rows, krows
 
