@@ -20,8 +20,9 @@
 namespace spmm {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kSms = 152, kCtas = 3 * kSms;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
+constexpr int kForwardCtas = 5, kBackwardCtas = 3;      // that share an SM
+constexpr int kSms = 152, kCtas = kForwardCtas * kSms;
 
 // Strided [B, T, heads, D] tensors: what is read, with its weight, and what is written.
 struct HeadFrom {
@@ -386,7 +387,7 @@ __device__ __forceinline__ void forward_heads(const HeadArgs &a, const HeadWalk 
 
 // A warp takes a token's queries, keys and (append) values, or every splits-th of their rows.
 template <typename T, bool INTER, int LANES>
-__global__ void __launch_bounds__(kThreads, 3) k_heads_rotate(const __grid_constant__ HeadArgs a) {
+__global__ void __launch_bounds__(kThreads, kForwardCtas) k_heads_rotate(const __grid_constant__ HeadArgs a) {
     __shared__ HeadAngles told[kWarps];
     const HeadLane l(a, INTER);
     const HeadWalk &w = a.walk;
@@ -499,7 +500,7 @@ __device__ __forceinline__ void backward_heads(const HeadArgs &a, const HeadWalk
 // The weights' gradients: a lane's sums over its rows, then over the rows of the
 // warp, the warps of the CTA and, by a second kernel, the CTAs, each in a fixed order.
 template <typename T, bool INTER, int LANES>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBackwardCtas)
     k_heads_backward(const __grid_constant__ HeadArgs a) {
     __shared__ HeadAngles told[kWarps];
     const HeadLane l(a, INTER);
@@ -536,10 +537,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
         __syncthreads();
-        if ((int)threadIdx.x < a.D) {
+        for (int j = threadIdx.x; j < a.D; j += kThreads) {
             float v = 0.0f;
-            for (int i = 0; i < kWarps; ++i) v += sums[i * 256 + threadIdx.x];
-            out[threadIdx.x] = v;
+            for (int i = 0; i < kWarps; ++i) v += sums[i * 256 + j];
+            out[j] = v;
         }
     };
     float *out = a.parts + (int64_t)blockIdx.x * 2 * a.D;
@@ -547,24 +548,25 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (a.x[1].w) total(dwk, out + a.D);
 }
 
-// A weight's gradient is the sum of the CTAs' parts: 32 columns a CTA, its warps in turn over
-// the parts; CTAs y = 0 for the queries', 1 for the keys'.
+// A weight's gradient is the sum of the CTAs' parts: 8 columns a CTA, 128 parts at a time, then
+// over the lanes and warps; CTAs y = 0 for the queries', 1 for the keys'. (A row of 8 parts is
+// a sector; with 32 columns a CTA the eight CTAs took 6 us for 2048 parts of heads of 128.)
 __global__ void __launch_bounds__(1024) k_heads_weights(const float *parts, int n, int D, int w32,
                                                         int half, void *dwq, void *dwk) {
-    __shared__ float sums[32][33];
+    __shared__ float sums[32][9];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int j = blockIdx.x * 32 + lane;
+    const int j = blockIdx.x * 8 + (lane & 7);             // (D is a multiple of 16)
     void *out = blockIdx.y ? dwk : dwq;
     if (!out) return;
+    parts += blockIdx.y * D + j;
     float x = 0.0f;
-    if (j < D) {
-        parts += blockIdx.y * D + j;
 #pragma unroll 8
-        for (int i = warp; i < n; i += 32) x += parts[(int64_t)i * 2 * D];
-    }
-    sums[warp][lane] = x;
+    for (int i = warp * 4 + (lane >> 3); i < n; i += 128) x += parts[(int64_t)i * 2 * D];
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    x += __shfl_xor_sync(0xffffffffu, x, 16);
+    if (lane < 8) sums[warp][lane] = x;
     __syncthreads();
-    if (warp || j >= D) return;
+    if (threadIdx.x >= 8) return;
     x = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) x += sums[i][lane];
@@ -656,9 +658,11 @@ HeadArgs forward_args(const spmm_heads_shape *s, const spmm_rows &q, const spmm_
     return a;
 }
 
-// Backward: CTAs that each add up a part of the weights' gradients. (With two to an SM, which
-// stay for all tokens, a training step of 2 x 4096 took 82 us, with 8 times as many 66.)
-constexpr unsigned kParts = 16 * kSms;
+// Backward: CTAs that each add up a part of the weights' gradients, three times as many as the
+// SMs hold. A training step of 2 x 4096 tokens, 16 + 2 heads of 128, took 57 us with 9 or 6 for
+// each SM, 61 with 14 (a token a warp: more parts to add up), 85 with 2 (the last ones' tokens
+// alone on the GPU).
+constexpr unsigned kParts = 9 * kSms;
 HeadArgs backward_args(const spmm_heads_shape *s, unsigned &grid) {
     HeadArgs a = shared_args(s);
     a.walk = walk(a, std::max(s->Hq, s->Hk));
@@ -789,7 +793,7 @@ spmm_status spmm_heads_rotate_backward(const spmm_heads_shape *s, spmm_rows grad
                       cs);
     });
     if (err == cudaSuccess && sums) {
-        k_heads_weights<<<dim3((unsigned)((s->D + 31) / 32), 2), 1024, 0, cs>>>(
+        k_heads_weights<<<dim3((unsigned)(s->D / 8), 2), 1024, 0, cs>>>(
             a.parts, (int)grid, a.D, a.w32, s->dtype == SPMM_F16, s->wq ? dwq : nullptr,
             s->wk ? dwk : nullptr);
         count_launch();
