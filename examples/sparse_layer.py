@@ -1,14 +1,14 @@
 """A sparse transformer layer: attention over selected key blocks, then routed experts.
 
 Both halves are products with a matrix that the layer itself chooses in every call
-(queries x key blocks, tokens x slots). The script runs one training step on a
-prompt, then the last tokens of the same prompt one at a time over a cache, and
-compares the two.
+(queries x key blocks, tokens x slots). Queries and keys are normed head by head and
+turned by their position before the one; in the other each expert's rows are multiplied
+with that expert's matrices. The script runs one training step on a prompt, then the last
+tokens of the same prompt one at a time over a cache, and compares the two.
 
     python examples/sparse_layer.py [--tokens 1024] [--device cuda:0]
 
-The projections and the experts' own products are plain torch; the layer has no
-normalisation and its gradients stop at its input's projections.
+The projections are plain torch; the gradients stop at the layer's input's projections.
 """
 from __future__ import annotations
 
@@ -38,6 +38,9 @@ class SparseLayer:
         self.w_qkv = weight(H, (heads + 2 * kv_heads) * dim)
         self.w_out, self.w_gate = weight(H, H), weight(H, experts)
         self.w_up, self.w_down = weight(experts, H, inner), weight(experts, inner, H)
+        self.rotation = sdm.HeadRotation(dim, device=device)
+        self.norms = {name: 1 + 0.1 * torch.randn(dim, generator=g, device=device)
+                      for name in ("q_weight", "k_weight")}
 
     def qkv(self, x):
         B, T, _ = x.shape
@@ -50,56 +53,49 @@ class SparseLayer:
         weights = torch.softmax(top.values, dim=1)
         return sdm.ExpertRoutes(top.indices.to(torch.int32), self.experts), weights
 
-    def run_experts(self, xs, offsets):
-        ys = torch.zeros_like(xs)
-        at = offsets.tolist()
-        for e in range(self.experts):
-            rows = slice(at[e], at[e + 1])
-            ys[rows] = torch.relu(xs[rows] @ self.w_up[e]) @ self.w_down[e]
-        return ys
-
     def mlp(self, h):
         routes, weights = self.route(h)
         xs = routes.dispatch(h)
-        ys = self.run_experts(xs, routes.offsets)
-        return routes.combine(ys, weights), (routes, weights, xs, ys)
+        up = routes.product(xs, self.w_up)
+        inner = torch.relu(up)
+        ys = routes.product(inner, self.w_down)
+        return routes.combine(ys, weights), (routes, weights, xs, up, inner, ys)
 
     def prompt(self, x):
         """x [B, T, H] -> the layer's output, and what the backward pass and a cache need."""
         B, T, H = x.shape
-        q, k, v = self.qkv(x)
+        q0, k0, v = self.qkv(x)
+        q, k = self.rotation.rotate(q0, k0, **self.norms)
         means = sdm.block_means(k, self.block)
         sel = sdm.select_blocks(q, means, self.n, self.block, T)
         out, lse = sel.attend(q, k, v)
         h = x + out.view(B, T, H) @ self.w_out
         y, kept = self.mlp(h.view(B * T, H))
-        return h + y.view(B, T, H), (q, k, v, means, sel, out, lse, *kept)
+        return h + y.view(B, T, H), (q, k, v, means, sel, out, lse, q0, k0, *kept)
 
     def prompt_backward(self, grad, saved):
-        """Gradients of q, k, v, the experts' inputs' rows, and the router's weights."""
-        q, k, v, _, sel, out, lse, routes, weights, xs, ys = saved
+        """Gradients of the projections, the norms, the experts' matrices, their inputs' rows
+        and the router's weights."""
+        q, k, v, _, sel, out, lse, q0, k0, routes, weights, xs, up, inner, ys = saved
         B, T, H = grad.shape
         rows = grad.reshape(B * T, H)
         dys, dweights = routes.combine_backward(rows, ys, weights)
-        dxs = torch.zeros_like(xs)
-        at = routes.offsets.tolist()
-        for e in range(self.experts):
-            r = slice(at[e], at[e + 1])
-            up = xs[r] @ self.w_up[e]
-            dxs[r] = torch.where(up > 0, dys[r] @ self.w_down[e].T, 0) @ self.w_up[e].T
+        dinner, dw_down = routes.product_backward(dys, inner, self.w_down)
+        dxs, dw_up = routes.product_backward(torch.where(up > 0, dinner, 0), xs, self.w_up)
         dh = rows + routes.dispatch_backward(dxs)
         dout = (dh @ self.w_out.T).view(B, T, self.heads, self.dim)
         dq, dk, dv = sel.backward(dout, q, k, v, out, lse)
-        return {"dq": dq, "dk": dk, "dv": dv, "dh": dh.view(B, T, H), "dweights": dweights}
+        dq, dk, dnorm_q, dnorm_k = self.rotation.rotate_backward(dq, dk, q0, k0, **self.norms)
+        return {"dq": dq, "dk": dk, "dv": dv, "dh": dh.view(B, T, H), "dweights": dweights,
+                "dw_up": dw_up, "dw_down": dw_down, "dnorm_q": dnorm_q, "dnorm_k": dnorm_k}
 
     def token(self, x, cache_k, cache_v, means, lengths):
         """One more token of each sequence: x [B, 1, H]. The caches hold lengths[b] keys
         and are written at that position; lengths and means are brought up to date."""
         B = x.shape[0]
         q, k, v = self.qkv(x)
-        b, at = torch.arange(B, device=x.device), lengths.long()
-        cache_k[b, at], cache_v[b, at] = k[:, 0], v[:, 0]
         lengths += 1
+        q = self.rotation.append(q, k, v, cache_k, cache_v, lengths, **self.norms)
         sdm.block_means(cache_k, self.block, lengths, out=means, new_keys=1)
         sel = sdm.select_blocks(q, means, self.n, self.block, cache_k.shape[1], lengths)
         out, _ = sel.attend(q, cache_k, cache_v)
