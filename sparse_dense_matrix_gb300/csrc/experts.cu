@@ -14,7 +14,7 @@
 // up to 256, of which each holds half of either operand and 128 of m of the result. A
 // warp's thread copies the operands' tiles of 64 of k into a ring of stages (tensor
 // copies), another (of the pair's first CTA) issues the products into one of two
-// accumulators in tensor memory, and four warps write the other one out meanwhile.
+// accumulators in tensor memory, and eight warps write the other one out meanwhile.
 #include <cudaTypedefs.h>
 
 #include "umma.cuh"
@@ -25,8 +25,8 @@ namespace {
 constexpr int kSms = 152;
 constexpr int kDepth = 64;           // of k in a stage: a row of 128 bytes
 constexpr int kRowsM = 128;          // of m in a CTA's tile
-constexpr int kThreads = 256;        // copies, products, four warps of results, the tiles' list,
-                                     // ends of segments
+constexpr int kResults = 8;          // warps that write results out
+constexpr int kThreads = 128 + 32 * kResults;    // copies, products, tiles' list, segments' ends first
 constexpr int kTilesAhead = 4;
 constexpr int kSmemMax = 227 * 1024;
 
@@ -49,10 +49,9 @@ template <int NT_, int NC_> struct ExpertShape {
     static constexpr int stage = a_bytes + b_bytes;
     static constexpr int stages = 192 * 1024 / stage;
     static constexpr int columns = 2 * NT;
-    // results: 32 rows of 64 bytes for each of four warps, the rows 80 bytes apart, so
-    // that eight of them fall in different banks
-    static constexpr int out_pitch = 80, out_bytes = 4 * 32 * out_pitch;
-    static constexpr int at_out = stages * stage, at_offsets = at_out + out_bytes;
+    // results: 32 rows of 64 bytes for each warp
+    static constexpr int out_bytes = 32 * 64;
+    static constexpr int at_out = stages * stage, at_offsets = at_out + kResults * out_bytes;
     static size_t bytes(int E) { return 1024 + at_offsets + sizeof(int32_t) * 2 * ((size_t)E + 1); }
 };
 
@@ -403,12 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ready[i], 1);
-            mbar_init(&taken[i], 4 * NC);
+            mbar_init(&taken[i], kResults * NC);
         }
         for (int i = 0; i < kTilesAhead; ++i) {
             mbar_init(&listed[i], 1);
-            // a thread of copies, one of products, four warps of results, ends of segments
-            mbar_init(&read[i], 5 + (rank == 0) + GRAD);
+            // a thread of copies, one of products, the warps of results, ends of segments
+            mbar_init(&read[i], 1 + (rank == 0) + kResults + GRAD);
         }
         mbar_init(&drained, 1);
         mbar_init_fence();
@@ -425,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     TileRing ring{tile_ring, listed, read, 0, 0};
     ExpertTile x;
 
-    if (warp == 6) {
+    if (warp == 2) {
         // ------------------------------------------------------ the tiles' list
         if (lane == 0) {
             const int tiles = list.template tiles<GRAD>(p);
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             }
         }
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == 3) {
         // ------------------------------------------------------ ends of segments
         // rows of k past the expert's last, up to a step of products, are set to 0
         uint32_t count = 0, ends = 0;            // stages so far
@@ -619,12 +618,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         __syncwarp();
     } else {
         // ------------------------------------------------------ results
-        const int quarter = warp & 3;            // the lanes of tensor memory it may read
-        const uint32_t out_smem = smem + S::at_out + quarter * 32 * S::out_pitch;
-        // where this lane's column of a transposed store lies, and its part of a row to write
-        const uint32_t put = out_smem + ((lane >> 4) * 8 + (lane & 7)) * S::out_pitch +
-                             ((lane >> 3) & 1) * 16;
-        const uint32_t get = out_smem + (lane >> 2) * S::out_pitch + (lane & 3) * 16;
+        // two warps to a quarter of tensor memory's lanes (a warp reads those of its number mod
+        // 4), each every other 32 columns
+        const int quarter = warp & 3, c0 = (warp - 4) / 4 * 32;
+        // A row's four 16-byte chunks are permuted by half its number, so that eight rows' fall in
+        // different banks, and two whole rows'.
+        const uint32_t out_smem = smem + S::at_out + (warp - 4) * S::out_bytes;
+        auto chunk = [&](int row, int c) {
+            return out_smem + row * 64 + (((c ^ (row >> 1)) & 3) << 4);
+        };
+        const int put_row = (lane >> 4) * 8 + (lane & 7), put_c = (lane >> 3) & 1;
         int acc = 0;
         uint32_t parity = 0;
         bool ok = true;
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             const int m = x.m0 + rank * kRowsM + quarter * 32 + (lane & 3) * 8;
             T *out = (T *)p.out + (GRAD ? x.e * p.o_se + x.n0 * p.o_ld : (int64_t)x.r0 * p.o_ld) + m;
             if (x.k == 0) {
-                for (int n = lane >> 2; m < p.M && n < x.n; n += 8)
+                for (int n = c0 / 4 + (lane >> 2); m < p.M && n < x.n; n += 16)
                     *(uint4 *)(out + n * p.o_ld) = make_uint4(0, 0, 0, 0);
                 continue;
             }
@@ -640,9 +643,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             mma_fence_after();
             const uint32_t d = tmem + acc * NT + ((uint32_t)quarter << 21);
             uint32_t v[2][16];
-            tmem_ld16x32(d, v[0]);
-            tmem_ld16x32(d + (16u << 16), v[1]);
-            for (int c = 0; c < x.n; c += 32) {
+            if (c0 < x.n) {
+                tmem_ld16x32(d + c0, v[0]);
+                tmem_ld16x32(d + (16u << 16) + c0, v[1]);
+            }
+            // handed back as soon as the last columns are in registers; no memory is (a release
+            // would wait for the stores)
+            auto hand_back = [&] {
+                mma_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive(&taken[acc]);
+                    else arrive_first_relaxed(&taken[acc]);
+                }
+            };
+            if (c0 >= x.n) hand_back();
+            for (int c = c0; c < x.n; c += 64) {
                 tmem_wait_ld();
                 uint32_t y[2][8];
 #pragma unroll
@@ -651,30 +667,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                     for (int i = 0; i < 8; ++i)
                         y[h][i] = pack2<T>(__uint_as_float(v[h][2 * i]),
                                            __uint_as_float(v[h][2 * i + 1]));
-                if (c + 32 < x.n) {              // on their way while these are written
-                    tmem_ld16x32(d + c + 32, v[0]);
-                    tmem_ld16x32(d + (16u << 16) + c + 32, v[1]);
+                if (c + 64 < x.n) {              // on their way while these are written
+                    tmem_ld16x32(d + c + 64, v[0]);
+                    tmem_ld16x32(d + (16u << 16) + c + 64, v[1]);
                 } else {
-                    mma_fence_before();
-                    __syncwarp();
-                    // no memory is handed over (a release would wait for the stores)
-                    if (lane == 0) {
-                        if (rank == 0) mbar_arrive(&taken[acc]);
-                        else arrive_first_relaxed(&taken[acc]);
-                    }
+                    hand_back();
                 }
                 __syncwarp();                    // the rows before are read
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int i = 0; i < 4; i += 2)
-                        stsm4_t(put + i * 8 * S::out_pitch + h * 32, y[h][2 * i], y[h][2 * i + 1],
+                        stsm4_t(chunk(put_row + i * 8, put_c + 2 * h), y[h][2 * i], y[h][2 * i + 1],
                                 y[h][2 * i + 2], y[h][2 * i + 3]);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int n = c + i * 8 + (lane >> 2);
-                    const uint4 z = lds16(get + i * 8 * S::out_pitch);
+                    const uint4 z = lds16(chunk(i * 8 + (lane >> 2), lane & 3));
                     if (m < p.M && n < x.n) *(uint4 *)(out + n * p.o_ld) = z;
                 }
             }
@@ -685,8 +695,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
             const int64_t kept = list.first[p.E];
             uint4 *out = (uint4 *)((T *)p.out + kept * p.o_ld);
             const int64_t n = (p.P - kept) * p.o_ld / 8;
-            for (int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x - 64; i < n;
-                 i += (int64_t)gridDim.x * 128)
+            constexpr int threads = 32 * kResults;
+            for (int64_t i = (int64_t)blockIdx.x * threads + threadIdx.x - 128; i < n;
+                 i += (int64_t)gridDim.x * threads)
                 out[i] = make_uint4(0, 0, 0, 0);
         }
         __syncwarp();
