@@ -121,8 +121,8 @@ spmm_status spmm_routes_combine_backward(int dtype, const void *dout, int64_t ld
  *        for every expert).
  * With w transposed (w_sh and w_sf, H and F exchanged) it is the gradient of xs.
  * dtype is SPMM_BF16 or SPMM_F16, H and F multiples of 8 up to 2^20, E at most
- * SPMM_ROUTES_MAX_EXPERTS, P < 2^31 (else SPMM_ERR_UNSUPPORTED); pointers are
- * 16-byte aligned.
+ * SPMM_ROUTES_MAX_EXPERTS, P below 2^31 - 2^16, strides below 2^38 (else
+ * SPMM_ERR_UNSUPPORTED); pointers are 16-byte aligned.
  */
 spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_t w_se,
                                 int64_t w_sh, int64_t w_sf, const int32_t *offsets, int64_t P,
@@ -131,7 +131,7 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
 /*
  * spmm_routes_product_weights -- the gradient of the matrices:
  *   dw[e, h, f] = sum over the slots s of e of xs[s, h] dys[s, f]; 0 without slots.
- *   dw : device, written whole, strides as w's above (but dw_se > 0 for E > 1).
+ *   dw : device, written whole, strides as w's above, no two elements in one place.
  */
 spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *dys,
                                         const int32_t *offsets, int64_t P, int64_t E, int64_t H,

@@ -720,7 +720,7 @@ spmm_status check_sizes(int dtype, const int32_t *offsets, int64_t P, int64_t E,
     if (!dtype_ok(dtype) || !offsets || P < 0 || E < 0 || H < 0 || F < 0)
         return SPMM_ERR_INVALID_ARG;
     if (dtype == SPMM_F32 || H % 8 || F % 8 || H > (1 << 20) || F > (1 << 20) ||
-        E > SPMM_ROUTES_MAX_EXPERTS || P > INT32_MAX)
+        E > SPMM_ROUTES_MAX_EXPERTS || P > INT32_MAX - 65536)   // (slots and a tile: 32 bits)
         return SPMM_ERR_UNSUPPORTED;
     return SPMM_OK;
 }
@@ -802,10 +802,10 @@ cudaError_t launch(int dtype, const ExpertArgs &p, int64_t most, cudaStream_t s)
 }
 
 // Tiles of up to 32 slots while the experts have no more than 8 on average. A product is then
-// bound by the matrices' bytes and by the latency of its copies, of which such tiles have nine
-// stages in flight instead of six. Measured, in microseconds, against the pairs' tiles
-// of 256: 8 slots of 64 experts, 2048 x 1024, SMALL1 and 13.7; 512 of 64 SMALL2 and 37.6; 16 on average,
-// 2048 of 128, 2048 x 768, 56 and 52.
+// bound by the matrices' bytes and by the latency of its copies: tiles of one CTA give twice
+// as many of them. Measured, in microseconds, against the pairs' tiles of 256 (2048 x 1024): 8
+// slots of 64 experts 10.0 and 12.0, 512 of 64 32.4 and 35.6; 16 on average, 2048 slots of 128
+// (2048 x 768), 53.1 and 50.9; 64 on average, 512 of 8 (2048 x 2048), 16.1 and 11.5.
 bool few_slots(int64_t P, int64_t E) { return P <= 8 * E; }
 
 template <int NT, int NC>
@@ -876,7 +876,8 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
     const spmm_status st = check_sizes(dtype, offsets, P, E, H, F);
     if (st != SPMM_OK) return st;
     if (E == 0 || H == 0 || F == 0) return SPMM_OK;
-    if (!aligned(dw) || !strides_ok(dw_se, dw_sh, dw_sf) || (E > 1 && dw_se == 0))
+    if (!aligned(dw) || !strides_ok(dw_se, dw_sh, dw_sf) || (E > 1 && dw_se == 0) ||
+        (dw_sf == 1 ? dw_sh < F : dw_sf < H))    // rows on top of one another
         return SPMM_ERR_INVALID_ARG;
     if (P && (!aligned(xs) || !aligned(dys))) return SPMM_ERR_INVALID_ARG;
     const bool by_f = dw_sf == 1;                // m = f, else m = h

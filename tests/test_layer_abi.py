@@ -31,7 +31,7 @@ def weights(L, dtype=1, xs=PTR, dys=PTR, offsets=PTR, P=8, E=3, H=16, F=24, dw=P
     (dict(dtype=3), INVALID), (dict(dtype=0), UNSUPPORTED), (dict(P=-1), INVALID),
     (dict(E=-1), INVALID), (dict(H=-8), INVALID), (dict(offsets=None), INVALID),
     (dict(H=12), UNSUPPORTED), (dict(F=20), UNSUPPORTED), (dict(E=2049), UNSUPPORTED),
-    (dict(P=1 << 31), UNSUPPORTED), (dict(H=1 << 21), UNSUPPORTED), (dict(F=1 << 21), UNSUPPORTED),
+    (dict(P=1 << 31), UNSUPPORTED), (dict(P=(1 << 31) - 65536), UNSUPPORTED), (dict(H=1 << 21), UNSUPPORTED), (dict(F=1 << 21), UNSUPPORTED),
     (dict(xs=None), INVALID), (dict(xs=ODD), INVALID), (dict(se=-8), INVALID),
     (dict(se=4), INVALID), (dict(sh=20), INVALID), (dict(sh=24, sf=8), INVALID),
     (dict(sh=0), INVALID), (dict(sh=1, sf=0), INVALID), (dict(sh=1, sf=12), INVALID)])
@@ -44,7 +44,9 @@ def test_products_refuse_outputs(m):
     for bad in (None, ODD):
         assert product(m.lib, ys=bad) == INVALID and product(m.lib, w=bad) == INVALID
         assert weights(m.lib, dw=bad) == INVALID and weights(m.lib, dys=bad) == INVALID
-    assert weights(m.lib, se=0) == INVALID       # experts' gradients on top of one another
+    for bad in (dict(se=0), dict(sh=16), dict(sh=1, sf=8)):      # on top of one another
+        assert weights(m.lib, **bad) == INVALID
+    assert product(m.lib, sh=1 << 38) == UNSUPPORTED and product(m.lib, se=1 << 38) == UNSUPPORTED
     # nothing to do is no error, and needs no device
     assert product(m.lib, P=0, xs=None, ys=None) == 0 and product(m.lib, F=0, ys=None) == 0
     assert weights(m.lib, E=0, dw=None) == 0 and weights(m.lib, H=0, dw=None) == 0
