@@ -15,6 +15,14 @@
 // warp's thread copies the operands' tiles of 64 of k into a ring of stages (tensor
 // copies), another (of the pair's first CTA) issues the products into one of two
 // accumulators in tensor memory, and eight warps write the other one out meanwhile.
+//
+// Measured (bf16): 131072 slots of 128 experts that differ in popularity, 2048 x 1024, 340 us,
+// 1.62 PFLOP/s, of the rows 350, of the matrices 409 (DRAM at 47%, the tensor pipe active 85%
+// of the SMs' active cycles at the 1.6 GHz that power leaves); one expert with 8192 slots,
+// 8192 x 8192, 603, 655 and 560 us, next to 555 of the library's product of that size. 512 slots of
+// 128 experts, 2048 x 768 (226 MB of matrices), 37 us, 6.1 TB/s. 8 slots of 8 experts, 2048 x
+// 1024, 10 us, of which 2.4 pass before the first product is issued and 6 by 32 stages of
+// one CTA after another on 64 SMs.
 #include <cudaTypedefs.h>
 
 #include "umma.cuh"

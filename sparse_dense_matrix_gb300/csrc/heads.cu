@@ -15,6 +15,13 @@
 // A warp works the angles out once, a pair to a lane, and hands them round in shared memory.
 // Two rows are worked on side by side, as one row's chain (its sum over the lanes, the
 // root, the products) leaves the pipes idle, and four more are on their way meanwhile.
+//
+// Measured: 8192 tokens of 32 + 4 heads of 128 in bf16 (151 MB) 31 us, 4.9 TB/s; the same
+// walk without the arithmetic takes 24 us, a norm 2 and the angles 2 of the rest. A
+// training step of 2 x 4096 tokens of 16 + 2 heads 16 us forward (4.7 TB/s, partly from L2)
+// and 41 backward (113 MB; 2.8 TB/s). Bound by instructions: about 130 for a warp's 32 x 8
+// elements forward and 200 backward, issued in half of the cycles by the 20 and 12 warps
+// that fit an SM's registers.
 #include "blocks.cuh"
 
 namespace spmm {

@@ -165,6 +165,10 @@ def test_calls_of_several_threads(sdm, cuda_device):
         try:
             torch.cuda.set_device(dev)
             s = torch.cuda.Stream()
+            try:                                 # captured waits that gave up before, elsewhere
+                sdm.dynamic_sync(s)
+            except sdm.SpmmError:
+                pass
             with torch.cuda.stream(s):
                 for _ in range(150):
                     got = run()
