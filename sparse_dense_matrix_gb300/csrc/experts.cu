@@ -372,6 +372,10 @@ template <int NC> __device__ __forceinline__ void pair_barrier() {
         asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Rows [from, to) of `panels` panels of 64 rows set to 0, by one warp.
 __device__ __forceinline__ void zero_rows(uint32_t operand, int panels, int from, int to) {
     const int lane = threadIdx.x & 31, n = (to - from) * 8;
@@ -423,6 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     if (warp == 1) {
         alloc_columns<NC>(&tmem_slot, S::columns);
         mma_fence_before();
+    } else if (threadIdx.x == 64 && p.P > 0) {   // the first copies find the maps at hand
+        prefetch_map(&p.a_map);
+        prefetch_map(&p.b_map);
     }
     const ExpertList list = expert_list<NT, GRAD>(
         p, (int32_t *)(smem_raw + (smem - smem_addr(smem_raw)) + S::at_offsets));
