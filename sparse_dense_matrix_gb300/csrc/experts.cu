@@ -9,7 +9,8 @@
 //   gradient   m = f (h where h is adjacent in dw), n = h (f), k = a slot: A = dys^T,
 //              B = xs^T, both MN-major. The ragged index is the summed one: rows past
 //              the expert's last are the next expert's, and are set to 0 in shared
-//              memory before they are used (0 times a NaN is none of this expert's).
+//              memory before they are used (0 times a NaN is none of this expert's). Few
+//              experts with many slots are summed in parts, which a second kernel adds up.
 // CTAs stay and take tiles of 128 x up to 256 in turn, or pairs of CTAs tiles of 256 x
 // up to 256, of which each holds half of either operand and 128 of m of the result. A
 // warp's thread copies the operands' tiles of 64 of k into a ring of stages (tensor
@@ -47,6 +48,8 @@ struct ExpertArgs {
     int E, M, N, K;                  // N: gradient; K: product
     int a_step;                      // 0: one matrix for every expert
     int tiles_m, tiles_n;
+    int splits;                      // gradient: parts of an expert's slots
+    float *parts;                    // with more than one, [splits][E][M][N]
     int32_t *err;
 };
 
@@ -67,6 +70,7 @@ struct ExpertTile {
     int e, n, m0, n0;                // m0, n0: first of m (of the pair's), of n (gradient)
     int r0;                          // first slot: of n (product), of k (gradient)
     int k;                           // length of k
+    int part;                        // gradient: which of the expert's
 };
 
 // Shared memory's view of the experts: first slots, and the tiles of slots before each expert
@@ -75,7 +79,7 @@ struct ExpertList {
     const int32_t *first, *before;
     template <bool GRAD>
     __device__ __forceinline__ int tiles(const ExpertArgs &p) const {
-        return (GRAD ? p.E * p.tiles_n : before[p.E]) * p.tiles_m;
+        return (GRAD ? p.E * p.splits * p.tiles_n : before[p.E]) * p.tiles_m;
     }
     template <typename S, bool GRAD>
     __device__ __forceinline__ ExpertTile tile(const ExpertArgs &p, int t) const {
@@ -84,11 +88,19 @@ struct ExpertList {
         x.m0 = t % p.tiles_m * (kRowsM * S::NC);
         const int u = t / p.tiles_m;
         if (GRAD) {
-            x.e = before[u / p.tiles_n];
+            const int v = u / p.tiles_n;
+            x.e = before[v / p.splits];
             x.n0 = u % p.tiles_n * NT;
             x.n = min(NT, p.N - x.n0);
             x.r0 = first[x.e];
             x.k = first[x.e + 1] - first[x.e];
+            x.part = v % p.splits;
+            if (p.splits > 1) {                  // (whole stages, but for the last part's end)
+                const int per = ((x.k + p.splits - 1) / p.splits + kDepth - 1) / kDepth * kDepth;
+                const int64_t at = (int64_t)x.part * per;
+                x.k = (int)max((int64_t)0, min((int64_t)per, x.k - at));
+                x.r0 = (int)min(x.r0 + at, p.P);
+            }
         } else {
             int lo = 0, hi = p.E - 1;            // the last expert with before[e] <= u
             while (lo < hi) {
@@ -97,7 +109,7 @@ struct ExpertList {
                 else hi = mid - 1;
             }
             x.e = lo;
-            x.n0 = 0;
+            x.n0 = x.part = 0;
             // an expert's slots in equal parts
             const int rows = first[lo + 1] - first[lo], parts = before[lo + 1] - before[lo];
             const int per = ((rows + parts - 1) / parts + S::STEP - 1) / S::STEP * S::STEP;
@@ -654,6 +666,46 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
         while (ring.take_warp(x, ok, p.err)) {
             const int m = x.m0 + rank * kRowsM + quarter * 32 + (lane & 3) * 8;
             T *out = (T *)p.out + (GRAD ? x.e * p.o_se + x.n0 * p.o_ld : (int64_t)x.r0 * p.o_ld) + m;
+            if (GRAD && p.splits > 1) {
+                // fp32, as the registers hold them: two adjacent n of a row of m
+                float *part = p.parts + ((int64_t)x.part * p.E + x.e) * p.M * p.N + x.n0;
+                const int row = x.m0 + rank * kRowsM + quarter * 32 + (lane >> 2);
+                if (x.k > 0) {
+                    if (!warp_wait(&ready[acc], parity, p.err)) break;
+                    mma_fence_after();
+                }
+                const uint32_t d = tmem + acc * NT + ((uint32_t)quarter << 21);
+                for (int c = c0; c < x.n; c += 64) {
+                    uint32_t v[2][16] = {};
+                    if (x.k > 0) {
+                        tmem_ld16x32(d + c, v[0]);
+                        tmem_ld16x32(d + (16u << 16) + c, v[1]);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int m = row + 16 * h + 8 * (i & 1);
+                            const int n = c + 8 * (i >> 1) + 2 * (lane & 3);
+                            if (m < p.M && n < x.n)
+                                *(float2 *)(part + (int64_t)m * p.N + n) =
+                                    make_float2(__uint_as_float(v[h][2 * i]),
+                                                __uint_as_float(v[h][2 * i + 1]));
+                        }
+                }
+                if (x.k > 0) {
+                    mma_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive(&taken[acc]);
+                        else arrive_first_relaxed(&taken[acc]);
+                    }
+                    acc ^= 1;
+                    parity ^= acc == 0;
+                }
+                continue;
+            }
             if (x.k == 0) {
                 for (int n = c0 / 4 + (lane >> 2); m < p.M && n < x.n; n += 16)
                     *(uint4 *)(out + n * p.o_ld) = make_uint4(0, 0, 0, 0);
@@ -725,6 +777,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
     // (of a pair: neither leaves, or gives its tensor memory back, before both are done)
     pair_barrier<NC>();
     if (warp == 1) free_columns<NC>(tmem, S::columns);
+}
+
+// dw[e, n, m] (m adjacent, strides o_se and o_ld) = the sum of the parts [splits][E][M][N], in
+// their order: 32 x 32 elements a CTA, turned over in shared memory.
+template <typename T>
+__global__ void __launch_bounds__(256) k_experts_sum(const float *parts, int splits, int E, int M,
+                                                     int N, T *out, int64_t o_se, int64_t o_ld) {
+    __shared__ float tile[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tiles_n = (N + 31) / 32, m0 = blockIdx.x / tiles_n * 32, n0 = blockIdx.x % tiles_n * 32;
+    const int64_t e = blockIdx.y, one = (int64_t)M * N;
+    for (int i = warp; i < 32; i += 8) {
+        const int m = m0 + i, n = n0 + lane;
+        float x = 0.0f;
+        if (m < M && n < N) {
+            const float *p = parts + e * one + (int64_t)m * N + n;
+#pragma unroll 4
+            for (int j = 0; j < splits; ++j) x += p[j * E * one];
+        }
+        tile[i][lane] = x;
+    }
+    __syncthreads();
+    for (int i = warp; i < 32; i += 8) {
+        const int n = n0 + i, m = m0 + lane;
+        if (m < M && n < N) out[e * o_se + n * o_ld + m] = from_f32<T>(tile[lane][i]);
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -844,7 +922,27 @@ cudaError_t weights(int dtype, ExpertArgs &p, cudaStream_t s) {
     constexpr int NT = 256;
     p.tiles_m = (p.M + kRowsM * NC - 1) / (kRowsM * NC);
     p.tiles_n = (p.N + NT - 1) / NT;
-    return launch<NT, NC, true, true>(dtype, p, (int64_t)p.E * p.tiles_m * p.tiles_n, s);
+    cudaError_t e = launch<NT, NC, true, true>(
+        dtype, p, (int64_t)p.E * p.splits * p.tiles_m * p.tiles_n, s);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const dim3 grid((unsigned)(((p.M + 31) / 32) * ((p.N + 31) / 32)), (unsigned)p.E);
+    if (dtype == SPMM_BF16)
+        k_experts_sum<<<grid, 256, 0, s>>>(p.parts, p.splits, p.E, p.M, p.N, (__nv_bfloat16 *)p.out,
+                                           p.o_se, p.o_ld);
+    else
+        k_experts_sum<<<grid, 256, 0, s>>>(p.parts, p.splits, p.E, p.M, p.N, (__half *)p.out, p.o_se,
+                                           p.o_ld);
+    count_launch();
+    return cudaGetLastError();
+}
+
+// Parts of an expert's slots in the gradient: as many as fill the pairs of CTAs that its tiles
+// leave idle, while a part has at least 512 slots of an average expert. (65536 slots of one
+// expert, 2048 x 1024: 170 us in two parts, 277 in one; 131072, 351 and 644.)
+int64_t weight_splits(int64_t P, int64_t E, int64_t H, int64_t F) {
+    if (E == 0 || H == 0 || F == 0) return 1;
+    const int64_t tiles = E * ((H + 255) / 256) * ((F + 255) / 256);
+    return std::max<int64_t>(1, std::min(kSms / 2 / tiles, P / (E * 512)));
 }
 
 }  // namespace
@@ -883,10 +981,20 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
     return cuda_status(e);
 }
 
+int64_t spmm_routes_product_weights_workspace(int64_t P, int64_t E, int64_t H, int64_t F) {
+    using namespace spmm;
+    if (P < 0 || E < 0 || H < 0 || F < 0 || E > SPMM_ROUTES_MAX_EXPERTS || H > (1 << 20) ||
+        F > (1 << 20) || P > INT32_MAX)
+        return 0;
+    const int64_t splits = weight_splits(P, E, H, F);
+    return splits > 1 ? splits * E * H * F * (int64_t)sizeof(float) : 0;
+}
+
 spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *dys,
                                         const int32_t *offsets, int64_t P, int64_t E, int64_t H,
                                         int64_t F, void *dw, int64_t dw_se, int64_t dw_sh,
-                                        int64_t dw_sf, void *stream) {
+                                        int64_t dw_sf, void *work, int64_t work_bytes,
+                                        void *stream) {
     using namespace spmm;
     const spmm_status st = check_sizes(dtype, offsets, P, E, H, F);
     if (st != SPMM_OK) return st;
@@ -895,8 +1003,12 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
         (dw_sf == 1 ? dw_sh < F : dw_sf < H))    // rows on top of one another
         return SPMM_ERR_INVALID_ARG;
     if (P && (!aligned(xs) || !aligned(dys))) return SPMM_ERR_INVALID_ARG;
+    const int64_t need = spmm_routes_product_weights_workspace(P, E, H, F);
+    if (need && (!aligned(work) || work_bytes < need)) return SPMM_ERR_INVALID_ARG;
     const bool by_f = dw_sf == 1;                // m = f, else m = h
     ExpertArgs p{};
+    p.splits = (int)weight_splits(P, E, H, F);
+    p.parts = (float *)work;
     p.M = (int)(by_f ? F : H);
     p.N = (int)(by_f ? H : F);
     if (E * ((p.M + kRowsM - 1) / kRowsM) * ((p.N + 255) / 256) > (1 << 30)) return SPMM_ERR_UNSUPPORTED;

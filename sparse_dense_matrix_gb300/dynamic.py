@@ -61,8 +61,9 @@ def _declare():
         "spmm_routes_combine_backward": ([i32, vp, i64, vp, vp, vp, vp, i64, i64, i64, i64, vp, vp,
                                           vp], i32),
         "spmm_routes_product": ([i32, vp, vp, i64, i64, i64, vp, i64, i64, i64, i64, vp, vp], i32),
+        "spmm_routes_product_weights_workspace": ([i64] * 4, i64),
         "spmm_routes_product_weights": ([i32, vp, vp, vp, i64, i64, i64, i64, vp, i64, i64, i64,
-                                         vp], i32),
+                                         vp, i64, vp], i32),
         "spmm_blocks_means": ([S, _Rows, i64, vp, vp], i32),
         "spmm_blocks_select_workspace": ([S], i64),
         "spmm_blocks_select": ([S, _Rows, vp, vp, vp, i64, vp], i32),
@@ -342,12 +343,14 @@ class ExpertRoutes:
         E, dt, offsets, handle = self.num_experts, _DTYPE[xs.dtype], self._routes[1], self._on_stream()
         dxs = torch.empty_like(xs)
         dw = torch.empty_like(w)
+        need = lib.spmm_routes_product_weights_workspace(P, E, H, F)
+        work = torch.empty(need, dtype=torch.uint8, device=self.device).data_ptr() if need else None
         st = lib.spmm_routes_product(dt, grad.data_ptr(), at, se, sf, sh, offsets, P, E, F, H,
                                      dxs.data_ptr(), handle)
         if st:
             _check(st, "spmm_routes_product")
         st = lib.spmm_routes_product_weights(dt, xs.data_ptr(), grad.data_ptr(), offsets, P, E, H, F,
-                                             *_matrix_strides(dw, "dw"), handle)
+                                             *_matrix_strides(dw, "dw"), work, need, handle)
         if st:
             _check(st, "spmm_routes_product_weights")
         return dxs, dw

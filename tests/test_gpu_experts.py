@@ -309,3 +309,26 @@ def test_refusals(sdm, cuda_device):
     for bad in (grad[:, :16], grad[:4], grad.half(), grad.t().contiguous().t()):
         with pytest.raises((ValueError, TypeError)):
             routes.product_backward(bad, xs, w)
+
+
+@pytest.mark.parametrize("stored", ["in_out", "out_in"])
+@pytest.mark.parametrize("T,E,H,F,last", [
+    (5000, 1, 72, 264, 5000),                    # one expert, parts of unlike lengths
+    (4096, 2, 128, 128, 4096),                   # an expert without slots
+    (1537, 1, 8, 8, 1537), (2600, 2, 520, 40, 2599), (9000, 3, 136, 296, 700)])
+def test_slots_summed_in_parts(sdm, cuda_device, T, E, H, F, last, stored):
+    """Few experts with many slots: the matrices' gradient is summed in parts of them, of which
+    some may have no slot at all."""
+    from sparse_dense_matrix_gb300 import dynamic
+    assert dynamic.lib.spmm_routes_product_weights_workspace(T, E, H, F) > 0
+    dt = torch.float16
+    ids = torch.zeros(T, dtype=torch.int32)
+    ids[:last] = E - 1
+    routes = sdm.ExpertRoutes(ids[:, None].to(cuda_device), E)
+    xs, dys = (randn(cuda_device, 1 + i, T, n).to(dt) for i, n in enumerate((H, F)))
+    w = matrices(cuda_device, 3, E, H, F, dt, stored)
+    want = expected(routes.offsets, xs, w, dys)
+    for _ in range(2):                           # the scratch holds the first call's parts
+        for g, (x, tol) in zip(routes.product_backward(dys, xs, w), want[1:]):
+            ref.close(g, x, tol)
+    sdm.dynamic_sync()

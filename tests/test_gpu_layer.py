@@ -214,7 +214,8 @@ def test_outputs_are_written_whole(sdm, cuda_device):
         else:
             sh, sf = (F, 1) if name == "dw" else (1, H)
             st = dynamic.lib.spmm_routes_product_weights(1, xs.data_ptr(), grad.data_ptr(), off, P, E,
-                                                         H, F, out.data_ptr(), H * F, sh, sf, stream)
+                                                         H, F, out.data_ptr(), H * F, sh, sf, None, 0,
+                                                         stream)
             ref = want[2] if name == "dw" else want[2].transpose(1, 2).contiguous()
         assert st == 0
         torch.cuda.synchronize()
@@ -241,7 +242,7 @@ def test_bad_offsets_stay_in_bounds(sdm, cuda_device):
         assert L.spmm_routes_product(2, xs.data_ptr(), w.data_ptr(), H * F, F, 1, offsets.data_ptr(),
                                      P, E, H, F, ys.data_ptr(), stream) == 0
         assert L.spmm_routes_product_weights(2, xs.data_ptr(), grad.data_ptr(), offsets.data_ptr(), P,
-                                             E, H, F, dw.data_ptr(), H * F, F, 1, stream) == 0
+                                             E, H, F, dw.data_ptr(), H * F, F, 1, None, 0, stream) == 0
         sdm.dynamic_sync()
         for e in range(E):
             rows = slice(clamped[e], clamped[e + 1])

@@ -23,8 +23,9 @@ def product(L, dtype=1, xs=PTR, w=PTR, se=16 * 24, sh=24, sf=1, offsets=PTR, P=8
 
 
 def weights(L, dtype=1, xs=PTR, dys=PTR, offsets=PTR, P=8, E=3, H=16, F=24, dw=PTR, se=16 * 24,
-            sh=24, sf=1):
-    return L.spmm_routes_product_weights(dtype, xs, dys, offsets, P, E, H, F, dw, se, sh, sf, None)
+            sh=24, sf=1, work=None, need=0):
+    return L.spmm_routes_product_weights(dtype, xs, dys, offsets, P, E, H, F, dw, se, sh, sf, work,
+                                         need, None)
 
 
 @pytest.mark.parametrize("bad,status", [
@@ -47,6 +48,13 @@ def test_products_refuse_outputs(m):
     for bad in (dict(se=0), dict(sh=16), dict(sh=1, sf=8)):      # on top of one another
         assert weights(m.lib, **bad) == INVALID
     assert product(m.lib, sh=1 << 38) == UNSUPPORTED and product(m.lib, se=1 << 38) == UNSUPPORTED
+    # few experts with many slots: their parts need scratch
+    size = m.lib.spmm_routes_product_weights_workspace
+    assert size(8, 3, 16, 24) == 0 and size(1 << 20, 64, 4096, 4096) == 0 and size(-1, 3, 16, 24) == 0
+    need = size(100000, 3, 16, 24)
+    assert need == 25 * 3 * 16 * 24 * 4          # 76 pairs of CTAs for three tiles
+    assert weights(m.lib, P=100000) == INVALID and weights(m.lib, P=100000, work=ODD, need=need) == INVALID
+    assert weights(m.lib, P=100000, work=PTR, need=need - 1) == INVALID
     # nothing to do is no error, and needs no device
     assert product(m.lib, P=0, xs=None, ys=None) == 0 and product(m.lib, F=0, ys=None) == 0
     assert weights(m.lib, E=0, dw=None) == 0 and weights(m.lib, H=0, dw=None) == 0
