@@ -18,7 +18,7 @@
 // accumulators in tensor memory, and eight warps write the other one out meanwhile.
 //
 // Measured (bf16): 131072 slots of 128 experts that differ in popularity, 2048 x 1024, 340 us,
-// 1.62 PFLOP/s, of the rows 350, of the matrices 409 (DRAM at 47%, the tensor pipe active 85%
+// 1.62 PFLOP/s, of the rows 350, of the matrices 409 (DRAM at 47%, the tensor pipe active 83%
 // of the SMs' active cycles at the 1.6 GHz that power leaves); one expert with 8192 slots,
 // 8192 x 8192, 603, 655 and 560 us, next to 555 of the library's product of that size. 512 slots of
 // 128 experts, 2048 x 768 (226 MB of matrices), 37 us, 6.1 TB/s. 8 slots of 8 experts, 2048 x
