@@ -936,13 +936,29 @@ cudaError_t weights(int dtype, ExpertArgs &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Parts of an expert's slots in the gradient: as many as fill the pairs of CTAs that its tiles
-// leave idle, while a part has at least 512 slots of an average expert. (65536 slots of one
-// expert, 2048 x 1024: 170 us in two parts, 277 in one; 131072, 351 and 644.)
+// Parts of an expert's slots in the gradient: the number that is done soonest by an estimate,
+// in microseconds, for experts alike: a pair's 64 slots of a tile take 0.31, a tile's beginning
+// and end 1; parts take a launch more (4) and are written and read once at 5 TB/s.
+// Measured with one part and with this many: 65536 slots of one expert, 256 x 256, 276 us and 36
+// (54 parts), 2048 x 1024, 277 and 168 (7); 16384 of four experts, 512 x 512, 24 and 19 (4); 4096
+// of one, 256 x 256, 24 and 16 (13), 1024 x 1024, 24 and 20 (4).
 int64_t weight_splits(int64_t P, int64_t E, int64_t H, int64_t F) {
     if (E == 0 || H == 0 || F == 0) return 1;
-    const int64_t tiles = E * ((H + 255) / 256) * ((F + 255) / 256);
-    return std::max<int64_t>(1, std::min(kSms / 2 / tiles, P / (E * 512)));
+    constexpr int64_t pairs = kSms / 2;
+    const int64_t tiles = E * ((H + 255) / 256) * ((F + 255) / 256), slots = P / E;
+    if (tiles >= 2 * pairs) return 1;
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t n = 1; n <= pairs && (n == 1 || n * 128 <= slots); ++n) {
+        const double us = (double)((tiles * n + pairs - 1) / pairs) *
+                              ((double)((slots / n + 63) / 64) * 0.31 + 1.0) +
+                          (n > 1 ? 4.0 + (double)(n * E * H * F) * 1.6e-6 : 0.0);
+        if (n == 1 || us < least) {
+            best = n;
+            least = us;
+        }
+    }
+    return best;
 }
 
 }  // namespace
