@@ -344,13 +344,15 @@ class ExpertRoutes:
         dxs = torch.empty_like(xs)
         dw = torch.empty_like(w)
         need = lib.spmm_routes_product_weights_workspace(P, E, H, F)
-        work = torch.empty(need, dtype=torch.uint8, device=self.device).data_ptr() if need else None
+        # (held until the last launch: a freed one another thread on this stream could be given)
+        work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         st = lib.spmm_routes_product(dt, grad.data_ptr(), at, se, sf, sh, offsets, P, E, F, H,
                                      dxs.data_ptr(), handle)
         if st:
             _check(st, "spmm_routes_product")
         st = lib.spmm_routes_product_weights(dt, xs.data_ptr(), grad.data_ptr(), offsets, P, E, H, F,
-                                             *_matrix_strides(dw, "dw"), work, need, handle)
+                                             *_matrix_strides(dw, "dw"),
+                                             None if work is None else work.data_ptr(), need, handle)
         if st:
             _check(st, "spmm_routes_product_weights")
         return dxs, dw

@@ -1,0 +1,103 @@
+"""The matrices' gradient of few experts with many slots, whose parts go through scratch, in
+threads that share a stream, on other streams and in a captured graph."""
+import threading
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def sdm(cuda_device):
+    import sparse_dense_matrix_gb300 as m
+    return m
+
+
+def randn(dev, seed, *shape):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    return torch.randn(*shape, generator=g, device=dev)
+
+
+def told(sdm, stream=None):
+    """A stream hears of captured waits that gave up before: it is asked first."""
+    try:
+        sdm.dynamic_sync(stream)
+    except sdm.SpmmError:
+        pass
+
+
+def problem(sdm, dev, seed, T=5000, E=1, H=72, F=264):
+    from sparse_dense_matrix_gb300 import dynamic
+    assert dynamic.lib.spmm_routes_product_weights_workspace(T, E, H, F) > 0
+    ids = torch.arange(T, dtype=torch.int32, device=dev)[:, None] % E
+    xs, grad, w = (randn(dev, 3 * seed + i, *s).bfloat16()
+                   for i, s in enumerate(((T, H), (T, F), (E, H, F))))
+    return sdm.ExpertRoutes(ids.contiguous(), E), grad, xs, w
+
+
+def test_threads_that_share_a_stream(sdm, cuda_device):
+    dev = cuda_device
+    work = [problem(sdm, dev, i, E=1 + i % 2) for i in range(4)]
+    want = [r.product_backward(*a) for r, *a in work]
+    torch.cuda.synchronize()
+    told(sdm)
+    failed = []
+
+    def thread(i):
+        try:
+            torch.cuda.set_device(dev)
+            r, *a = work[i]
+            for _ in range(200):
+                # blocks of the scratch's and other sizes, written and given back at once
+                for n in (1 << 20, 72 * 264 * 39 * 4, 100):
+                    torch.empty(n, dtype=torch.uint8, device=dev).fill_(255)
+                got = r.product_backward(*a)
+            torch.cuda.synchronize()
+            if not all(torch.equal(x, y) for x, y in zip(want[i], got)):
+                failed.append("results differ")
+        except Exception as e:  # noqa: BLE001 (reported below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    sdm.dynamic_sync()
+
+
+def test_streams_and_graph(sdm, cuda_device):
+    dev = cuda_device
+    r, grad, xs, w = problem(sdm, dev, 7)
+    want = r.product_backward(grad, xs, w)
+    side = [torch.cuda.Stream() for _ in range(3)]
+    for s in side:
+        told(sdm, s)
+    torch.cuda.synchronize()
+    got = []
+    for s in side:
+        got.append(r.product_backward(grad, xs, w, stream=s))
+        with torch.cuda.stream(s):
+            got.append(r.product_backward(grad, xs, w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(want, g))
+    for s in side:
+        sdm.dynamic_sync(s)
+    # two graphs, replayed in turn and at once
+    graphs, kept = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            kept.append(r.product_backward(grad, xs, w))
+    grad.copy_(randn(dev, 50, *grad.shape))
+    torch.cuda.synchronize()
+    for s, g in zip(side, graphs):
+        with torch.cuda.stream(s):
+            for _ in range(20):
+                g.replay()
+    torch.cuda.synchronize()
+    want = r.product_backward(grad, xs, w)
+    assert all(torch.equal(a, b) for k in kept for a, b in zip(want, k))
+    sdm.dynamic_sync()

@@ -1,0 +1,71 @@
+"""The binding of the experts' products and of the heads without a GPU: the library's calls are
+stood in for, and tensors are the host's."""
+import weakref
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def dynamic():
+    import __graft_entry__
+    __graft_entry__.build()
+    import sparse_dense_matrix_gb300.dynamic as dynamic
+    return dynamic
+
+
+class Calls:
+    """The library, with some of its calls replaced."""
+
+    def __init__(self, lib, **calls):
+        self._lib = lib
+        self.__dict__.update(calls)
+
+    def __getattr__(self, name):
+        return getattr(self._lib, name)
+
+
+def host_routes(dynamic, monkeypatch, T, k, E):
+    """Routes whose tensors are the host's, and a binding that takes such."""
+    monkeypatch.setattr(dynamic, "_elsewhere", lambda dev, stream: None)
+    monkeypatch.setattr(dynamic, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(dynamic, "_tensor", lambda t, *a, **kw: t)
+    r = dynamic.ExpertRoutes.__new__(dynamic.ExpertRoutes)
+    r.device, r.num_experts, r.T, r.k, r._stream = torch.device("cpu"), E, T, k, 0
+    r.slots = torch.zeros(T, k, dtype=torch.int32)
+    r.offsets = torch.zeros(E + 1, dtype=torch.int32)
+    r._routes = (r.slots.data_ptr(), r.offsets.data_ptr(), T, k, E)
+    return r
+
+
+def test_gradients_scratch_is_held_until_its_last_launch(dynamic, monkeypatch):
+    """A tensor that nothing refers to goes back to the allocator: another thread on the same
+    stream could be given the scratch of the matrices' gradient before it is used."""
+    T, E, H, F = 5000, 1, 72, 264
+    need = dynamic.lib.spmm_routes_product_weights_workspace(T, E, H, F)
+    assert need > 0
+    routes = host_routes(dynamic, monkeypatch, T, 1, E)
+    made, seen, empty = [], [], torch.empty
+
+    def make(*args, **kw):
+        t = empty(*args, **kw)
+        if t.dtype == torch.uint8:
+            made.append((weakref.ref(t), t.data_ptr()))
+        return t
+
+    def launch(name):
+        def call(*args):
+            assert len(made) == 1 and made[0][0]() is not None, f"{name}: the scratch is gone"
+            seen.append(name)
+            if name == "weights":
+                assert args[-3:-1] == (made[0][1], need)
+            return 0
+        return call
+
+    monkeypatch.setattr(dynamic, "lib", Calls(dynamic.lib, spmm_routes_product=launch("rows"),
+                                              spmm_routes_product_weights=launch("weights")))
+    monkeypatch.setattr(torch, "empty", make)
+    xs, grad = (torch.zeros(T, n, dtype=torch.bfloat16) for n in (H, F))
+    routes.product_backward(grad, xs, torch.zeros(E, H, F, dtype=torch.bfloat16))
+    assert seen == ["rows", "weights"]
