@@ -160,9 +160,11 @@ struct HeadPlace {
 };
 
 // Sines and cosines of the warp's tokens' pairs, times the magnitude. The turn is cut to the
-// nearest half (exactly, in integers) before it becomes a float. What is left, x of at
-// most pi / 2, is off by 2^-24 of itself and goes into the two functions' power series,
-// whose first terms left out, x^13 / 13! and x^14 / 14!, are below 2^-24.
+// nearest half (exactly, in integers) before it becomes a float: with all of its 64 bits, as the
+// slowest pair's angles near position 0 are a few millionths of a radian, and its sine is
+// as exact as any. What is left, x of at most pi / 2, is off by at most 3 x 2^-24 of itself (its
+// conversion, the constant, their product) and goes into the two functions' power
+// series, whose first terms left out, x^13 / 13! and x^14 / 14!, are below 2^-24.
 struct HeadAngles {
     float c[128], s[128];            // of a warp: tokens x R / 2, at most 32 / lanes x 4 lanes
 };
@@ -175,10 +177,10 @@ __device__ __forceinline__ void angles(const HeadArgs &a, const HeadWalk &w, int
         const int64_t p =
             __shfl_sync(0xffffffffu, pos, (w.tokens == 1 ? 0 : token * w.at_once * a.lanes) & 31);
         if (i >= pairs * w.tokens) continue;
-        const uint32_t t = (uint32_t)(((uint64_t)p * __ldg(a.turns + (i - token * pairs))) >> 32);
+        const uint64_t t = (uint64_t)p * __ldg(a.turns + (i - token * pairs));
         // the sign of both functions: whether the nearest half turn is an odd one
-        const uint32_t odd = (t + (1u << 30)) & (1u << 31);
-        const float x = (float)(int32_t)(t ^ odd) * 1.46291807926716e-9f;    // 2 pi / 2^32
+        const uint32_t odd = ((uint32_t)(t >> 32) + (1u << 30)) & (1u << 31);
+        const float x = (float)(int64_t)(t ^ (uint64_t)odd << 32) * 3.40612158008655e-19f;  // 2 pi / 2^64
         const float y = x * x;
         float sx = fmaf(y, -1.0f / 39916800, 1.0f / 362880);
         sx = fmaf(y, sx, -1.0f / 5040);
