@@ -132,7 +132,8 @@ spmm_status spmm_routes_product(int dtype, const void *xs, const void *w, int64_
  * spmm_routes_product_weights -- the gradient of the matrices:
  *   dw[e, h, f] = sum over the slots s of e of xs[s, h] dys[s, f]; 0 without slots.
  *   dw : device, written whole, strides as w's above, no two elements in one place.
- * Scratch: for few experts with many slots, whose slots are then summed in parts.
+ * Scratch: for few experts with many slots, and for more than 2^24 slots, which are then
+ * summed in parts.
  */
 int64_t spmm_routes_product_weights_workspace(int64_t P, int64_t E, int64_t H, int64_t F);
 spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *dys,

@@ -942,18 +942,22 @@ cudaError_t weights(int dtype, ExpertArgs &p, cudaStream_t s) {
 // Measured with one part and with this many: 65536 slots of one expert, 256 x 256, 276 us and 36
 // (54 parts), 2048 x 1024, 277 and 168 (7); 16384 of four experts, 512 x 512, 24 and 19 (4); 4096
 // of one, 256 x 256, 24 and 16 (13), 1024 x 1024, 24 and 20 (4).
+// However the slots are spread, no part has more than kPartSlots: one expert may hold all of them,
+// and who waits for a tile's sum waits for all of its stages, 0.08 s of a limit of 0.5.
+constexpr int64_t kPartSlots = (int64_t)1 << 24;
 int64_t weight_splits(int64_t P, int64_t E, int64_t H, int64_t F) {
     if (E == 0 || H == 0 || F == 0) return 1;
     constexpr int64_t pairs = kSms / 2;
+    const int64_t fewest = std::max<int64_t>(1, (P + kPartSlots - 1) / kPartSlots);
     const int64_t tiles = E * ((H + 255) / 256) * ((F + 255) / 256), slots = P / E;
-    if (tiles >= 2 * pairs) return 1;
-    int64_t best = 1;
+    if (tiles >= 2 * pairs) return fewest;
+    int64_t best = fewest;
     double least = 0.0;
-    for (int64_t n = 1; n <= pairs && (n == 1 || n * 128 <= slots); ++n) {
+    for (int64_t n = fewest; n == fewest || (n <= pairs && n * 128 <= slots); ++n) {
         const double us = (double)((tiles * n + pairs - 1) / pairs) *
                               ((double)((slots / n + 63) / 64) * 0.31 + 1.0) +
                           (n > 1 ? 4.0 + (double)(n * E * H * F) * 1.6e-6 : 0.0);
-        if (n == 1 || us < least) {
+        if (n == fewest || us < least) {
             best = n;
             least = us;
         }
@@ -1027,7 +1031,8 @@ spmm_status spmm_routes_product_weights(int dtype, const void *xs, const void *d
     p.parts = (float *)work;
     p.M = (int)(by_f ? F : H);
     p.N = (int)(by_f ? H : F);
-    if (E * ((p.M + kRowsM - 1) / kRowsM) * ((p.N + 255) / 256) > (1 << 30)) return SPMM_ERR_UNSUPPORTED;
+    if (E * p.splits * ((p.M + kRowsM - 1) / kRowsM) * ((p.N + 255) / 256) > (1 << 30))
+        return SPMM_ERR_UNSUPPORTED;
     p.offsets = offsets;
     p.out = dw;
     p.o_se = dw_se;

@@ -101,3 +101,37 @@ def test_streams_and_graph(sdm, cuda_device):
     want = r.product_backward(grad, xs, w)
     assert all(torch.equal(a, b) for k in kept for a, b in zip(want, k))
     sdm.dynamic_sync()
+
+
+def test_one_of_many_experts_holds_all_slots(sdm, cuda_device):
+    """More than 2^24 slots of one of 160 experts: as many tiles as there are SMs, of which one
+    has all the work. It is summed in parts."""
+    import dynamic_ref as ref
+    from sparse_dense_matrix_gb300 import dynamic
+    dev, dt = cuda_device, torch.bfloat16
+    T, E, H, F, hot = (1 << 24) + 12345, 160, 8, 16, 77
+    assert dynamic.lib.spmm_routes_product_weights_workspace(T, E, H, F) == 2 * E * H * F * 4
+    ids = torch.full((T, 1), hot, dtype=torch.int32, device=dev)
+    ids[-100:] = 3
+    routes = sdm.ExpertRoutes(ids, E)
+    xs, grad = (torch.zeros(T, n, dtype=dt, device=dev) for n in (H, F))
+    # rows at the parts' ends and beginnings; the others add 0, exactly
+    half = (T - 100 + 1) // 2
+    some = torch.tensor([0, 99, 100, 101, 63 + 100, 4000000, half + 90, half + 110, half + 170,
+                         (1 << 24) - 1, 1 << 24, T - 1], device=dev)
+    xs[some], grad[some] = randn(dev, 1, len(some), H).to(dt), randn(dev, 2, len(some), F).to(dt)
+    w = randn(dev, 3, E, H, F).to(dt)
+    told(sdm)
+    dxs, dw = routes.product_backward(grad, xs, w)
+    sdm.dynamic_sync()
+    for e, at in ((3, some[some < 100]), (hot, some[some >= 100])):
+        x, g = xs[at].double(), grad[at].double()
+        want, mag = x.T @ g, x.abs().T @ g.abs()
+        # as many terms as there are rows, what an instruction may cut off of them, one rounding
+        ref.close(dw[e], want, ref.U[dt] * want.abs() + (len(at) + 32) * ref.E32 * mag)
+        dw[e] = 0
+        want, mag = g @ w[e].double().T, g.abs() @ w[e].double().abs().T
+        ref.close(dxs[at], want, ref.U[dt] * want.abs() + (F + 32) * ref.E32 * mag)
+    assert not dw.any()
+    dxs[some] = 0
+    assert not dxs.any()

@@ -69,3 +69,14 @@ def test_gradients_scratch_is_held_until_its_last_launch(dynamic, monkeypatch):
     xs, grad = (torch.zeros(T, n, dtype=torch.bfloat16) for n in (H, F))
     routes.product_backward(grad, xs, torch.zeros(E, H, F, dtype=torch.bfloat16))
     assert seen == ["rows", "weights"]
+
+
+@pytest.mark.parametrize("E,H,F", [(1, 8, 8), (152, 8, 8), (160, 256, 256), (2048, 64, 64),
+                                   (8, 1024, 1024), (3, 4096, 8)])
+def test_no_part_of_the_gradient_is_longer_than_its_waits(dynamic, E, H, F):
+    """One expert may hold all of the slots. 64 of them take 0.31 us, a wait gives up after
+    0.5 s: parts of at most 2^24 slots keep to a sixth of that."""
+    size = dynamic.lib.spmm_routes_product_weights_workspace
+    for P in (1 << 24, (1 << 24) + 1, 1 << 28, (1 << 31) - 65537):
+        parts = max(1, size(P, E, H, F) // (E * H * F * 4))
+        assert -(-P // parts) <= 1 << 24, (P, parts)
