@@ -537,6 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_experts(const __grid_constant__
                     }
                 }
             }
+            // The last stages' products are awaited too: their arrivals at `empty` (a pair's
+            // at both CTAs') are in nobody else's order, and must be there before the CTA ends.
+            for (int i = 0; ok && i < S::stages; ++i) {
+                ok = mbar_wait(&empty[stage], parity, p.err);
+                if (++stage == S::stages) {
+                    stage = 0;
+                    parity ^= 1;
+                }
+            }
             // another thread gave up: see the copies in flight land before the CTA ends
             // (those of a pair's second CTA are counted by the first: it waits for a while)
             if (!ok && rank == 1) mbar_wait(&drained, 0, p.err);

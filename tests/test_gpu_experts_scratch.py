@@ -135,3 +135,29 @@ def test_one_of_many_experts_holds_all_slots(sdm, cuda_device):
     assert not dw.any()
     dxs[some] = 0
     assert not dxs.any()
+
+
+def test_launches_right_behind_one_another(sdm, cuda_device):
+    """Products of pairs and of single CTAs, their gradients and the attention's tile kernels in
+    turn on the same SMs: each begins with barriers of its own in the shared memory that the
+    one before has just left."""
+    dev, dt = cuda_device, torch.bfloat16
+    E, H, F = 8, 256, 264
+    ids = torch.arange(2000, dtype=torch.int32, device=dev)[:, None] * 5 % E
+    many, few = sdm.ExpertRoutes(ids.contiguous(), E), sdm.ExpertRoutes(ids[:40].contiguous(), E)
+    xs, grad, w = (randn(dev, i, *s).to(dt)
+                   for i, s in enumerate(((2000, H), (2000, F), (E, H, F))))
+    q, k, v = (randn(dev, 3 + i, 1, 300, n, 64).to(dt) for i, n in enumerate((8, 2, 2)))
+    sel = sdm.select_blocks(q, sdm.block_means(k, 64), 3, 64, 300)
+
+    def step():
+        return [many.product(xs, w), sel.attend(q, k, v)[0], few.product(xs[:40], w),
+                *many.product_backward(grad, xs, w), sel.attend(q, k, v)[0],
+                *few.product_backward(grad[:40], xs[:40], w)]
+
+    told(sdm)
+    want = step()
+    for _ in range(100):
+        got = step()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    sdm.dynamic_sync()
