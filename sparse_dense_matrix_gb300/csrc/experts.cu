@@ -37,6 +37,7 @@ constexpr int kRowsM = 128;          // of m in a CTA's tile
 constexpr int kResults = 8;          // warps that write results out
 constexpr int kThreads = 128 + 32 * kResults;    // copies, products, tiles' list, segments' ends first
 constexpr int kTilesAhead = 4;
+constexpr int kSizes = 128;          // sizes that experts are sorted by (gradient)
 constexpr int kSmemMax = 227 * 1024;
 
 struct ExpertArgs {
@@ -63,7 +64,7 @@ template <int NT_, int NC_> struct ExpertShape {
     // results: 32 rows of 64 bytes for each warp
     static constexpr int out_bytes = 32 * 64;
     static constexpr int at_out = stages * stage, at_offsets = at_out + kResults * out_bytes;
-    static size_t bytes(int E) { return 1024 + at_offsets + sizeof(int32_t) * 2 * ((size_t)E + 1); }
+    static constexpr size_t bytes(int E) { return 1024 + at_offsets + sizeof(int32_t) * 2 * ((size_t)E + 1); }
 };
 
 struct ExpertTile {
@@ -149,18 +150,17 @@ __device__ __forceinline__ ExpertList expert_list(const ExpertArgs &p, int32_t *
             // like length follow one another, and CTAs that take them in turn end at about
             // the same time (65536 slots of 64 experts, the largest with 5 times the mean: 263
             // us without it, 229 with, 222 if they take them there and back).
-            constexpr int kKeys = 128;
-            __shared__ int32_t keys[kKeys];
+            __shared__ int32_t keys[kSizes];
             auto key = [&](int e) {
-                return kKeys - 1 - (__float_as_int((float)(first[e + 1] - first[e])) + 0x200000 -
+                return kSizes - 1 - (__float_as_int((float)(first[e + 1] - first[e])) + 0x200000 -
                                     __float_as_int(1.0f)) / 0x200000;
             };
-            for (int i = threadIdx.x; i < kKeys; i += 32) keys[i] = 0;
+            for (int i = threadIdx.x; i < kSizes; i += 32) keys[i] = 0;
             __syncwarp();
             for (int e = threadIdx.x; e < p.E; e += 32)
-                atomicAdd(&keys[min(max(key(e), 0), kKeys - 1)], 1);
+                atomicAdd(&keys[min(max(key(e), 0), kSizes - 1)], 1);
             __syncwarp();
-            for (int i0 = 0; i0 < kKeys; i0 += 32) {
+            for (int i0 = 0; i0 < kSizes; i0 += 32) {
                 const int mine = keys[i0 + threadIdx.x];
                 int x = mine;
 #pragma unroll
@@ -174,7 +174,7 @@ __device__ __forceinline__ ExpertList expert_list(const ExpertArgs &p, int32_t *
             __syncwarp();
             for (int e0 = 0; e0 < p.E; e0 += 32) {
                 const int e = e0 + (int)threadIdx.x;
-                const int k = e < p.E ? min(max(key(e), 0), kKeys - 1) : kKeys;
+                const int k = e < p.E ? min(max(key(e), 0), kSizes - 1) : kSizes;
                 const uint32_t same = __match_any_sync(0xffffffffu, k);
                 const int rank = __popc(same & ((1u << threadIdx.x) - 1));
                 if (e < p.E) before[keys[k] + rank] = e;
@@ -868,7 +868,10 @@ template <typename T, int NT, int NC, bool A_MN, bool GRAD>
 cudaError_t launch(const ExpertArgs &p, int64_t most, cudaStream_t s) {
     using S = ExpertShape<NT, NC>;
     // the kernel's limit is the process's: always the largest, as another thread may set it
-    static_assert(S::at_offsets + 1024 + 8 * (SPMM_ROUTES_MAX_EXPERTS + 1) <= kSmemMax, "fits");
+    // (besides: barriers, the tiles' ring, the tensor memory's address, the sort's sizes)
+    constexpr size_t fixed = sizeof(uint64_t) * (4 * S::stages + 2 * 2 + 1 + 2 * kTilesAhead) +
+                             sizeof(ExpertTile) * kTilesAhead + 16 + GRAD * sizeof(int32_t) * kSizes;
+    static_assert(S::bytes(SPMM_ROUTES_MAX_EXPERTS) + fixed <= kSmemMax, "fits");
     // (and once for each device)
     static std::atomic<uint64_t> done{0};
     int dev = 0;
