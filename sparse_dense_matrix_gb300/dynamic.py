@@ -184,17 +184,27 @@ class ExpertRoutes:
 
     def _sort(self, ids):
         T, k, E = self.T, self.k, self.num_experts
-        self._stream = stream = _raw_stream(self.device.index)
         self.slots = torch.empty_like(ids)
         self.offsets = ids.new_empty(E + 1)
         need = lib.spmm_routes_workspace(T, k, E)
         work = _scratch(ids, need)
-        # what every product's call begins its list of routes with
-        self._routes = (self.slots.data_ptr(), self.offsets.data_ptr(), T, k, E)
+        self._tell()
         st = lib.spmm_routes_sort(ids.data_ptr(), T, k, E, *self._routes[:2],
-                                  None if work is None else work.data_ptr(), need, stream)
+                                  None if work is None else work.data_ptr(), need, self._stream)
         if st:
             _check(st, "spmm_routes_sort")
+
+    def _tell(self):
+        """What every call begins its list of routes with, and the stream they were made on."""
+        self._routes = (self.slots.data_ptr(), self.offsets.data_ptr(), self.T, self.k,
+                        self.num_experts)
+        self._stream = _raw_stream(self.device.index)
+
+    def __setstate__(self, state):
+        # (a copy, or what a file held: its tensors are others)
+        self.__dict__.update(state)
+        self.device = self.slots.device
+        self._tell()
 
     def _on_stream(self):
         """The current stream, which the routes' own tensors are now used on."""

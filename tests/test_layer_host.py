@@ -1,5 +1,7 @@
 """The binding of the experts' products and of the heads without a GPU: the library's calls are
 stood in for, and tensors are the host's."""
+import copy
+import pickle
 import weakref
 
 import pytest
@@ -80,3 +82,17 @@ def test_no_part_of_the_gradient_is_longer_than_its_waits(dynamic, E, H, F):
     for P in (1 << 24, (1 << 24) + 1, 1 << 28, (1 << 31) - 65537):
         parts = max(1, size(P, E, H, F) // (E * H * F * 4))
         assert -(-P // parts) <= 1 << 24, (P, parts)
+
+
+def copies(x):
+    """x copied, copied whole, and written out and read again."""
+    return copy.copy(x), copy.deepcopy(x), pickle.loads(pickle.dumps(x))
+
+
+def test_copies_of_routes_use_their_own_tensors(dynamic, monkeypatch):
+    """Not the original's, which may be gone by the time the copy is used."""
+    routes = host_routes(dynamic, monkeypatch, 7, 2, 3)
+    for r in copies(routes):
+        assert r._routes == (r.slots.data_ptr(), r.offsets.data_ptr(), 7, 2, 3)
+        assert torch.equal(r.slots, routes.slots) and r.device == routes.device
+        assert r._stream == 0
