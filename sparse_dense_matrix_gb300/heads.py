@@ -167,11 +167,20 @@ class HeadRotation:
             raise ValueError("device must be a CUDA device (there is no CPU path)")
         with torch.cuda.device(device):
             self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
-            self.device = self.turns.device
-            self._stream = _raw_stream(self.device.index)
-        self._turns = self.turns.data_ptr() or None
+        self._tell()
         self._interleaved = 1 if layout == "interleaved" else 0
         self._weight_shape = (self.dim,)
+
+    def _tell(self):
+        """Where the frequencies are, and the stream they were made on."""
+        self.device = self.turns.device
+        self._turns = self.turns.data_ptr() or None
+        self._stream = _raw_stream(self.device.index)
+
+    def __setstate__(self, state):
+        # (a copy, as a model's are made, or what a file held: its tensor is another)
+        self.__dict__.update(state)
+        self._tell()
 
     def _on_stream(self):
         """The current stream, which the frequencies are now used on."""

@@ -46,3 +46,15 @@ def test_copied_routes(sdm, cuda_device, how):
     overwrite(dev)
     xs = other.dispatch(x)
     assert torch.equal(xs, want[0]) and torch.equal(other.product(xs, w), want[1])
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, written])
+def test_copied_rotation(sdm, cuda_device, how):
+    dev = cuda_device
+    rot, q = sdm.HeadRotation(128, device=dev), randn(dev, 1, 2, 50, 4, 128)
+    want = rot.rotate(q)[0]
+    other = how(rot)
+    del rot
+    torch.cuda.synchronize()
+    overwrite(dev)
+    assert torch.equal(other.rotate(q)[0], want)

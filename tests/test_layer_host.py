@@ -96,3 +96,15 @@ def test_copies_of_routes_use_their_own_tensors(dynamic, monkeypatch):
         assert r._routes == (r.slots.data_ptr(), r.offsets.data_ptr(), 7, 2, 3)
         assert torch.equal(r.slots, routes.slots) and r.device == routes.device
         assert r._stream == 0
+
+
+@pytest.mark.parametrize("rotary", [64, 0])
+def test_copies_of_a_rotation_use_their_own_frequencies(dynamic, monkeypatch, rotary):
+    import sparse_dense_matrix_gb300.heads as heads
+    monkeypatch.setattr(heads, "_raw_stream", lambda index: 0)
+    rot = heads.HeadRotation.__new__(heads.HeadRotation)
+    rot.turns, rot.dim, rot.rotary_dim = torch.arange(rotary // 2), 64, rotary
+    rot.device, rot._turns, rot._stream = rot.turns.device, rot.turns.data_ptr() or None, 0
+    for r in copies(rot):
+        assert r._turns == (r.turns.data_ptr() or None) and torch.equal(r.turns, rot.turns)
+        assert r._stream == 0 and r.dim == 64
