@@ -536,6 +536,16 @@ class BlockSelection:
         self.causal, self._lengths, self._kept = bool(causal), None, None
         self._stream = _raw_stream(self.device.index)
 
+    def __setstate__(self, state):
+        # (a copy, or what a file held: its tensors are others)
+        self.__dict__.update(state)
+        self.device, self._lists = self._mem.device, self._mem.data_ptr()
+        if self._kept is not None:
+            self._lengths = self._kept.data_ptr()
+        elif self._lengths is not None:          # behind the lists
+            self._lengths = self._lists + 4 * (self._mem.numel() - self._shape[0])
+        self._stream = _raw_stream(self.device.index)
+
     def _on_stream(self):
         """The current stream, which the selection's own tensors are now used on."""
         stream = _raw_stream(self.device.index)

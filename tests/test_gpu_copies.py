@@ -58,3 +58,20 @@ def test_copied_rotation(sdm, cuda_device, how):
     torch.cuda.synchronize()
     overwrite(dev)
     assert torch.equal(other.rotate(q)[0], want)
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, written])
+@pytest.mark.parametrize("lengths", [False, True])
+def test_copied_selection(sdm, cuda_device, lengths, how):
+    dev = cuda_device
+    q, k, v = (randn(dev, i, 2, 70, h, 64).bfloat16() for i, h in enumerate((4, 2, 2)))
+    L = torch.tensor([70, 41], dtype=torch.int32, device=dev) if lengths else None
+    sel = sdm.select_blocks(q, sdm.block_means(k, 16, L), 3, 16, 70, L)
+    want = sel.attend(q, k, v)
+    given = sdm.BlockSelection(sel.blocks.clone(), 16, 70, L)
+    others = [how(sel), how(given)]
+    del sel, given
+    torch.cuda.synchronize()
+    overwrite(dev)
+    for other in others:
+        assert all(torch.equal(a, b) for a, b in zip(other.attend(q, k, v), want))

@@ -108,3 +108,28 @@ def test_copies_of_a_rotation_use_their_own_frequencies(dynamic, monkeypatch, ro
     for r in copies(rot):
         assert r._turns == (r.turns.data_ptr() or None) and torch.equal(r.turns, rot.turns)
         assert r._stream == 0 and r.dim == 64
+
+
+@pytest.mark.parametrize("lengths", ["none", "behind the lists", "asked for", "given"])
+def test_copies_of_a_selection_use_their_own_lists(dynamic, monkeypatch, lengths):
+    monkeypatch.setattr(dynamic, "_raw_stream", lambda index: 0)
+    B, Tq, Hk, n = shape = (3, 2, 2, 4)
+    size = B * Tq * Hk * n
+    sel = dynamic.BlockSelection.__new__(dynamic.BlockSelection)
+    own = lengths in ("behind the lists", "asked for")
+    mem = torch.arange(size + 3, dtype=torch.int32) if own else \
+        torch.arange(size, dtype=torch.int32).view(shape)
+    sel._set(mem, shape, 16, 100, True)
+    if own:
+        sel._lengths = sel._lists + 4 * size
+        if lengths == "asked for":
+            assert sel.lengths.tolist() == [size, size + 1, size + 2]
+    elif lengths == "given":
+        sel._keep(torch.tensor([5, 6, 7], dtype=torch.int32))
+    for s in copies(sel):
+        assert s._lists == s._mem.data_ptr() and torch.equal(s.blocks, sel.blocks)
+        if lengths == "none":
+            assert s._lengths is None and s.lengths is None
+        else:
+            assert s._lengths == s.lengths.data_ptr() and torch.equal(s.lengths, sel.lengths)
+        assert s._stream == 0 and s.num_keys == 100
