@@ -76,7 +76,7 @@ def _frequencies(R, base, scaling):
     if kind != "none" and not (s is not None and math.isfinite(s) and s > 0):
         raise ValueError(f"scaling {kind!r} needs a positive factor, got {s}")
     length = how.get("original_length")
-    if "original_length" in wants[kind] and not (length is not None and length > 0):
+    if "original_length" in wants[kind] and not (length is not None and 0 < length < math.inf):
         raise ValueError(f"scaling {kind!r} needs a positive original_length, got {length}")
     unknown = sorted(set(how) - set(wants[kind]))
     if unknown:
@@ -93,6 +93,8 @@ def _frequencies(R, base, scaling):
             return R * math.log(length / (math.tau * turns)) / (2 * math.log(base))
 
         fast, slow = how.get("fast", 32.0), how.get("slow", 1.0)
+        if not math.inf > fast >= slow > 0:
+            raise ValueError(f"scaling 'parts' needs fast >= slow > 0, got {fast} and {slow}")
         lo = max(0, math.floor(pair(fast)))
         hi = min(R - 1, math.ceil(pair(slow)))
         ramp = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 1e-3))) for i in range(R // 2)]
@@ -160,6 +162,8 @@ class HeadRotation:
         self.dim, self.rotary_dim, self.layout = int(dim), int(R), layout
         self.frequencies = f
         self.magnitude = m if magnitude is None else float(magnitude)
+        if not math.isfinite(self.magnitude):
+            raise ValueError(f"magnitude must be finite, got {self.magnitude}")
         turns = [round(x / math.tau % 1.0 * 2 ** 64) % 2 ** 64 for x in f]
         turns = [x - 2 ** 64 if x >= 2 ** 63 else x for x in turns]
         device = torch.device(device)

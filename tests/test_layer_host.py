@@ -1,6 +1,7 @@
 """The binding of the experts' products and of the heads without a GPU: the library's calls are
 stood in for, and tensors are the host's."""
 import copy
+import math
 import pickle
 import weakref
 
@@ -133,3 +134,33 @@ def test_copies_of_a_selection_use_their_own_lists(dynamic, monkeypatch, lengths
         else:
             assert s._lengths == s.lengths.data_ptr() and torch.equal(s.lengths, sel.lengths)
         assert s._stream == 0 and s.num_keys == 100
+
+
+@pytest.mark.parametrize("how", [
+    {"kind": "parts", "slow": 0.0}, {"kind": "parts", "slow": -1.0}, {"kind": "parts", "fast": 0.0},
+    {"kind": "parts", "fast": 0.5}, {"kind": "parts", "fast": math.inf},
+    {"kind": "parts", "fast": math.nan}, {"kind": "parts", "slow": math.nan},
+    {"kind": "parts", "original_length": math.inf}, {"kind": "bands", "original_length": math.inf},
+    {"kind": "parts", "magnitude": math.nan}])
+def test_scalings_without_a_meaning_are_refused(dynamic, how):
+    import sparse_dense_matrix_gb300 as sdm
+    with pytest.raises(ValueError, match="scaling|magnitude"):
+        sdm.HeadRotation(64, scaling={"factor": 2.0, "original_length": 4096, **how})
+
+
+@pytest.mark.parametrize("magnitude", [math.nan, math.inf])
+def test_magnitude_is_finite(dynamic, magnitude):
+    import sparse_dense_matrix_gb300 as sdm
+    with pytest.raises(ValueError, match="magnitude"):
+        sdm.HeadRotation(64, magnitude=magnitude)
+
+
+def test_parts_between_equal_numbers_of_turns(dynamic):
+    """A step between two neighbouring pairs."""
+    import sparse_dense_matrix_gb300.heads as heads
+    how = {"kind": "parts", "factor": 8.0, "original_length": 4096, "fast": 8.0, "slow": 8.0}
+    f, _ = heads._frequencies(64, 1e4, how)
+    plain, _ = heads._frequencies(64, 1e4, None)
+    turns = [4096 * p / math.tau for p in plain]
+    assert all(x == p for x, p, t in zip(f, plain, turns) if t > 8.0)
+    assert all(abs(x * 8 / p - 1) < 1e-14 for x, p, t in zip(f, plain, turns) if t < 8.0)
