@@ -274,6 +274,7 @@ spmm_status spmm_heads_rotate(const spmm_heads_shape *s, spmm_rows q, spmm_rows 
  * their positions and the values v [B, T, Hk, D] as they are into another. Needs
  * lengths (those after the new tokens) and no positions. Keys at positions outside
  * [0, Tk) are not written; every other row of the caches stays as it is.
+ * The caches overlap neither each other nor q, k and v.
  */
 spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows k, spmm_rows v,
                               void *q_out, spmm_rows cache_k, spmm_rows cache_v, int64_t Tk,

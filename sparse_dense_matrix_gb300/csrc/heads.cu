@@ -745,7 +745,8 @@ spmm_status spmm_heads_append(const spmm_heads_shape *s, spmm_rows q, spmm_rows 
     const int e = dtype_bytes(s->dtype);
     if (s->Hq && (!rows_ok(q, e) || !q_out || (uintptr_t)q_out % 16)) return SPMM_ERR_INVALID_ARG;
     if (!rows_ok(k, e) || !rows_ok(v, e)) return SPMM_ERR_INVALID_ARG;
-    if (Tk && (!written_ok(cache_k, e, s, Tk) || !written_ok(cache_v, e, s, Tk)))
+    if (Tk && (!written_ok(cache_k, e, s, Tk) || !written_ok(cache_v, e, s, Tk) ||
+               cache_k.data == cache_v.data))    // keys and values in one place
         return SPMM_ERR_INVALID_ARG;
     HeadArgs a = forward_args(s, q, k, q_out, nullptr);
     a.from[2] = from(v, s->Hk, nullptr);

@@ -279,7 +279,7 @@ class HeadRotation:
 
         ``lengths``: each sequence's keys with the new ones, its last T. Keys at positions
         outside the cache (before the sequence's start, past its rows) are not written, and
-        no other row is."""
+        no other row is. The caches overlap neither each other nor q, k and v."""
         ctx = _elsewhere(self.device, stream)
         if ctx is not None:
             with ctx:
@@ -299,6 +299,8 @@ class HeadRotation:
         if cache_v.shape != want or (B, Hk, D) != (shape[0], shape[2], shape[3]):
             raise ValueError(f"cache_k and cache_v must be [{s.B}, rows, {s.Hk}, {s.D}], got "
                              f"{list(want)} and {list(cache_v.shape)}")
+        if ck.data == cv.data and cache_k.numel():
+            raise ValueError("cache_k and cache_v are in one place")
         for c, name in ((cache_k, "cache_k"), (cache_v, "cache_v")):
             strides = c.stride()
             if 0 in strides and any(n > 1 and x == 0 for n, x in zip(want, strides)):

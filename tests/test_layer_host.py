@@ -164,3 +164,38 @@ def test_parts_between_equal_numbers_of_turns(dynamic):
     turns = [4096 * p / math.tau for p in plain]
     assert all(x == p for x, p, t in zip(f, plain, turns) if t > 8.0)
     assert all(abs(x * 8 / p - 1) < 1e-14 for x, p, t in zip(f, plain, turns) if t < 8.0)
+
+
+def test_caches_in_one_place_are_refused(dynamic, monkeypatch):
+    """Keys and values would be written over one another."""
+    import ctypes
+    import sparse_dense_matrix_gb300.heads as heads
+    R, out = heads._Rows, ctypes.c_void_p(4096)              # (never read)
+    s = heads._HeadsShape(2, 3, 4, 2, 64, 32, 1, 0, 0, 1e-6, 1.0, 4096, None, 0, 0, 4096, None, None)
+    r, c, d = (R(4096 << i, 8192, 256, 64) for i in (0, 10, 20))
+    append = heads.lib.spmm_heads_append
+    assert append(s, r, r, r, out, c, c, 10, None) == 1
+    for bad in (R(None, 0, 0, 0), R(4104, 8192, 256, 64), R(4096, 0, 256, 64), R(4096, 8192, 0, 64),
+                R(4096, 8192, 256, 0)):                      # the others' checks stand
+        assert append(s, r, r, r, out, bad, d, 10, None) == 1
+        assert append(s, r, r, r, out, c, bad, 10, None) == 1
+
+    # the binding's own message, before the library is called
+    monkeypatch.setattr(heads, "_elsewhere", lambda dev, stream: None)
+    monkeypatch.setattr(heads, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(dynamic, "_tensor", lambda t, *a, **kw: t)
+    calls = []
+    monkeypatch.setattr(heads, "lib", Calls(heads.lib, spmm_heads_append=lambda *a: calls.append(a)))
+    rot = heads.HeadRotation.__new__(heads.HeadRotation)
+    rot.turns, rot.dim, rot.rotary_dim, rot.magnitude = torch.zeros(32).long(), 64, 64, 1.0
+    rot._interleaved, rot._weight_shape = 0, (64,)
+    rot._tell()
+    q, k, v = (torch.zeros(2, 1, n, 64) for n in (4, 2, 2))
+    ck, L = torch.zeros(2, 8, 2, 64), torch.ones(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="in one place"):
+        rot.append(q, k, v, ck, ck, L)
+    assert not calls
+    both = torch.zeros(2, 8, 2, 2, 64)                       # side by side is another thing
+    rot.append(q, k, v, both[:, :, 0], both[:, :, 1], L)
+    rot.append(q, k, v, ck[:, :0], ck[:, :0], L)             # and no rows have no place
+    assert len(calls) == 2
