@@ -483,6 +483,10 @@ class SparseAdj:
             raise ValueError("the max backward needs the forward's argmax")
         return self._t.maxpool_backward(argmax, grad, B=B)
 
+    def __reduce_ex__(self, protocol):
+        # (a copy would hold the same plan, and free it a second time)
+        raise TypeError("a SparseAdj cannot be copied or pickled: it holds a plan on its device")
+
     def close(self) -> None:
         for t in (getattr(self, "_t", None), getattr(self, "_tmean", None)):
             if t is not None:

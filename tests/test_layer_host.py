@@ -199,3 +199,13 @@ def test_caches_in_one_place_are_refused(dynamic, monkeypatch):
     rot.append(q, k, v, both[:, :, 0], both[:, :, 1], L)
     rot.append(q, k, v, ck[:, :0], ck[:, :0], L)             # and no rows have no place
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, pickle.dumps])
+def test_plans_are_not_copied(dynamic, how):
+    """Two of them would free one plan."""
+    import sparse_dense_matrix_gb300 as sdm
+    adj = sdm.SparseAdj.__new__(sdm.SparseAdj)
+    adj._plan = adj._t = adj._tmean = None
+    with pytest.raises(TypeError, match="cannot be copied"):
+        how(adj)
