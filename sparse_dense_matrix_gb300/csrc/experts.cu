@@ -17,13 +17,13 @@
 // copies), another (of the pair's first CTA) issues the products into one of two
 // accumulators in tensor memory, and eight warps write the other one out meanwhile.
 //
-// Measured (bf16): 131072 slots of 128 experts that differ in popularity, 2048 x 1024, 340 us,
-// 1.62 PFLOP/s, of the rows 350, of the matrices 409 (DRAM at 47%, the tensor pipe active 83%
-// of the SMs' active cycles at the 1.6 GHz that power leaves); one expert with 8192 slots,
-// 8192 x 8192, 603, 655 and 560 us, next to 555 of the library's product of that size. 512 slots of
-// 128 experts, 2048 x 768 (226 MB of matrices), 37 us, 6.1 TB/s. 8 slots of 8 experts, 2048 x
-// 1024, 10 us, of which 2.4 pass before the first product is issued and 6 by 32 stages of
-// one CTA after another on 64 SMs.
+// Measured (bf16): 131072 slots of 128 experts that differ in popularity, 2048 x 1024, 333 us for 20
+// calls in a row, 1.65 PFLOP/s, and 350 for 200 (power lowers the clock to 1.6 GHz), of the rows
+// 342, of the matrices 407 (DRAM at 47%, the tensor pipe active 83% of the SMs' active cycles); one
+// expert with 8192 slots, 8192 x 8192, 595, 591 and 597 us, next to 543 of the library's product of
+// that size. 512 slots of 128 experts, 2048 x 768 (226 MB of matrices are reached), 41 us, 5.5
+// TB/s. 8 slots of 8 experts, 2048 x 1024, 10 us (12 as a replayed graph), of which 2.4 pass before
+// the first product is issued and 6 by 32 stages of one CTA after another on 64 SMs.
 #include <cudaTypedefs.h>
 
 #include "umma.cuh"

@@ -16,12 +16,14 @@
 // Two rows are worked on side by side, as one row's chain (its sum over the lanes, the
 // root, the products) leaves the pipes idle, and four more are on their way meanwhile.
 //
-// Measured: 8192 tokens of 32 + 4 heads of 128 in bf16 (151 MB) 31 us, 4.9 TB/s; the same
-// walk without the arithmetic takes 24 us, a norm 2 and the angles 2 of the rest. A
-// training step of 2 x 4096 tokens of 16 + 2 heads 16 us forward (4.7 TB/s, partly from L2)
-// and 41 backward (113 MB; 2.8 TB/s). Bound by instructions: about 130 for a warp's 32 x 8
-// elements forward and 200 backward, issued in half of the cycles by the 20 and 12 warps
-// that fit an SM's registers.
+// Measured (replayed graphs): 8192 tokens of 32 + 4 heads of 128 in bf16 (151 MB) 33 to 35 us, 4.4
+// TB/s, heads of 64 18.5, 96 33, 256 (half as many) 36; in fp32 (302 MB) 54 us, 5.6 TB/s. A
+// training step of 2 x 4096 tokens of 16 + 2 heads 18.5 us forward and 43 backward (113 MB, 2.7
+// TB/s), in fp32 33 and 53. The walk without the arithmetic took 24 of 31 us, a norm 2 and the
+// angles 2 of the rest. Bound by latency: instructions issue in 56% and 46% of the cycles (forward,
+// backward), and the 20 and 12 warps that fit an SM's registers (27% and 17% of its places)
+// wait, for each that issues, 2.1 and 1.5 for memory, 1.5 and 1.5 for the instruction before and
+// 0.9 and 0.6 for the shuffles and shared memory.
 #include "blocks.cuh"
 
 namespace spmm {
