@@ -102,6 +102,12 @@ def _lent(dev, *tensors):
             t.record_stream(stream)
 
 
+# In place of the stream that an object's tensors were made on, where that is not known (a
+# copy's may be the original's own, or made on any stream): the first stream that uses them is
+# lent them, as every other one is, and is what is remembered then.
+_UNKNOWN = -1
+
+
 def _tensor(t, name, dtypes, ndim, dev=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -188,29 +194,31 @@ class ExpertRoutes:
         self.offsets = ids.new_empty(E + 1)
         need = lib.spmm_routes_workspace(T, k, E)
         work = _scratch(ids, need)
-        self._tell()
+        self._tell(_raw_stream(self.device.index))
         st = lib.spmm_routes_sort(ids.data_ptr(), T, k, E, *self._routes[:2],
                                   None if work is None else work.data_ptr(), need, self._stream)
         if st:
             _check(st, "spmm_routes_sort")
 
-    def _tell(self):
+    def _tell(self, stream):
         """What every call begins its list of routes with, and the stream they were made on."""
         self._routes = (self.slots.data_ptr(), self.offsets.data_ptr(), self.T, self.k,
                         self.num_experts)
-        self._stream = _raw_stream(self.device.index)
+        self._stream = stream
 
     def __setstate__(self, state):
         # (a copy, or what a file held: its tensors are others)
         self.__dict__.update(state)
         self.device = self.slots.device
-        self._tell()
+        self._tell(_UNKNOWN)
 
     def _on_stream(self):
         """The current stream, which the routes' own tensors are now used on."""
         stream = _raw_stream(self.device.index)
         if stream != self._stream:
             _lent(self.device, self.slots, self.offsets)
+            if self._stream == _UNKNOWN:
+                self._stream = stream
         return stream
 
     def _by_token(self, x, name):
@@ -544,13 +552,15 @@ class BlockSelection:
             self._lengths = self._kept.data_ptr()
         elif self._lengths is not None:          # behind the lists
             self._lengths = self._lists + 4 * (self._mem.numel() - self._shape[0])
-        self._stream = _raw_stream(self.device.index)
+        self._stream = _UNKNOWN
 
     def _on_stream(self):
         """The current stream, which the selection's own tensors are now used on."""
         stream = _raw_stream(self.device.index)
         if stream != self._stream:
             _lent(self.device, self._mem, self._kept)
+            if self._stream == _UNKNOWN:
+                self._stream = stream
         return stream
 
     def _keep(self, lengths):

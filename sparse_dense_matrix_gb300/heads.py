@@ -17,8 +17,8 @@ import math
 import torch
 
 from . import _check, lib
-from .dynamic import (_DTYPE, _INT, _Rows, _dense, _elsewhere, _heads, _lent, _like, _raw_stream,
-                      _tensor)
+from .dynamic import (_DTYPE, _INT, _UNKNOWN, _Rows, _dense, _elsewhere, _heads, _lent, _like,
+                      _raw_stream, _tensor)
 
 __all__ = ["HeadRotation"]
 
@@ -171,26 +171,28 @@ class HeadRotation:
             raise ValueError("device must be a CUDA device (there is no CPU path)")
         with torch.cuda.device(device):
             self.turns = torch.tensor(turns, dtype=torch.int64).to(device)
-        self._tell()
+        self._tell(_raw_stream(self.turns.device.index))
         self._interleaved = 1 if layout == "interleaved" else 0
         self._weight_shape = (self.dim,)
 
-    def _tell(self):
+    def _tell(self, stream):
         """Where the frequencies are, and the stream they were made on."""
         self.device = self.turns.device
         self._turns = self.turns.data_ptr() or None
-        self._stream = _raw_stream(self.device.index)
+        self._stream = stream
 
     def __setstate__(self, state):
         # (a copy, as a model's are made, or what a file held: its tensor is another)
         self.__dict__.update(state)
-        self._tell()
+        self._tell(_UNKNOWN)
 
     def _on_stream(self):
         """The current stream, which the frequencies are now used on."""
         stream = _raw_stream(self.device.index)
         if stream != self._stream:
             _lent(self.device, self.turns)
+            if self._stream == _UNKNOWN:
+                self._stream = stream
         return stream
 
     def _weight(self, w, name, dtype):

@@ -75,3 +75,29 @@ def test_copied_selection(sdm, cuda_device, lengths, how):
     overwrite(dev)
     for other in others:
         assert all(torch.equal(a, b) for a, b in zip(other.attend(q, k, v), want))
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy])
+def test_copies_on_another_stream_keep_their_memory(sdm, cuda_device, how):
+    """A copy made and used on another stream than the original, whose tensors it may share."""
+    dev, side = cuda_device, torch.cuda.Stream()
+    q = randn(dev, 1, 1, 4096, 8, 128)
+    rot = sdm.HeadRotation(128, device=dev)
+    want = rot.rotate(q)[0]
+    del rot
+    for _ in range(2):
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        rot = sdm.HeadRotation(128, device=dev)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            other = how(rot)
+            torch.cuda._sleep(200_000_000)       # 0.1 s
+            got = other.rotate(q)[0]
+        ptr, nbytes = other.turns.data_ptr(), other.turns.numel() * 8
+        del rot, other
+        keep = [torch.empty(nbytes, dtype=torch.uint8, device=dev) for _ in range(20)]
+        assert not side.query(), "the side stream is done already: nothing was tested"
+        assert not any(t.data_ptr() < ptr + nbytes and ptr < t.data_ptr() + nbytes for t in keep)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

@@ -90,13 +90,24 @@ def copies(x):
     return copy.copy(x), copy.deepcopy(x), pickle.loads(pickle.dumps(x))
 
 
+def first_use_lends(module, monkeypatch, x, tensors):
+    """A copy's tensors may be the original's, of another stream's memory: the first stream that
+    uses them is lent them, whichever it is, and others each time."""
+    lent = []
+    monkeypatch.setattr(module, "_lent", lambda dev, *t: lent.append(t))
+    for stream, count in ((0, 1), (0, 1), (7, 2), (7, 3), (0, 3)):
+        monkeypatch.setattr(module, "_raw_stream", lambda index: stream)
+        assert x._on_stream() == stream and len(lent) == count
+        assert len(lent[-1]) == len(tensors) and all(a is b for a, b in zip(lent[-1], tensors))
+
+
 def test_copies_of_routes_use_their_own_tensors(dynamic, monkeypatch):
     """Not the original's, which may be gone by the time the copy is used."""
     routes = host_routes(dynamic, monkeypatch, 7, 2, 3)
     for r in copies(routes):
         assert r._routes == (r.slots.data_ptr(), r.offsets.data_ptr(), 7, 2, 3)
         assert torch.equal(r.slots, routes.slots) and r.device == routes.device
-        assert r._stream == 0
+        first_use_lends(dynamic, monkeypatch, r, [r.slots, r.offsets])
 
 
 @pytest.mark.parametrize("rotary", [64, 0])
@@ -108,7 +119,8 @@ def test_copies_of_a_rotation_use_their_own_frequencies(dynamic, monkeypatch, ro
     rot.device, rot._turns, rot._stream = rot.turns.device, rot.turns.data_ptr() or None, 0
     for r in copies(rot):
         assert r._turns == (r.turns.data_ptr() or None) and torch.equal(r.turns, rot.turns)
-        assert r._stream == 0 and r.dim == 64
+        assert r.dim == 64
+        first_use_lends(heads, monkeypatch, r, [r.turns])
 
 
 @pytest.mark.parametrize("lengths", ["none", "behind the lists", "asked for", "given"])
@@ -133,7 +145,8 @@ def test_copies_of_a_selection_use_their_own_lists(dynamic, monkeypatch, lengths
             assert s._lengths is None and s.lengths is None
         else:
             assert s._lengths == s.lengths.data_ptr() and torch.equal(s.lengths, sel.lengths)
-        assert s._stream == 0 and s.num_keys == 100
+        assert s.num_keys == 100
+        first_use_lends(dynamic, monkeypatch, s, [s._mem, s._kept])
 
 
 @pytest.mark.parametrize("how", [
@@ -189,7 +202,7 @@ def test_caches_in_one_place_are_refused(dynamic, monkeypatch):
     rot = heads.HeadRotation.__new__(heads.HeadRotation)
     rot.turns, rot.dim, rot.rotary_dim, rot.magnitude = torch.zeros(32).long(), 64, 64, 1.0
     rot._interleaved, rot._weight_shape = 0, (64,)
-    rot._tell()
+    rot._tell(0)
     q, k, v = (torch.zeros(2, 1, n, 64) for n in (4, 2, 2))
     ck, L = torch.zeros(2, 8, 2, 64), torch.ones(2, dtype=torch.int32)
     with pytest.raises(ValueError, match="in one place"):
